@@ -21,7 +21,8 @@
  *    bounded wait that ran out, a plan that does not fit) never trap: the kernel
  *    ORs an EP_STATUS_* bit into the caller's `status` word, skips the offending
  *    access and returns. Read the word after the stream has synchronised.
- *  - All device pointers must be 16-byte aligned.
+ *  - All device pointers must be 16-byte aligned (the router, its gradient, the
+ *    combine's gradient and the 4-bit products ask less where they say so).
  *  - Logical ranks: on one GPU, the receive buffers of the other ranks are simply
  *    other device allocations; with peer access they may be peer memory.
  */
@@ -448,6 +449,177 @@ typedef struct {
 } ep_combine_args;
 
 int ep_combine_reduce(const ep_config *cfg, const ep_combine_args *args, ep_stream_t stream);
+
+/* ------------------------------------------------- router and its gradient */
+
+/*
+ * ep_route -- a rank's routing decision: the experts of every token (what ep_plan
+ * reads) and their gates (what ep_combine_reduce reads), from the router's logits.
+ * The pages start from a finished routing; these calls have no counterpart there.
+ * E = n_ranks * n_local_experts; cfg's K, N, msg_bytes and my_rank play no part.
+ *   logits          [num_tokens][E] fp32 or bf16 (logits_dtype), element aligned, rows
+ *                   logits_stride elements apart (0: E)
+ *   score           EP_SCORE_SIGMOID: s_i = 1 / (1 + e^-l_i); EP_SCORE_SOFTMAX: the
+ *                   softmax of the token's logits
+ *   bias            NULL, or [E] fp32, finite: added to the scores for the choice of the
+ *                   experts only (a load-balance bias), never to the gates
+ *   n_groups        the E experts in n_groups equal groups of consecutive ids (0 or 1:
+ *                   one group); a token chooses inside its best topk_groups groups
+ *   group_top       a group is worth its group_top (1 or 2) best experts: 1 by their
+ *                   choice value, 2 by the sum of the values (scores without a bias)
+ *   renormalize     nonzero: the chosen experts' scores are divided by their sum
+ *   scale           factor of all gates
+ *   topk_ids        [num_tokens][top_k] out, by descending choice value
+ *   gates           [num_tokens][top_k] fp32 out, or NULL
+ * The choice value is score + bias, without a bias the logit itself (the scores grow
+ * with it); equal values and equal groups go to the lower id. A logit of -inf or of
+ * its type's lowest value masks the expert: it has score 0, counts for no group, and is
+ * chosen, lowest ids first, only where too few others are left (in the chosen groups);
+ * its gate is 0. So every token gets top_k distinct valid ids, and one whose experts
+ * are all masked gets zero gates. A NaN logit ranks as masked and makes the token's
+ * gates NaN, as does +inf under the softmax.
+ * Limits (EP_ERR_UNSUPPORTED): top_k <= 32. EP_ERR_INVALID_ARG: n_groups does not
+ * divide E, or topk_groups groups have fewer than top_k experts.
+ */
+#define EP_SCORE_SOFTMAX 0
+#define EP_SCORE_SIGMOID 1
+#define EP_LOGITS_F32 0
+#define EP_LOGITS_BF16 1
+
+typedef struct {
+    const void *logits;
+    int64_t logits_stride;
+    int32_t logits_dtype;
+    int32_t score;
+    const float *bias;
+    int32_t n_groups;
+    int32_t topk_groups;
+    int32_t group_top;
+    int32_t renormalize;
+    float scale;
+    int32_t *topk_ids;
+    float *gates;
+} ep_route_args;
+
+int ep_route(const ep_config *cfg, const ep_route_args *args, ep_stream_t stream);
+
+/*
+ * ep_route_backward -- gradient of the gates with respect to the logits, the choice of
+ * the experts taken as given (no gradient through it, nor to the bias).
+ *   logits, logits_stride, logits_dtype, score, renormalize, scale   as in ep_route
+ *   topk_ids        [num_tokens][top_k] distinct experts of each token
+ *   dgates          [num_tokens][top_k] fp32
+ *   dlogits         [num_tokens][E] out in the logits' type, rows dlogits_stride
+ *                   elements apart (0: E); every element is written
+ *   status          EP_STATUS_ROUTING for an id outside [0, E): the slot is left out
+ * Masked experts get 0. Intermediate values are fp32, rounded once to dlogits.
+ * dlogits may be the logits themselves (same address and stride): a token's logits are
+ * read before its gradient is written.
+ */
+typedef struct {
+    const void *logits;
+    int64_t logits_stride;
+    int32_t logits_dtype;
+    int32_t score;
+    int32_t renormalize;
+    float scale;
+    const int32_t *topk_ids;
+    const float *dgates;
+    void *dlogits;
+    int64_t dlogits_stride;
+    uint32_t *status;
+} ep_route_backward_args;
+
+int ep_route_backward(const ep_config *cfg, const ep_route_backward_args *args,
+                      ep_stream_t stream);
+
+/*
+ * ep_combine_backward -- gradient of ep_combine_reduce's sum on rank cfg->my_rank.
+ *   recv_buf        the rows that were combined (ep_combine_reduce's recv_buf); no
+ *                   signal is waited for: the combine that came before has acquired them.
+ *                   NULL where dgates is
+ *   gates           [num_tokens][top_k] fp32; NULL where drows is
+ *   dout            [num_tokens][N] bf16
+ *   dgates          [num_tokens][top_k] fp32 out, or NULL:
+ *                   dgates[t][j] = sum_n dout[t][n] * row(t, j)[n], summed in fp32 in a
+ *                   fixed order
+ *   drows           [num_tokens][top_k][N] bf16 out (recv_buf's layout), or NULL:
+ *                   drow(t, j)[n] = bf16(gates[t][j] * dout[t][n]). May be recv_buf.
+ * At least one of dgates and drows is given. N is a multiple of 8 (as in the combine).
+ */
+typedef struct {
+    const uint8_t *recv_buf;
+    const float *gates;
+    const void *dout;
+    float *dgates;
+    void *drows;
+} ep_combine_backward_args;
+
+int ep_combine_backward(const ep_config *cfg, const ep_combine_backward_args *args,
+                        ep_stream_t stream);
+
+/* ------------------------------------------- expert products, 4-bit weights */
+
+/*
+ * ep_matvec_w4 -- the expert products of a few rows (decode) on 4-bit weights:
+ *   y[m][n] = sum_k W_e[n][k] * a[m][k]  for the rows m of local expert e,
+ * bf16 activations, fp32 sums, bf16 results. K and N come from cfg (cfg->dtype is
+ * EP_BF16); it needs K % 32 == 0 and takes any N >= 1. The weights of an expert
+ * without rows are not read.
+ *   A               [max_rows][K] bf16 in plan order, 16-byte aligned; or NULL: row m is
+ *                   the token gather_idx[m] names in x_ptrs (as ep_dispatch_gather reads
+ *                   them, [max_tokens_per_rank][K] bf16 each), without a dispatch call
+ *   W               [E_l][N][K/2] bytes, 16-byte aligned: the code of column 2i in byte
+ *                   i's low four bits, that of 2i+1 in its high four
+ *   w_format        EP_W4_INT:  W = (code - zero) * scale, codes 0..15;
+ *                               w_scales [E_l][N][K/group_size] bf16, w_zeros the same
+ *                               shape in bytes (0..15), or NULL: zero = 8 everywhere;
+ *                               group_size 32, 64 or 128, dividing K
+ *                   EP_W4_E2M1: codes are e2m1 numbers (0, .5, 1, 1.5, 2, 3, 4, 6 and
+ *                               their negatives from code 8 on); w_scales
+ *                               [E_l][N][K/32] bytes, scale = 2^(byte - 127) (255: NaN);
+ *                               group_size 32, w_zeros NULL
+ *   expert_offsets  [E_l+1] the plan (ep_plan)
+ *   max_rows        rows allocated for A (or gather_idx) and C
+ *   local_activation  EP_ACT_NONE: C = bf16(y). EP_ACT_SWIGLU: W holds the N/2 gate rows,
+ *                   then the N/2 up rows, and C[m][i] = bf16(SiLU(y[m][i]) * y[m][N/2+i])
+ *                   (N even)
+ *   C               [max_rows][N] bf16 out, or [max_rows][N/2]; rows past the plan's row
+ *                   count are not written
+ *   workspace       device memory of ep_matvec_w4_sizes bytes, zero before the first call
+ *                   that uses it; a call that ends without a status bit leaves it ready
+ *                   for the next. Calls that may run at the same time need one each.
+ *   status          EP_STATUS_BOUNDS for a gather index outside the token tables (that
+ *                   row of C is not written) or expert offsets that do not rise from
+ *                   >= 0 to <= max_rows (nothing is written); EP_STATUS_TIMEOUT if a bounded wait inside the kernel ran out
+ * Sums over k are taken in a fixed order: a call's result depends on its inputs alone
+ * (and on the GPU's number of SMs), not on timing.
+ */
+#define EP_W4_INT 0
+#define EP_W4_E2M1 1
+
+typedef struct {
+    const void *A;
+    const void *x_ptrs[EP_MAX_RANKS];
+    const int32_t *gather_idx;
+    const void *W;
+    const void *w_scales;
+    const uint8_t *w_zeros;
+    int32_t w_format;
+    int32_t group_size;
+    const int32_t *expert_offsets;
+    int64_t max_rows;
+    int32_t local_activation;
+    void *C;
+    void *workspace;
+    int64_t workspace_bytes;
+    uint32_t *status;
+} ep_w4_args;
+
+/* Workspace bytes of any ep_matvec_w4 call with this configuration. Host only. */
+int ep_matvec_w4_sizes(const ep_config *cfg, int64_t *workspace_bytes);
+
+int ep_matvec_w4(const ep_config *cfg, const ep_w4_args *args, ep_stream_t stream);
 
 /* ------------------------------------------------- peers in other processes */
 

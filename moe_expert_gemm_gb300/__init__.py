@@ -38,6 +38,13 @@ EP_STATUS_INTERNAL = 0x10
 EP_BF16 = 0
 EP_FP8_1D2D = 1
 
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
+EP_LOGITS_F32 = 0
+EP_LOGITS_BF16 = 1
+EP_W4_INT = 0
+EP_W4_E2M1 = 1
+
 _c_i32, _c_i64, _c_u64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p
 
 
@@ -87,6 +94,33 @@ class ep_swiglu_args(ctypes.Structure):
                 ("inter", _c_i32)]
 
 
+class ep_route_args(ctypes.Structure):
+    _fields_ = [("logits", _vp), ("logits_stride", _c_i64), ("logits_dtype", _c_i32),
+                ("score", _c_i32), ("bias", _vp), ("n_groups", _c_i32), ("topk_groups", _c_i32),
+                ("group_top", _c_i32), ("renormalize", _c_i32), ("scale", ctypes.c_float),
+                ("topk_ids", _vp), ("gates", _vp)]
+
+
+class ep_route_backward_args(ctypes.Structure):
+    _fields_ = [("logits", _vp), ("logits_stride", _c_i64), ("logits_dtype", _c_i32),
+                ("score", _c_i32), ("renormalize", _c_i32), ("scale", ctypes.c_float),
+                ("topk_ids", _vp), ("dgates", _vp), ("dlogits", _vp),
+                ("dlogits_stride", _c_i64), ("status", _vp)]
+
+
+class ep_combine_backward_args(ctypes.Structure):
+    _fields_ = [("recv_buf", _vp), ("gates", _vp), ("dout", _vp), ("dgates", _vp),
+                ("drows", _vp)]
+
+
+class ep_w4_args(ctypes.Structure):
+    _fields_ = [("A", _vp), ("x_ptrs", _vp * EP_MAX_RANKS), ("gather_idx", _vp), ("W", _vp),
+                ("w_scales", _vp), ("w_zeros", _vp), ("w_format", _c_i32),
+                ("group_size", _c_i32), ("expert_offsets", _vp), ("max_rows", _c_i64),
+                ("local_activation", _c_i32), ("C", _vp), ("workspace", _vp),
+                ("workspace_bytes", _c_i64), ("status", _vp)]
+
+
 EP_IPC_HANDLE_BYTES = 64
 
 
@@ -105,7 +139,9 @@ _lib = None
 
 EXPORTS = ("ep_plan_sizes", "ep_plan", "grouped_gemm_combine_send", "ep_combine_reduce",
            "ep_strerror", "grouped_gemm_combine_send_noalloc", "ep_scatter_send",
-           "ep_dispatch_gather", "ep_swiglu", "ep_ipc_export", "ep_ipc_import", "ep_ipc_close")
+           "ep_dispatch_gather", "ep_swiglu", "ep_ipc_export", "ep_ipc_import", "ep_ipc_close",
+           "ep_route", "ep_route_backward", "ep_combine_backward", "ep_matvec_w4_sizes",
+           "ep_matvec_w4")
 
 
 def load(build_if_missing: bool = True):
@@ -133,9 +169,16 @@ def load(build_if_missing: bool = True):
     L.ep_ipc_export.argtypes = [_vp, ctypes.POINTER(ep_ipc_handle)]
     L.ep_ipc_import.argtypes = [ctypes.POINTER(ep_ipc_handle), ctypes.POINTER(_vp)]
     L.ep_ipc_close.argtypes = [ctypes.POINTER(ep_ipc_handle), _vp]
+    for f, args in (("ep_route", ep_route_args), ("ep_route_backward", ep_route_backward_args),
+                    ("ep_combine_backward", ep_combine_backward_args),
+                    ("ep_matvec_w4", ep_w4_args)):
+        getattr(L, f).argtypes = [ctypes.POINTER(ep_config), ctypes.POINTER(args), _vp]
+    L.ep_matvec_w4_sizes.argtypes = [ctypes.POINTER(ep_config), ctypes.POINTER(_c_i64)]
     for f in ("ep_plan_sizes", "ep_plan", "grouped_gemm_combine_send", "ep_combine_reduce",
               "grouped_gemm_combine_send_noalloc", "ep_scatter_send", "ep_dispatch_gather",
-              "ep_swiglu", "ep_ipc_export", "ep_ipc_import", "ep_ipc_close"):
+              "ep_swiglu", "ep_ipc_export", "ep_ipc_import", "ep_ipc_close",
+              "ep_route", "ep_route_backward", "ep_combine_backward", "ep_matvec_w4_sizes",
+              "ep_matvec_w4"):
         getattr(L, f).restype = ctypes.c_int
     L.ep_strerror.argtypes = [ctypes.c_int]
     L.ep_strerror.restype = ctypes.c_char_p
@@ -217,6 +260,37 @@ def ep_swiglu(cfg: ep_config, args: ep_swiglu_args, stream=None) -> int:
 def ep_combine_reduce(cfg: ep_config, args: ep_combine_args, stream=None) -> int:
     return _check(load().ep_combine_reduce(ctypes.byref(cfg), ctypes.byref(args),
                                            stream_handle(stream)), "ep_combine_reduce")
+
+
+def ep_route(cfg: ep_config, args: ep_route_args, stream=None) -> int:
+    """The router: every token's experts (topk_ids) and gates from its logits."""
+    return _check(load().ep_route(ctypes.byref(cfg), ctypes.byref(args),
+                                  stream_handle(stream)), "ep_route")
+
+
+def ep_route_backward(cfg: ep_config, args: ep_route_backward_args, stream=None) -> int:
+    """Gradient of the gates with respect to the router's logits."""
+    return _check(load().ep_route_backward(ctypes.byref(cfg), ctypes.byref(args),
+                                           stream_handle(stream)), "ep_route_backward")
+
+
+def ep_combine_backward(cfg: ep_config, args: ep_combine_backward_args, stream=None) -> int:
+    """Gradients of the combine's sum: of the gates, of the combined rows."""
+    return _check(load().ep_combine_backward(ctypes.byref(cfg), ctypes.byref(args),
+                                             stream_handle(stream)), "ep_combine_backward")
+
+
+def ep_matvec_w4_sizes(cfg: ep_config) -> int:
+    """Workspace bytes of ep_matvec_w4 (zero the workspace before its first use)."""
+    out = _c_i64(0)
+    _check(load().ep_matvec_w4_sizes(ctypes.byref(cfg), ctypes.byref(out)), "ep_matvec_w4_sizes")
+    return int(out.value)
+
+
+def ep_matvec_w4(cfg: ep_config, args: ep_w4_args, stream=None) -> int:
+    """Expert products of a few rows on 4-bit weights with group scales."""
+    return _check(load().ep_matvec_w4(ctypes.byref(cfg), ctypes.byref(args),
+                                      stream_handle(stream)), "ep_matvec_w4")
 
 
 def ep_ipc_export(dev_ptr) -> ep_ipc_handle:

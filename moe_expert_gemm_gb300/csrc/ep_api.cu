@@ -122,6 +122,25 @@ bool pick_m_fastest(int64_t rows, int64_t tile_rows, int64_t n_blocks, int64_t K
     return m_fast < n_fast;
 }
 
+bool aligned_to(const void *p, uintptr_t bytes)
+{
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0;
+}
+
+constexpr int kMaxRouteTopK = 32;  // one lane of a warp per slot
+
+int logit_bytes(int dtype)
+{
+    return dtype == EP_LOGITS_BF16 ? 2 : 4;
+}
+
+bool valid_logits(int dtype, int score, int64_t stride, int E)
+{
+    return (dtype == EP_LOGITS_F32 || dtype == EP_LOGITS_BF16) &&
+           (score == EP_SCORE_SOFTMAX || score == EP_SCORE_SIGMOID) &&
+           (stride == 0 || (stride >= E && stride <= INT32_MAX));
+}
+
 int cuda_status(cudaError_t e)
 {
     return e == cudaSuccess ? EP_OK : EP_ERR_CUDA;
@@ -497,6 +516,204 @@ int ep_combine_reduce(const ep_config *cfg, const ep_combine_args *a, ep_stream_
     p.signal_mode = cfg->signal_mode;
     p.overlap_previous = a->overlap_previous;
     return cuda_status(ep::launch_combine(p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int ep_route(const ep_config *cfg, const ep_route_args *a, ep_stream_t stream)
+{
+    int rc = check_config(cfg);
+    if (rc != EP_OK)
+        return rc;
+    if (!a)
+        return EP_ERR_INVALID_ARG;
+    const int E = cfg->n_ranks * cfg->n_local_experts;
+    const int n_groups = a->n_groups > 1 ? a->n_groups : 1;
+    const int topk_groups = n_groups > 1 ? a->topk_groups : 1;
+    if (!valid_logits(a->logits_dtype, a->score, a->logits_stride, E) || a->n_groups < 0)
+        return EP_ERR_INVALID_ARG;
+    if (n_groups > 1 && (E % n_groups != 0 || topk_groups < 1 || topk_groups > n_groups ||
+                         (a->group_top != 1 && a->group_top != 2)))
+        return EP_ERR_INVALID_ARG;
+    if (cfg->top_k > topk_groups * (E / n_groups))
+        return EP_ERR_INVALID_ARG;  // fewer experts in the chosen groups than slots
+    if (cfg->top_k > kMaxRouteTopK)
+        return EP_ERR_UNSUPPORTED;
+    if (cfg->num_tokens == 0)
+        return EP_OK;
+    if (!a->logits || !a->topk_ids || !aligned_to(a->logits, logit_bytes(a->logits_dtype)) ||
+        !aligned_to(a->bias, 4) || !aligned_to(a->topk_ids, 4) || !aligned_to(a->gates, 4))
+        return EP_ERR_INVALID_ARG;
+    const int num_sms = sm_count();
+    if (num_sms <= 0)
+        return EP_ERR_CUDA;
+    ep::RouteParams p;
+    p.T = cfg->num_tokens;
+    p.E = E;
+    p.top_k = cfg->top_k;
+    p.n_groups = n_groups;
+    p.topk_groups = topk_groups;
+    p.group_top = a->group_top;
+    p.score = a->score;
+    p.renormalize = a->renormalize ? 1 : 0;
+    p.bf16 = a->logits_dtype == EP_LOGITS_BF16;
+    p.stride = a->logits_stride ? a->logits_stride : E;
+    p.scale = a->scale;
+    p.logits = a->logits;
+    p.bias = a->bias;
+    p.topk_ids = a->topk_ids;
+    p.gates = a->gates;
+    return cuda_status(ep::launch_route(p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int ep_route_backward(const ep_config *cfg, const ep_route_backward_args *a, ep_stream_t stream)
+{
+    int rc = check_config(cfg);
+    if (rc != EP_OK)
+        return rc;
+    if (!a)
+        return EP_ERR_INVALID_ARG;
+    const int E = cfg->n_ranks * cfg->n_local_experts;
+    if (!valid_logits(a->logits_dtype, a->score, a->logits_stride, E) ||
+        (a->dlogits_stride != 0 && a->dlogits_stride < E))
+        return EP_ERR_INVALID_ARG;
+    if (cfg->top_k > kMaxRouteTopK)
+        return EP_ERR_UNSUPPORTED;
+    if (cfg->num_tokens == 0)
+        return EP_OK;
+    const int b = logit_bytes(a->logits_dtype);
+    if (!a->logits || !a->topk_ids || !a->dgates || !a->dlogits || !a->status ||
+        !aligned_to(a->logits, b) || !aligned_to(a->dlogits, b) || !aligned_to(a->topk_ids, 4) ||
+        !aligned_to(a->dgates, 4) || !aligned_to(a->status, 4))
+        return EP_ERR_INVALID_ARG;
+    const int num_sms = sm_count();
+    if (num_sms <= 0)
+        return EP_ERR_CUDA;
+    ep::RouteBackwardParams p;
+    p.T = cfg->num_tokens;
+    p.E = E;
+    p.top_k = cfg->top_k;
+    p.score = a->score;
+    p.renormalize = a->renormalize ? 1 : 0;
+    p.bf16 = a->logits_dtype == EP_LOGITS_BF16;
+    p.stride = a->logits_stride ? a->logits_stride : E;
+    p.dstride = a->dlogits_stride ? a->dlogits_stride : E;
+    p.scale = a->scale;
+    p.logits = a->logits;
+    p.topk_ids = a->topk_ids;
+    p.dgates = a->dgates;
+    p.dlogits = a->dlogits;
+    p.status = a->status;
+    return cuda_status(
+        ep::launch_route_backward(p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int ep_combine_backward(const ep_config *cfg, const ep_combine_backward_args *a,
+                        ep_stream_t stream)
+{
+    int rc = check_config(cfg);
+    if (rc != EP_OK)
+        return rc;
+    if (!a || (!a->dgates && !a->drows) || cfg->N % 8 != 0)
+        return EP_ERR_INVALID_ARG;
+    if (cfg->num_tokens == 0)
+        return EP_OK;
+    if (!a->dout || (a->dgates && !a->recv_buf) || (a->drows && !a->gates) ||
+        !aligned16(a->dout) || !aligned16(a->recv_buf) || !aligned16(a->drows) ||
+        !aligned_to(a->gates, 4) || !aligned_to(a->dgates, 4))
+        return EP_ERR_INVALID_ARG;
+    const int num_sms = sm_count();
+    if (num_sms <= 0)
+        return EP_ERR_CUDA;
+    ep::CombineBackwardParams p;
+    p.T = cfg->num_tokens;
+    p.top_k = cfg->top_k;
+    p.N = cfg->N;
+    p.recv_buf = a->recv_buf;
+    p.gates = a->gates;
+    p.dout = static_cast<const uint8_t *>(a->dout);
+    p.dgates = a->dgates;
+    p.drows = static_cast<uint8_t *>(a->drows);
+    return cuda_status(
+        ep::launch_combine_backward(p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int ep_matvec_w4_sizes(const ep_config *cfg, int64_t *workspace_bytes)
+{
+    int rc = check_config(cfg);
+    if (rc != EP_OK)
+        return rc;
+    if (!workspace_bytes)
+        return EP_ERR_INVALID_ARG;
+    *workspace_bytes = ep::w4_workspace_bytes();
+    return EP_OK;
+}
+
+int ep_matvec_w4(const ep_config *cfg, const ep_w4_args *a, ep_stream_t stream)
+{
+    int rc = check_config(cfg);
+    if (rc != EP_OK)
+        return rc;
+    if (!a)
+        return EP_ERR_INVALID_ARG;
+    if (cfg->dtype != EP_BF16 || cfg->K % 32 != 0)
+        return EP_ERR_UNSUPPORTED;  // bf16 activations; weight rows of whole 16-byte pieces
+    if (a->w_format == EP_W4_E2M1) {
+        if (a->group_size != 32 || a->w_zeros)
+            return EP_ERR_INVALID_ARG;
+    } else if (a->w_format == EP_W4_INT) {
+        if ((a->group_size != 32 && a->group_size != 64 && a->group_size != 128) ||
+            cfg->K % a->group_size != 0)
+            return EP_ERR_INVALID_ARG;
+    } else {
+        return EP_ERR_INVALID_ARG;
+    }
+    if (a->local_activation != EP_ACT_NONE &&
+        (a->local_activation != EP_ACT_SWIGLU || cfg->N % 2 != 0))
+        return EP_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(cfg->n_local_experts) * cfg->N >= INT32_MAX)
+        return EP_ERR_UNSUPPORTED;  // weight rows are counted in 32 bits
+    if (!a->W || !a->w_scales || !a->expert_offsets || !a->C || !a->workspace || !a->status)
+        return EP_ERR_INVALID_ARG;
+    if (!aligned16(a->A) || !aligned16(a->W) || !aligned16(a->workspace) ||
+        !aligned_to(a->w_scales, a->w_format == EP_W4_E2M1 ? 1 : 2) || !aligned_to(a->C, 2) ||
+        !aligned_to(a->expert_offsets, 4) || !aligned_to(a->status, 4))
+        return EP_ERR_INVALID_ARG;
+    if (a->max_rows < 1 || a->max_rows > INT32_MAX ||
+        a->workspace_bytes < ep::w4_workspace_bytes())
+        return EP_ERR_INVALID_ARG;
+    ep::W4Params p;
+    std::memset(&p, 0, sizeof p);
+    if (!a->A) {
+        if (!a->gather_idx || !aligned_to(a->gather_idx, 4))
+            return EP_ERR_INVALID_ARG;
+        for (int r = 0; r < cfg->n_ranks; ++r) {
+            if (!a->x_ptrs[r] || !aligned16(a->x_ptrs[r]))
+                return EP_ERR_INVALID_ARG;
+            p.x[r] = static_cast<const uint8_t *>(a->x_ptrs[r]);
+        }
+    }
+    const int num_sms = sm_count();
+    if (num_sms <= 0)
+        return EP_ERR_CUDA;
+    p.n_ranks = cfg->n_ranks;
+    p.El = cfg->n_local_experts;
+    p.top_k = cfg->top_k;
+    p.T = cfg->num_tokens;
+    p.K = cfg->K;
+    p.N = cfg->N;
+    p.format = a->w_format;
+    p.group = a->group_size;
+    p.swiglu = a->local_activation == EP_ACT_SWIGLU ? 1 : 0;
+    p.max_rows = a->max_rows;
+    p.A = static_cast<const uint8_t *>(a->A);
+    p.gather_idx = a->gather_idx;
+    p.W = static_cast<const uint8_t *>(a->W);
+    p.scales = a->w_scales;
+    p.zeros = a->w_zeros;
+    p.expert_offsets = a->expert_offsets;
+    p.C = static_cast<uint8_t *>(a->C);
+    p.workspace = static_cast<uint8_t *>(a->workspace);
+    p.status = a->status;
+    return cuda_status(ep::launch_matvec_w4(p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 const char *ep_strerror(int code)

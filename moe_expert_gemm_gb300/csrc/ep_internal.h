@@ -128,6 +128,56 @@ struct CombineParams {
     int overlap_previous;  // EP_OVERLAP_*: programmatic dependent of the previous kernel
 };
 
+// The router (ep_route.cu).
+struct RouteParams {
+    int T, E, top_k, n_groups, topk_groups, group_top, score, renormalize;
+    int bf16;  // logits type
+    int64_t stride;
+    float scale;
+    const void *logits;
+    const float *bias;
+    int32_t *topk_ids;
+    float *gates;
+};
+
+struct RouteBackwardParams {
+    int T, E, top_k, score, renormalize;
+    int bf16;
+    int64_t stride, dstride;
+    float scale;
+    const void *logits;
+    const int32_t *topk_ids;
+    const float *dgates;
+    void *dlogits;
+    uint32_t *status;
+};
+
+struct CombineBackwardParams {
+    int T, top_k, N;
+    const uint8_t *recv_buf;
+    const float *gates;
+    const uint8_t *dout;
+    float *dgates;
+    uint8_t *drows;
+};
+
+// The expert products on 4-bit weights (ep_matvec_w4.cu).
+struct W4Params {
+    int n_ranks, El, top_k, T, K, N;
+    int format, group, swiglu;
+    int64_t max_rows;
+    const uint8_t *A;
+    const uint8_t *x[EP_MAX_RANKS];
+    const int32_t *gather_idx;
+    const uint8_t *W;
+    const void *scales;
+    const uint8_t *zeros;
+    const int32_t *expert_offsets;
+    uint8_t *C;
+    uint8_t *workspace;
+    uint32_t *status;
+};
+
 // A checked grouped_gemm_combine_send call, ready to launch: prepare_send runs every
 // host check (returning EP_ERR_* with nothing enqueued), encodes the tensor maps and
 // picks the kernel; launch_prepared_send enqueues it (EP_OK or EP_ERR_CUDA).
@@ -154,5 +204,10 @@ cudaError_t launch_combine(const CombineParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_scatter(const ScatterParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_dispatch_gather(const DispatchParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_swiglu(const SwigluParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_route(const RouteParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_route_backward(const RouteBackwardParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_combine_backward(const CombineBackwardParams &p, int num_sms, cudaStream_t s);
+int64_t w4_workspace_bytes();
+cudaError_t launch_matvec_w4(const W4Params &p, int num_sms, cudaStream_t s);
 
 }  // namespace ep
