@@ -709,11 +709,19 @@ int ep_matvec_w4(const ep_config *cfg, const ep_w4_args *a, ep_stream_t stream)
     p.W = static_cast<const uint8_t *>(a->W);
     p.scales = a->w_scales;
     p.zeros = a->w_zeros;
+    p.scale_vec = cfg->K % 256 == 0 && aligned16(a->w_scales) && aligned_to(a->w_zeros, 8);
     p.expert_offsets = a->expert_offsets;
     p.C = static_cast<uint8_t *>(a->C);
     p.workspace = static_cast<uint8_t *>(a->workspace);
     p.status = a->status;
-    return cuda_status(ep::launch_matvec_w4(p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
+    // steps of 128 bytes (256 codes) by 64 weight rows
+    CUtensorMap tw;
+    if (!encode_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->W, static_cast<uint64_t>(cfg->K) / 2,
+                   static_cast<uint64_t>(cfg->n_local_experts) * cfg->N,
+                   static_cast<uint64_t>(cfg->K) / 2, 128, 64))
+        return EP_ERR_CUDA;
+    return cuda_status(
+        ep::launch_matvec_w4(tw, p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 const char *ep_strerror(int code)

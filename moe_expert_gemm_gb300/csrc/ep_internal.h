@@ -165,6 +165,7 @@ struct CombineBackwardParams {
 struct W4Params {
     int n_ranks, El, top_k, T, K, N;
     int format, group, swiglu;
+    int scale_vec;  // a step's scales (and zero points) of a row are one aligned piece
     int64_t max_rows;
     const uint8_t *A;
     const uint8_t *x[EP_MAX_RANKS];
@@ -208,6 +209,7 @@ cudaError_t launch_route(const RouteParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_route_backward(const RouteBackwardParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_combine_backward(const CombineBackwardParams &p, int num_sms, cudaStream_t s);
 int64_t w4_workspace_bytes();
-cudaError_t launch_matvec_w4(const W4Params &p, int num_sms, cudaStream_t s);
+cudaError_t launch_matvec_w4(const CUtensorMap &tw, const W4Params &p, int num_sms,
+                             cudaStream_t s);
 
 }  // namespace ep

@@ -1,6 +1,27 @@
 // Expert products of a few rows on 4-bit weights: C[m][n] = sum_k W_e[n][k] a[m][k].
 //
-// One warp forms one output element: its lanes walk the weight row 8 codes at a time.
+// Every weight of an expert that has rows is read once and meets a handful of activation
+// rows, so the call is bound by the weights' bytes, N*K/2 per expert, as long as the codes
+// become multiplicands fast enough. The weights are therefore the 16-row operand of the
+// warp's 16x8x16 bf16 matrix instruction and the activation rows its 8 columns: 8 rows
+// cost the same unpacking as one.
+//
+//  * A code becomes an exact bf16 multiple of (q - zero), or of its e2m1 value, in a mask
+//    and a fused multiply-add (unpack_int, unpack_e2m1). The sum over a group of k runs in
+//    fp32 on these numbers; the group's scale multiplies that sum in fp32, so no weight is
+//    ever rounded.
+//  * The order of k inside a matrix instruction is free. A thread's 32-bit word of a
+//    weight row holds 8 consecutive codes, whose halves are the pairs (0,4) (1,5) (2,6)
+//    (3,7); the activations are laid into shared memory in that order.
+//  * Work is counted in steps of 256 k by 128 weight rows (16 KB), ordered by expert,
+//    column tile, chunk of 8*NT rows and k, and cut into equal runs, one per thread
+//    block, wherever the cuts fall. A tile cut between blocks is joined through the
+//    workspace: every block leaves its fp32 partial sums there, the last one to arrive
+//    adds them in block order.
+//  * Thread block: one producer thread streams the weights with TMA into a ring of
+//    stages; four staging warps bring the activation rows and scales of a step;
+//    eight consumer warps own 16 weight rows each (8 of the tile's first half and 8 of
+//    its second: with SwiGLU the gate and the up row of the same output).
 #include <cuda_bf16.h>
 
 #include "ep_internal.h"
@@ -8,104 +29,710 @@
 
 namespace ep {
 
-constexpr int kW4Threads = 256;
+namespace {
 
-__device__ __forceinline__ float e2m1_value(uint32_t code)
+constexpr int kTileRows = 128;                   // weight rows of a step
+constexpr int kStepK = 256;                      // k of a step: 128 bytes of codes a row
+constexpr int kStepBytes = kTileRows * kStepK / 2;
+constexpr int kConsumers = 8, kStagers = 4;      // warps
+constexpr int kW4Threads = 32 * (1 + kStagers + kConsumers);
+constexpr int kMaxStages = 5;
+constexpr int kW4MaxBlocks = 320;
+constexpr int kMaxNT = 4;
+constexpr int kSmemPerBlock = 113 * 1024;        // two blocks on an SM
+constexpr uint64_t kW4TimeoutNs = 2000000000ull;
+
+struct Shared {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    int64_t first_unit[EP_MAX_LOCAL_EXPERTS + 1];  // units before each expert
+    int offsets[EP_MAX_LOCAL_EXPERTS + 1];
+    int bad;
+    int abort;
+    int last;
+};
+
+// Weights, activations, scales and zero points (both bf16) of a step; a multiple of the
+// 1 KB the swizzled weight tiles start on.
+constexpr int stage_bytes(int NT, int GS)
 {
-    const float mag = code & 6 ? static_cast<float>(2 + (code & 1)) * static_cast<float>(1 << ((code >> 1 & 3) - 1)) * 0.5f
-                               : 0.5f * (code & 1);
-    return code & 8 ? -mag : mag;
+    return (kStepBytes + NT * 8 * kStepK * 2 + kTileRows * GS * 4 + 1023) / 1024 * 1024;
 }
 
-__device__ float w4_dot(const W4Params &p, int e, int64_t n, const uint8_t *a, int lane)
+constexpr int stages_of(int NT, int GS)
 {
-    const int64_t row = static_cast<int64_t>(e) * p.N + n;
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(p.W + row * (p.K / 2));
-    const int groups = p.K / p.group;
-    float sum = 0.f;
-    for (int c = lane; c < p.K / 8; c += 32) {
-        const uint32_t codes = __ldg(w + c);
-        const uint4 av = __ldg(reinterpret_cast<const uint4 *>(a) + c);
-        const uint32_t x[4] = {av.x, av.y, av.z, av.w};
-        const int64_t g = row * groups + c * 8 / p.group;
-        float scale, zero = 8.f;
-        if (p.format == EP_W4_E2M1) {
-            const uint32_t b = __ldg(static_cast<const uint8_t *>(p.scales) + g);
-            scale = b == 255 ? NAN : b ? __uint_as_float(b << 23) : 0x1p-127f;
+    const int n = (kSmemPerBlock - 1024 - static_cast<int>(sizeof(Shared))) / stage_bytes(NT, GS);
+    return n > kMaxStages ? kMaxStages : n;
+}
+
+// Staging warps work in teams, team i on every `teams`-th step. A team may look at a
+// stage's barrier only when at most one of its phases is open (a wait knows a phase's
+// parity alone), so there are no more teams than stages.
+constexpr int teams_of(int NT, int GS)
+{
+    return stages_of(NT, GS) < kStagers ? stages_of(NT, GS) : kStagers;
+}
+
+constexpr int smem_bytes(int NT, int GS)
+{
+    return 1024 + stages_of(NT, GS) * stage_bytes(NT, GS) + static_cast<int>(sizeof(Shared));
+}
+
+// One block's share of one tile: steps [s0, s1) of `steps`.
+struct Segment {
+    int e, m0, m1, n0;  // expert, its rows [m0, m1), first column
+    int s0, s1;
+    int64_t first;      // number of the tile's first step
+};
+
+struct Walk {
+    int64_t total, at, end;
+    int64_t blocks;  // that have work: every run has a step
+    int steps, tiles;
+
+    __device__ Walk(const W4Params &p, const Shared &sh, int tile_cols, int cols)
+    {
+        steps = (p.K + kStepK - 1) / kStepK;
+        tiles = (cols + tile_cols - 1) / tile_cols;
+        total = sh.first_unit[p.El] * steps;
+        blocks = total < gridDim.x ? total : gridDim.x;
+        const bool idle = blockIdx.x >= blocks;
+        at = idle ? 0 : total * blockIdx.x / blocks;
+        end = idle ? 0 : total * (blockIdx.x + 1) / blocks;
+    }
+
+    // The block whose run holds step i.
+    __device__ int owner(int64_t i) const
+    {
+        return static_cast<int>(((i + 1) * blocks - 1) / total);
+    }
+
+    __device__ bool next(const W4Params &p, const Shared &sh, int chunk_rows, int tile_cols,
+                         Segment &s)
+    {
+        if (at >= end)
+            return false;
+        const int64_t unit = at / steps;
+        s.first = unit * steps;
+        s.s0 = static_cast<int>(at - s.first);
+        s.s1 = static_cast<int>(end - s.first < steps ? end - s.first : steps);
+        at = s.first + s.s1;
+        int lo = 0, hi = p.El;  // first_unit[lo] <= unit < first_unit[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (sh.first_unit[mid] <= unit)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        s.e = lo;
+        const int64_t u = unit - sh.first_unit[lo];
+        const int r0 = sh.offsets[lo], r1 = sh.offsets[lo + 1];
+        const int chunks = (r1 - r0 + chunk_rows - 1) / chunk_rows;
+        const int tile = static_cast<int>(u / chunks);
+        s.m0 = r0 + static_cast<int>(u - static_cast<int64_t>(tile) * chunks) * chunk_rows;
+        s.m1 = r1 - s.m0 < chunk_rows ? r1 : s.m0 + chunk_rows;
+        s.n0 = tile * tile_cols;
+        return true;
+    }
+};
+
+// Activation row m: in A, or the token the plan names; NULL for a bad gather index.
+__device__ __forceinline__ const uint8_t *row_of(const W4Params &p, int m)
+{
+    if (p.A)
+        return p.A + static_cast<int64_t>(m) * p.K * 2;
+    const int64_t gi = __ldg(p.gather_idx + m);
+    const int64_t Tk = static_cast<int64_t>(p.T) * p.top_k;
+    if (gi < 0 || gi >= Tk * p.n_ranks)
+        return nullptr;
+    const int64_t rk = gi / Tk;
+    return p.x[rk] + (gi - rk * Tk) / p.top_k * p.K * 2;
+}
+
+// N 32-bit words at once (N = 1, 2 or 4), to or from shared memory.
+template <int N>
+__device__ __forceinline__ void copy_words(void *dst, const void *src)
+{
+    if constexpr (N == 1)
+        *static_cast<uint32_t *>(dst) = *static_cast<const uint32_t *>(src);
+    else if constexpr (N == 2)
+        *static_cast<uint2 *>(dst) = *static_cast<const uint2 *>(src);
+    else
+        *static_cast<uint4 *>(dst) = *static_cast<const uint4 *>(src);
+}
+
+// GS bytes or halves from global memory as they lie there: one aligned load, or (VEC
+// false) one by one, the ones past `have` left out.
+template <int BYTES, bool VEC>
+struct Piece {
+    static constexpr int kWords = (BYTES + 3) / 4;
+    uint32_t w[kWords];
+
+    template <typename T>
+    __device__ __forceinline__ void load(const T *from, int have)
+    {
+        if constexpr (VEC && BYTES == 16)
+            *this = from_uint4(__ldg(reinterpret_cast<const uint4 *>(from)));
+        else if constexpr (VEC && BYTES == 8) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(from));
+            w[0] = v.x, w[1] = v.y;
+        } else if constexpr (VEC && BYTES == 4)
+            w[0] = __ldg(reinterpret_cast<const uint32_t *>(from));
+        else if constexpr (VEC)
+            w[0] = __ldg(reinterpret_cast<const unsigned short *>(from));
+        else {
+            constexpr int kPer = 4 / sizeof(T);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                w[i] = 0;
+#pragma unroll
+            for (int i = 0; i < BYTES / static_cast<int>(sizeof(T)); ++i)
+                if (i < have)
+                    w[i / kPer] |= static_cast<uint32_t>(__ldg(from + i)) << (8 * sizeof(T) * (i % kPer));
+        }
+    }
+
+    static __device__ __forceinline__ Piece from_uint4(uint4 v)
+    {
+        Piece r;
+        r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+        return r;
+    }
+};
+
+// A weight row's scales and zero points of one step, on their way to shared memory as GS
+// bf16 numbers each. Nothing is done with them between load and store, so that the loads
+// of several rows are under way at once.
+template <int GS, bool E2M1, bool VEC>
+struct Scales {
+    Piece<E2M1 ? GS : 2 * GS, VEC> scale;
+    Piece<GS, VEC> zero;
+
+    // `have` of the step's groups exist, from index `at` on.
+    __device__ __forceinline__ void load(const W4Params &p, int64_t at, int have)
+    {
+        if constexpr (E2M1) {
+            scale.load(static_cast<const uint8_t *>(p.scales) + at, have);
         } else {
-            scale = __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const unsigned short *>(p.scales) + g)) << 16);
+            scale.load(static_cast<const unsigned short *>(p.scales) + at, have);
             if (p.zeros)
-                zero = __ldg(p.zeros + g);
-        }
-        float part = 0.f;
+                zero.load(p.zeros + at, have);
+            else
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t q = codes >> 4 * i & 15;
-            const float v = p.format == EP_W4_E2M1 ? e2m1_value(q) : static_cast<float>(q) - zero;
-            part = fmaf(v, __uint_as_float(i & 1 ? x[i / 2] & 0xFFFF0000u : x[i / 2] << 16), part);
+                for (int i = 0; i < zero.kWords; ++i)
+                    zero.w[i] = 0x08080808u;
         }
-        sum = fmaf(scale, part, sum);
     }
+
+    __device__ __forceinline__ void store(uint8_t *to_scale, uint8_t *to_zero) const
+    {
+        alignas(16) uint32_t out[GS / 2];
+        if constexpr (E2M1) {
+            // 2^(e - 127) as bf16: e in the exponent bits; 2^-127 is subnormal
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
+            for (int i = 0; i < GS; ++i) {
+                const uint32_t e = scale.w[i / 4] >> (8 * (i % 4)) & 255;
+                const uint32_t h = e == 255 ? 0x7FC0u : e == 0 ? 0x0040u : e << 7;
+                out[i / 2] = i % 2 ? out[i / 2] | h << 16 : h;
+            }
+            copy_words<GS / 2>(to_scale, out);
+        } else {
+#pragma unroll
+            for (int i = 0; i < GS / 2; ++i)
+                out[i] = scale.w[i];
+            copy_words<GS / 2>(to_scale, out);
+#pragma unroll
+            for (int i = 0; i < GS; ++i) {  // -zero / 64: small integers, exact
+                const float z = static_cast<float>(zero.w[i / 4] >> (8 * (i % 4)) & 15) * -0.015625f;
+                const uint32_t h = __float_as_uint(z) >> 16;
+                out[i / 2] = i % 2 ? out[i / 2] | h << 16 : h;
+            }
+            copy_words<GS / 2>(to_zero, out);
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
-__global__ void __launch_bounds__(kW4Threads) matvec_w4_kernel(const W4Params p)
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kW4Threads + threadIdx.x) >> 5;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * kW4Threads / 32;
-    const int64_t m_total = __ldg(p.expert_offsets + p.El);
-    bool bad = false;
-    for (int e = lane; e <= p.El; e += 32) {
-        const int lo = e ? __ldg(p.expert_offsets + e - 1) : 0, hi = __ldg(p.expert_offsets + e);
-        bad |= hi < lo || hi > p.max_rows;
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// 8 codes -> the bf16 pairs (0,4) (1,5) (2,6) (3,7), each (code - zero) / 64. The low four
+// bits of a bf16 number alone are the subnormal code * 2^-133; its bits 4..7 alone are
+// code * 2^-129, subnormal or in the first binade, where the spacing is the same. So a
+// mask and one fused multiply-add do it, exactly; `minus_zero` is -zero / 64.
+__device__ __forceinline__ void unpack_int(uint32_t w, uint32_t minus_zero, uint32_t (&v)[4])
+{
+    constexpr uint32_t two127 = 0x7F007F00u, two123 = 0x7D007D00u;
+    const uint32_t h = w >> 8;
+    v[0] = bf16x2_fma(w & 0x000F000Fu, two127, minus_zero);
+    v[1] = bf16x2_fma(w & 0x00F000F0u, two123, minus_zero);
+    v[2] = bf16x2_fma(h & 0x000F000Fu, two127, minus_zero);
+    v[3] = bf16x2_fma(h & 0x00F000F0u, two123, minus_zero);
+}
+constexpr float kIntScale = 64.f;
+
+// e2m1: a code's four bits go to bits 15..12 (for the sign) and 9..6 (exponent and
+// mantissa) of its half at once by a multiplication; the number so formed is 2^-126 times
+// the code's value.
+__device__ __forceinline__ void unpack_e2m1(uint32_t w, uint32_t (&v)[4])
+{
+    constexpr uint32_t two126 = 0x7E807E80u;
+    const uint32_t h = w >> 8;
+    v[0] = bf16x2_mul(((w & 0x000F000Fu) * 0x1040u) & 0x81C081C0u, two126);
+    v[1] = bf16x2_mul(((w & 0x00F000F0u) * 0x0104u) & 0x81C081C0u, two126);
+    v[2] = bf16x2_mul(((h & 0x000F000Fu) * 0x1040u) & 0x81C081C0u, two126);
+    v[3] = bf16x2_mul(((h & 0x00F000F0u) * 0x0104u) & 0x81C081C0u, two126);
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1,
+                                         const float (&c)[4])
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+          "f"(c[3]));
+}
+
+__device__ __forceinline__ void give_up(const W4Params &p, Shared &sh)
+{
+    atomicOr(p.status, EP_STATUS_TIMEOUT);
+    *reinterpret_cast<volatile int *>(&sh.abort) = 1;
+}
+
+// Stores a thread's sums of a whole tile: acc[nt][0..1] are rows 8nt+2q, +1 of the first
+// weight row, acc[nt][2..3] of the second.
+template <int NT>
+__device__ __forceinline__ void store_tile(const W4Params &p, const Segment &s,
+                                           const float (&acc)[NT][4], int row_in_half, int q)
+{
+    const int cols = p.swiglu ? p.N / 2 : p.N;
+    const int n = s.n0 + row_in_half;
+    const float back = p.format == EP_W4_INT ? kIntScale : 1.f;
+    __nv_bfloat16 *C = reinterpret_cast<__nv_bfloat16 *>(p.C);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int m = s.m0 + 8 * nt + 2 * q + h;
+            if (m >= s.m1 || (!p.A && !row_of(p, m)))
+                continue;
+            __nv_bfloat16 *out = C + static_cast<int64_t>(m) * cols;
+            if (p.swiglu) {
+                if (n < cols)
+                    out[n] = __float2bfloat16_rn(silu_f32(acc[nt][h] * back) * (acc[nt][2 + h] * back));
+            } else {
+                if (n < cols)
+                    out[n] = __float2bfloat16_rn(acc[nt][h] * back);
+                if (n + 64 < cols)
+                    out[n + 64] = __float2bfloat16_rn(acc[nt][2 + h] * back);
+            }
+        }
+}
+
+}  // namespace
+
+// NT: groups of 8 activation rows a pass over the weights serves. GS: scale groups of a
+// step (256 / group size). VEC: they are one aligned piece (W4Params::scale_vec).
+template <int NT, int GS, bool E2M1, bool VEC>
+__global__ void __launch_bounds__(kW4Threads, 2)
+    matvec_w4_kernel(const __grid_constant__ CUtensorMap tw, const W4Params p)
+{
+    constexpr int kStages = stages_of(NT, GS);
+    constexpr int kStage = stage_bytes(NT, GS);
+    constexpr int kTeams = teams_of(NT, GS), kTeam = kStagers / kTeams;  // warps of a team
+    constexpr int kXOff = kStepBytes, kScaleOff = kXOff + NT * 8 * kStepK * 2;
+    constexpr int kZeroOff = kScaleOff + kTileRows * GS * 2;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    Shared &sh = *reinterpret_cast<Shared *>(ring + kStages * kStage);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        tma_prefetch_map(&tw);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.full[i], 1 + kTeam);  // the producer, the staging warps
+            mbar_init(&sh.empty[i], kConsumers);
+        }
+        fence_mbar_init();
+        sh.abort = 0;
+        sh.bad = 0;
     }
-    if (__any_sync(0xffffffffu, bad)) {
-        if (warp == 0 && lane == 0)
+    __syncthreads();
+    // units of every expert: chunks of its rows x column tiles
+    const int tile_cols = p.swiglu ? 64 : kTileRows;
+    const int cols = p.swiglu ? p.N / 2 : p.N;
+    for (int e = tid; e <= p.El; e += kW4Threads) {
+        const int hi = __ldg(p.expert_offsets + e);
+        const int lo = e ? __ldg(p.expert_offsets + e - 1) : 0;
+        sh.offsets[e] = hi;
+        if (hi < lo || hi > p.max_rows)
+            sh.bad = 1;
+    }
+    __syncthreads();
+    if (sh.bad) {
+        if (blockIdx.x == 0 && tid == 0)
             atomicOr(p.status, EP_STATUS_BOUNDS);
         return;
     }
-    const int cols = p.swiglu ? p.N / 2 : p.N;
-    for (int64_t u = warp; u < m_total * cols; u += warps) {
-        const int64_t m = u / cols;
-        const int n = static_cast<int>(u - m * cols);
-        int e = 0;
-        while (e + 1 < p.El && __ldg(p.expert_offsets + e + 1) <= m)
-            ++e;
-        const uint8_t *a;
-        if (p.A) {
-            a = p.A + m * p.K * 2;
-        } else {
-            const int64_t gi = __ldg(p.gather_idx + m);
-            const int64_t Tk = static_cast<int64_t>(p.T) * p.top_k;
-            const int64_t rk = gi / Tk, t = (gi - rk * Tk) / p.top_k;
-            if (gi < 0 || rk >= p.n_ranks) {
-                if (lane == 0)
-                    atomicOr(p.status, EP_STATUS_BOUNDS);
-                continue;
+    if (warp == 0) {
+        const int64_t tiles = (cols + tile_cols - 1) / tile_cols;
+        int64_t base = 0;
+        for (int e0 = 0; e0 < p.El; e0 += 32) {
+            const int e = e0 + lane;
+            int64_t u = 0;
+            if (e < p.El)
+                u = (sh.offsets[e + 1] - sh.offsets[e] + 8 * NT - 1) / (8 * NT) * tiles;
+            int64_t inc = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o)
+                    inc += v;
             }
-            a = p.x[rk] + t * p.K * 2;
+            if (e < p.El)
+                sh.first_unit[e] = base + inc - u;
+            base += __shfl_sync(0xffffffffu, inc, 31);
         }
-        float y = w4_dot(p, e, n, a, lane);
-        if (p.swiglu)
-            y = silu_f32(y) * w4_dot(p, e, n + p.N / 2, a, lane);
         if (lane == 0)
-            reinterpret_cast<__nv_bfloat16 *>(p.C)[m * cols + n] = __float2bfloat16_rn(y);
+            sh.first_unit[p.El] = base;
+    }
+    __syncthreads();
+
+    volatile int *abort_flag = &sh.abort;
+    Walk walk(p, sh, tile_cols, cols);
+    Segment seg;
+    int stage = 0;
+    uint32_t phase = 0;
+    auto advance = [&] {
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ producer: weights by TMA
+        if (lane != 0)
+            return;
+        int64_t issued = 0;
+        bool ok = true;
+        while (ok && walk.next(p, sh, 8 * NT, tile_cols, seg)) {
+            const int y0 = seg.e * p.N + seg.n0;
+            const int y1 = p.swiglu ? y0 + p.N / 2 : y0 + 64;
+            for (int k = seg.s0; k < seg.s1; ++k) {
+                if (!mbar_wait(&sh.empty[stage], phase ^ 1, kW4TimeoutNs, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *dst = ring + stage * kStage;
+                mbar_arrive_expect_tx(&sh.full[stage], kStepBytes);
+                tma_load_2d(dst, &tw, &sh.full[stage], k * (kStepK / 2), y0);
+                tma_load_2d(dst + kStepBytes / 2, &tw, &sh.full[stage], k * (kStepK / 2), y1);
+                ++issued;
+                advance();
+            }
+        }
+        if (!ok) {
+            give_up(p, sh);
+            // the copies in flight land before the block's shared memory goes away
+            volatile int no_abort = 0;
+            for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+                mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, 1000000, &no_abort);
+        }
+        return;
+    }
+
+    if (warp <= kStagers) {
+        // ---------------------------- staging: activation rows, scales and zero points
+        if (warp - 1 >= kTeams * kTeam)
+            return;
+        int turn = (warp - 1) % kTeams;  // steps until this team's next
+        const int member = (warp - 1) / kTeams;
+        constexpr int kRowSets = 4 / kTeam;  // of 32 weight rows, this warp's
+        const int groups = p.K / (kStepK / GS);
+        const int b = lane >> 2, q = lane & 3;  // this lane's 8 activations: 32 b + 8 q ...
+        bool ok = true;
+        while (ok && walk.next(p, sh, 8 * NT, tile_cols, seg)) {
+            const int rows = seg.m1 - seg.m0;
+            // lane i: where the segment's row i lies
+            unsigned long long mine = 0;
+            if (lane < rows) {
+                mine = reinterpret_cast<unsigned long long>(row_of(p, seg.m0 + lane));
+                if (!mine)
+                    atomicOr(p.status, EP_STATUS_BOUNDS);
+            }
+            // where this lane's weight rows have their scales (rows past the last column
+            // take the last one's: nobody stores what comes of them)
+            int64_t scale_at[kRowSets];
+#pragma unroll
+            for (int i = 0; i < kRowSets; ++i) {
+                const int r = (member * kRowSets + i) * 32 + lane;
+                int n = seg.n0 + (r < 64 || !p.swiglu ? r : r - 64);
+                n = n < cols ? n : cols - 1;
+                scale_at[i] = (static_cast<int64_t>(seg.e) * p.N + n +
+                               (r >= 64 && p.swiglu ? cols : 0)) * groups;
+            }
+            for (int k = seg.s0; k < seg.s1; ++k, turn = turn == 0 ? kTeams - 1 : turn - 1) {
+                if (turn != 0) {
+                    advance();
+                    continue;
+                }
+                // all loads first, then the wait for the stage, then the stores
+                Scales<GS, E2M1, VEC> sc[kRowSets];
+#pragma unroll
+                for (int i = 0; i < kRowSets; ++i)
+                    sc[i].load(p, scale_at[i] + k * GS, groups - k * GS);
+                const int k0 = k * kStepK + lane * 8;
+                uint4 v[4];
+                auto load_rows = [&](int r0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 *from = reinterpret_cast<const uint4 *>(
+                            __shfl_sync(0xffffffffu, mine, r0 + i));
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (from && k0 < p.K)
+                            v[i] = __ldg(from + k0 / 8);
+                    }
+                };
+                load_rows(member * 4);
+                ok = __all_sync(0xffffffffu, mbar_wait(&sh.empty[stage], phase ^ 1, kW4TimeoutNs,
+                                                       abort_flag));
+                if (!ok)
+                    break;
+                uint8_t *dst = ring + stage * kStage;
+                // (columns of the matrix instruction past the last row hold whatever they held:
+                // they only reach results that nobody stores)
+                for (int r0 = member * 4; r0 < rows; r0 += kTeam * 4) {
+                    if (r0 != member * 4)
+                        load_rows(r0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (r0 + i >= rows)
+                            break;
+                        uint4 o;
+                        o.x = __byte_perm(v[i].x, v[i].z, 0x5410);
+                        o.y = __byte_perm(v[i].x, v[i].z, 0x7632);
+                        o.z = __byte_perm(v[i].y, v[i].w, 0x5410);
+                        o.w = __byte_perm(v[i].y, v[i].w, 0x7632);
+                        const int nt = (r0 + i) / 8, g = (r0 + i) % 8;
+                        *reinterpret_cast<uint4 *>(dst + kXOff + ((b * NT + nt) * 32 + g * 4 + q) * 16) = o;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kRowSets; ++i) {
+                    const int r = (member * kRowSets + i) * 32 + lane;
+                    sc[i].store(dst + kScaleOff + r * GS * 2, dst + kZeroOff + r * GS * 2);
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sh.full[stage]);
+                advance();
+            }
+        }
+        if (!ok && lane == 0)
+            give_up(p, sh);
+        return;
+    }
+
+    // ------------------------------------------------------------------ consumers
+    const int cw = warp - 1 - kStagers, g = lane >> 2, q = lane & 3;
+    const int row = 8 * cw + g;  // in each half of the tile
+    const int ctid = cw * 32 + lane;
+    const int at0 = row * 128 + (g << 4) + q * 4;
+    float *partial = reinterpret_cast<float *>(p.workspace + kW4MaxBlocks * 16);
+    constexpr int kSlot = kConsumers * 32 * NT * 4;  // floats of one partial tile
+    int *counters = reinterpret_cast<int *>(p.workspace);
+    while (walk.next(p, sh, 8 * NT, tile_cols, seg)) {
+        const int nts = (seg.m1 - seg.m0 + 7) / 8;
+        float acc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[nt][i] = 0.f;
+        bool ok = true;
+        for (int k = seg.s0; k < seg.s1; ++k) {
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(&sh.full[stage], phase, kW4TimeoutNs, abort_flag));
+            if (!ok)
+                break;
+            const uint8_t *src = ring + stage * kStage;
+            alignas(16) uint32_t scale0[GS / 2], scale1[GS / 2];
+            copy_words<GS / 2>(scale0, src + kScaleOff + row * GS * 2);
+            copy_words<GS / 2>(scale1, src + kScaleOff + (64 + row) * GS * 2);
+            alignas(16) uint32_t zero0[GS / 2], zero1[GS / 2];
+            if constexpr (!E2M1) {
+                copy_words<GS / 2>(zero0, src + kZeroOff + row * GS * 2);
+                copy_words<GS / 2>(zero1, src + kZeroOff + (64 + row) * GS * 2);
+            }
+            float part[NT][4];
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                const int gr = b * GS / 8;
+                const bool first = b * GS % 8 == 0 || GS == 8;
+                const bool last = (b + 1) * GS % 8 == 0 || GS == 8;
+                const int at = at0 ^ (b << 4);  // the 128-byte swizzle: 16-byte piece b ^ row % 8
+                const uint32_t w0 = *reinterpret_cast<const uint32_t *>(src + at);
+                const uint32_t w1 = *reinterpret_cast<const uint32_t *>(src + kStepBytes / 2 + at);
+                uint32_t a0[4], a1[4];
+                if (E2M1) {
+                    unpack_e2m1(w0, a0);
+                    unpack_e2m1(w1, a1);
+                } else {
+                    // the group's -zero / 64 in both halves
+                    const uint32_t sel = gr & 1 ? 0x3232u : 0x1010u;
+                    unpack_int(w0, __byte_perm(zero0[gr / 2], 0u, sel), a0);
+                    unpack_int(w1, __byte_perm(zero1[gr / 2], 0u, sel), a1);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (NT > 1 && nt >= nts)
+                        break;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(
+                        src + kXOff + ((b * NT + nt) * 32 + lane) * 16);
+                    const float none[4] = {0.f, 0.f, 0.f, 0.f};
+                    if (first)
+                        mma_bf16(part[nt], a0[0], a1[0], a0[1], a1[1], x.x, x.y, none);
+                    else
+                        mma_bf16(part[nt], a0[0], a1[0], a0[1], a1[1], x.x, x.y, part[nt]);
+                    mma_bf16(part[nt], a0[2], a1[2], a0[3], a1[3], x.z, x.w, part[nt]);
+                }
+                if (last) {
+                    const float s0 = __uint_as_float(
+                        gr & 1 ? scale0[gr / 2] & 0xFFFF0000u : scale0[gr / 2] << 16);
+                    const float s1 = __uint_as_float(
+                        gr & 1 ? scale1[gr / 2] & 0xFFFF0000u : scale1[gr / 2] << 16);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (NT > 1 && nt >= nts)
+                            break;
+                        acc[nt][0] = fmaf(s0, part[nt][0], acc[nt][0]);
+                        acc[nt][1] = fmaf(s0, part[nt][1], acc[nt][1]);
+                        acc[nt][2] = fmaf(s1, part[nt][2], acc[nt][2]);
+                        acc[nt][3] = fmaf(s1, part[nt][3], acc[nt][3]);
+                    }
+                }
+            }
+            // the copy that refills the stage goes through the async proxy: without this
+            // fence reads of the stage may still be under way when it lands
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.empty[stage]);
+            advance();
+        }
+        // a warp that gave up takes all consumers with it (they meet at barriers below)
+        if (!ok && lane == 0)
+            give_up(p, sh);
+        if (!named_bar_and(1, kConsumers * 32, ok))
+            return;
+        if (seg.s0 == 0 && seg.s1 == walk.steps) {
+            store_tile<NT>(p, seg, acc, row, q);
+            continue;
+        }
+        // a cut tile: leave the sums, the last block to arrive adds all of them up. A
+        // block's run ends inside at most one tile and begins inside at most one: two slots.
+        const int c0 = walk.owner(seg.first), c1 = walk.owner(seg.first + walk.steps - 1);
+        float4 *mine = reinterpret_cast<float4 *>(
+            partial + (blockIdx.x * 2 + (seg.s0 == 0 ? 1 : 0)) * static_cast<int64_t>(kSlot));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            if (nt < nts)
+                __stcg(mine + nt * kConsumers * 32 + ctid,
+                       make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]));
+        __threadfence();
+        named_bar_sync(1, kConsumers * 32);
+        if (ctid == 0) {
+            const int before = atom_add_acq_rel_gpu(counters + c0, 1);
+            sh.last = before == c1 - c0;
+            if (sh.last)
+                counters[c0] = 0;  // ready for the next call
+        }
+        named_bar_sync(1, kConsumers * 32);
+        if (!sh.last)
+            continue;
+        __threadfence();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[nt][i] = 0.f;
+        for (int c = c0; c <= c1; ++c) {
+            const float4 *theirs = reinterpret_cast<const float4 *>(
+                partial + (c * 2 + (c == c0 ? 1 : 0)) * static_cast<int64_t>(kSlot));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                if (nt < nts) {
+                    const float4 v = __ldcg(theirs + nt * kConsumers * 32 + ctid);
+                    acc[nt][0] += v.x;
+                    acc[nt][1] += v.y;
+                    acc[nt][2] += v.z;
+                    acc[nt][3] += v.w;
+                }
+        }
+        store_tile<NT>(p, seg, acc, row, q);
     }
 }
 
 int64_t w4_workspace_bytes()
 {
-    return 16;
+    return kW4MaxBlocks * 16 +
+           2ll * kW4MaxBlocks * kConsumers * 32 * kMaxNT * 4 * static_cast<int64_t>(sizeof(float));
 }
 
-cudaError_t launch_matvec_w4(const W4Params &p, int num_sms, cudaStream_t s)
+template <int NT, int GS, bool E2M1, bool VEC>
+static cudaError_t launch_w4(const CUtensorMap &tw, const W4Params &p, int grid, cudaStream_t s)
 {
-    matvec_w4_kernel<<<8 * num_sms, kW4Threads, 0, s>>>(p);
+    const auto kern = matvec_w4_kernel<NT, GS, E2M1, VEC>;
+    constexpr int smem = smem_bytes(NT, GS);
+    static_assert(stages_of(NT, GS) >= 2, "the ring needs two stages");
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    kern<<<grid, kW4Threads, smem, s>>>(tw, p);
     return cudaGetLastError();
+}
+
+template <int NT, bool VEC>
+static cudaError_t launch_nt(const CUtensorMap &tw, const W4Params &p, int grid, cudaStream_t s)
+{
+    if (p.format == EP_W4_E2M1)
+        return launch_w4<NT, 8, true, VEC>(tw, p, grid, s);
+    switch (p.group) {
+    case 32:
+        return launch_w4<NT, 8, false, VEC>(tw, p, grid, s);
+    case 64:
+        return launch_w4<NT, 4, false, VEC>(tw, p, grid, s);
+    default:
+        return launch_w4<NT, 2, false, VEC>(tw, p, grid, s);
+    }
+}
+
+cudaError_t launch_matvec_w4(const CUtensorMap &tw, const W4Params &p, int num_sms, cudaStream_t s)
+{
+    // rows a pass serves: what an expert is expected to get, at most what it can get
+    const int64_t tokens = static_cast<int64_t>(p.T) * p.n_ranks;
+    int64_t rows = (tokens * p.top_k + static_cast<int64_t>(p.n_ranks) * p.El - 1) /
+                   (static_cast<int64_t>(p.n_ranks) * p.El);
+    rows = rows < p.max_rows ? rows : p.max_rows;
+    const int grid = 2 * num_sms < kW4MaxBlocks ? 2 * num_sms : kW4MaxBlocks;
+    if (rows <= 8)
+        return p.scale_vec ? launch_nt<1, true>(tw, p, grid, s) : launch_nt<1, false>(tw, p, grid, s);
+    if (rows <= 16)
+        return p.scale_vec ? launch_nt<2, true>(tw, p, grid, s) : launch_nt<2, false>(tw, p, grid, s);
+    return p.scale_vec ? launch_nt<4, true>(tw, p, grid, s) : launch_nt<4, false>(tw, p, grid, s);
 }
 
 }  // namespace ep
