@@ -680,6 +680,11 @@ int ep_matvec_w4(const ep_config *cfg, const ep_w4_args *a, ep_stream_t stream)
     if (a->max_rows < 1 || a->max_rows > INT32_MAX ||
         a->workspace_bytes < ep::w4_workspace_bytes())
         return EP_ERR_INVALID_ARG;
+    // the kernel's steps are counted in 32 bits: at most so many chunks of 8 rows, each by N/64 tiles by
+    // K/256 steps
+    if ((a->max_rows / 8 + cfg->n_local_experts) * ((cfg->N + 63ll) / 64) *
+            ((cfg->K + 255ll) / 256) >= INT32_MAX)
+        return EP_ERR_UNSUPPORTED;
     ep::W4Params p;
     std::memset(&p, 0, sizeof p);
     if (!a->A) {
@@ -702,6 +707,7 @@ int ep_matvec_w4(const ep_config *cfg, const ep_w4_args *a, ep_stream_t stream)
     p.N = cfg->N;
     p.format = a->w_format;
     p.group = a->group_size;
+    p.steps = (cfg->K + 255) / 256;
     p.swiglu = a->local_activation == EP_ACT_SWIGLU ? 1 : 0;
     p.max_rows = a->max_rows;
     p.A = static_cast<const uint8_t *>(a->A);

@@ -165,6 +165,7 @@ struct CombineBackwardParams {
 struct W4Params {
     int n_ranks, El, top_k, T, K, N;
     int format, group, swiglu;
+    int steps;      // of 256 k
     int scale_vec;  // a step's scales (and zero points) of a row are one aligned piece
     int64_t max_rows;
     const uint8_t *A;

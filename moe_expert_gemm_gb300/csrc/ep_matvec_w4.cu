@@ -15,9 +15,9 @@
 //    (3,7); the activations are laid into shared memory in that order.
 //  * Work is counted in steps of 256 k by 128 weight rows (16 KB), ordered by expert,
 //    column tile, chunk of 8*NT rows and k, and cut into equal runs, one per thread
-//    block, wherever the cuts fall. A tile cut between blocks is joined through the
-//    workspace: every block leaves its fp32 partial sums there, the last one to arrive
-//    adds them in block order.
+//    block, of whole tiles or wherever the cuts fall (Walk). A tile cut between blocks is
+//    joined through the workspace: every block leaves its fp32 partial sums there, the
+//    last one to arrive adds them in block order.
 //  * Thread block: one producer thread streams the weights with TMA into a ring of
 //    stages; four staging warps bring the activation rows and scales of a step;
 //    eight consumer warps own 16 weight rows each (8 of the tile's first half and 8 of
@@ -42,13 +42,45 @@ constexpr int kMaxNT = 4;
 constexpr int kSmemPerBlock = 113 * 1024;        // two blocks on an SM
 constexpr uint64_t kW4TimeoutNs = 2000000000ull;
 
+// One block's share of one tile: steps [s0, s1).
+struct Segment {
+    int e, m0, m1, n0;  // expert, its rows [m0, m1), first column
+    int s0, s1;
+    int first;          // number of the tile's first step
+};
+
+// How the steps are cut into the blocks' runs. A tile's steps are kept together as long
+// as that costs less than the joining of cut tiles, which takes about as long as
+// kJoinSteps steps (1-token down projection of 8 experts, 4096 x 1536 each: 256 whole
+// tiles on 256 blocks).
+constexpr int kJoinSteps = 3;
+
+struct Runs {
+    int per, rest;  // pieces of every run; the first `rest` runs have one more
+    int piece;      // steps of a piece: 1, or a tile's
+
+    // The block whose run holds step i (of runs cut at any step).
+    __device__ int owner(int i) const
+    {
+        return i < rest * (per + 1) ? i / (per + 1) : rest + (i - rest * (per + 1)) / per;
+    }
+};
+
+// Where a block's run begins: the tile (expert, number among its units), its step, and
+// the steps to go.
+struct Start {
+    int e, u, s0, first, todo;
+};
+
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    int64_t first_unit[EP_MAX_LOCAL_EXPERTS + 1];  // units before each expert
     int offsets[EP_MAX_LOCAL_EXPERTS + 1];
     int bad;
     int abort;
-    int last;
+    Runs runs;
+    Start start;
+    Segment cut[2];  // the tiles the block's run begins and ends inside
+    int last[2];
 };
 
 // Weights, activations, scales and zero points (both bf16) of a step; a multiple of the
@@ -77,61 +109,51 @@ constexpr int smem_bytes(int NT, int GS)
     return 1024 + stages_of(NT, GS) * stage_bytes(NT, GS) + static_cast<int>(sizeof(Shared));
 }
 
-// One block's share of one tile: steps [s0, s1) of `steps`.
-struct Segment {
-    int e, m0, m1, n0;  // expert, its rows [m0, m1), first column
-    int s0, s1;
-    int64_t first;      // number of the tile's first step
-};
-
+// The segments of this block's run, one after the other.
+template <int CHUNK>
 struct Walk {
-    int64_t total, at, end;
-    int64_t blocks;  // that have work: every run has a step
+    int e, u, s0, first, todo;  // the next segment's expert, unit in it, step, ...
+    int tile, chunk, chunks;    // of that unit; chunks 0: not yet known
     int steps, tiles;
 
-    __device__ Walk(const W4Params &p, const Shared &sh, int tile_cols, int cols)
+    __device__ Walk(const W4Params &p, const Shared &sh, int tiles_)
+        : e(sh.start.e), u(sh.start.u), s0(sh.start.s0), first(sh.start.first),
+          todo(sh.start.todo), tile(0), chunk(0), chunks(0), steps(p.steps), tiles(tiles_)
     {
-        steps = (p.K + kStepK - 1) / kStepK;
-        tiles = (cols + tile_cols - 1) / tile_cols;
-        total = sh.first_unit[p.El] * steps;
-        blocks = total < gridDim.x ? total : gridDim.x;
-        const bool idle = blockIdx.x >= blocks;
-        at = idle ? 0 : total * blockIdx.x / blocks;
-        end = idle ? 0 : total * (blockIdx.x + 1) / blocks;
     }
 
-    // The block whose run holds step i.
-    __device__ int owner(int64_t i) const
+    __device__ __forceinline__ bool next(const Shared &sh, int tile_cols, Segment &s)
     {
-        return static_cast<int>(((i + 1) * blocks - 1) / total);
-    }
-
-    __device__ bool next(const W4Params &p, const Shared &sh, int chunk_rows, int tile_cols,
-                         Segment &s)
-    {
-        if (at >= end)
+        if (todo <= 0)
             return false;
-        const int64_t unit = at / steps;
-        s.first = unit * steps;
-        s.s0 = static_cast<int>(at - s.first);
-        s.s1 = static_cast<int>(end - s.first < steps ? end - s.first : steps);
-        at = s.first + s.s1;
-        int lo = 0, hi = p.El;  // first_unit[lo] <= unit < first_unit[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (sh.first_unit[mid] <= unit)
-                lo = mid;
-            else
-                hi = mid;
+        if (chunks == 0) {  // the run's first segment
+            chunks = static_cast<int>(
+                (static_cast<unsigned>(sh.offsets[e + 1] - sh.offsets[e]) + CHUNK - 1) / CHUNK);
+            tile = chunks == 1 ? u : u / chunks;
+            chunk = u - tile * chunks;
         }
-        s.e = lo;
-        const int64_t u = unit - sh.first_unit[lo];
-        const int r0 = sh.offsets[lo], r1 = sh.offsets[lo + 1];
-        const int chunks = (r1 - r0 + chunk_rows - 1) / chunk_rows;
-        const int tile = static_cast<int>(u / chunks);
-        s.m0 = r0 + static_cast<int>(u - static_cast<int64_t>(tile) * chunks) * chunk_rows;
-        s.m1 = r1 - s.m0 < chunk_rows ? r1 : s.m0 + chunk_rows;
+        const int r0 = sh.offsets[e], r1 = sh.offsets[e + 1];
+        s.e = e;
+        s.m0 = r0 + chunk * CHUNK;
+        s.m1 = r1 - s.m0 < CHUNK ? r1 : s.m0 + CHUNK;
         s.n0 = tile * tile_cols;
+        s.first = first;
+        s.s0 = s0;
+        s.s1 = todo < steps - s0 ? s0 + todo : steps;
+        todo -= s.s1 - s.s0;
+        s0 = 0;
+        first += steps;
+        if (++chunk == chunks) {
+            chunk = 0;
+            if (++tile == tiles && todo > 0) {
+                tile = 0;
+                do {  // the next expert with rows: there is one, as there are steps to go
+                    ++e;
+                    chunks = static_cast<int>(
+                        (static_cast<unsigned>(sh.offsets[e + 1] - sh.offsets[e]) + CHUNK - 1) / CHUNK);
+                } while (chunks == 0);
+            }
+        }
         return true;
     }
 };
@@ -141,12 +163,13 @@ __device__ __forceinline__ const uint8_t *row_of(const W4Params &p, int m)
 {
     if (p.A)
         return p.A + static_cast<int64_t>(m) * p.K * 2;
-    const int64_t gi = __ldg(p.gather_idx + m);
-    const int64_t Tk = static_cast<int64_t>(p.T) * p.top_k;
-    if (gi < 0 || gi >= Tk * p.n_ranks)
+    // (tokens * top_k of all ranks fit 31 bits)
+    const uint32_t gi = static_cast<uint32_t>(__ldg(p.gather_idx + m));
+    const uint32_t Tk = static_cast<uint32_t>(p.T) * p.top_k;
+    if (gi >= Tk * p.n_ranks)
         return nullptr;
-    const int64_t rk = gi / Tk;
-    return p.x[rk] + (gi - rk * Tk) / p.top_k * p.K * 2;
+    const uint32_t rk = gi / Tk;
+    return p.x[rk] + static_cast<int64_t>((gi - rk * Tk) / p.top_k) * p.K * 2;
 }
 
 // N 32-bit words at once (N = 1, 2 or 4), to or from shared memory.
@@ -359,7 +382,9 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     Shared &sh = *reinterpret_cast<Shared *>(ring + kStages * kStage);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    if (tid == 0) {
+    const int tile_cols = p.swiglu ? 64 : kTileRows;
+    const int cols = p.swiglu ? p.N / 2 : p.N;
+    if (warp == 1 && lane == 0) {
         tma_prefetch_map(&tw);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.full[i], 1 + kTeam);  // the producer, the staging warps
@@ -367,51 +392,87 @@ __global__ void __launch_bounds__(kW4Threads, 2)
         }
         fence_mbar_init();
         sh.abort = 0;
-        sh.bad = 0;
+        sh.cut[0].e = sh.cut[1].e = -1;
     }
-    __syncthreads();
-    // units of every expert: chunks of its rows x column tiles
-    const int tile_cols = p.swiglu ? 64 : kTileRows;
-    const int cols = p.swiglu ? p.N / 2 : p.N;
-    for (int e = tid; e <= p.El; e += kW4Threads) {
-        const int hi = __ldg(p.expert_offsets + e);
-        const int lo = e ? __ldg(p.expert_offsets + e - 1) : 0;
-        sh.offsets[e] = hi;
-        if (hi < lo || hi > p.max_rows)
-            sh.bad = 1;
-    }
-    __syncthreads();
-    if (sh.bad) {
-        if (blockIdx.x == 0 && tid == 0)
-            atomicOr(p.status, EP_STATUS_BOUNDS);
-        return;
-    }
+    const int tiles = (cols + tile_cols - 1) / tile_cols;
     if (warp == 0) {
-        const int64_t tiles = (cols + tile_cols - 1) / tile_cols;
-        int64_t base = 0;
-        for (int e0 = 0; e0 < p.El; e0 += 32) {
-            const int e = e0 + lane;
-            int64_t u = 0;
-            if (e < p.El)
-                u = (sh.offsets[e + 1] - sh.offsets[e] + 8 * NT - 1) / (8 * NT) * tiles;
-            int64_t inc = u;
+        // units of every expert (chunks of its rows x column tiles), their sums, and from
+        // them where this block's run begins
+        constexpr int kSets = EP_MAX_LOCAL_EXPERTS / 32;
+        int lo[kSets], hi[kSets], upto[kSets];
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+            const int e = 32 * i + lane;
+            lo[i] = e < p.El ? __ldg(p.expert_offsets + e) : 0;
+            hi[i] = e < p.El ? __ldg(p.expert_offsets + e + 1) : 0;
+        }
+        int units = 0;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+            upto[i] = 0;
+            if (32 * i >= p.El)
+                break;
+            bad |= lo[i] < 0 || hi[i] < lo[i] || hi[i] > p.max_rows;
+            int sum = static_cast<int>((static_cast<unsigned>(hi[i] - lo[i]) + 8 * NT - 1) / (8 * NT)) * tiles;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+                const int v = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o)
-                    inc += v;
+                    sum += v;
             }
-            if (e < p.El)
-                sh.first_unit[e] = base + inc - u;
-            base += __shfl_sync(0xffffffffu, inc, 31);
+            upto[i] = units + sum;
+            units = __shfl_sync(0xffffffffu, upto[i], 31);
         }
-        if (lane == 0)
-            sh.first_unit[p.El] = base;
+        bad = __any_sync(0xffffffffu, bad);
+        const int grid = static_cast<int>(gridDim.x), block = static_cast<int>(blockIdx.x);
+        const int total = units * p.steps;
+        const bool whole = (units + grid - 1) / grid * p.steps <= (total + grid - 1) / grid + kJoinSteps;
+        Runs runs;
+        runs.piece = whole ? p.steps : 1;
+        runs.per = (whole ? units : total) / grid;
+        runs.rest = (whole ? units : total) - runs.per * grid;
+        const int at = (block * runs.per + (block < runs.rest ? block : runs.rest)) * runs.piece;
+        const int todo = (runs.per + (block < runs.rest)) * runs.piece;
+        const int unit = at / p.steps;
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+            if (32 * i >= p.El)
+                break;
+            const int e = 32 * i + lane;
+            if (e < p.El) {
+                sh.offsets[e] = lo[i];
+                if (e == p.El - 1)
+                    sh.offsets[p.El] = hi[i];
+            }
+        }
+        if (lane == 0) {
+            sh.bad = bad;
+            sh.runs = runs;
+            if (bad && block == 0)
+                atomicOr(p.status, EP_STATUS_BOUNDS);
+        }
+        // the expert whose units hold `unit`
+        int base = 0;
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+            if (32 * i >= p.El)
+                break;
+            const int up = __shfl_up_sync(0xffffffffu, upto[i], 1);
+            const int from = lane == 0 ? base : up;
+            if (from <= unit && unit < upto[i])
+                sh.start = Start{32 * i + lane, unit - from, at - unit * p.steps, unit * p.steps, todo};
+            base = __shfl_sync(0xffffffffu, upto[i], 31);
+        }
+        if (lane == 0 && unit >= units)
+            sh.start.todo = 0;
     }
     __syncthreads();
+    if (sh.bad)
+        return;
 
     volatile int *abort_flag = &sh.abort;
-    Walk walk(p, sh, tile_cols, cols);
+    Walk<8 * NT> walk(p, sh, tiles);
     Segment seg;
     int stage = 0;
     uint32_t phase = 0;
@@ -428,7 +489,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
             return;
         int64_t issued = 0;
         bool ok = true;
-        while (ok && walk.next(p, sh, 8 * NT, tile_cols, seg)) {
+        while (ok && walk.next(sh, tile_cols, seg)) {
             const int y0 = seg.e * p.N + seg.n0;
             const int y1 = p.swiglu ? y0 + p.N / 2 : y0 + 64;
             for (int k = seg.s0; k < seg.s1; ++k) {
@@ -464,7 +525,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
         const int groups = p.K / (kStepK / GS);
         const int b = lane >> 2, q = lane & 3;  // this lane's 8 activations: 32 b + 8 q ...
         bool ok = true;
-        while (ok && walk.next(p, sh, 8 * NT, tile_cols, seg)) {
+        while (ok && walk.next(sh, tile_cols, seg)) {
             const int rows = seg.m1 - seg.m0;
             // lane i: where the segment's row i lies
             unsigned long long mine = 0;
@@ -552,9 +613,10 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     const int ctid = cw * 32 + lane;
     const int at0 = row * 128 + (g << 4) + q * 4;
     float *partial = reinterpret_cast<float *>(p.workspace + kW4MaxBlocks * 16);
-    constexpr int kSlot = kConsumers * 32 * NT * 4;  // floats of one partial tile
+    constexpr int64_t kSlot = kConsumers * 32 * NT * 4;  // floats of one partial tile
     int *counters = reinterpret_cast<int *>(p.workspace);
-    while (walk.next(p, sh, 8 * NT, tile_cols, seg)) {
+    bool ok = true;
+    while (walk.next(sh, tile_cols, seg)) {
         const int nts = (seg.m1 - seg.m0 + 7) / 8;
         float acc[NT][4];
 #pragma unroll
@@ -562,7 +624,6 @@ __global__ void __launch_bounds__(kW4Threads, 2)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 acc[nt][i] = 0.f;
-        bool ok = true;
         for (int k = seg.s0; k < seg.s1; ++k) {
             ok = __all_sync(0xffffffffu,
                             mbar_wait(&sh.full[stage], phase, kW4TimeoutNs, abort_flag));
@@ -633,45 +694,58 @@ __global__ void __launch_bounds__(kW4Threads, 2)
                 mbar_arrive(&sh.empty[stage]);
             advance();
         }
-        // a warp that gave up takes all consumers with it (they meet at barriers below)
-        if (!ok && lane == 0)
-            give_up(p, sh);
-        if (!named_bar_and(1, kConsumers * 32, ok))
-            return;
+        if (!ok)
+            break;
         if (seg.s0 == 0 && seg.s1 == walk.steps) {
             store_tile<NT>(p, seg, acc, row, q);
             continue;
         }
-        // a cut tile: leave the sums, the last block to arrive adds all of them up. A
-        // block's run ends inside at most one tile and begins inside at most one: two slots.
-        const int c0 = walk.owner(seg.first), c1 = walk.owner(seg.first + walk.steps - 1);
-        float4 *mine = reinterpret_cast<float4 *>(
-            partial + (blockIdx.x * 2 + (seg.s0 == 0 ? 1 : 0)) * static_cast<int64_t>(kSlot));
+        // a cut tile: leave the sums in the block's slot for the tile its run begins
+        // inside (0) or ends inside (1)
+        const int slot = seg.s0 == 0 ? 1 : 0;
+        float4 *mine = reinterpret_cast<float4 *>(partial + (blockIdx.x * 2 + slot) * kSlot);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
             if (nt < nts)
                 __stcg(mine + nt * kConsumers * 32 + ctid,
                        make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]));
-        __threadfence();
-        named_bar_sync(1, kConsumers * 32);
-        if (ctid == 0) {
-            const int before = atom_add_acq_rel_gpu(counters + c0, 1);
-            sh.last = before == c1 - c0;
-            if (sh.last)
+        if (ctid == 0)
+            sh.cut[slot] = seg;
+    }
+    // The cut tiles, after all else: of a tile's blocks the last one to come here adds
+    // the sums of all of them, in block order. A warp that gave up takes all consumers
+    // with it here, where they meet first.
+    if (!ok && lane == 0)
+        give_up(p, sh);
+    if (sh.runs.piece > 1)
+        return;  // runs of whole tiles
+    __threadfence();
+    if (!named_bar_and(1, kConsumers * 32, ok))
+        return;
+    if (cw < 2 && lane == 0) {
+        const Segment &cut = sh.cut[cw];
+        int last = 0;
+        if (cut.e >= 0) {
+            const int c0 = sh.runs.owner(cut.first), c1 = sh.runs.owner(cut.first + walk.steps - 1);
+            last = atom_add_acq_rel_gpu(counters + c0, 1) == c1 - c0;
+            if (last)
                 counters[c0] = 0;  // ready for the next call
         }
-        named_bar_sync(1, kConsumers * 32);
-        if (!sh.last)
+        sh.last[cw] = last;
+    }
+    named_bar_sync(1, kConsumers * 32);
+    __threadfence();
+    for (int slot = 0; slot < 2; ++slot) {
+        if (!sh.last[slot])
             continue;
-        __threadfence();
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[nt][i] = 0.f;
+        seg = sh.cut[slot];
+        const int nts = (seg.m1 - seg.m0 + 7) / 8;
+        const int c0 = sh.runs.owner(seg.first), c1 = sh.runs.owner(seg.first + walk.steps - 1);
+        float acc[NT][4] = {};
+#pragma unroll 4
         for (int c = c0; c <= c1; ++c) {
-            const float4 *theirs = reinterpret_cast<const float4 *>(
-                partial + (c * 2 + (c == c0 ? 1 : 0)) * static_cast<int64_t>(kSlot));
+            const float4 *theirs =
+                reinterpret_cast<const float4 *>(partial + (c * 2 + (c == c0 ? 1 : 0)) * kSlot);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
                 if (nt < nts) {
