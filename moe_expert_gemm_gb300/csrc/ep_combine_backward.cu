@@ -1,14 +1,18 @@
 // Gradient of the gate-weighted combine out[t] = sum_j g[t, j] * row(t, j):
 //   dgates[t, j] = <dout[t], row(t, j)>,   drow(t, j) = g[t, j] * dout[t].
-// HBM-bound: the rows are read once, their gradient written once. One block takes one
-// token.
+// HBM-bound: every row is read once and its gradient written once; a token's dout comes
+// from HBM once and from the L1 for its other rows, which are handled side by side.
+// A warp takes a row; kUnroll 16-byte pieces of the row and of dout a lane are under way at
+// once. Where there are fewer rows than warps to keep the memory busy, a block of eight
+// warps takes a row and joins their sums in warp order.
 #include <cuda_bf16.h>
 
 #include "ep_internal.h"
 
 namespace ep {
 
-constexpr int kCombineBwdThreads = 256;
+constexpr int kCombineBwdWarps = 8;
+constexpr int kUnroll = 4;
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -19,60 +23,113 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&b);
 }
 
-__global__ void __launch_bounds__(kCombineBwdThreads)
-    combine_backward_kernel(const CombineBackwardParams p)
+// Pieces first, first + step, ... of one row; returns the lane's part of <dout, row>.
+template <bool DGATES, bool DROWS>
+__device__ __forceinline__ float row_pieces(const uint4 *dout, const uint4 *row, uint4 *drow, float g,
+                                            int first, int step, int pieces)
 {
-    __shared__ float part[kCombineBwdThreads / 32];
-    const int64_t t = blockIdx.x;
-    const int vecs = p.N / 8;
-    const uint4 *dout = reinterpret_cast<const uint4 *>(p.dout + t * p.N * 2);
-    for (int j = 0; j < p.top_k; ++j) {
-        const int64_t row = (t * p.top_k + j) * p.N * 2;
-        const float g = p.drows ? __ldg(p.gates + t * p.top_k + j) : 0.f;
-        float sum = 0.f;
-        for (int v = threadIdx.x; v < vecs; v += kCombineBwdThreads) {
-            const uint4 dv = __ldg(dout + v);
-            const uint32_t d[4] = {dv.x, dv.y, dv.z, dv.w};
-            if (p.dgates) {
-                const uint4 rv = *(reinterpret_cast<const uint4 *>(p.recv_buf + row) + v);
-                const uint32_t r[4] = {rv.x, rv.y, rv.z, rv.w};
+    float sum = 0.f;
+    for (int v0 = first; v0 < pieces; v0 += kUnroll * step) {
+        uint4 d[kUnroll], r[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int v = v0 + u * step;
+            if (v < pieces) {
+                d[u] = __ldg(dout + v);
+                if (DGATES)
+                    r[u] = __ldcs(row + v);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int v = v0 + u * step;
+            if (v >= pieces)
+                break;
+            const uint32_t dw[4] = {d[u].x, d[u].y, d[u].z, d[u].w};
+            if (DGATES) {
+                const uint32_t rw[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    sum = fmaf(bf16_lo(d[h]), bf16_lo(r[h]), sum);
-                    sum = fmaf(bf16_hi(d[h]), bf16_hi(r[h]), sum);
+                    sum = fmaf(bf16_lo(dw[h]), bf16_lo(rw[h]), sum);
+                    sum = fmaf(bf16_hi(dw[h]), bf16_hi(rw[h]), sum);
                 }
             }
-            if (p.drows) {
+            if (DROWS) {
                 uint32_t o[4];
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
-                    o[h] = pack_bf16(g * bf16_lo(d[h]), g * bf16_hi(d[h]));
-                *(reinterpret_cast<uint4 *>(p.drows + row) + v) = make_uint4(o[0], o[1], o[2], o[3]);
+                    o[h] = pack_bf16(g * bf16_lo(dw[h]), g * bf16_hi(dw[h]));
+                __stcs(drow + v, make_uint4(o[0], o[1], o[2], o[3]));
             }
         }
-        if (!p.dgates)
-            continue;
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (threadIdx.x % 32 == 0)
-            part[threadIdx.x / 32] = sum;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            float all = 0.f;
-            for (int w = 0; w < kCombineBwdThreads / 32; ++w)
-                all += part[w];
-            p.dgates[t * p.top_k + j] = all;
-        }
-        __syncthreads();
     }
+    return sum;
+}
+
+// WPR: warps of a row, 1 or all of the block.
+template <bool DGATES, bool DROWS, int WPR>
+__global__ void __launch_bounds__(32 * kCombineBwdWarps)
+    combine_backward_kernel(const CombineBackwardParams p)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int pieces = p.N / 8;
+    const int64_t rows = static_cast<int64_t>(p.T) * p.top_k;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kCombineBwdWarps / WPR);
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * (kCombineBwdWarps / WPR) + (WPR == 1 ? warp : 0);
+         row < rows; row += stride) {
+        const int64_t t = row / p.top_k;
+        const float g = DROWS ? __ldg(p.gates + row) : 0.f;
+        float sum = row_pieces<DGATES, DROWS>(
+            reinterpret_cast<const uint4 *>(p.dout) + t * pieces,
+            reinterpret_cast<const uint4 *>(p.recv_buf) + row * pieces,
+            reinterpret_cast<uint4 *>(p.drows) + row * pieces, g, WPR == 1 ? lane : threadIdx.x,
+            32 * WPR, pieces);
+        if constexpr (DGATES) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if constexpr (WPR == 1) {
+                if (lane == 0)
+                    p.dgates[row] = sum;
+            } else {
+                __shared__ float part[WPR];
+                if (lane == 0)
+                    part[warp] = sum;
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    float all = 0.f;
+                    for (int w = 0; w < WPR; ++w)
+                        all += part[w];
+                    p.dgates[row] = all;
+                }
+                __syncthreads();
+            }
+        }
+    }
+}
+
+template <bool DGATES, bool DROWS>
+static cudaError_t launch_form(const CombineBackwardParams &p, int num_sms, cudaStream_t s)
+{
+    const int64_t rows = static_cast<int64_t>(p.T) * p.top_k;
+    // a block to a row up to two rows an SM, and only where its warps all find work
+    if (rows <= 2 * num_sms && p.N >= 8 * 32 * kCombineBwdWarps) {
+        combine_backward_kernel<DGATES, DROWS, kCombineBwdWarps>
+            <<<static_cast<unsigned>(rows), 32 * kCombineBwdWarps, 0, s>>>(p);
+    } else {
+        const int64_t blocks = (rows + kCombineBwdWarps - 1) / kCombineBwdWarps;
+        const int64_t most = static_cast<int64_t>(num_sms) * 1024;
+        combine_backward_kernel<DGATES, DROWS, 1>
+            <<<static_cast<unsigned>(blocks < most ? blocks : most), 32 * kCombineBwdWarps, 0, s>>>(p);
+    }
+    return cudaGetLastError();
 }
 
 cudaError_t launch_combine_backward(const CombineBackwardParams &p, int num_sms, cudaStream_t s)
 {
-    (void)num_sms;
-    combine_backward_kernel<<<p.T, kCombineBwdThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    if (p.dgates && p.drows)
+        return launch_form<true, true>(p, num_sms, s);
+    return p.dgates ? launch_form<true, false>(p, num_sms, s) : launch_form<false, true>(p, num_sms, s);
 }
 
 }  // namespace ep

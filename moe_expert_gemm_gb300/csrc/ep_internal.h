@@ -132,6 +132,9 @@ struct CombineParams {
 struct RouteParams {
     int T, E, top_k, n_groups, topk_groups, group_top, score, renormalize;
     int bf16;  // logits type
+    // set by the launcher: experts of a group, lanes of a warp for one (log2), rows (and
+    // the bias) can be loaded in aligned pieces, a group's worth is a sum of two
+    int per, lanes_log2, vec, two_of_group;
     int64_t stride;
     float scale;
     const void *logits;

@@ -8,7 +8,19 @@
 //                 sigmoid dl_j = a_j (1 - s_j) (dg_j - c);
 //   plain:        softmax dl_i = s_i ([i chosen] dg_i - sum_j dg_j s_j),
 //                 sigmoid dl_j = s_j (1 - s_j) dg_j;
-// each times `scale`. One warp takes one token.
+// each times `scale`.
+//
+// The bytes are one pass over the logits; what has to be kept down is the instructions
+// for a token. Forms, by the number of experts:
+//  * route_thread_kernel, E <= 16: a thread takes a token, its experts in registers.
+//  * route_warp_kernel, E <= 256 (groups: a power of two): a warp takes a token, 8 values
+//    a lane. A choice value that needs an exponential and a division is first taken
+//    approximately; the k-th largest of the lanes' maxima bounds the k-th choice from
+//    below, which leaves hardly more than k candidates. Those go to one lane each, get
+//    their exact fp32 value there, and are ranked by counting. Where the approximation
+//    cannot decide (groups closer than its error, NaN, too few unmasked experts, more than
+//    32 candidates) the token is done over by route_token.
+//  * route_token_kernel: everything else, by scanning shared memory.
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -29,12 +41,45 @@ __device__ __forceinline__ uint32_t choice_key(float v)
 }
 constexpr uint32_t kKeyOut = 0, kKeyMasked = 1;
 
+template <int W>
+__device__ __forceinline__ void store_vec(float *p, const float *v)
+{
+    if constexpr (W == 4)
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else if constexpr (W == 2)
+        *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+    else
+        *p = v[0];
+}
+
+template <int W>
+__device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float *v)
+{
+    if constexpr (W == 1) {
+        *p = __float2bfloat16_rn(v[0]);
+    } else {
+        uint32_t w[W / 2];
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+            const __nv_bfloat162 b = __float22bfloat162_rn(make_float2(v[2 * i], v[2 * i + 1]));
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        if constexpr (W == 8)
+            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (W == 4)
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint32_t *>(p) = w[0];
+    }
+}
+
+// (Plain loads: a gradient may be written over its logits.)
 template <typename T>
 struct Logit;
 template <>
 struct Logit<float> {
     static constexpr float lowest = -FLT_MAX;
-    static __device__ __forceinline__ float load(const float *p) { return __ldg(p); }
+    static __device__ __forceinline__ float load(const float *p) { return *p; }
     static __device__ __forceinline__ void store(float *p, float v) { *p = v; }
 };
 template <>
@@ -42,8 +87,7 @@ struct Logit<__nv_bfloat16> {
     static constexpr float lowest = -3.3895313892515355e38f;  // -(2 - 2^-7) * 2^127
     static __device__ __forceinline__ float load(const __nv_bfloat16 *p)
     {
-        return __uint_as_float(
-            static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short *>(p))) << 16);
+        return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const unsigned short *>(p)) << 16);
     }
     static __device__ __forceinline__ void store(__nv_bfloat16 *p, float v)
     {
@@ -72,19 +116,15 @@ __device__ __forceinline__ float warp_max(float x)
     return x;
 }
 
-// Shared memory of a warp: E choice keys and E scores.
+// One token by one warp, whatever its logits; smem holds E choice keys and E scores.
 template <typename T>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams p)
+__device__ __noinline__ void route_token(const RouteParams &p, int64_t t, uint32_t *key)
 {
-    extern __shared__ uint32_t smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
     const int E = p.E, k = p.top_k;
-    uint32_t *key = smem + static_cast<int64_t>(warp) * 2 * E;
     float *score = reinterpret_cast<float *>(key + E);
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRouteThreads / 32) + warp;
-    if (t >= p.T)
-        return;
     const T *l = static_cast<const T *>(p.logits) + t * p.stride;
+    __syncwarp();  // the caller's use of the memory is over
 
     float top = -INFINITY;
     bool nan = false;
@@ -198,9 +238,441 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
     }
 }
 
+template <typename T>
+__global__ void __launch_bounds__(kRouteThreads) route_token_kernel(const __grid_constant__ RouteParams p)
+{
+    extern __shared__ uint32_t smem[];
+    const int warp = threadIdx.x >> 5;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRouteThreads / 32) + warp;
+    if (t < p.T)
+        route_token<T>(p, t, smem + static_cast<int64_t>(warp) * 2 * p.E);
+}
+
+// A lane's experts in route_warp_kernel: group lane / lanes (of 32 / n_groups lanes each),
+// members i * lanes + lane % lanes, or, W at a time, pieces of W consecutive members.
+template <int VPL, int W>
+struct LaneExperts {
+    int first, per, lanes_log2, sub;
+
+    __device__ __forceinline__ LaneExperts(const RouteParams &p, int lane)
+    {
+        per = p.per;
+        lanes_log2 = p.lanes_log2;
+        sub = lane & ((1 << lanes_log2) - 1);
+        first = (lane >> lanes_log2) * per;
+    }
+    __device__ __forceinline__ int member(int i) const
+    {
+        return ((i / W) << lanes_log2) * W + sub * W + i % W;
+    }
+};
+
+// W values at once (as many as their bytes allow), W * sizeof(T) aligned.
+template <int W>
+__device__ __forceinline__ void load_vec(const float *p, float *out)
+{
+    if constexpr (W == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        out[0] = v.x, out[1] = v.y, out[2] = v.z, out[3] = v.w;
+    } else if constexpr (W == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        out[0] = v.x, out[1] = v.y;
+    } else {
+        out[0] = *p;
+    }
+}
+
+template <int W>
+__device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float *out)
+{
+    if constexpr (W == 1) {
+        out[0] = Logit<__nv_bfloat16>::load(p);
+    } else {
+        uint32_t w[W / 2];
+        if constexpr (W == 8) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else if constexpr (W == 4) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x, w[1] = v.y;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        }
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+            out[2 * i] = __uint_as_float(w[i] << 16);
+            out[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+// How far a choice value (or a sum of two) taken with the fast exponential and reciprocal
+// may lie from the fp32 formula's: e^-x is off by a few units in 2^-22 relative plus
+// |x| 2^-23, which the sigmoid's slope turns into less than 2^-21 absolute; a softmax
+// score is off by less; the addition of the bias rounds once on either side.
+__device__ __forceinline__ float choice_error(float v)
+{
+    return 0x1p-20f + 0x1p-22f * fabsf(v);
+}
+
+constexpr int kRouteWarps = 8;  // of a block of route_warp_kernel
+
+// VEC: a lane's members come in pieces of W, loaded at once.
+template <typename T, int VPL, bool VEC>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __grid_constant__ RouteParams p)
+{
+    constexpr int kMost = 16 / static_cast<int>(sizeof(T));
+    constexpr int W = VEC ? (VPL < kMost ? VPL : kMost) : 1;
+    constexpr int WB = VEC ? (VPL < 4 ? VPL : 4) : 1;  // of the bias
+    extern __shared__ uint32_t smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
+    if (t >= p.T)
+        return;
+    uint32_t *own = smem + static_cast<int64_t>(warp) * (2 * p.E > 64 ? 2 * p.E : 64);
+    const int k = p.top_k;
+    const bool sigmoid = p.score == EP_SCORE_SIGMOID;
+    const LaneExperts<VPL, W> at(p, lane);
+    const T *row = static_cast<const T *>(p.logits) + t * p.stride + at.first;
+    float x[VPL], v[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; i += W) {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            x[i + j] = -INFINITY;
+        if (at.member(i) < at.per)  // a piece is whole or missing
+            load_vec<W>(row + at.member(i), x + i);
+    }
+    if (p.bias) {
+        const float *b = p.bias + at.first;
+#pragma unroll
+        for (int i = 0; i < VPL; i += WB) {
+#pragma unroll
+            for (int j = 0; j < WB; ++j)
+                v[i + j] = 0.f;
+            if (at.member(i) < at.per)
+                load_vec<WB>(b + at.member(i), v + i);
+        }
+    }
+    bool odd = false;
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        odd |= isnan(x[i]);
+        if (!(x[i] > Logit<T>::lowest))
+            x[i] = -INFINITY;  // masked (or missing): out of the fast path's running
+        top = fmaxf(top, x[i]);
+    }
+    // of the whole row, for the scores of the softmax
+    float total = 1.f;
+    if (!sigmoid && (p.bias || !p.renormalize || p.two_of_group)) {
+        top = warp_max(top);
+        odd |= !(fabsf(top) < INFINITY);
+        total = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            total += expf(x[i] - top);
+        total = warp_sum(total);
+    }
+    const float rtotal = 1.f / total;
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const float s = sigmoid ? __fdividef(1.f, 1.f + __expf(-x[i])) : __expf(x[i] - top) * rtotal;
+            v[i] = x[i] == -INFINITY ? -INFINITY : s + v[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            v[i] = x[i];
+    }
+
+    if (p.topk_groups < p.n_groups) {
+        // the two best of the group, over its lanes
+        float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            float w = v[i];
+            if (p.two_of_group && !p.bias)
+                w = x[i] == -INFINITY ? -INFINITY
+                    : sigmoid         ? __fdividef(1.f, 1.f + __expf(-x[i]))
+                                      : __expf(x[i] - top);
+            b = fmaxf(b, fminf(a, w));
+            a = fmaxf(a, w);
+        }
+        for (int o = 1; o < 1 << p.lanes_log2; o <<= 1) {
+            const float a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
+            b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+            a = fmaxf(a, a2);
+        }
+        const float worth = !p.two_of_group || b == -INFINITY ? a : a + b;
+        const bool exact = !p.two_of_group && !p.bias;
+        const int mine = lane >> p.lanes_log2;
+        int better = 0;
+        bool close = false;
+        for (int g = 0; g < p.n_groups; ++g) {
+            const float w = __shfl_sync(kFull, worth, g << p.lanes_log2);
+            better += w > worth || (w == worth && g < mine);
+            close |= g != mine && fabsf(w - worth) <= 4.f * choice_error(w);
+        }
+        odd |= close && !exact;
+        if (better >= p.topk_groups) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                v[i] = -INFINITY;
+        }
+    }
+
+    // the k-th largest of the lanes' maxima is at most the k-th largest of all
+    float most = v[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i)
+        most = fmaxf(most, v[i]);
+    uint32_t key = choice_key(most), kth = 0;
+    for (int j = 0; j < k; ++j) {
+        kth = __reduce_max_sync(kFull, key);
+        key = key == kth ? 0 : key;
+    }
+    float bar = __uint_as_float(kth >> 31 ? kth ^ 0x80000000u : ~kth);
+    odd |= kth <= choice_key(-INFINITY);
+    if (p.bias)
+        bar -= 2.f * choice_error(bar);
+    int n = 0;  // candidates: (logit, expert)
+    if (!__any_sync(kFull, odd)) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const bool in = v[i] >= bar;
+            const unsigned who = __ballot_sync(kFull, in);
+            const int to = n + __popc(who & ((1u << lane) - 1));
+            if (in && to < 32) {
+                own[to] = __float_as_uint(x[i]);
+                own[32 + to] = at.first + at.member(i);
+            }
+            n += __popc(who);
+        }
+    }
+    if (n == 0 || n > 32 || n < k) {
+        route_token<T>(p, t, own);
+        return;
+    }
+    __syncwarp();
+    float cx = -INFINITY, s = 0.f;
+    int id = p.E;
+    uint32_t ck = 0;
+    if (lane < n) {
+        cx = __uint_as_float(own[lane]);
+        id = own[32 + lane];
+        float cv = cx;
+        if (sigmoid)
+            s = sigmoid_f32(cx);
+        else if (p.bias || !p.renormalize)
+            s = expf(cx - top) / total;
+        if (p.bias)
+            cv = s + __ldg(p.bias + id);
+        ck = choice_key(cv);
+    }
+    int rank = 0;
+    for (int c = 0; c < n; ++c) {
+        const uint32_t ok = __shfl_sync(kFull, ck, c);
+        const int oi = __shfl_sync(kFull, id, c);
+        rank += ok > ck || (ok == ck && oi < id);
+    }
+    const bool chosen = lane < n && rank < k;
+    if (!sigmoid && p.renormalize) {
+        const float m = warp_max(chosen ? cx : -INFINITY);
+        s = expf(cx - m);
+    }
+    s = chosen ? s : 0.f;
+    if (p.renormalize) {
+        const float sum = warp_sum(s);
+        s = sum == 0.f ? 0.f : s / sum;
+    }
+    if (!chosen)
+        return;
+    p.topk_ids[t * k + rank] = id;
+    if (p.gates)
+        p.gates[t * k + rank] = s * p.scale;
+}
+
+// A thread a token, E <= EP.
+template <typename T, int EP>
+__global__ void __launch_bounds__(128) route_thread_kernel(const __grid_constant__ RouteParams p)
+{
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (t >= p.T)
+        return;
+    const int E = p.E, k = p.top_k;
+    const bool sigmoid = p.score == EP_SCORE_SIGMOID;
+    const T *l = static_cast<const T *>(p.logits) + t * p.stride;
+    constexpr int W = 16 / sizeof(T) < EP ? 16 / sizeof(T) : EP;
+    float x[EP];
+    if (p.vec && E == EP) {
+#pragma unroll
+        for (int i = 0; i < EP; i += W)
+            load_vec<W>(l + i, x + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < EP; ++i)
+            x[i] = i < E ? Logit<T>::load(l + i) : -INFINITY;
+    }
+    bool nan = false;
+    float top = -INFINITY, total = 0.f;
+#pragma unroll
+    for (int i = 0; i < EP; ++i) {
+        nan |= isnan(x[i]);
+        if (!(x[i] > Logit<T>::lowest))
+            x[i] = -INFINITY;
+        top = fmaxf(top, x[i]);
+    }
+    if (!sigmoid && (p.bias || !p.renormalize)) {
+#pragma unroll
+        for (int i = 0; i < EP; ++i)
+            total += x[i] == -INFINITY ? 0.f : expf(x[i] - top);
+    }
+    auto score = [&](float y) {
+        return y == -INFINITY ? 0.f : sigmoid ? sigmoid_f32(y) : expf(y - top) / total;
+    };
+    uint32_t key[EP];
+#pragma unroll
+    for (int i = 0; i < EP; ++i) {
+        const float v = p.bias && i < E ? score(x[i]) + __ldg(p.bias + i) : x[i];
+        key[i] = i >= E ? kKeyOut : x[i] == -INFINITY ? kKeyMasked : choice_key(v);
+    }
+    float sx[EP], m = -INFINITY;  // logits of the chosen
+#pragma unroll
+    for (int j = 0; j < EP; ++j) {
+        if (j >= k)
+            break;
+        uint32_t best = kKeyOut;
+        int id = 0;
+        sx[j] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EP; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                id = i;
+                sx[j] = x[i];
+            }
+#pragma unroll
+        for (int i = 0; i < EP; ++i)
+            key[i] = i == id ? kKeyOut : key[i];
+        m = fmaxf(m, sx[j]);
+        p.topk_ids[t * k + j] = id;
+    }
+    if (!p.gates)
+        return;
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < EP; ++j) {
+        if (j >= k)
+            break;
+        sx[j] = !sigmoid && p.renormalize ? (sx[j] == -INFINITY ? 0.f : expf(sx[j] - m)) : score(sx[j]);
+        sum += sx[j];
+    }
+#pragma unroll
+    for (int j = 0; j < EP; ++j) {
+        if (j >= k)
+            break;
+        float a = sx[j];
+        if (p.renormalize)
+            a = sum == 0.f ? 0.f : a / sum;
+        p.gates[t * k + j] = nan ? NAN : a * p.scale;
+    }
+}
+
+// The gradient of a token by a warp, VPL values a lane in pieces of W. The dense value
+// (0, or -s_i c of the plain softmax) goes to every logit first, the chosen ones' over it:
+// a warp's later stores follow its earlier ones.
+template <typename T, int VPL, bool VEC>
+__global__ void __launch_bounds__(32 * kRouteWarps)
+    route_backward_warp_kernel(const __grid_constant__ RouteBackwardParams p)
+{
+    constexpr int kMost = 16 / static_cast<int>(sizeof(T));
+    constexpr int W = VEC ? (VPL < kMost ? VPL : kMost) : 1;
+    const int lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+    if (t >= p.T)
+        return;
+    const int E = p.E, k = p.top_k;
+    const T *l = static_cast<const T *>(p.logits) + t * p.stride;
+    T *out = static_cast<T *>(p.dlogits) + t * p.dstride;
+    auto expert = [&](int i) { return (i / W) * 32 * W + lane * W + i % W; };
+    const bool dense = p.score == EP_SCORE_SOFTMAX && !p.renormalize;
+    float y[VPL];
+    if (dense) {
+#pragma unroll
+        for (int i = 0; i < VPL; i += W) {
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                y[i + j] = -INFINITY;
+            if (expert(i) < E)
+                load_vec<W>(l + expert(i), y + i);
+        }
+    }
+    int id = lane < k ? __ldg(p.topk_ids + t * k + lane) : -1;
+    float dg = lane < k ? __ldg(p.dgates + t * k + lane) : 0.f;
+    if (lane < k && (id < 0 || id >= E)) {
+        atomicOr(p.status, EP_STATUS_ROUTING);
+        id = -1;
+    }
+    const float x = id >= 0 ? Logit<T>::load(l + id) : -INFINITY;
+    const bool live = id >= 0 && !(x <= Logit<T>::lowest);
+    if (!live)
+        dg = 0.f;
+    float dl;
+    if (dense) {
+        float top = -INFINITY, total = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            top = fmaxf(top, y[i]);
+        top = warp_max(top);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            y[i] = y[i] <= Logit<T>::lowest ? 0.f : expf(y[i] - top);
+            total += y[i];
+        }
+        total = warp_sum(total);
+        const float rtotal = 1.f / total;
+        const float s = live ? expf(x - top) * rtotal : 0.f;
+        const float part = live ? dg * s : 0.f;
+        const float c = warp_sum(part);
+        dl = part - s * c;
+        const float cr = c * rtotal * p.scale;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            y[i] = y[i] == 0.f ? 0.f : -y[i] * cr;
+    } else {
+        float a = 0.f, slope = 1.f;
+        if (p.score == EP_SCORE_SOFTMAX) {
+            const float m = warp_max(live ? x : -INFINITY);
+            a = live ? expf(x - m) : 0.f;
+        } else if (live) {
+            a = sigmoid_f32(x);
+            slope = sigmoid_f32(-x);
+        }
+        if (p.renormalize) {
+            const float sum = warp_sum(a);
+            a = sum == 0.f ? 0.f : a / sum;
+            dg -= warp_sum(dg * a);
+        }
+        dl = a == 0.f ? 0.f : a * slope * dg;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            y[i] = 0.f;
+    }
+    __syncwarp();  // every lane has read its logits (they may be what is written)
+#pragma unroll
+    for (int i = 0; i < VPL; i += W)
+        if (expert(i) < E)
+            store_vec<W>(out + expert(i), y + i);
+    __syncwarp();
+    if (live)
+        Logit<T>::store(out + id, dl * p.scale);
+}
+
 // Shared memory of a warp: the E gradients of its token.
 template <typename T>
-__global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const RouteBackwardParams p)
+__global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const __grid_constant__ RouteBackwardParams p)
 {
     extern __shared__ uint32_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -267,29 +739,119 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const Rou
 }
 
 template <typename Kern, typename Params>
-static cudaError_t launch_rows(Kern kern, const Params &p, int64_t warp_bytes, cudaStream_t s)
+static cudaError_t launch_rows(Kern kern, const Params &p, int warps, int64_t warp_bytes,
+                               cudaStream_t s)
 {
-    const int warps = kRouteThreads / 32;
     const int smem = static_cast<int>(warps * warp_bytes);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess)
-        return e;
-    kern<<<static_cast<unsigned>((p.T + warps - 1) / warps), kRouteThreads, smem, s>>>(p);
+    if (smem > 48 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess)
+            return e;
+    }
+    kern<<<static_cast<unsigned>((static_cast<int64_t>(p.T) + warps - 1) / warps), 32 * warps, smem,
+           s>>>(p);
     return cudaGetLastError();
+}
+
+static bool aligned(const void *p, int64_t bytes)
+{
+    return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0;
+}
+
+// Values a lane takes of each: 1, 2, 4 or 8.
+static int lane_values(int per_lane)
+{
+    return per_lane <= 1 ? 1 : per_lane <= 2 ? 2 : per_lane <= 4 ? 4 : 8;
+}
+
+template <typename T, int VPL>
+static cudaError_t launch_route_vpl(const RouteParams &p, cudaStream_t s)
+{
+    const int64_t bytes = 4 * (2 * p.E > 64 ? 2 * p.E : 64);
+    return p.vec ? launch_rows(route_warp_kernel<T, VPL, true>, p, kRouteWarps, bytes, s)
+                 : launch_rows(route_warp_kernel<T, VPL, false>, p, kRouteWarps, bytes, s);
+}
+
+template <typename T>
+static cudaError_t launch_route_type(RouteParams p, cudaStream_t s)
+{
+    constexpr int most = 16 / sizeof(T);
+    const int groups = p.topk_groups < p.n_groups ? p.n_groups : 1;  // that matter
+    p.n_groups = groups;
+    if (groups == 1)
+        p.topk_groups = 1;
+    p.two_of_group = groups > 1 && p.group_top == 2;
+    if (p.E <= 16 && groups == 1) {
+        const int ep = p.E <= 8 ? 8 : 16;
+        p.vec = aligned(p.logits, 16) && p.stride % most == 0;
+        const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(p.T) + 127) / 128);
+        if (ep == 8)
+            route_thread_kernel<T, 8><<<blocks, 128, 0, s>>>(p);
+        else
+            route_thread_kernel<T, 16><<<blocks, 128, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    int lanes_log2 = 5;
+    while (lanes_log2 > 0 && 32 >> lanes_log2 < groups)
+        --lanes_log2;
+    p.per = p.E / groups;
+    p.lanes_log2 = lanes_log2;
+    const int per_lane = (p.per + (1 << lanes_log2) - 1) >> lanes_log2;
+    if (32 >> lanes_log2 != groups || per_lane > 8)
+        return launch_rows(route_token_kernel<T>, p, kRouteThreads / 32, 8ll * p.E, s);
+    const int vpl = lane_values(per_lane), w = vpl < most ? vpl : most, wb = vpl < 4 ? vpl : 4;
+    p.vec = p.per % w == 0 && p.per % wb == 0 && p.stride % w == 0 &&
+            aligned(p.logits, w * static_cast<int>(sizeof(T))) && aligned(p.bias, 4 * wb);
+    switch (vpl) {
+    case 1:
+        return launch_route_vpl<T, 1>(p, s);
+    case 2:
+        return launch_route_vpl<T, 2>(p, s);
+    case 4:
+        return launch_route_vpl<T, 4>(p, s);
+    default:
+        return launch_route_vpl<T, 8>(p, s);
+    }
 }
 
 cudaError_t launch_route(const RouteParams &p, int num_sms, cudaStream_t s)
 {
     (void)num_sms;
-    return p.bf16 ? launch_rows(route_kernel<__nv_bfloat16>, p, 8ll * p.E, s)
-                  : launch_rows(route_kernel<float>, p, 8ll * p.E, s);
+    return p.bf16 ? launch_route_type<__nv_bfloat16>(p, s) : launch_route_type<float>(p, s);
+}
+
+template <typename T, int VPL>
+static cudaError_t launch_backward_vpl(const RouteBackwardParams &p, cudaStream_t s)
+{
+    constexpr int most = 16 / sizeof(T), w = VPL < most ? VPL : most;
+    const bool vec = p.E % w == 0 && p.stride % w == 0 && p.dstride % w == 0 &&
+                     aligned(p.logits, w * sizeof(T)) && aligned(p.dlogits, w * sizeof(T));
+    return vec ? launch_rows(route_backward_warp_kernel<T, VPL, true>, p, kRouteWarps, 0, s)
+               : launch_rows(route_backward_warp_kernel<T, VPL, false>, p, kRouteWarps, 0, s);
+}
+
+template <typename T>
+static cudaError_t launch_backward_type(const RouteBackwardParams &p, cudaStream_t s)
+{
+    if (p.E > 256)
+        return launch_rows(route_backward_kernel<T>, p, kRouteThreads / 32, 4ll * p.E, s);
+    switch (lane_values((p.E + 31) / 32)) {
+    case 1:
+        return launch_backward_vpl<T, 1>(p, s);
+    case 2:
+        return launch_backward_vpl<T, 2>(p, s);
+    case 4:
+        return launch_backward_vpl<T, 4>(p, s);
+    default:
+        return launch_backward_vpl<T, 8>(p, s);
+    }
 }
 
 cudaError_t launch_route_backward(const RouteBackwardParams &p, int num_sms, cudaStream_t s)
 {
     (void)num_sms;
-    return p.bf16 ? launch_rows(route_backward_kernel<__nv_bfloat16>, p, 4ll * p.E, s)
-                  : launch_rows(route_backward_kernel<float>, p, 4ll * p.E, s);
+    return p.bf16 ? launch_backward_type<__nv_bfloat16>(p, s) : launch_backward_type<float>(p, s);
 }
 
 }  // namespace ep
