@@ -135,6 +135,7 @@ struct RouteParams {
     // set by the launcher: experts of a group, lanes of a warp for one (log2), rows (and
     // the bias) can be loaded in aligned pieces, a group's worth is a sum of two
     int per, lanes_log2, vec, two_of_group;
+    int warp_words;  // of shared memory
     int64_t stride;
     float scale;
     const void *logits;

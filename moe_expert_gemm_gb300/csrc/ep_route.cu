@@ -41,6 +41,11 @@ __device__ __forceinline__ uint32_t choice_key(float v)
 }
 constexpr uint32_t kKeyOut = 0, kKeyMasked = 1;
 
+__device__ __forceinline__ float key_value(uint32_t key)
+{
+    return __uint_as_float(key >> 31 ? key ^ 0x80000000u : ~key);
+}
+
 template <int W>
 __device__ __forceinline__ void store_vec(float *p, const float *v)
 {
@@ -100,6 +105,21 @@ __device__ __forceinline__ float sigmoid_f32(float x)
     return 1.f / (1.f + expf(-x));
 }
 
+// Approximations (errors: choice_error). e^x by 2^(x log2 e).
+__device__ __forceinline__ float fast_exp(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+    return y;
+}
+
+__device__ __forceinline__ float fast_sigmoid(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + fast_exp(-x)));
+    return y;
+}
+
 __device__ __forceinline__ float warp_sum(float x)
 {
 #pragma unroll
@@ -116,7 +136,10 @@ __device__ __forceinline__ float warp_max(float x)
     return x;
 }
 
-// One token by one warp, whatever its logits; smem holds E choice keys and E scores.
+// One token by one warp, whatever its logits; `key` points to kTokenWords * E words: choice
+// keys, scores, groups' worths.
+constexpr int kTokenWords = 3;
+
 template <typename T>
 __device__ __noinline__ void route_token(const RouteParams &p, int64_t t, uint32_t *key)
 {
@@ -156,9 +179,9 @@ __device__ __noinline__ void route_token(const RouteParams &p, int64_t t, uint32
     __syncwarp();
 
     if (p.topk_groups < p.n_groups) {
-        // every lane ranks its groups against all others
         const int per = E / p.n_groups;
-        auto worth = [&](int g) -> uint32_t {
+        uint32_t *worth = key + 2 * E;
+        for (int g = lane; g < p.n_groups; g += 32) {
             uint32_t best = kKeyMasked, second = kKeyMasked;
             float s_best = 0.f, s_second = 0.f;
             for (int i = g * per; i < (g + 1) * per; ++i) {
@@ -169,32 +192,25 @@ __device__ __noinline__ void route_token(const RouteParams &p, int64_t t, uint32
                     second = key[i], s_second = score[i];
                 }
             }
-            if (p.group_top == 1 || best == kKeyMasked)
-                return best;
-            if (p.bias) {
-                const uint32_t a = best >> 31 ? best ^ 0x80000000u : ~best;
-                const uint32_t b = second >> 31 ? second ^ 0x80000000u : ~second;
-                s_best = __uint_as_float(a);
-                s_second = second == kKeyMasked ? 0.f : __uint_as_float(b);
+            if (p.group_top == 2 && best != kKeyMasked) {
+                if (p.bias) {
+                    s_best = key_value(best);
+                    s_second = second == kKeyMasked ? 0.f : key_value(second);
+                }
+                best = choice_key(s_best + s_second);
             }
-            return choice_key(s_best + s_second);
-        };
-        uint64_t out = 0;  // this lane's groups that are not among the best
-        for (int g = lane, n = 0; g < p.n_groups; g += 32, ++n) {
-            const uint32_t w = worth(g);
-            int better = 0;
-            for (int h = 0; h < p.n_groups; ++h) {
-                const uint32_t o = worth(h);
-                better += o > w || (o == w && h < g);
-            }
-            if (better >= p.topk_groups)
-                out |= 1ull << n;
+            worth[g] = best;
         }
         __syncwarp();
-        for (int g = lane, n = 0; g < p.n_groups; g += 32, ++n)
-            if (out >> n & 1)
+        for (int g = lane; g < p.n_groups; g += 32) {
+            const uint32_t w = worth[g];
+            int better = 0;
+            for (int h = 0; h < p.n_groups; ++h)
+                better += worth[h] > w || (worth[h] == w && h < g);
+            if (better >= p.topk_groups)
                 for (int i = g * per; i < (g + 1) * per; ++i)
                     key[i] = kKeyOut;
+        }
         __syncwarp();
     }
 
@@ -245,7 +261,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_token_kernel(const __grid
     const int warp = threadIdx.x >> 5;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRouteThreads / 32) + warp;
     if (t < p.T)
-        route_token<T>(p, t, smem + static_cast<int64_t>(warp) * 2 * p.E);
+        route_token<T>(p, t, smem + static_cast<int64_t>(warp) * kTokenWords * p.E);
 }
 
 // A lane's experts in route_warp_kernel: group lane / lanes (of 32 / n_groups lanes each),
@@ -317,8 +333,11 @@ __device__ __forceinline__ float choice_error(float v)
 
 constexpr int kRouteWarps = 8;  // of a block of route_warp_kernel
 
+// What the experts are chosen by: the logit, or sigmoid or softmax score plus bias.
+enum Choice { kByLogit, kBySigmoid, kBySoftmax };
+
 // VEC: a lane's members come in pieces of W, loaded at once.
-template <typename T, int VPL, bool VEC>
+template <typename T, int VPL, bool VEC, Choice BY>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __grid_constant__ RouteParams p)
 {
     constexpr int kMost = 16 / static_cast<int>(sizeof(T));
@@ -329,7 +348,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __gr
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
     if (t >= p.T)
         return;
-    uint32_t *own = smem + static_cast<int64_t>(warp) * (2 * p.E > 64 ? 2 * p.E : 64);
+    uint32_t *own = smem + static_cast<int64_t>(warp) * p.warp_words;
     const int k = p.top_k;
     const bool sigmoid = p.score == EP_SCORE_SIGMOID;
     const LaneExperts<VPL, W> at(p, lane);
@@ -343,7 +362,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __gr
         if (at.member(i) < at.per)  // a piece is whole or missing
             load_vec<W>(row + at.member(i), x + i);
     }
-    if (p.bias) {
+    if constexpr (BY != kByLogit) {
         const float *b = p.bias + at.first;
 #pragma unroll
         for (int i = 0; i < VPL; i += WB) {
@@ -354,18 +373,26 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __gr
                 load_vec<WB>(b + at.member(i), v + i);
         }
     }
-    bool odd = false;
-    float top = -INFINITY;
+    bool odd = false, usual = true;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        odd |= isnan(x[i]);
-        if (!(x[i] > Logit<T>::lowest))
-            x[i] = -INFINITY;  // masked (or missing): out of the fast path's running
-        top = fmaxf(top, x[i]);
+    for (int i = 0; i < VPL; ++i)
+        usual &= x[i] > Logit<T>::lowest;
+    usual = __all_sync(kFull, usual);  // no expert masked, missing or NaN
+    if (!usual) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            odd |= isnan(x[i]);
+            if (!(x[i] > Logit<T>::lowest))
+                x[i] = -INFINITY;
+        }
     }
     // of the whole row, for the scores of the softmax
-    float total = 1.f;
-    if (!sigmoid && (p.bias || !p.renormalize || p.two_of_group)) {
+    float top = 0.f, total = 1.f;
+    if (BY == kBySoftmax || (BY == kByLogit && !sigmoid && (!p.renormalize || p.two_of_group))) {
+        top = x[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i)
+            top = fmaxf(top, x[i]);
         top = warp_max(top);
         odd |= !(fabsf(top) < INFINITY);
         total = 0.f;
@@ -374,12 +401,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __gr
             total += expf(x[i] - top);
         total = warp_sum(total);
     }
-    const float rtotal = 1.f / total;
-    if (p.bias) {
+    if constexpr (BY != kByLogit) {
+        const float rtotal = 1.f / total;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const float s = sigmoid ? __fdividef(1.f, 1.f + __expf(-x[i])) : __expf(x[i] - top) * rtotal;
-            v[i] = x[i] == -INFINITY ? -INFINITY : s + v[i];
+        for (int i = 0; i < VPL; ++i)
+            v[i] += BY == kBySigmoid ? fast_sigmoid(x[i]) : fast_exp(x[i] - top) * rtotal;
+        if (!usual) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                v[i] = x[i] == -INFINITY ? -INFINITY : v[i];
         }
     } else {
 #pragma unroll
@@ -390,15 +420,21 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __gr
     if (p.topk_groups < p.n_groups) {
         // the two best of the group, over its lanes
         float a = -INFINITY, b = -INFINITY;
+        if (BY == kByLogit && p.two_of_group) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            float w = v[i];
-            if (p.two_of_group && !p.bias)
-                w = x[i] == -INFINITY ? -INFINITY
-                    : sigmoid         ? __fdividef(1.f, 1.f + __expf(-x[i]))
-                                      : __expf(x[i] - top);
-            b = fmaxf(b, fminf(a, w));
-            a = fmaxf(a, w);
+            for (int i = 0; i < VPL; ++i) {
+                const float w = x[i] == -INFINITY ? -INFINITY
+                                : sigmoid         ? fast_sigmoid(x[i])
+                                                  : fast_exp(x[i] - top);
+                b = fmaxf(b, fminf(a, w));
+                a = fmaxf(a, w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                b = fmaxf(b, fminf(a, v[i]));
+                a = fmaxf(a, v[i]);
+            }
         }
         for (int o = 1; o < 1 << p.lanes_log2; o <<= 1) {
             const float a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
@@ -406,17 +442,31 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __gr
             a = fmaxf(a, a2);
         }
         const float worth = !p.two_of_group || b == -INFINITY ? a : a + b;
-        const bool exact = !p.two_of_group && !p.bias;
-        const int mine = lane >> p.lanes_log2;
-        int better = 0;
-        bool close = false;
-        for (int g = 0; g < p.n_groups; ++g) {
-            const float w = __shfl_sync(kFull, worth, g << p.lanes_log2);
-            better += w > worth || (w == worth && g < mine);
-            close |= g != mine && fabsf(w - worth) <= 4.f * choice_error(w);
+        bool keep;
+        if (BY == kByLogit && !p.two_of_group) {  // the worth is a logit: exact, ties to the lower group
+            const int mine = lane >> p.lanes_log2;
+            int better = 0;
+            for (int g = 0; g < p.n_groups; ++g) {
+                const float w = __shfl_sync(kFull, worth, g << p.lanes_log2);
+                better += w > worth || (w == worth && g < mine);
+            }
+            keep = better < p.topk_groups;
+        } else {
+            // the topk_groups-th largest worth and the one after it: too near each other
+            // (or equal), and the fp32 formula has to tell
+            const uint32_t mine = choice_key(worth);
+            uint32_t left = mine, last = 0;
+            for (int g = 0; g < p.topk_groups; ++g) {
+                last = __reduce_max_sync(kFull, left);
+                left = left == last ? 0 : left;
+            }
+            keep = mine >= last;
+            const float bar = key_value(last), after = key_value(__reduce_max_sync(kFull, left));
+            const unsigned kept = __ballot_sync(kFull, keep);
+            odd |= !(bar - after > 4.f * choice_error(bar)) ||
+                   __popc(kept) != p.topk_groups << p.lanes_log2;
         }
-        odd |= close && !exact;
-        if (better >= p.topk_groups) {
+        if (!keep) {
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
                 v[i] = -INFINITY;
@@ -433,49 +483,56 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __gr
         kth = __reduce_max_sync(kFull, key);
         key = key == kth ? 0 : key;
     }
-    float bar = __uint_as_float(kth >> 31 ? kth ^ 0x80000000u : ~kth);
+    float bar = key_value(kth);
     odd |= kth <= choice_key(-INFINITY);
-    if (p.bias)
+    if (BY != kByLogit)
         bar -= 2.f * choice_error(bar);
-    int n = 0;  // candidates: (logit, expert)
-    if (!__any_sync(kFull, odd)) {
+    uint32_t mine = 0;  // this lane's candidates
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const bool in = v[i] >= bar;
-            const unsigned who = __ballot_sync(kFull, in);
+    for (int i = 0; i < VPL; ++i)
+        mine |= v[i] >= bar ? 1u << i : 0u;
+    int n = 0;  // candidates in all
+    if (!__any_sync(kFull, odd)) {
+        unsigned who;
+        while ((who = __ballot_sync(kFull, mine != 0)) != 0 && n <= 32) {
             const int to = n + __popc(who & ((1u << lane) - 1));
-            if (in && to < 32) {
-                own[to] = __float_as_uint(x[i]);
-                own[32 + to] = at.first + at.member(i);
-            }
+            if (mine && to < 32)
+                own[to] = at.first + at.member(__ffs(mine) - 1);
+            mine &= mine - 1;
             n += __popc(who);
         }
     }
-    if (n == 0 || n > 32 || n < k) {
+    if (n < k || n > 32) {
         route_token<T>(p, t, own);
         return;
     }
     __syncwarp();
+    // a candidate a lane, with its value as the fp32 formula has it; in the order (value,
+    // lower id first) as one number
     float cx = -INFINITY, s = 0.f;
     int id = p.E;
-    uint32_t ck = 0;
+    uint64_t order = 0;
     if (lane < n) {
-        cx = __uint_as_float(own[lane]);
-        id = own[32 + lane];
+        id = own[lane];
+        cx = Logit<T>::load(static_cast<const T *>(p.logits) + t * p.stride + id);
         float cv = cx;
         if (sigmoid)
             s = sigmoid_f32(cx);
-        else if (p.bias || !p.renormalize)
+        else if (BY == kBySoftmax || !p.renormalize)
             s = expf(cx - top) / total;
-        if (p.bias)
+        if (BY != kByLogit)
             cv = s + __ldg(p.bias + id);
-        ck = choice_key(cv);
+        order = static_cast<uint64_t>(choice_key(cv)) << 32 | ~static_cast<uint32_t>(id);
     }
+    __syncwarp();
+    uint64_t *orders = reinterpret_cast<uint64_t *>(own);
+    orders[lane] = order;
+    __syncwarp();
     int rank = 0;
-    for (int c = 0; c < n; ++c) {
-        const uint32_t ok = __shfl_sync(kFull, ck, c);
-        const int oi = __shfl_sync(kFull, id, c);
-        rank += ok > ck || (ok == ck && oi < id);
+    for (int c = 0; c < n; c += 4) {  // (past n they are 0)
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(orders + c);
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(orders + c + 2);
+        rank += (u.x > order) + (u.y > order) + (w.x > order) + (w.y > order);
     }
     const bool chosen = lane < n && rank < k;
     if (!sigmoid && p.renormalize) {
@@ -768,9 +825,15 @@ static int lane_values(int per_lane)
 template <typename T, int VPL>
 static cudaError_t launch_route_vpl(const RouteParams &p, cudaStream_t s)
 {
-    const int64_t bytes = 4 * (2 * p.E > 64 ? 2 * p.E : 64);
-    return p.vec ? launch_rows(route_warp_kernel<T, VPL, true>, p, kRouteWarps, bytes, s)
-                 : launch_rows(route_warp_kernel<T, VPL, false>, p, kRouteWarps, bytes, s);
+    const int64_t bytes = 4 * p.warp_words;
+    if (!p.bias)
+        return p.vec ? launch_rows(route_warp_kernel<T, VPL, true, kByLogit>, p, kRouteWarps, bytes, s)
+                     : launch_rows(route_warp_kernel<T, VPL, false, kByLogit>, p, kRouteWarps, bytes, s);
+    if (p.score == EP_SCORE_SIGMOID)
+        return p.vec ? launch_rows(route_warp_kernel<T, VPL, true, kBySigmoid>, p, kRouteWarps, bytes, s)
+                     : launch_rows(route_warp_kernel<T, VPL, false, kBySigmoid>, p, kRouteWarps, bytes, s);
+    return p.vec ? launch_rows(route_warp_kernel<T, VPL, true, kBySoftmax>, p, kRouteWarps, bytes, s)
+                 : launch_rows(route_warp_kernel<T, VPL, false, kBySoftmax>, p, kRouteWarps, bytes, s);
 }
 
 template <typename T>
@@ -799,7 +862,9 @@ static cudaError_t launch_route_type(RouteParams p, cudaStream_t s)
     p.lanes_log2 = lanes_log2;
     const int per_lane = (p.per + (1 << lanes_log2) - 1) >> lanes_log2;
     if (32 >> lanes_log2 != groups || per_lane > 8)
-        return launch_rows(route_token_kernel<T>, p, kRouteThreads / 32, 8ll * p.E, s);
+        return launch_rows(route_token_kernel<T>, p, kRouteThreads / 32, 4ll * kTokenWords * p.E, s);
+    // 32 candidates' orders, or a token done over; 16-byte pieces
+    p.warp_words = ((kTokenWords * p.E > 64 ? kTokenWords * p.E : 64) + 3) / 4 * 4;
     const int vpl = lane_values(per_lane), w = vpl < most ? vpl : most, wb = vpl < 4 ? vpl : 4;
     p.vec = p.per % w == 0 && p.per % wb == 0 && p.stride % w == 0 &&
             aligned(p.logits, w * static_cast<int>(sizeof(T))) && aligned(p.bias, 4 * wb);
