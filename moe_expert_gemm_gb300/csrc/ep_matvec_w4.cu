@@ -12,16 +12,18 @@
 //    ever rounded.
 //  * The order of k inside a matrix instruction is free. A thread's 32-bit word of a
 //    weight row holds 8 consecutive codes, whose halves are the pairs (0,4) (1,5) (2,6)
-//    (3,7); the activations are laid into shared memory in that order.
-//  * Work is counted in steps of 256 k by 128 weight rows (16 KB), ordered by expert,
-//    column tile, chunk of 8*NT rows and k, and cut into equal runs, one per thread
-//    block, of whole tiles or wherever the cuts fall (Walk). A tile cut between blocks is
-//    joined through the workspace: every block leaves its fp32 partial sums there, the
-//    last one to arrive adds them in block order.
-//  * Thread block: one producer thread streams the weights with TMA into a ring of
-//    stages; four staging warps bring the activation rows and scales of a step;
-//    eight consumer warps own 16 weight rows each (8 of the tile's first half and 8 of
-//    its second: with SwiGLU the gate and the up row of the same output).
+//    (3,7); one operand's pairs are reordered to meet the other's: the activations' where
+//    a pass serves 8 rows, else the weights'.
+//  * Work is counted in steps of 256 k by 128 * R weight rows (16 KB * R), ordered by
+//    expert, column tile, chunk of 8 * NT rows and k, and cut into equal runs, one per
+//    thread block, of whole tiles or wherever the cuts fall (Runs). A tile cut between
+//    blocks is joined through the workspace: every block leaves its fp32 partial sums
+//    there, the last one to arrive adds them in block order.
+//  * Thread block: a producer warp streams the weights (TMA, 128-byte swizzle) and the
+//    activation rows (a bulk copy each, so that they may lie anywhere) into a ring of
+//    stages; two warps bring the scales; eight consumer warps for each of the tile's R
+//    parts own 16 weight rows each (8 of the part's first half and 8 of its second: with
+//    SwiGLU the gate and the up row of the same output).
 #include <cuda_bf16.h>
 
 #include "ep_internal.h"
@@ -31,15 +33,15 @@ namespace ep {
 
 namespace {
 
-constexpr int kTileRows = 128;                   // weight rows of a step
+constexpr int kPartRows = 128;                   // weight rows of a part of a tile
 constexpr int kStepK = 256;                      // k of a step: 128 bytes of codes a row
-constexpr int kStepBytes = kTileRows * kStepK / 2;
-constexpr int kConsumers = 8, kStagers = 4;      // warps
-constexpr int kW4Threads = 32 * (1 + kStagers + kConsumers);
+constexpr int kPartBytes = kPartRows * kStepK / 2;
+constexpr int kXPitch = kStepK * 2 + 64;         // bytes of an activation row of a step; the
+                                                 // padding spreads 8 rows over the banks
+constexpr int kPartWarps = 8, kScalers = 2;      // warps: consumers of a part, for scales
 constexpr int kMaxStages = 5;
-constexpr int kW4MaxBlocks = 320;
-constexpr int kMaxNT = 4;
-constexpr int kSmemPerBlock = 113 * 1024;        // two blocks on an SM
+constexpr int kW4MaxBlocks = 320;                // at two blocks an SM
+constexpr int kMaxAccs = 16;                     // NT * R at one block an SM
 constexpr uint64_t kW4TimeoutNs = 2000000000ull;
 
 // One block's share of one tile: steps [s0, s1).
@@ -83,30 +85,35 @@ struct Shared {
     int last[2];
 };
 
-// Weights, activations, scales and zero points (both bf16) of a step; a multiple of the
-// 1 KB the swizzled weight tiles start on.
-constexpr int stage_bytes(int NT, int GS)
+constexpr int threads_of(int R)
 {
-    return (kStepBytes + NT * 8 * kStepK * 2 + kTileRows * GS * 4 + 1023) / 1024 * 1024;
+    return 32 * (1 + kScalers + R * kPartWarps);
 }
 
-constexpr int stages_of(int NT, int GS)
+// Blocks of an SM: the widest form needs an SM's registers and shared memory.
+constexpr int blocks_per_sm(int R)
 {
-    const int n = (kSmemPerBlock - 1024 - static_cast<int>(sizeof(Shared))) / stage_bytes(NT, GS);
+    return R == 1 ? 2 : 1;
+}
+
+// Weights, activations, scales and zero points (both bf16) of a step; a multiple of the
+// 1 KB the swizzled weight tiles start on.
+constexpr int stage_bytes(int NT, int R, int GS, bool E2M1)
+{
+    return (R * kPartBytes + NT * 8 * kXPitch + R * kPartRows * GS * (E2M1 ? 2 : 4) + 1023) / 1024 * 1024;
+}
+
+constexpr int stages_of(int NT, int R, int GS, bool E2M1)
+{
+    const int n = (226 / blocks_per_sm(R) * 1024 - 1024 - static_cast<int>(sizeof(Shared))) /
+                  stage_bytes(NT, R, GS, E2M1);
     return n > kMaxStages ? kMaxStages : n;
 }
 
-// Staging warps work in teams, team i on every `teams`-th step. A team may look at a
-// stage's barrier only when at most one of its phases is open (a wait knows a phase's
-// parity alone), so there are no more teams than stages.
-constexpr int teams_of(int NT, int GS)
+constexpr int smem_bytes(int NT, int R, int GS, bool E2M1)
 {
-    return stages_of(NT, GS) < kStagers ? stages_of(NT, GS) : kStagers;
-}
-
-constexpr int smem_bytes(int NT, int GS)
-{
-    return 1024 + stages_of(NT, GS) * stage_bytes(NT, GS) + static_cast<int>(sizeof(Shared));
+    return 1024 + stages_of(NT, R, GS, E2M1) * stage_bytes(NT, R, GS, E2M1) +
+           static_cast<int>(sizeof(Shared));
 }
 
 // The segments of this block's run, one after the other.
@@ -289,32 +296,60 @@ __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t 
     return d;
 }
 
-// 8 codes -> the bf16 pairs (0,4) (1,5) (2,6) (3,7), each (code - zero) / 64. The low four
-// bits of a bf16 number alone are the subnormal code * 2^-133; its bits 4..7 alone are
-// code * 2^-129, subnormal or in the first binade, where the spacing is the same. So a
-// mask and one fused multiply-add do it, exactly; `minus_zero` is -zero / 64.
+// Halves of words with the codes 0 and 4, and 1 and 5, of eight -> the pairs (0,1), (4,5).
+__device__ __forceinline__ void in_order(uint32_t &v04, uint32_t &v15)
+{
+    const uint32_t v = __byte_perm(v04, v15, 0x5410);
+    v15 = __byte_perm(v04, v15, 0x7632);
+    v04 = v;
+}
+
+// 8 codes -> bf16 pairs, each (code - zero) / 64: (0,4) (1,5) (2,6) (3,7), or IN_ORDER (0,1)
+// (2,3) (4,5) (6,7). The low four bits of a bf16 number alone are the subnormal code *
+// 2^-133; its bits 4..7 alone are code * 2^-129, subnormal or in the first binade, where
+// the spacing is the same. So a mask and one fused multiply-add do it, exactly;
+// `minus_zero` is -zero / 64.
+template <bool IN_ORDER>
 __device__ __forceinline__ void unpack_int(uint32_t w, uint32_t minus_zero, uint32_t (&v)[4])
 {
-    constexpr uint32_t two127 = 0x7F007F00u, two123 = 0x7D007D00u;
+    constexpr uint32_t two127 = 0x7F00u, two123 = 0x7D00u;
     const uint32_t h = w >> 8;
-    v[0] = bf16x2_fma(w & 0x000F000Fu, two127, minus_zero);
-    v[1] = bf16x2_fma(w & 0x00F000F0u, two123, minus_zero);
-    v[2] = bf16x2_fma(h & 0x000F000Fu, two127, minus_zero);
-    v[3] = bf16x2_fma(h & 0x00F000F0u, two123, minus_zero);
+    uint32_t a = w & 0x000F000Fu, b = w & 0x00F000F0u, c = h & 0x000F000Fu, d = h & 0x00F000F0u;
+    if (IN_ORDER) {
+        in_order(a, b);
+        in_order(c, d);
+        constexpr uint32_t up = two123 << 16 | two127;
+        v[0] = bf16x2_fma(a, up, minus_zero);
+        v[1] = bf16x2_fma(c, up, minus_zero);
+        v[2] = bf16x2_fma(b, up, minus_zero);
+        v[3] = bf16x2_fma(d, up, minus_zero);
+    } else {
+        v[0] = bf16x2_fma(a, two127 * 0x10001u, minus_zero);
+        v[1] = bf16x2_fma(b, two123 * 0x10001u, minus_zero);
+        v[2] = bf16x2_fma(c, two127 * 0x10001u, minus_zero);
+        v[3] = bf16x2_fma(d, two123 * 0x10001u, minus_zero);
+    }
 }
 constexpr float kIntScale = 64.f;
 
 // e2m1: a code's four bits go to bits 15..12 (for the sign) and 9..6 (exponent and
 // mantissa) of its half at once by a multiplication; the number so formed is 2^-126 times
 // the code's value.
+template <bool IN_ORDER>
 __device__ __forceinline__ void unpack_e2m1(uint32_t w, uint32_t (&v)[4])
 {
     constexpr uint32_t two126 = 0x7E807E80u;
     const uint32_t h = w >> 8;
-    v[0] = bf16x2_mul(((w & 0x000F000Fu) * 0x1040u) & 0x81C081C0u, two126);
-    v[1] = bf16x2_mul(((w & 0x00F000F0u) * 0x0104u) & 0x81C081C0u, two126);
-    v[2] = bf16x2_mul(((h & 0x000F000Fu) * 0x1040u) & 0x81C081C0u, two126);
-    v[3] = bf16x2_mul(((h & 0x00F000F0u) * 0x0104u) & 0x81C081C0u, two126);
+    uint32_t a = (w & 0x000F000Fu) * 0x1040u, b = (w & 0x00F000F0u) * 0x0104u;
+    uint32_t c = (h & 0x000F000Fu) * 0x1040u, d = (h & 0x00F000F0u) * 0x0104u;
+    if (IN_ORDER) {
+        in_order(a, b);
+        in_order(c, d);
+    }
+    v[0] = bf16x2_mul(a & 0x81C081C0u, two126);
+    v[IN_ORDER ? 2 : 1] = bf16x2_mul(b & 0x81C081C0u, two126);
+    v[IN_ORDER ? 1 : 2] = bf16x2_mul(c & 0x81C081C0u, two126);
+    v[3] = bf16x2_mul(d & 0x81C081C0u, two126);
 }
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -334,16 +369,16 @@ __device__ __forceinline__ void give_up(const W4Params &p, Shared &sh)
     *reinterpret_cast<volatile int *>(&sh.abort) = 1;
 }
 
-// Stores a thread's sums of a whole tile: acc[nt][0..1] are rows 8nt+2q, +1 of the first
-// weight row, acc[nt][2..3] of the second.
+// Stores a thread's sums of a whole tile: acc[nt][0..1] are rows 8nt+2q, +1 of its first
+// weight row, column n of the tile's results, acc[nt][2..3] of its second.
 template <int NT>
 __device__ __forceinline__ void store_tile(const W4Params &p, const Segment &s,
-                                           const float (&acc)[NT][4], int row_in_half, int q)
+                                           const float (&acc)[NT][4], int n, int q)
 {
     const int cols = p.swiglu ? p.N / 2 : p.N;
-    const int n = s.n0 + row_in_half;
     const float back = p.format == EP_W4_INT ? kIntScale : 1.f;
     __nv_bfloat16 *C = reinterpret_cast<__nv_bfloat16 *>(p.C);
+    n += s.n0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -352,42 +387,47 @@ __device__ __forceinline__ void store_tile(const W4Params &p, const Segment &s,
             if (m >= s.m1 || (!p.A && !row_of(p, m)))
                 continue;
             __nv_bfloat16 *out = C + static_cast<int64_t>(m) * cols;
+            const float a = acc[nt][h] * back, b = acc[nt][2 + h] * back;
             if (p.swiglu) {
                 if (n < cols)
-                    out[n] = __float2bfloat16_rn(silu_f32(acc[nt][h] * back) * (acc[nt][2 + h] * back));
+                    out[n] = __float2bfloat16_rn(silu_f32(a) * b);
             } else {
                 if (n < cols)
-                    out[n] = __float2bfloat16_rn(acc[nt][h] * back);
+                    out[n] = __float2bfloat16_rn(a);
                 if (n + 64 < cols)
-                    out[n + 64] = __float2bfloat16_rn(acc[nt][2 + h] * back);
+                    out[n + 64] = __float2bfloat16_rn(b);
             }
         }
 }
 
 }  // namespace
 
-// NT: groups of 8 activation rows a pass over the weights serves. GS: scale groups of a
-// step (256 / group size). VEC: they are one aligned piece (W4Params::scale_vec).
-template <int NT, int GS, bool E2M1, bool VEC>
-__global__ void __launch_bounds__(kW4Threads, 2)
+// NT: groups of 8 activation rows a pass over the weights serves. R: parts of a tile. GS:
+// scale groups of a step (256 / group size). VEC: K is whole steps, a step's scales one
+// aligned piece (W4Params::scale_vec).
+template <int NT, int R, int GS, bool E2M1, bool VEC>
+__global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
     matvec_w4_kernel(const __grid_constant__ CUtensorMap tw, const W4Params p)
 {
-    constexpr int kStages = stages_of(NT, GS);
-    constexpr int kStage = stage_bytes(NT, GS);
-    constexpr int kTeams = teams_of(NT, GS), kTeam = kStagers / kTeams;  // warps of a team
-    constexpr int kXOff = kStepBytes, kScaleOff = kXOff + NT * 8 * kStepK * 2;
-    constexpr int kZeroOff = kScaleOff + kTileRows * GS * 2;
+    constexpr int kConsumers = R * kPartWarps;
+    constexpr int kStages = stages_of(NT, R, GS, E2M1);
+    constexpr int kStage = stage_bytes(NT, R, GS, E2M1);
+    constexpr int kXOff = R * kPartBytes, kScaleOff = kXOff + NT * 8 * kXPitch;
+    constexpr int kZeroOff = kScaleOff + R * kPartRows * GS * 2;
+    // a scale warp may look at a stage's barrier only when at most one of its phases is open
+    // (a wait knows a phase's parity alone): no more scale warps than stages
+    static_assert(kStages >= kScalers, "the ring is too short");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     Shared &sh = *reinterpret_cast<Shared *>(ring + kStages * kStage);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    const int tile_cols = p.swiglu ? 64 : kTileRows;
+    const int part_cols = p.swiglu ? 64 : kPartRows, tile_cols = R * part_cols;
     const int cols = p.swiglu ? p.N / 2 : p.N;
     if (warp == 1 && lane == 0) {
         tma_prefetch_map(&tw);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], 1 + kTeam);  // the producer, the staging warps
+            mbar_init(&sh.full[i], 2);  // the producer, a scale warp
             mbar_init(&sh.empty[i], kConsumers);
         }
         fence_mbar_init();
@@ -484,69 +524,80 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     };
 
     if (warp == 0) {
-        // ------------------------------------------------ producer: weights by TMA
-        if (lane != 0)
-            return;
-        int64_t issued = 0;
+        // ------------------------------------ producer: weights and activation rows
+        int issued = 0;
         bool ok = true;
         while (ok && walk.next(sh, tile_cols, seg)) {
+            const int rows = seg.m1 - seg.m0;
+            const uint8_t *mine[(NT + 3) / 4];  // rows lane, lane + 32 of the segment
+            int found = 0;
+#pragma unroll
+            for (int i = 0; i < (NT + 3) / 4; ++i) {
+                mine[i] = 32 * i + lane < rows ? row_of(p, seg.m0 + 32 * i + lane) : nullptr;
+                if (32 * i + lane < rows && !mine[i])
+                    atomicOr(p.status, EP_STATUS_BOUNDS);
+                found += __popc(__ballot_sync(0xffffffffu, mine[i] != nullptr));
+            }
             const int y0 = seg.e * p.N + seg.n0;
-            const int y1 = p.swiglu ? y0 + p.N / 2 : y0 + 64;
+            const int to_up = p.swiglu ? cols : 64;
             for (int k = seg.s0; k < seg.s1; ++k) {
-                if (!mbar_wait(&sh.empty[stage], phase ^ 1, kW4TimeoutNs, abort_flag)) {
-                    ok = false;
+                ok = __all_sync(0xffffffffu, mbar_wait(&sh.empty[stage], phase ^ 1, kW4TimeoutNs,
+                                                       abort_flag));
+                if (!ok)
                     break;
-                }
                 uint8_t *dst = ring + stage * kStage;
-                mbar_arrive_expect_tx(&sh.full[stage], kStepBytes);
-                tma_load_2d(dst, &tw, &sh.full[stage], k * (kStepK / 2), y0);
-                tma_load_2d(dst + kStepBytes / 2, &tw, &sh.full[stage], k * (kStepK / 2), y1);
+                const uint32_t x_bytes =
+                    VEC || k * kStepK + kStepK <= p.K ? kStepK * 2 : (p.K - k * kStepK) * 2;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sh.full[stage], R * kPartBytes + found * x_bytes);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        tma_load_2d(dst + r * kPartBytes, &tw, &sh.full[stage], k * (kStepK / 2),
+                                    y0 + r * part_cols);
+                        tma_load_2d(dst + r * kPartBytes + kPartBytes / 2, &tw, &sh.full[stage],
+                                    k * (kStepK / 2), y0 + r * part_cols + to_up);
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < (NT + 3) / 4; ++i)
+                    if (mine[i])
+                        bulk_load(dst + kXOff + (32 * i + lane) * kXPitch, mine[i] + k * (kStepK * 2),
+                                  x_bytes, &sh.full[stage]);
                 ++issued;
                 advance();
             }
         }
-        if (!ok) {
+        if (!ok && lane == 0) {
             give_up(p, sh);
             // the copies in flight land before the block's shared memory goes away
             volatile int no_abort = 0;
-            for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+            for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
                 mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, 1000000, &no_abort);
         }
         return;
     }
 
-    if (warp <= kStagers) {
-        // ---------------------------- staging: activation rows, scales and zero points
-        if (warp - 1 >= kTeams * kTeam)
-            return;
-        int turn = (warp - 1) % kTeams;  // steps until this team's next
-        const int member = (warp - 1) / kTeams;
-        constexpr int kRowSets = 4 / kTeam;  // of 32 weight rows, this warp's
+    if (warp <= kScalers) {
+        // ------------------------------------------------- scales and zero points
+        bool turn = warp == 1;  // this warp's step, the other's, ...
+        constexpr int kRowSets = R * kPartRows / 32;
         const int groups = p.K / (kStepK / GS);
-        const int b = lane >> 2, q = lane & 3;  // this lane's 8 activations: 32 b + 8 q ...
         bool ok = true;
         while (ok && walk.next(sh, tile_cols, seg)) {
-            const int rows = seg.m1 - seg.m0;
-            // lane i: where the segment's row i lies
-            unsigned long long mine = 0;
-            if (lane < rows) {
-                mine = reinterpret_cast<unsigned long long>(row_of(p, seg.m0 + lane));
-                if (!mine)
-                    atomicOr(p.status, EP_STATUS_BOUNDS);
-            }
             // where this lane's weight rows have their scales (rows past the last column
             // take the last one's: nobody stores what comes of them)
             int64_t scale_at[kRowSets];
 #pragma unroll
             for (int i = 0; i < kRowSets; ++i) {
-                const int r = (member * kRowSets + i) * 32 + lane;
-                int n = seg.n0 + (r < 64 || !p.swiglu ? r : r - 64);
+                const int r = 32 * i + lane, part = r / kPartRows, in = r % kPartRows;
+                int n = seg.n0 + part * part_cols + (p.swiglu ? in % 64 : in);
                 n = n < cols ? n : cols - 1;
                 scale_at[i] = (static_cast<int64_t>(seg.e) * p.N + n +
-                               (r >= 64 && p.swiglu ? cols : 0)) * groups;
+                               (p.swiglu && in >= 64 ? cols : 0)) * groups;
             }
-            for (int k = seg.s0; k < seg.s1; ++k, turn = turn == 0 ? kTeams - 1 : turn - 1) {
-                if (turn != 0) {
+            for (int k = seg.s0; k < seg.s1; ++k, turn = !turn) {
+                if (!turn) {
                     advance();
                     continue;
                 }
@@ -555,45 +606,14 @@ __global__ void __launch_bounds__(kW4Threads, 2)
 #pragma unroll
                 for (int i = 0; i < kRowSets; ++i)
                     sc[i].load(p, scale_at[i] + k * GS, groups - k * GS);
-                const int k0 = k * kStepK + lane * 8;
-                uint4 v[4];
-                auto load_rows = [&](int r0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint4 *from = reinterpret_cast<const uint4 *>(
-                            __shfl_sync(0xffffffffu, mine, r0 + i));
-                        v[i] = make_uint4(0, 0, 0, 0);
-                        if (from && k0 < p.K)
-                            v[i] = __ldg(from + k0 / 8);
-                    }
-                };
-                load_rows(member * 4);
                 ok = __all_sync(0xffffffffu, mbar_wait(&sh.empty[stage], phase ^ 1, kW4TimeoutNs,
                                                        abort_flag));
                 if (!ok)
                     break;
                 uint8_t *dst = ring + stage * kStage;
-                // (columns of the matrix instruction past the last row hold whatever they held:
-                // they only reach results that nobody stores)
-                for (int r0 = member * 4; r0 < rows; r0 += kTeam * 4) {
-                    if (r0 != member * 4)
-                        load_rows(r0);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (r0 + i >= rows)
-                            break;
-                        uint4 o;
-                        o.x = __byte_perm(v[i].x, v[i].z, 0x5410);
-                        o.y = __byte_perm(v[i].x, v[i].z, 0x7632);
-                        o.z = __byte_perm(v[i].y, v[i].w, 0x5410);
-                        o.w = __byte_perm(v[i].y, v[i].w, 0x7632);
-                        const int nt = (r0 + i) / 8, g = (r0 + i) % 8;
-                        *reinterpret_cast<uint4 *>(dst + kXOff + ((b * NT + nt) * 32 + g * 4 + q) * 16) = o;
-                    }
-                }
 #pragma unroll
                 for (int i = 0; i < kRowSets; ++i) {
-                    const int r = (member * kRowSets + i) * 32 + lane;
+                    const int r = 32 * i + lane;
                     sc[i].store(dst + kScaleOff + r * GS * 2, dst + kZeroOff + r * GS * 2);
                 }
                 __syncwarp();
@@ -608,10 +628,12 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     }
 
     // ------------------------------------------------------------------ consumers
-    const int cw = warp - 1 - kStagers, g = lane >> 2, q = lane & 3;
-    const int row = 8 * cw + g;  // in each half of the tile
+    const int cw = warp - 1 - kScalers, g = lane >> 2, q = lane & 3;
+    const int part_of = cw / kPartWarps, row = 8 * (cw % kPartWarps) + g;  // in each half of it
     const int ctid = cw * 32 + lane;
-    const int at0 = row * 128 + (g << 4) + q * 4;
+    const int at0 = part_of * kPartBytes + row * 128 + (g << 4) + q * 4;
+    const int scale0 = kScaleOff + (part_of * kPartRows + row) * GS * 2;
+    const int zero0 = scale0 + kZeroOff - kScaleOff;
     float *partial = reinterpret_cast<float *>(p.workspace + kW4MaxBlocks * 16);
     constexpr int64_t kSlot = kConsumers * 32 * NT * 4;  // floats of one partial tile
     int *counters = reinterpret_cast<int *>(p.workspace);
@@ -630,55 +652,66 @@ __global__ void __launch_bounds__(kW4Threads, 2)
             if (!ok)
                 break;
             const uint8_t *src = ring + stage * kStage;
-            alignas(16) uint32_t scale0[GS / 2], scale1[GS / 2];
-            copy_words<GS / 2>(scale0, src + kScaleOff + row * GS * 2);
-            copy_words<GS / 2>(scale1, src + kScaleOff + (64 + row) * GS * 2);
-            alignas(16) uint32_t zero0[GS / 2], zero1[GS / 2];
-            if constexpr (!E2M1) {
-                copy_words<GS / 2>(zero0, src + kZeroOff + row * GS * 2);
-                copy_words<GS / 2>(zero1, src + kZeroOff + (64 + row) * GS * 2);
+            const int blocks = VEC || (k + 1) * kStepK <= p.K ? 8 : (p.K - k * kStepK) / 32;
+            // a row's scales and zero points as words of two; where registers are short
+            // (NT = 8) they are fetched one by one instead
+            alignas(16) uint32_t scale[2][GS / 2], zero[2][GS / 2] = {};
+            if constexpr (NT < 8) {
+                copy_words<GS / 2>(scale[0], src + scale0);
+                copy_words<GS / 2>(scale[1], src + scale0 + 64 * GS * 2);
+                if constexpr (!E2M1) {
+                    copy_words<GS / 2>(zero[0], src + zero0);
+                    copy_words<GS / 2>(zero[1], src + zero0 + 64 * GS * 2);
+                }
             }
+            auto scale_of = [&](int h, int gr) {
+                if constexpr (NT < 8)
+                    return __uint_as_float(gr & 1 ? scale[h][gr / 2] & 0xFFFF0000u : scale[h][gr / 2] << 16);
+                else
+                    return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(
+                                               src + scale0 + (h * 64 * GS + gr) * 2)) << 16);
+            };
+            auto zero_of = [&](int h, int gr) {  // in both halves
+                if constexpr (NT < 8)
+                    return __byte_perm(zero[h][gr / 2], 0u, gr & 1 ? 0x3232u : 0x1010u);
+                else
+                    return *reinterpret_cast<const uint16_t *>(src + zero0 + (h * 64 * GS + gr) * 2) * 0x10001u;
+            };
             float part[NT][4];
 #pragma unroll
             for (int b = 0; b < 8; ++b) {
+                if (!VEC && b >= blocks)
+                    break;
                 const int gr = b * GS / 8;
                 const bool first = b * GS % 8 == 0 || GS == 8;
                 const bool last = (b + 1) * GS % 8 == 0 || GS == 8;
                 const int at = at0 ^ (b << 4);  // the 128-byte swizzle: 16-byte piece b ^ row % 8
-                const uint32_t w0 = *reinterpret_cast<const uint32_t *>(src + at);
-                const uint32_t w1 = *reinterpret_cast<const uint32_t *>(src + kStepBytes / 2 + at);
-                uint32_t a0[4], a1[4];
-                if (E2M1) {
-                    unpack_e2m1(w0, a0);
-                    unpack_e2m1(w1, a1);
-                } else {
-                    // the group's -zero / 64 in both halves
-                    const uint32_t sel = gr & 1 ? 0x3232u : 0x1010u;
-                    unpack_int(w0, __byte_perm(zero0[gr / 2], 0u, sel), a0);
-                    unpack_int(w1, __byte_perm(zero1[gr / 2], 0u, sel), a1);
+                uint32_t a[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t *>(src + h * (kPartBytes / 2) + at);
+                    if constexpr (E2M1)
+                        unpack_e2m1<(NT > 1)>(w, a[h]);
+                    else
+                        unpack_int<(NT > 1)>(w, zero_of(h, gr), a[h]);
                 }
+                const float s0 = last ? scale_of(0, gr) : 0.f, s1 = last ? scale_of(1, gr) : 0.f;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     if (NT > 1 && nt >= nts)
                         break;
-                    const uint4 x = *reinterpret_cast<const uint4 *>(
-                        src + kXOff + ((b * NT + nt) * 32 + lane) * 16);
+                    uint4 x = *reinterpret_cast<const uint4 *>(
+                        src + kXOff + (nt * 8 + g) * kXPitch + b * 64 + q * 16);
+                    if constexpr (NT == 1)
+                        x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                                       __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
                     const float none[4] = {0.f, 0.f, 0.f, 0.f};
                     if (first)
-                        mma_bf16(part[nt], a0[0], a1[0], a0[1], a1[1], x.x, x.y, none);
+                        mma_bf16(part[nt], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y, none);
                     else
-                        mma_bf16(part[nt], a0[0], a1[0], a0[1], a1[1], x.x, x.y, part[nt]);
-                    mma_bf16(part[nt], a0[2], a1[2], a0[3], a1[3], x.z, x.w, part[nt]);
-                }
-                if (last) {
-                    const float s0 = __uint_as_float(
-                        gr & 1 ? scale0[gr / 2] & 0xFFFF0000u : scale0[gr / 2] << 16);
-                    const float s1 = __uint_as_float(
-                        gr & 1 ? scale1[gr / 2] & 0xFFFF0000u : scale1[gr / 2] << 16);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if (NT > 1 && nt >= nts)
-                            break;
+                        mma_bf16(part[nt], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y, part[nt]);
+                    mma_bf16(part[nt], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w, part[nt]);
+                    if (last) {
                         acc[nt][0] = fmaf(s0, part[nt][0], acc[nt][0]);
                         acc[nt][1] = fmaf(s0, part[nt][1], acc[nt][1]);
                         acc[nt][2] = fmaf(s1, part[nt][2], acc[nt][2]);
@@ -697,7 +730,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
         if (!ok)
             break;
         if (seg.s0 == 0 && seg.s1 == walk.steps) {
-            store_tile<NT>(p, seg, acc, row, q);
+            store_tile<NT>(p, seg, acc, part_of * part_cols + row, q);
             continue;
         }
         // a cut tile: leave the sums in the block's slot for the tile its run begins
@@ -742,7 +775,6 @@ __global__ void __launch_bounds__(kW4Threads, 2)
         const int nts = (seg.m1 - seg.m0 + 7) / 8;
         const int c0 = sh.runs.owner(seg.first), c1 = sh.runs.owner(seg.first + walk.steps - 1);
         float acc[NT][4] = {};
-#pragma unroll 4
         for (int c = c0; c <= c1; ++c) {
             const float4 *theirs =
                 reinterpret_cast<const float4 *>(partial + (c * 2 + (c == c0 ? 1 : 0)) * kSlot);
@@ -756,57 +788,64 @@ __global__ void __launch_bounds__(kW4Threads, 2)
                     acc[nt][3] += v.w;
                 }
         }
-        store_tile<NT>(p, seg, acc, row, q);
+        store_tile<NT>(p, seg, acc, part_of * part_cols + row, q);
     }
 }
 
 int64_t w4_workspace_bytes()
 {
-    return kW4MaxBlocks * 16 +
-           2ll * kW4MaxBlocks * kConsumers * 32 * kMaxNT * 4 * static_cast<int64_t>(sizeof(float));
+    // counters, and two partial tiles a block: NT <= 4 at two blocks an SM, or
+    // NT * R <= kMaxAccs at one
+    return kW4MaxBlocks * 16 + kW4MaxBlocks / 2 * 2ll * kPartWarps * 32 * kMaxAccs * 16;
 }
 
-template <int NT, int GS, bool E2M1, bool VEC>
-static cudaError_t launch_w4(const CUtensorMap &tw, const W4Params &p, int grid, cudaStream_t s)
+template <int NT, int R, int GS, bool E2M1, bool VEC>
+static cudaError_t launch_w4(const CUtensorMap &tw, const W4Params &p, int num_sms, cudaStream_t s)
 {
-    const auto kern = matvec_w4_kernel<NT, GS, E2M1, VEC>;
-    constexpr int smem = smem_bytes(NT, GS);
-    static_assert(stages_of(NT, GS) >= 2, "the ring needs two stages");
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static_assert(NT * R * blocks_per_sm(R) <= kMaxAccs, "the workspace is too small");
+    const auto kern = matvec_w4_kernel<NT, R, GS, E2M1, VEC>;
+    constexpr int smem = smem_bytes(NT, R, GS, E2M1), most = kW4MaxBlocks / 2 * blocks_per_sm(R);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
         return e;
-    kern<<<grid, kW4Threads, smem, s>>>(tw, p);
+    const int grid = blocks_per_sm(R) * num_sms;
+    kern<<<grid < most ? grid : most, threads_of(R), smem, s>>>(tw, p);
     return cudaGetLastError();
 }
 
-template <int NT, bool VEC>
-static cudaError_t launch_nt(const CUtensorMap &tw, const W4Params &p, int grid, cudaStream_t s)
+template <int NT, int R, bool VEC>
+static cudaError_t launch_nt(const CUtensorMap &tw, const W4Params &p, int num_sms, cudaStream_t s)
 {
     if (p.format == EP_W4_E2M1)
-        return launch_w4<NT, 8, true, VEC>(tw, p, grid, s);
+        return launch_w4<NT, R, 8, true, VEC>(tw, p, num_sms, s);
     switch (p.group) {
     case 32:
-        return launch_w4<NT, 8, false, VEC>(tw, p, grid, s);
+        return launch_w4<NT, R, 8, false, VEC>(tw, p, num_sms, s);
     case 64:
-        return launch_w4<NT, 4, false, VEC>(tw, p, grid, s);
+        return launch_w4<NT, R, 4, false, VEC>(tw, p, num_sms, s);
     default:
-        return launch_w4<NT, 2, false, VEC>(tw, p, grid, s);
+        return launch_w4<NT, R, 2, false, VEC>(tw, p, num_sms, s);
     }
 }
 
-cudaError_t launch_matvec_w4(const CUtensorMap &tw, const W4Params &p, int num_sms, cudaStream_t s)
+template <bool VEC>
+static cudaError_t launch_vec(const CUtensorMap &tw, const W4Params &p, int num_sms, cudaStream_t s)
 {
     // rows a pass serves: what an expert is expected to get, at most what it can get
     const int64_t tokens = static_cast<int64_t>(p.T) * p.n_ranks;
     int64_t rows = (tokens * p.top_k + static_cast<int64_t>(p.n_ranks) * p.El - 1) /
                    (static_cast<int64_t>(p.n_ranks) * p.El);
     rows = rows < p.max_rows ? rows : p.max_rows;
-    const int grid = 2 * num_sms < kW4MaxBlocks ? 2 * num_sms : kW4MaxBlocks;
     if (rows <= 8)
-        return p.scale_vec ? launch_nt<1, true>(tw, p, grid, s) : launch_nt<1, false>(tw, p, grid, s);
+        return launch_nt<1, 1, VEC>(tw, p, num_sms, s);
     if (rows <= 16)
-        return p.scale_vec ? launch_nt<2, true>(tw, p, grid, s) : launch_nt<2, false>(tw, p, grid, s);
-    return p.scale_vec ? launch_nt<4, true>(tw, p, grid, s) : launch_nt<4, false>(tw, p, grid, s);
+        return launch_nt<2, 1, VEC>(tw, p, num_sms, s);
+    return launch_nt<8, 2, VEC>(tw, p, num_sms, s);
+}
+
+cudaError_t launch_matvec_w4(const CUtensorMap &tw, const W4Params &p, int num_sms, cudaStream_t s)
+{
+    return p.scale_vec ? launch_vec<true>(tw, p, num_sms, s) : launch_vec<false>(tw, p, num_sms, s);
 }
 
 }  // namespace ep
