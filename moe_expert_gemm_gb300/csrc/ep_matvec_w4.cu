@@ -10,21 +10,26 @@
 //    and a fused multiply-add (unpack_int, unpack_e2m1). The sum over a group of k runs in
 //    fp32 on these numbers; the group's scale multiplies that sum in fp32, so no weight is
 //    ever rounded.
-//  * The order of k inside a matrix instruction is free. A thread's 32-bit word of a
-//    weight row holds 8 consecutive codes, whose halves are the pairs (0,4) (1,5) (2,6)
-//    (3,7); one operand's pairs are reordered to meet the other's: the activations' where
-//    a pass serves 8 rows, else the weights'.
+//  * e2m1 scales are powers of two, which the codes can take on exactly in bf16: there a
+//    group needs no sum of its own (as long as the scale is at most 2; else it gets one).
+//  * The order of k inside a matrix instruction is free. A thread's words of a weight row
+//    (as many at once as a scale group of k feeds the four threads of a row) hold 8
+//    consecutive codes each, whose halves are the pairs (0,4) (1,5) (2,6) (3,7). Up to 16
+//    rows a pass the activations are laid into shared memory in that order, past that the
+//    weights' pairs are put in order.
 //  * Work is counted in steps of 256 k by 128 * R weight rows (16 KB * R), ordered by
 //    expert, column tile, chunk of 8 * NT rows and k, and cut into equal runs, one per
 //    thread block, of whole tiles or wherever the cuts fall (Runs). A tile cut between
 //    blocks is joined through the workspace: every block leaves its fp32 partial sums
 //    there, the last one to arrive adds them in block order.
-//  * Thread block: a producer warp streams the weights (TMA, 128-byte swizzle) and the
-//    activation rows (a bulk copy each, so that they may lie anywhere) into a ring of
-//    stages; two warps bring the scales; eight consumer warps for each of the tile's R
-//    parts own 16 weight rows each (8 of the part's first half and 8 of its second: with
-//    SwiGLU the gate and the up row of the same output).
+//  * Thread block: a producer warp streams the weights (TMA, 128-byte swizzle) into a ring
+//    of stages; staging warps bring the scales and the activation rows (past 16 rows the
+//    producer brings those, by a bulk copy each); eight consumer warps for each of the
+//    tile's R parts own 16 weight rows each (8 of the part's first half and 8 of its
+//    second: with SwiGLU the gate and the up row of the same output).
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "ep_internal.h"
 #include "ep_ptx.cuh"
@@ -36,9 +41,10 @@ namespace {
 constexpr int kPartRows = 128;                   // weight rows of a part of a tile
 constexpr int kStepK = 256;                      // k of a step: 128 bytes of codes a row
 constexpr int kPartBytes = kPartRows * kStepK / 2;
-constexpr int kXPitch = kStepK * 2 + 64;         // bytes of an activation row of a step; the
-                                                 // padding spreads 8 rows over the banks
-constexpr int kPartWarps = 8, kScalers = 2;      // warps: consumers of a part, for scales
+constexpr int kXPitch = kStepK * 2 + 64;         // bytes of an activation row of a step that
+                                                 // lies as it is; the padding spreads 8 rows
+                                                 // over the banks
+constexpr int kPartWarps = 8;                    // consumer warps of a part
 constexpr int kMaxStages = 5;
 constexpr int kW4MaxBlocks = 320;                // at two blocks an SM
 constexpr int kMaxAccs = 16;                     // NT * R at one block an SM
@@ -76,6 +82,8 @@ struct Start {
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
+    int sums_apart[kMaxStages];  // e2m1: the stage's scales need sums by group
+    int skips;                   // rows with a bad gather index were met
     int offsets[EP_MAX_LOCAL_EXPERTS + 1];
     int bad;
     int abort;
@@ -85,9 +93,20 @@ struct Shared {
     int last[2];
 };
 
-constexpr int threads_of(int R)
+// The activations of up to 16 rows are laid out by the staging warps.
+constexpr bool x_staged(int NT)
 {
-    return 32 * (1 + kScalers + R * kPartWarps);
+    return NT <= 2;
+}
+
+constexpr int stagers_of(int NT)
+{
+    return x_staged(NT) ? 3 : 2;
+}
+
+constexpr int threads_of(int NT, int R)
+{
+    return 32 * (1 + stagers_of(NT) + R * kPartWarps);
 }
 
 // Blocks of an SM: the widest form needs an SM's registers and shared memory.
@@ -100,7 +119,8 @@ constexpr int blocks_per_sm(int R)
 // 1 KB the swizzled weight tiles start on.
 constexpr int stage_bytes(int NT, int R, int GS, bool E2M1)
 {
-    return (R * kPartBytes + NT * 8 * kXPitch + R * kPartRows * GS * (E2M1 ? 2 : 4) + 1023) / 1024 * 1024;
+    return (R * kPartBytes + NT * 8 * (x_staged(NT) ? kStepK * 2 : kXPitch) +
+            R * kPartRows * GS * (E2M1 ? 2 : 4) + 1023) / 1024 * 1024;
 }
 
 constexpr int stages_of(int NT, int R, int GS, bool E2M1)
@@ -254,15 +274,28 @@ struct Scales {
         }
     }
 
-    __device__ __forceinline__ void store(uint8_t *to_scale, uint8_t *to_zero) const
+    // e2m1: whether a scale is too large for the codes to take on.
+    __device__ __forceinline__ bool large() const
+    {
+        uint32_t most = 0;
+        if constexpr (E2M1) {
+#pragma unroll
+            for (int i = 0; i < GS; ++i)
+                most = max(most, scale.w[i / 4] >> (8 * (i % 4)) & 255);
+        }
+        return most > 128;
+    }
+
+    __device__ __forceinline__ void store(uint8_t *to_scale, uint8_t *to_zero, bool apart) const
     {
         alignas(16) uint32_t out[GS / 2];
         if constexpr (E2M1) {
-            // 2^(e - 127) as bf16: e in the exponent bits; 2^-127 is subnormal
 #pragma unroll
             for (int i = 0; i < GS; ++i) {
                 const uint32_t e = scale.w[i / 4] >> (8 * (i % 4)) & 255;
-                const uint32_t h = e == 255 ? 0x7FC0u : e == 0 ? 0x0040u : e << 7;
+                // 2^(e - 1), the factor of a code as unpack_e2m1 forms it, or apart from
+                // the codes 2^(e - 127) (bf16: the exponent bits; 2^-127 is subnormal)
+                const uint32_t h = !apart ? (e + 126) << 7 : e == 255 ? 0x7FC0u : e == 0 ? 0x0040u : e << 7;
                 out[i / 2] = i % 2 ? out[i / 2] | h << 16 : h;
             }
             copy_words<GS / 2>(to_scale, out);
@@ -331,14 +364,15 @@ __device__ __forceinline__ void unpack_int(uint32_t w, uint32_t minus_zero, uint
     }
 }
 constexpr float kIntScale = 64.f;
+constexpr uint32_t kTwo126 = 0x7E807E80u;
 
 // e2m1: a code's four bits go to bits 15..12 (for the sign) and 9..6 (exponent and
 // mantissa) of its half at once by a multiplication; the number so formed is 2^-126 times
-// the code's value.
+// the code's value. `factor`, in both halves, is 2^126 or that times the scale: with two
+// significant bits the product is exact down to the smallest scale.
 template <bool IN_ORDER>
-__device__ __forceinline__ void unpack_e2m1(uint32_t w, uint32_t (&v)[4])
+__device__ __forceinline__ void unpack_e2m1(uint32_t w, uint32_t factor, uint32_t (&v)[4])
 {
-    constexpr uint32_t two126 = 0x7E807E80u;
     const uint32_t h = w >> 8;
     uint32_t a = (w & 0x000F000Fu) * 0x1040u, b = (w & 0x00F000F0u) * 0x0104u;
     uint32_t c = (h & 0x000F000Fu) * 0x1040u, d = (h & 0x00F000F0u) * 0x0104u;
@@ -346,10 +380,10 @@ __device__ __forceinline__ void unpack_e2m1(uint32_t w, uint32_t (&v)[4])
         in_order(a, b);
         in_order(c, d);
     }
-    v[0] = bf16x2_mul(a & 0x81C081C0u, two126);
-    v[IN_ORDER ? 2 : 1] = bf16x2_mul(b & 0x81C081C0u, two126);
-    v[IN_ORDER ? 1 : 2] = bf16x2_mul(c & 0x81C081C0u, two126);
-    v[3] = bf16x2_mul(d & 0x81C081C0u, two126);
+    v[0] = bf16x2_mul(a & 0x81C081C0u, factor);
+    v[IN_ORDER ? 2 : 1] = bf16x2_mul(b & 0x81C081C0u, factor);
+    v[IN_ORDER ? 1 : 2] = bf16x2_mul(c & 0x81C081C0u, factor);
+    v[3] = bf16x2_mul(d & 0x81C081C0u, factor);
 }
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -373,7 +407,7 @@ __device__ __forceinline__ void give_up(const W4Params &p, Shared &sh)
 // weight row, column n of the tile's results, acc[nt][2..3] of its second.
 template <int NT>
 __device__ __forceinline__ void store_tile(const W4Params &p, const Segment &s,
-                                           const float (&acc)[NT][4], int n, int q)
+                                           const float (&acc)[NT][4], int n, int q, bool skips)
 {
     const int cols = p.swiglu ? p.N / 2 : p.N;
     const float back = p.format == EP_W4_INT ? kIntScale : 1.f;
@@ -384,7 +418,7 @@ __device__ __forceinline__ void store_tile(const W4Params &p, const Segment &s,
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int m = s.m0 + 8 * nt + 2 * q + h;
-            if (m >= s.m1 || (!p.A && !row_of(p, m)))
+            if (m >= s.m1 || (skips && !row_of(p, m)))
                 continue;
             __nv_bfloat16 *out = C + static_cast<int64_t>(m) * cols;
             const float a = acc[nt][h] * back, b = acc[nt][2 + h] * back;
@@ -406,17 +440,23 @@ __device__ __forceinline__ void store_tile(const W4Params &p, const Segment &s,
 // scale groups of a step (256 / group size). VEC: K is whole steps, a step's scales one
 // aligned piece (W4Params::scale_vec).
 template <int NT, int R, int GS, bool E2M1, bool VEC>
-__global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
+__global__ void __launch_bounds__(threads_of(NT, R), blocks_per_sm(R))
     matvec_w4_kernel(const __grid_constant__ CUtensorMap tw, const W4Params p)
 {
-    constexpr int kConsumers = R * kPartWarps;
+    constexpr int kConsumers = R * kPartWarps, kStagers = stagers_of(NT);
+    constexpr bool kStageX = x_staged(NT);
     constexpr int kStages = stages_of(NT, R, GS, E2M1);
     constexpr int kStage = stage_bytes(NT, R, GS, E2M1);
-    constexpr int kXOff = R * kPartBytes, kScaleOff = kXOff + NT * 8 * kXPitch;
+    constexpr int kXOff = R * kPartBytes;
+    constexpr int kScaleOff = kXOff + NT * 8 * (kStageX ? kStepK * 2 : kXPitch);
     constexpr int kZeroOff = kScaleOff + R * kPartRows * GS * 2;
-    // a scale warp may look at a stage's barrier only when at most one of its phases is open
-    // (a wait knows a phase's parity alone): no more scale warps than stages
-    static_assert(kStages >= kScalers, "the ring is too short");
+    // Staging warps take turns. One may look at a stage's barrier only when at most one of
+    // its phases is open (a wait knows a phase's parity alone), so no more of them take part
+    // than there are stages.
+    constexpr int kTurns = kStagers < kStages ? kStagers : kStages;
+    // Words of a weight row a thread of the row's four takes at once: their 32 * kWords
+    // codes belong to one scale group.
+    constexpr int kWords = !kStageX || GS == 8 ? 1 : 8 / GS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     Shared &sh = *reinterpret_cast<Shared *>(ring + kStages * kStage);
@@ -427,11 +467,12 @@ __global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
     if (warp == 1 && lane == 0) {
         tma_prefetch_map(&tw);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], 2);  // the producer, a scale warp
+            mbar_init(&sh.full[i], 2);  // the producer, a staging warp
             mbar_init(&sh.empty[i], kConsumers);
         }
         fence_mbar_init();
         sh.abort = 0;
+        sh.skips = 0;
         sh.cut[0].e = sh.cut[1].e = -1;
     }
     const int tiles = (cols + tile_cols - 1) / tile_cols;
@@ -524,20 +565,24 @@ __global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
     };
 
     if (warp == 0) {
-        // ------------------------------------ producer: weights and activation rows
+        // --------------------- producer: weights (and, where not staged, activation rows)
+        constexpr int kSets = kStageX ? 0 : (NT + 3) / 4;
         int issued = 0;
         bool ok = true;
         while (ok && walk.next(sh, tile_cols, seg)) {
             const int rows = seg.m1 - seg.m0;
-            const uint8_t *mine[(NT + 3) / 4];  // rows lane, lane + 32 of the segment
+            const uint8_t *mine[kSets + 1];  // rows lane, lane + 32 of the segment
             int found = 0;
 #pragma unroll
-            for (int i = 0; i < (NT + 3) / 4; ++i) {
+            for (int i = 0; i < kSets; ++i) {
                 mine[i] = 32 * i + lane < rows ? row_of(p, seg.m0 + 32 * i + lane) : nullptr;
-                if (32 * i + lane < rows && !mine[i])
+                if (32 * i + lane < rows && !mine[i]) {
                     atomicOr(p.status, EP_STATUS_BOUNDS);
+                    sh.skips = 1;
+                }
                 found += __popc(__ballot_sync(0xffffffffu, mine[i] != nullptr));
             }
+            __syncwarp();
             const int y0 = seg.e * p.N + seg.n0;
             const int to_up = p.swiglu ? cols : 64;
             for (int k = seg.s0; k < seg.s1; ++k) {
@@ -560,7 +605,7 @@ __global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
                 }
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < (NT + 3) / 4; ++i)
+                for (int i = 0; i < kSets; ++i)
                     if (mine[i])
                         bulk_load(dst + kXOff + (32 * i + lane) * kXPitch, mine[i] + k * (kStepK * 2),
                                   x_bytes, &sh.full[stage]);
@@ -578,13 +623,28 @@ __global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
         return;
     }
 
-    if (warp <= kScalers) {
-        // ------------------------------------------------- scales and zero points
-        bool turn = warp == 1;  // this warp's step, the other's, ...
+    if (warp <= kStagers) {
+        // -------------- staging: scales and zero points, up to 16 rows' activations
+        if (warp > kTurns)
+            return;
+        int turn = warp - 1;  // steps until this warp's next
         constexpr int kRowSets = R * kPartRows / 32;
+        constexpr int kBatch = kStageX ? 4 : 1;  // activation rows under way at once
         const int groups = p.K / (kStepK / GS);
+        // where a lane's piece (8 activations, in pair order) of a row goes: the place of the
+        // thread (row, q) that takes word w of its codes of block b
+        const int b = lane / (4 * kWords) * kWords + lane % kWords, q = lane / kWords % 4;
         bool ok = true;
         while (ok && walk.next(sh, tile_cols, seg)) {
+            const int rows = seg.m1 - seg.m0;
+            unsigned long long mine = 0;  // lane i: where the segment's row i lies
+            if (kStageX && lane < rows) {
+                mine = reinterpret_cast<unsigned long long>(row_of(p, seg.m0 + lane));
+                if (!mine) {
+                    atomicOr(p.status, EP_STATUS_BOUNDS);
+                    sh.skips = 1;
+                }
+            }
             // where this lane's weight rows have their scales (rows past the last column
             // take the last one's: nobody stores what comes of them)
             int64_t scale_at[kRowSets];
@@ -596,8 +656,8 @@ __global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
                 scale_at[i] = (static_cast<int64_t>(seg.e) * p.N + n +
                                (p.swiglu && in >= 64 ? cols : 0)) * groups;
             }
-            for (int k = seg.s0; k < seg.s1; ++k, turn = !turn) {
-                if (!turn) {
+            for (int k = seg.s0; k < seg.s1; ++k, turn = turn == 0 ? kTurns - 1 : turn - 1) {
+                if (turn != 0) {
                     advance();
                     continue;
                 }
@@ -606,15 +666,55 @@ __global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
 #pragma unroll
                 for (int i = 0; i < kRowSets; ++i)
                     sc[i].load(p, scale_at[i] + k * GS, groups - k * GS);
+                const int k0 = k * kStepK + lane * 8;
+                uint4 v[kBatch];
+                auto load_rows = [&](int r0) {
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        if (r0 + i >= rows)
+                            break;
+                        const uint4 *from = reinterpret_cast<const uint4 *>(
+                            __shfl_sync(0xffffffffu, mine, r0 + i));
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (from && (VEC || k0 < p.K))
+                            v[i] = __ldg(from + k0 / 8);
+                    }
+                };
+                if (kStageX)
+                    load_rows(0);
                 ok = __all_sync(0xffffffffu, mbar_wait(&sh.empty[stage], phase ^ 1, kW4TimeoutNs,
                                                        abort_flag));
                 if (!ok)
                     break;
                 uint8_t *dst = ring + stage * kStage;
+                // (columns of the matrix instruction past the last row hold whatever they held:
+                // they only reach results that nobody stores)
+                for (int r0 = 0; kStageX && r0 < rows; r0 += kBatch) {
+                    if (r0)
+                        load_rows(r0);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        if (r0 + i >= rows)
+                            break;
+                        const int row = r0 + i, to = (b * NT + row / 8) * 32 + row % 8 * 4 + q;
+                        *reinterpret_cast<uint4 *>(dst + kXOff + to * 16) = make_uint4(
+                            __byte_perm(v[i].x, v[i].z, 0x5410), __byte_perm(v[i].x, v[i].z, 0x7632),
+                            __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632));
+                    }
+                }
+                bool apart = false;
+                if (E2M1) {
+#pragma unroll
+                    for (int i = 0; i < kRowSets; ++i)
+                        apart |= sc[i].large();
+                    apart = __any_sync(0xffffffffu, apart);
+                    if (lane == 0)
+                        sh.sums_apart[stage] = apart;
+                }
 #pragma unroll
                 for (int i = 0; i < kRowSets; ++i) {
                     const int r = 32 * i + lane;
-                    sc[i].store(dst + kScaleOff + r * GS * 2, dst + kZeroOff + r * GS * 2);
+                    sc[i].store(dst + kScaleOff + r * GS * 2, dst + kZeroOff + r * GS * 2, apart);
                 }
                 __syncwarp();
                 if (lane == 0)
@@ -628,10 +728,12 @@ __global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
     }
 
     // ------------------------------------------------------------------ consumers
-    const int cw = warp - 1 - kScalers, g = lane >> 2, q = lane & 3;
+    const int cw = warp - 1 - kStagers, g = lane >> 2, q = lane & 3;
     const int part_of = cw / kPartWarps, row = 8 * (cw % kPartWarps) + g;  // in each half of it
     const int ctid = cw * 32 + lane;
-    const int at0 = part_of * kPartBytes + row * 128 + (g << 4) + q * 4;
+    // this thread's first words of a weight row, in the 128-byte swizzle (the 16-byte piece i
+    // of row r is at i ^ r % 8)
+    const int at0 = part_of * kPartBytes + row * 128 + ((q * kWords / 4 ^ g) << 4) + q * kWords % 4 * 4;
     const int scale0 = kScaleOff + (part_of * kPartRows + row) * GS * 2;
     const int zero0 = scale0 + kZeroOff - kScaleOff;
     float *partial = reinterpret_cast<float *>(p.workspace + kW4MaxBlocks * 16);
@@ -655,8 +757,9 @@ __global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
             const int blocks = VEC || (k + 1) * kStepK <= p.K ? 8 : (p.K - k * kStepK) / 32;
             // a row's scales and zero points as words of two; where registers are short
             // (NT = 8) they are fetched one by one instead
+            constexpr bool kScalesAtOnce = NT < 8;
             alignas(16) uint32_t scale[2][GS / 2], zero[2][GS / 2] = {};
-            if constexpr (NT < 8) {
+            if constexpr (kScalesAtOnce) {
                 copy_words<GS / 2>(scale[0], src + scale0);
                 copy_words<GS / 2>(scale[1], src + scale0 + 64 * GS * 2);
                 if constexpr (!E2M1) {
@@ -665,60 +768,76 @@ __global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
                 }
             }
             auto scale_of = [&](int h, int gr) {
-                if constexpr (NT < 8)
+                if constexpr (kScalesAtOnce)
                     return __uint_as_float(gr & 1 ? scale[h][gr / 2] & 0xFFFF0000u : scale[h][gr / 2] << 16);
                 else
                     return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(
                                                src + scale0 + (h * 64 * GS + gr) * 2)) << 16);
             };
-            auto zero_of = [&](int h, int gr) {  // in both halves
-                if constexpr (NT < 8)
-                    return __byte_perm(zero[h][gr / 2], 0u, gr & 1 ? 0x3232u : 0x1010u);
+            // in both halves of a word
+            auto twice = [&](const uint32_t (&words)[2][GS / 2], int at, int h, int gr) {
+                if constexpr (kScalesAtOnce)
+                    return __byte_perm(words[h][gr / 2], 0u, gr & 1 ? 0x3232u : 0x1010u);
                 else
-                    return *reinterpret_cast<const uint16_t *>(src + zero0 + (h * 64 * GS + gr) * 2) * 0x10001u;
+                    return *reinterpret_cast<const uint16_t *>(src + at + (h * 64 * GS + gr) * 2) * 0x10001u;
             };
-            float part[NT][4];
+            // The step's 8 blocks of 32 k. APART: a group's sum is formed on its own and
+            // scaled after; else the codes take on their scales.
+            auto step = [&](auto apart_) {
+                constexpr bool APART = decltype(apart_)::value;
+                float part[NT][4];
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                if (!VEC && b >= blocks)
-                    break;
-                const int gr = b * GS / 8;
-                const bool first = b * GS % 8 == 0 || GS == 8;
-                const bool last = (b + 1) * GS % 8 == 0 || GS == 8;
-                const int at = at0 ^ (b << 4);  // the 128-byte swizzle: 16-byte piece b ^ row % 8
-                uint32_t a[2][4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t *>(src + h * (kPartBytes / 2) + at);
-                    if constexpr (E2M1)
-                        unpack_e2m1<(NT > 1)>(w, a[h]);
-                    else
-                        unpack_int<(NT > 1)>(w, zero_of(h, gr), a[h]);
-                }
-                const float s0 = last ? scale_of(0, gr) : 0.f, s1 = last ? scale_of(1, gr) : 0.f;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if (NT > 1 && nt >= nts)
+                for (int b0 = 0; b0 < 8; b0 += kWords) {
+                    if (!VEC && b0 >= blocks)
                         break;
-                    uint4 x = *reinterpret_cast<const uint4 *>(
-                        src + kXOff + (nt * 8 + g) * kXPitch + b * 64 + q * 16);
-                    if constexpr (NT == 1)
-                        x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                                       __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-                    const float none[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (first)
-                        mma_bf16(part[nt], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y, none);
-                    else
-                        mma_bf16(part[nt], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y, part[nt]);
-                    mma_bf16(part[nt], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w, part[nt]);
-                    if (last) {
-                        acc[nt][0] = fmaf(s0, part[nt][0], acc[nt][0]);
-                        acc[nt][1] = fmaf(s0, part[nt][1], acc[nt][1]);
-                        acc[nt][2] = fmaf(s1, part[nt][2], acc[nt][2]);
-                        acc[nt][3] = fmaf(s1, part[nt][3], acc[nt][3]);
+                    alignas(16) uint32_t w[2][kWords];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        copy_words<kWords>(w[h], src + h * (kPartBytes / 2) + (at0 ^ (b0 << 4)));
+#pragma unroll
+                    for (int j = 0; j < kWords; ++j) {
+                        const int b = b0 + j, gr = b * GS / 8;
+                        const bool first = APART && (b * GS % 8 == 0 || GS == 8);
+                        const bool last = APART && ((b + 1) * GS % 8 == 0 || GS == 8);
+                        uint32_t a[2][4];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if constexpr (E2M1)
+                                unpack_e2m1<!kStageX>(w[h][j], APART ? kTwo126 : twice(scale, scale0, h, gr),
+                                                      a[h]);
+                            else
+                                unpack_int<!kStageX>(w[h][j], twice(zero, zero0, h, gr), a[h]);
+                        }
+                        const float s0 = last ? scale_of(0, gr) : 0.f, s1 = last ? scale_of(1, gr) : 0.f;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            // (two at a time: an odd last one costs less than a check each)
+                            if (nt > 0 && nt % 2 == 0 && nt >= nts)
+                                break;
+                            const uint4 x = *reinterpret_cast<const uint4 *>(
+                                kStageX ? src + kXOff + ((b * NT + nt) * 32 + lane) * 16
+                                        : src + kXOff + (nt * 8 + g) * kXPitch + b * 64 + q * 16);
+                            float(&d)[4] = APART ? part[nt] : acc[nt];
+                            const float none[4] = {0.f, 0.f, 0.f, 0.f};
+                            if (first)
+                                mma_bf16(d, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y, none);
+                            else
+                                mma_bf16(d, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y, d);
+                            mma_bf16(d, a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w, d);
+                            if (last) {
+                                acc[nt][0] = fmaf(s0, part[nt][0], acc[nt][0]);
+                                acc[nt][1] = fmaf(s0, part[nt][1], acc[nt][1]);
+                                acc[nt][2] = fmaf(s1, part[nt][2], acc[nt][2]);
+                                acc[nt][3] = fmaf(s1, part[nt][3], acc[nt][3]);
+                            }
+                        }
                     }
                 }
-            }
+            };
+            if (!E2M1 || sh.sums_apart[stage])
+                step(std::true_type{});
+            else
+                step(std::false_type{});
             // the copy that refills the stage goes through the async proxy: without this
             // fence reads of the stage may still be under way when it lands
             fence_proxy_async_shared();
@@ -730,7 +849,7 @@ __global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
         if (!ok)
             break;
         if (seg.s0 == 0 && seg.s1 == walk.steps) {
-            store_tile<NT>(p, seg, acc, part_of * part_cols + row, q);
+            store_tile<NT>(p, seg, acc, part_of * part_cols + row, q, sh.skips);
             continue;
         }
         // a cut tile: leave the sums in the block's slot for the tile its run begins
@@ -752,7 +871,7 @@ __global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
         give_up(p, sh);
     if (sh.runs.piece > 1)
         return;  // runs of whole tiles
-    __threadfence();
+    // (the barrier orders the block's partial sums before the release of one thread)
     if (!named_bar_and(1, kConsumers * 32, ok))
         return;
     if (cw < 2 && lane == 0) {
@@ -767,7 +886,6 @@ __global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
         sh.last[cw] = last;
     }
     named_bar_sync(1, kConsumers * 32);
-    __threadfence();
     for (int slot = 0; slot < 2; ++slot) {
         if (!sh.last[slot])
             continue;
@@ -788,7 +906,7 @@ __global__ void __launch_bounds__(threads_of(R), blocks_per_sm(R))
                     acc[nt][3] += v.w;
                 }
         }
-        store_tile<NT>(p, seg, acc, part_of * part_cols + row, q);
+        store_tile<NT>(p, seg, acc, part_of * part_cols + row, q, sh.skips);
     }
 }
 
@@ -809,7 +927,7 @@ static cudaError_t launch_w4(const CUtensorMap &tw, const W4Params &p, int num_s
     if (e != cudaSuccess)
         return e;
     const int grid = blocks_per_sm(R) * num_sms;
-    kern<<<grid < most ? grid : most, threads_of(R), smem, s>>>(tw, p);
+    kern<<<grid < most ? grid : most, threads_of(NT, R), smem, s>>>(tw, p);
     return cudaGetLastError();
 }
 
