@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 
 #include "ep_internal.h"
+#include "ep_ptx.cuh"
 
 namespace ep {
 
@@ -71,6 +72,8 @@ template <bool DGATES, bool DROWS, int WPR>
 __global__ void __launch_bounds__(32 * kCombineBwdWarps)
     combine_backward_kernel(const CombineBackwardParams p)
 {
+    griddep_launch_dependents();
+    griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int pieces = p.N / 8;
     const int64_t rows = static_cast<int64_t>(p.T) * p.top_k;
@@ -117,15 +120,15 @@ static cudaError_t launch_form(const CombineBackwardParams &p, int num_sms, cuda
     // row, at N = 2048 and 512 / 1024 rows 2.3 / 3.4 against 2.7 / 2.7.
     const int pieces = p.N / 8, threads = 32 * kCombineBwdWarps;
     if ((rows <= 16 * num_sms && pieces >= 2 * threads) || (rows <= 2 * num_sms && pieces >= threads)) {
-        combine_backward_kernel<DGATES, DROWS, kCombineBwdWarps>
-            <<<static_cast<unsigned>(rows), 32 * kCombineBwdWarps, 0, s>>>(p);
+        return launch_behind(combine_backward_kernel<DGATES, DROWS, kCombineBwdWarps>,
+                             static_cast<unsigned>(rows), 32 * kCombineBwdWarps, 0, s, p);
     } else {
         const int64_t blocks = (rows + kCombineBwdWarps - 1) / kCombineBwdWarps;
         const int64_t most = static_cast<int64_t>(num_sms) * 1024;
-        combine_backward_kernel<DGATES, DROWS, 1>
-            <<<static_cast<unsigned>(blocks < most ? blocks : most), 32 * kCombineBwdWarps, 0, s>>>(p);
+        return launch_behind(combine_backward_kernel<DGATES, DROWS, 1>,
+                             static_cast<unsigned>(blocks < most ? blocks : most),
+                             32 * kCombineBwdWarps, 0, s, p);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t launch_combine_backward(const CombineBackwardParams &p, int num_sms, cudaStream_t s)

@@ -68,6 +68,26 @@ inline cudaError_t launch_send_kernel(Kern kern, int grid, int threads, int smem
     return cudaLaunchKernelEx(&cfg, kern, ta, tb, p);
 }
 
+// Launch of a kernel that begins with griddep_wait(): its blocks may take the place of the
+// previous kernel's as those leave, and wait there for that kernel's end and memory. The
+// stream's order is kept.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_behind(void (*kern)(Params...), unsigned grid, unsigned threads, size_t smem,
+                                 cudaStream_t s, const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // The unfused send step (local C rows to the receive buffers, then signalling).
 struct ScatterParams {
     int n_ranks, my_rank, El, top_k, N, max_tokens;

@@ -476,6 +476,8 @@ __global__ void __launch_bounds__(threads_of(NT, R), blocks_per_sm(R))
         sh.cut[0].e = sh.cut[1].e = -1;
     }
     const int tiles = (cols + tile_cols - 1) / tile_cols;
+    griddep_launch_dependents();
+    griddep_wait();
     if (warp == 0) {
         // units of every expert (chunks of its rows x column tiles), their sums, and from
         // them where this block's run begins
@@ -927,8 +929,7 @@ static cudaError_t launch_w4(const CUtensorMap &tw, const W4Params &p, int num_s
     if (e != cudaSuccess)
         return e;
     const int grid = blocks_per_sm(R) * num_sms;
-    kern<<<grid < most ? grid : most, threads_of(NT, R), smem, s>>>(tw, p);
-    return cudaGetLastError();
+    return launch_behind(kern, grid < most ? grid : most, threads_of(NT, R), smem, s, tw, p);
 }
 
 template <int NT, int R, bool VEC>

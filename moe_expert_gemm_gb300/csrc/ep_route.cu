@@ -26,6 +26,7 @@
 #include <cfloat>
 
 #include "ep_internal.h"
+#include "ep_ptx.cuh"
 
 namespace ep {
 
@@ -257,6 +258,8 @@ __device__ __noinline__ void route_token(const RouteParams &p, int64_t t, uint32
 template <typename T>
 __global__ void __launch_bounds__(kRouteThreads) route_token_kernel(const __grid_constant__ RouteParams p)
 {
+    griddep_launch_dependents();
+    griddep_wait();
     extern __shared__ uint32_t smem[];
     const int warp = threadIdx.x >> 5;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRouteThreads / 32) + warp;
@@ -340,6 +343,8 @@ enum Choice { kByLogit, kBySigmoid, kBySoftmax };
 template <typename T, int VPL, bool VEC, Choice BY>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __grid_constant__ RouteParams p)
 {
+    griddep_launch_dependents();
+    griddep_wait();
     constexpr int kMost = 16 / static_cast<int>(sizeof(T));
     constexpr int W = VEC ? (VPL < kMost ? VPL : kMost) : 1;
     constexpr int WB = VEC ? (VPL < 4 ? VPL : 4) : 1;  // of the bias
@@ -555,6 +560,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __gr
 template <typename T, int EP>
 __global__ void __launch_bounds__(128) route_thread_kernel(const __grid_constant__ RouteParams p)
 {
+    griddep_launch_dependents();
+    griddep_wait();
     const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (t >= p.T)
         return;
@@ -644,6 +651,8 @@ template <typename T, int VPL, bool VEC>
 __global__ void __launch_bounds__(32 * kRouteWarps)
     route_backward_warp_kernel(const __grid_constant__ RouteBackwardParams p)
 {
+    griddep_launch_dependents();
+    griddep_wait();
     constexpr int kMost = 16 / static_cast<int>(sizeof(T));
     constexpr int W = VEC ? (VPL < kMost ? VPL : kMost) : 1;
     const int lane = threadIdx.x & 31;
@@ -731,6 +740,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 template <typename T>
 __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const __grid_constant__ RouteBackwardParams p)
 {
+    griddep_launch_dependents();
+    griddep_wait();
     extern __shared__ uint32_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = p.E, k = p.top_k;
@@ -806,9 +817,8 @@ static cudaError_t launch_rows(Kern kern, const Params &p, int warps, int64_t wa
         if (e != cudaSuccess)
             return e;
     }
-    kern<<<static_cast<unsigned>((static_cast<int64_t>(p.T) + warps - 1) / warps), 32 * warps, smem,
-           s>>>(p);
-    return cudaGetLastError();
+    return launch_behind(kern, static_cast<unsigned>((static_cast<int64_t>(p.T) + warps - 1) / warps),
+                         32 * warps, smem, s, p);
 }
 
 static bool aligned(const void *p, int64_t bytes)
@@ -849,11 +859,8 @@ static cudaError_t launch_route_type(RouteParams p, cudaStream_t s)
         const int ep = p.E <= 8 ? 8 : 16;
         p.vec = aligned(p.logits, 16) && p.stride % most == 0;
         const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(p.T) + 127) / 128);
-        if (ep == 8)
-            route_thread_kernel<T, 8><<<blocks, 128, 0, s>>>(p);
-        else
-            route_thread_kernel<T, 16><<<blocks, 128, 0, s>>>(p);
-        return cudaGetLastError();
+        return ep == 8 ? launch_behind(route_thread_kernel<T, 8>, blocks, 128, 0, s, p)
+                       : launch_behind(route_thread_kernel<T, 16>, blocks, 128, 0, s, p);
     }
     int lanes_log2 = 5;
     while (lanes_log2 > 0 && 32 >> lanes_log2 < groups)
