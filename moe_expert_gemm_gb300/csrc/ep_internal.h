@@ -236,5 +236,7 @@ cudaError_t launch_combine_backward(const CombineBackwardParams &p, int num_sms,
 int64_t w4_workspace_bytes();
 cudaError_t launch_matvec_w4(const CUtensorMap &tw, const W4Params &p, int num_sms,
                              cudaStream_t s);
+cudaError_t launch_matvec_w4_wide(const CUtensorMap &tw, const W4Params &p, int num_sms,
+                                  cudaStream_t s);
 
 }  // namespace ep

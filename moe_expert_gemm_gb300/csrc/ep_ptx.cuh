@@ -120,18 +120,6 @@ __device__ __forceinline__ uint64_t policy_evict_first()
     return p;
 }
 
-// Untiled bulk copy from global to shared memory (both addresses 16-byte aligned, bytes a
-// multiple of 16); completion is counted in bytes on `bar`.
-__device__ __forceinline__ void bulk_load(void *smem_dst, const void *src, uint32_t bytes,
-                                          uint64_t *bar)
-{
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            smem_u32(smem_dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
-        : "memory");
-}
-
 // Untiled bulk copy from shared to global memory on the TMA engine (both addresses
 // 16-byte aligned, bytes a multiple of 16), tracked per thread in bulk groups.
 __device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes)

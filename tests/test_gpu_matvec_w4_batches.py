@@ -74,10 +74,9 @@ def test_w4_batches_keep_infinities_in_their_rows(announced):
 @pytest.mark.parametrize("announced", [9, 17])
 def test_w4_batches_skip_bad_gather_indices(announced):
     T, K, N = 20, 320, 72
-    c = batch(Call(activations(T, K, 8), [T], weights(1, N, K, "int4z", 32, 9), "int4z", 32), announced)
+    c = batch(Call(activations(T, K, 8), [T], weights(1, N, K, "int4z", 32, 9), "int4z", 32),
+              max(T, announced))
     want = c.run()
-    c.cfg.num_tokens = max(T, announced)
-    c.cfg.max_tokens_per_rank = c.cfg.num_tokens
     x = torch.zeros(c.cfg.num_tokens, K, dtype=torch.bfloat16, device="cuda")
     x[:T] = c.A
     gi = torch.arange(T, dtype=torch.int32, device="cuda")
