@@ -269,6 +269,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int at0 = row * 128 + ((q * kWords / 4 ^ g) << 4) + q * kWords % 4 * 4;
     const int scale0 = kScaleOff + row * GS * 2;
     const int zero0 = scale0 + kZeroOff - kScaleOff;
+    float4 *const sums = reinterpret_cast<float4 *>(p.workspace + kMaxBlocks * 16);
+    constexpr int64_t kSlot = 32 * kConsumers * NT;  // fours of a partial tile
     bool ok = true;
     while (walk.next(sh.run, tile_cols, seg)) {
         const int nts = (seg.m1 - seg.m0 + 7) / 8;
@@ -363,16 +365,39 @@ __global__ void __launch_bounds__(kThreads, 2)
             break;
         if (seg.s0 == 0 && seg.s1 == walk.steps)
             store_tile<NT>(p, seg, acc, row, q, sh.run.skips);
-        else
-            leave_sums<NT, 32 * kConsumers>(p, sh.run, seg, acc, nts, ctid);
+        else {
+            // a cut tile: leave the sums in the block's slot for the tile its run begins inside
+            // (0) or ends inside (1)
+            const int slot = seg.s0 == 0 ? 1 : 0;
+            float4 *to = sums + (blockIdx.x * 2 + slot) * kSlot + ctid;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                if (nt < nts)
+                    __stcg(to + nt * 32 * kConsumers,
+                           make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]));
+            if (ctid == 0)
+                sh.run.cut[slot] = seg;
+        }
     }
     if (!ok && lane == 0)
         give_up(p, sh);
-    join_cut_tiles<NT, 32 * kConsumers>(
-        p, sh.run, ctid, ok, [](const Segment &s) { return (s.m1 - s.m0 + 7) / 8; },
-        [&](const Segment &s, const float(&acc)[NT][4]) {
-            store_tile<NT>(p, s, acc, row, q, sh.run.skips);
-        });
+    join_cut_tiles<32 * kConsumers>(p, sh.run, ctid, ok, [&](const Segment &s, int from, int to) {
+        const int nts = (s.m1 - s.m0 + 7) / 8;
+        float acc[NT][4] = {};
+        for (int b = from; b <= to; ++b) {
+            const float4 *theirs = sums + (b * 2 + (b == from ? 1 : 0)) * kSlot + ctid;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                if (nt < nts) {
+                    const float4 v = __ldcg(theirs + nt * 32 * kConsumers);
+                    acc[nt][0] += v.x;
+                    acc[nt][1] += v.y;
+                    acc[nt][2] += v.z;
+                    acc[nt][3] += v.w;
+                }
+        }
+        store_tile<NT>(p, s, acc, row, q, sh.run.skips);
+    });
 }
 
 int64_t w4_workspace_bytes()

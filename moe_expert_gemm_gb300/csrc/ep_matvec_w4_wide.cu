@@ -18,8 +18,11 @@
 //    eight; the staging warps lay the activations out in that order too, in the 128-byte
 //    swizzle that the matrix engine reads.
 //  * Thread block: warp 0 streams the weights (TMA), warp 1 issues the products, warps 2
-//    and 3 stage activations and scales, warps 4 to 11 unpack (warp i the tensor memory
-//    lanes 32 (i % 4) on, the k's first half or second) and store the results.
+//    to 5 stage activations and scales, warps 6 to 9 unpack (warp i the tensor memory
+//    lanes 32 (i % 4) on) and store the results. Codes, activations and unpacked weights
+//    have a ring each, so that nobody waits for more than what it reads.
+//  * What bounds it is the issue of instructions, 17 for a word of eight codes before all
+//    else; hence straight code for the staging warps, which have a row's piece in ten.
 #include "ep_w4.cuh"
 #include "ep_w4_scales.cuh"
 
@@ -32,35 +35,69 @@ namespace {
 constexpr int kRows = 64;                        // activation rows of a pass
 constexpr int kWeightBytes = kPartRows * kStepK / 2;
 constexpr int kAtomBytes = kRows * 128;          // 64 k of the activations
-constexpr int kXBytes = kAtomBytes * kStepK / 64;
-constexpr int kStages = 2;
-constexpr int kStagers = 2;
-constexpr int kUnpackers = 8;
+constexpr int kXK = 128;                         // k of a stage of activations: half a step
+constexpr int kXBytes = kAtomBytes * kXK / 64;
+constexpr int kStages = 3, kXStages = 3, kBuffers = 3;
+constexpr int kStagers = 4;
+constexpr int kUnpackers = 4;
 constexpr int kThreads = 32 * (2 + kStagers + kUnpackers);
-constexpr int kSums = 32;                        // a thread's sums of a tile
 constexpr uint32_t kTmemCols = 256;              // of a block: two blocks an SM
 constexpr uint32_t kACols = 64;                  // of a buffer of unpacked weights
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages];
-    uint64_t a_full[2], a_empty[2];
+    uint64_t full[kStages], empty[kStages];       // codes and scales
+    uint64_t x_full[kXStages], x_empty[kXStages];  // activations
+    uint64_t a_full[kBuffers], a_empty[kBuffers];  // unpacked weights
     uint64_t sums_full, drained;
     uint32_t tmem;
-    int large[kStages];  // e2m1: the stage holds scales past 2
+    int large[kStages][kStagers];  // e2m1: the stage holds scales past 2, of 32 weight rows
     int abort;
     RunInfo run;
-    float up[16 * 64];   // SwiGLU: 16 columns of the up rows' sums
+    float up[4 * 64];  // SwiGLU: 4 columns of the up rows' sums
 };
 
 constexpr int stage_bytes(int GS, bool E2M1)
 {
-    return (kWeightBytes + kXBytes + kPartRows * GS * (E2M1 ? 2 : 4) + 1023) / 1024 * 1024;
+    return (kWeightBytes + kPartRows * GS * (E2M1 ? 2 : 4) + 1023) / 1024 * 1024;
 }
 
 constexpr int smem_bytes(int GS, bool E2M1)
 {
-    return 1024 + kStages * stage_bytes(GS, E2M1) + static_cast<int>(sizeof(Shared));
+    return 1024 + kStages * stage_bytes(GS, E2M1) + kXStages * kXBytes + static_cast<int>(sizeof(Shared));
+}
+
+// The place of a block's sums of a cut tile: 64 columns of 128 rows, 4 columns by a row at a
+// time.
+__device__ __forceinline__ float4 *sums_of(const W4Params &p, int slot)
+{
+    return reinterpret_cast<float4 *>(p.workspace + kMaxBlocks * 16) +
+           static_cast<int64_t>(slot) * (kRows / 4 * kPartRows);
+}
+
+// mbar_wait for the many warps of this kernel: a waiting one is suspended for up to 10 us at
+// a time, as the polls of 28 warps an SM would take the unpacking ones' issue slots.
+__device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, uint64_t timeout_ns,
+                                          volatile int *abort)
+{
+    auto probe = [&] {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
+            : "memory");
+        return ok != 0;
+    };
+    if (probe())
+        return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!probe())
+        if (*abort || globaltimer_ns() - t0 > timeout_ns)
+            return false;
+    return true;
 }
 
 __device__ __forceinline__ void give_up(const W4Params &p, Shared &sh)
@@ -81,21 +118,7 @@ __device__ __forceinline__ void mma_f16_tmem(uint32_t d, uint32_t a, uint64_t b_
         : "memory");
 }
 
-// Thread i's N registers into lane (base + i), N consecutive columns.
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-        "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
+// Thread i's registers into lane (base + i), consecutive columns.
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[16])
 {
     asm volatile(
@@ -106,44 +129,76 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[1
         : "memory");
 }
 
+// 8 consecutive columns of lane (base + i) to thread i, when they are there.
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[8])
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+    tmem_ld_wait();
+    tmem_regs_ready(r);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        v[c] = __uint_as_float(r[c]);
+}
+
 __device__ __forceinline__ void tmem_store_wait()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Stores a thread's sums of a whole tile: row `row` of it, columns 32 * half + c.
+// Stores a thread's sums of a whole tile, row `row` of it and the segment's rows c0 .. c0 + 7.
 __device__ __forceinline__ void store_sums(const W4Params &p, Shared &sh, const Segment &s,
-                                           const float (&v)[kSums], int row, int half)
+                                           const float (&v)[8], int row, int c0)
 {
     const int cols = p.swiglu ? p.N / 2 : p.N;
     const float back = p.format == EP_W4_INT ? kIntScale : 1.f;
-    __nv_bfloat16 *C = reinterpret_cast<__nv_bfloat16 *>(p.C);
-    const bool skips = sh.run.skips;
-    auto put = [&](int m, int n, float y) {
-        if (m < s.m1 && n < cols && !(skips && !row_of(p, m)))
-            C[static_cast<int64_t>(m) * cols + n] = __float2bfloat16_rn(y);
-    };
-    const int m0 = s.m0 + 32 * half;
-    if (!p.swiglu) {
+    float up[8];
+    if (p.swiglu) {  // tile rows 64 on are the up rows of rows 0 on
+        float *const mine = sh.up + row % 64;
 #pragma unroll
-        for (int c = 0; c < kSums; ++c)
-            put(m0 + c, s.n0 + row, v[c] * back);
-        return;
-    }
-    // rows 64 on are the up rows of rows 0 on
+        for (int h = 0; h < 8; h += 4) {
+            if (row >= 64)
 #pragma unroll
-    for (int c0 = 0; c0 < kSums; c0 += 8) {
+                for (int c = 0; c < 4; ++c)
+                    mine[c * 64] = v[h + c] * back;
+            named_bar_sync(1, 32 * kUnpackers);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                up[h + c] = mine[c * 64];
+            named_bar_sync(1, 32 * kUnpackers);
+        }
         if (row >= 64)
+            return;
+    }
+    const int n = s.n0 + row;
+    if (n >= cols)
+        return;
+    __nv_bfloat16 *C = reinterpret_cast<__nv_bfloat16 *>(p.C) + static_cast<int64_t>(s.m0 + c0) * cols + n;
+    if (!sh.run.skips) {
+        const int end = s.m1 - s.m0 - c0;
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                sh.up[(8 * half + c) * 64 + row - 64] = v[c0 + c];
-        named_bar_sync(1, 32 * kUnpackers);
-        if (row < 64)
+        for (int c = 0; c < 8; ++c, C += cols) {
+            const float y = v[c] * back;
+            if (c < end)
+                *C = __float2bfloat16_rn(p.swiglu ? silu_f32(y) * up[c] : y);
+        }
+    } else {
+        float y[8];
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                put(m0 + c0 + c, s.n0 + row,
-                    silu_f32(v[c0 + c] * back) * (sh.up[(8 * half + c) * 64 + row] * back));
-        named_bar_sync(1, 32 * kUnpackers);
+        for (int c = 0; c < 8; ++c)
+            y[c] = p.swiglu ? silu_f32(v[c] * back) * up[c] : v[c] * back;
+#pragma unroll 1
+        for (int m = s.m0 + c0; m < s.m1 && m < s.m0 + c0 + 8; ++m, C += cols) {
+            if (row_of(p, m))
+                *C = __float2bfloat16_rn(y[0]);
+#pragma unroll
+            for (int c = 0; c < 7; ++c)
+                y[c] = y[c + 1];
+        }
     }
 }
 
@@ -154,13 +209,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     matvec_w4_wide_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ W4Params p)
 {
     constexpr int kStage = stage_bytes(GS, E2M1);
-    constexpr int kXOff = kWeightBytes, kScaleOff = kXOff + kXBytes;
-    constexpr int kZeroOff = kScaleOff + kPartRows * GS * 2;
+    constexpr int kScaleOff = kWeightBytes, kZeroOff = kScaleOff + kPartRows * GS * 2;
     // k of a buffer of unpacked weights: 64 columns of one number a weight or of two
     constexpr int kBatchK = E2M1 ? 128 : 64, kBatches = kStepK / kBatchK;
+    constexpr int kChunks = kBatchK / 32;  // of 32 k, of a buffer
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    Shared &sh = *reinterpret_cast<Shared *>(ring + kStages * kStage);
+    uint8_t *x_ring = ring + kStages * kStage;
+    Shared &sh = *reinterpret_cast<Shared *>(x_ring + kXStages * kXBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tile_cols = p.swiglu ? 64 : kPartRows;
     const int cols = p.swiglu ? p.N / 2 : p.N;
@@ -168,10 +224,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (tid == 64) {
         tma_prefetch_map(&tw);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], 2);                // the producer, a staging warp
-            mbar_init(&sh.empty[i], kUnpackers + 1);  // the unpacking warps, the products
+            mbar_init(&sh.full[i], kStagers + 1);     // the staging warps, the producer
+            mbar_init(&sh.empty[i], kUnpackers);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kXStages; ++i) {
+            mbar_init(&sh.x_full[i], kStagers);
+            mbar_init(&sh.x_empty[i], 1);
+        }
+        for (int i = 0; i < kBuffers; ++i) {
             mbar_init(&sh.a_full[i], kUnpackers);
             mbar_init(&sh.a_empty[i], 1);
         }
@@ -198,12 +258,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (sh.run.bad)
         walk.todo = 0;
     Segment seg;
-    int stage = 0;
-    uint32_t phase = 0;
-    auto advance = [&] {
-        if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
+    int stage = 0, xs = 0, buf = 0;
+    uint32_t phase = 0, x_phase = 0, buf_phase = 0;
+    auto advance = [](int &i, uint32_t &ph, int n) {
+        if (++i == n) {
+            i = 0;
+            ph ^= 1;
         }
     };
 
@@ -215,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             while (ok && walk.next(sh.run, tile_cols, seg)) {
                 const int y0 = seg.e * p.N + seg.n0, y1 = y0 + (p.swiglu ? cols : 64);
                 for (int k = seg.s0; k < seg.s1; ++k) {
-                    if (!mbar_wait(&sh.empty[stage], phase ^ 1, kTimeoutNs, abort_flag)) {
+                    if (!wait_long(&sh.empty[stage], phase ^ 1, kTimeoutNs, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -224,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     tma_load_2d(dst, &tw, &sh.full[stage], k * (kStepK / 2), y0);
                     tma_load_2d(dst + kWeightBytes / 2, &tw, &sh.full[stage], k * (kStepK / 2), y1);
                     ++issued;
-                    advance();
+                    advance(stage, phase, kStages);
                 }
             }
             if (!ok) {
@@ -232,45 +292,44 @@ __global__ void __launch_bounds__(kThreads, 2)
                 // the copies in flight land before the block's shared memory goes away
                 volatile int no_abort = 0;
                 for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-                    mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, 1000000, &no_abort);
+                    wait_long(&sh.full[i % kStages], (i / kStages) & 1, 1000000, &no_abort);
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------- products
         if (lane == 0) {
-            int batch = 0;  // of all: buffer batch % 2
             bool ok = true;
             while (ok && walk.next(sh.run, tile_cols, seg)) {
                 const uint32_t idesc = make_idesc(1u, 128, (seg.m1 - seg.m0 + 15) / 16 * 16);
                 for (int k = seg.s0; ok && k < seg.s1; ++k) {
-                    ok = mbar_wait(&sh.full[stage], phase, kTimeoutNs, abort_flag);
-                    const uint32_t x = smem_u32(ring + stage * kStage + kXOff);
                     const int here = VEC || (k + 1) * kStepK <= p.K ? kStepK : p.K - k * kStepK;
-                    for (int i = 0; ok && i < kBatches; ++i, ++batch) {
-                        const int buf = batch & 1;
-                        ok = mbar_wait(&sh.a_full[buf], (batch >> 1) & 1, kTimeoutNs, abort_flag);
+#pragma unroll 1
+                    for (int i = 0; i < kBatches; ++i) {
+                        constexpr int kPer = kXK / kBatchK;  // batches of a stage of activations
+                        ok = (i % kPer || wait_long(&sh.x_full[xs], x_phase, kTimeoutNs, abort_flag)) &&
+                             wait_long(&sh.a_full[buf], buf_phase, kTimeoutNs, abort_flag);
                         if (!ok)
                             break;
                         tc_fence_after();
                         const uint32_t a = tmem + kRows + buf * kACols;
+                        const uint32_t x = smem_u32(x_ring + xs * kXBytes) + i % kPer * kAtomBytes;
 #pragma unroll
                         for (int j = 0; j < kBatchK / 16; ++j) {
-                            const int at = i * kBatchK + j * 16;
-                            if (!VEC && at >= here)
+                            if (!VEC && i * kBatchK + j * 16 >= here)
                                 break;
-                            const uint64_t b =
-                                desc_kmajor_sw128(x + at / 64 * kAtomBytes + at % 64 * 2);
+                            const uint64_t b = desc_kmajor_sw128(x + j / 4 * kAtomBytes + j % 4 * 32);
                             mma_f16_tmem(tmem, a + j * 8, b, idesc, k > seg.s0 || i > 0 || j > 0);
                             if (!E2M1)
                                 mma_f16_tmem(tmem, a + kACols / 2 + j * 8, b, idesc, 1);
                         }
                         mma_commit(&sh.a_empty[buf]);
+                        advance(buf, buf_phase, kBuffers);
+                        if (i % kPer == kPer - 1) {
+                            mma_commit(&sh.x_empty[xs]);
+                            advance(xs, x_phase, kXStages);
+                        }
                     }
-                    if (!ok)
-                        break;
-                    mma_commit(&sh.empty[stage]);
-                    advance();
                 }
                 if (ok)
                     mma_commit(&sh.sums_full);
@@ -280,180 +339,172 @@ __global__ void __launch_bounds__(kThreads, 2)
             // every product issued has ended once this arrives
             mma_commit(&sh.drained);
             volatile int no_abort = 0;
-            mbar_wait(&sh.drained, 0, kTimeoutNs, &no_abort);
+            wait_long(&sh.drained, 0, kTimeoutNs, &no_abort);
         }
         __syncwarp();
     } else if (warp < 2 + kStagers) {
         // ----------------------------------------- staging: activations and scales
-        bool turn = warp == 2;  // this warp's step, the other's, ... (as many as stages: a
-                                // wait knows a phase's parity alone)
-        constexpr int kRowSets = kPartRows / 32, kBatch = 8;
+        const int part = warp - 2;  // of every eight rows two, and the scales of 32 weight rows
+        constexpr int kLoads = kRows / 8;
         const int groups = p.K / (kStepK / GS);
         bool ok = true;
         while (ok && walk.next(sh.run, tile_cols, seg)) {
             const int rows = seg.m1 - seg.m0;
-            unsigned long long mine[2];  // where the segment's rows lane, lane + 32 lie
+            // the segment's rows 8 i + 2 part and the next, half a warp each (rows that are not
+            // there are left as they are: nobody stores their sums)
+            const uint4 *from[kLoads];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool there = 32 * i + lane < rows;
-                mine[i] = there ? reinterpret_cast<unsigned long long>(row_of(p, seg.m0 + 32 * i + lane)) : 0;
-                if (there && !mine[i]) {
+            for (int i = 0; i < kLoads; ++i) {
+                const int m = seg.m0 + 8 * i + 2 * part + lane / 16;
+                from[i] = m < seg.m1 ? reinterpret_cast<const uint4 *>(row_of(p, m)) : nullptr;
+                if (m < seg.m1 && !from[i]) {
                     atomicOr(p.status, EP_STATUS_BOUNDS);
                     sh.run.skips = 1;
                 }
+                from[i] = from[i] ? from[i] + lane % 16 : nullptr;
             }
-            int64_t scale_at[kRowSets];
+            const int scale_row = 32 * part + lane;
+            int n = seg.n0 + (p.swiglu ? scale_row % 64 : scale_row);
+            n = n < cols ? n : cols - 1;  // (rows past the last column: nobody stores them)
+            const int64_t scale_at =
+                (static_cast<int64_t>(seg.e) * p.N + n + (p.swiglu && scale_row >= 64 ? cols : 0)) * groups;
+            Scales<GS, E2M1, VEC> sc;
+            uint4 v[kLoads] = {};
+            auto load_rows = [&](int k, int h) {  // k half h of step k
+                const int at = k * (kStepK / 8) + h * (kXK / 8);
+                const bool there = VEC || (at + lane % 16) * 8 < p.K;  // (no product reads the rest)
+                // (two blocks of straight code: a branch a row would take longer than the row)
+                auto load = [&](int i0) {
 #pragma unroll
-            for (int i = 0; i < kRowSets; ++i) {
-                const int r = 32 * i + lane;
-                int n = seg.n0 + (p.swiglu ? r % 64 : r);
-                n = n < cols ? n : cols - 1;  // (rows past the last column: nobody stores them)
-                scale_at[i] = (static_cast<int64_t>(seg.e) * p.N + n + (p.swiglu && r >= 64 ? cols : 0)) * groups;
-            }
-            for (int k = seg.s0; k < seg.s1; ++k, turn = !turn) {
-                if (!turn) {
-                    advance();
-                    continue;
-                }
-                Scales<GS, E2M1, VEC> sc[kRowSets];
-#pragma unroll
-                for (int i = 0; i < kRowSets; ++i)
-                    sc[i].load(p, scale_at[i] + k * GS, groups - k * GS);
-                const int k0 = k * kStepK + lane * 8;  // this lane's piece of a row
-                uint4 v[kBatch];
-                auto load_rows = [&](int r0) {
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        if (r0 + i >= rows)
-                            break;
-                        const uint4 *from = reinterpret_cast<const uint4 *>(
-                            __shfl_sync(0xffffffffu, r0 < 32 ? mine[0] : mine[1], (r0 + i) & 31));
-                        v[i] = make_uint4(0, 0, 0, 0);
-                        if (from && (VEC || k0 < p.K))
-                            v[i] = __ldg(from + k0 / 8);
-                    }
+                    for (int i = i0; i < i0 + kLoads / 2; ++i)
+                        if (from[i] && there)
+                            v[i] = __ldg(from[i] + at);
                 };
-                load_rows(0);
+                load(0);
+                if (rows > kRows / 2)
+                    load(kLoads / 2);
+            };
+            auto store_rows = [&] {
                 ok = __all_sync(0xffffffffu,
-                                mbar_wait(&sh.empty[stage], phase ^ 1, kTimeoutNs, abort_flag));
+                                wait_long(&sh.x_empty[xs], x_phase ^ 1, kTimeoutNs, abort_flag));
+                if (!ok)
+                    return;
+                const int r = 2 * part + lane / 16;  // (of eight: a swizzled row of 128 bytes)
+                uint8_t *x = x_ring + xs * kXBytes + lane % 16 / 8 * kAtomBytes + r * 128 + ((lane % 8 ^ r) << 4);
+                auto store = [&](int i0) {
+#pragma unroll
+                    for (int i = i0; i < i0 + kLoads / 2; ++i)
+                        *reinterpret_cast<uint4 *>(x + i * 1024) = make_uint4(
+                            __byte_perm(v[i].x, v[i].z, 0x5410), __byte_perm(v[i].x, v[i].z, 0x7632),
+                            __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632));
+                };
+                store(0);
+                if (rows > kRows / 2)
+                    store(kLoads / 2);
+                fence_proxy_async_shared();  // the products read them
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sh.x_full[xs]);
+                advance(xs, x_phase, kXStages);
+            };
+            sc.load(p, scale_at + seg.s0 * GS, groups - seg.s0 * GS);
+            load_rows(seg.s0, 0);
+            for (int k = seg.s0; k < seg.s1; ++k) {
+                ok = __all_sync(0xffffffffu,
+                                wait_long(&sh.empty[stage], phase ^ 1, kTimeoutNs, abort_flag));
                 if (!ok)
                     break;
                 uint8_t *dst = ring + stage * kStage;
-                uint8_t *x = dst + kXOff + lane / 8 * kAtomBytes;
-                for (int r0 = 0; r0 < rows; r0 += kBatch) {
-                    if (r0)
-                        load_rows(r0);
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        if (r0 + i >= rows)
-                            break;
-                        const int r = r0 + i;
-                        *reinterpret_cast<uint4 *>(x + r * 128 + ((lane % 8 ^ r % 8) << 4)) = make_uint4(
-                            __byte_perm(v[i].x, v[i].z, 0x5410), __byte_perm(v[i].x, v[i].z, 0x7632),
-                            __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632));
-                    }
-                }
-                bool large = false;
-                if (E2M1) {
-#pragma unroll
-                    for (int i = 0; i < kRowSets; ++i)
-                        large |= sc[i].large();
-                    large = __any_sync(0xffffffffu, large);
-                    if (lane == 0)
-                        sh.large[stage] = large;
-                }
-#pragma unroll
-                for (int i = 0; i < kRowSets; ++i) {
-                    const int r = 32 * i + lane;
-                    sc[i].store(dst + kScaleOff + r * GS * 2, dst + kZeroOff + r * GS * 2, large);
-                }
-                fence_proxy_async_shared();  // the products read the activations
+                const bool large = E2M1 && __any_sync(0xffffffffu, sc.large());
+                if (E2M1 && lane == 0)
+                    sh.large[stage][part] = large;
+                sc.store(dst + kScaleOff + scale_row * GS * 2, dst + kZeroOff + scale_row * GS * 2, large);
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&sh.full[stage]);
-                advance();
+                advance(stage, phase, kStages);
+                store_rows();
+                if (!ok)
+                    break;
+                load_rows(k, 1);
+                const bool more = k + 1 < seg.s1;
+                if (more)
+                    sc.load(p, scale_at + (k + 1) * GS, groups - (k + 1) * GS);
+                store_rows();
+                if (!ok)
+                    break;
+                if (more)
+                    load_rows(k + 1, 0);
             }
         }
         if (!ok && lane == 0)
             give_up(p, sh);
     } else {
         // ------------------------------------------------------ unpacking, results
-        const int quarter = warp & 3, half = (warp - 2 - kStagers) >> 2;
+        const int quarter = warp & 3;
         const int row = 32 * quarter + lane, utid = tid - 32 * (2 + kStagers);
         const uint32_t my_lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
         const uint8_t *const scale0 = ring + kScaleOff + row * GS * 2;
-        // fours of this thread's sums that belong to rows of the segment
-        auto used = [&](const Segment &s) {
-            const int n = (s.m1 - s.m0 - 32 * half + 3) / 4;
-            return n < 0 ? 0 : n > kSums / 4 ? kSums / 4 : n;
-        };
-        int batch = 0, segments = 0;
+        int segments = 0;
         bool ok = true;
         while (walk.next(sh.run, tile_cols, seg)) {
             for (int k = seg.s0; ok && k < seg.s1; ++k) {
                 ok = __all_sync(0xffffffffu,
-                                mbar_wait(&sh.full[stage], phase, kTimeoutNs, abort_flag));
+                                wait_long(&sh.full[stage], phase, kTimeoutNs, abort_flag));
                 if (!ok)
                     break;
                 const uint8_t *src = ring + stage * kStage;
-                const bool large = E2M1 && sh.large[stage];
-                for (int i = 0; i < kBatches; ++i, ++batch) {
-                    const int buf = batch & 1;
-                    // chunks of 32 k: two of four, or one of two
-                    constexpr int kChunks = kBatchK / 64;
-                    uint4 codes[kChunks];
-                    uint32_t scale[kChunks], zero[kChunks];
-#pragma unroll
-                    for (int j = 0; j < kChunks; ++j) {
-                        const int c = (2 * i + half) * kChunks + j, gr = c * GS / 8;
-                        codes[j] = *reinterpret_cast<const uint4 *>(src + row * 128 + ((c ^ row % 8) << 4));
-                        scale[j] = *reinterpret_cast<const uint16_t *>(scale0 + stage * kStage + gr * 2) * 0x10001u;
-                        if (!E2M1)
-                            zero[j] = *reinterpret_cast<const uint16_t *>(scale0 + stage * kStage + kZeroOff -
-                                                                          kScaleOff + gr * 2) * 0x10001u;
-                    }
-                    ok = __all_sync(0xffffffffu, mbar_wait(&sh.a_empty[buf], (batch >> 1 & 1) ^ 1, kTimeoutNs,
+                const bool large = E2M1 && sh.large[stage][quarter];
+                for (int i = 0; i < kBatches; ++i) {
+                    // (one after the other, the code has to stay small)
+                    uint32_t a = my_lanes + kRows + buf * kACols;
+                    ok = __all_sync(0xffffffffu, wait_long(&sh.a_empty[buf], buf_phase ^ 1, kTimeoutNs,
                                                            abort_flag));
                     if (!ok)
                         break;
                     tc_fence_after();
-                    const uint32_t a = my_lanes + kRows + buf * kACols + half * (16 * kChunks);
-                    if constexpr (E2M1) {
-                        uint32_t w[32];
+#pragma unroll 1
+                    for (int j = 0; j < kChunks; ++j, a += 16) {
+                        const int c = i * kChunks + j;
+                        const uint8_t *at = scale0 + stage * kStage + c * GS / 8 * 2;
+                        const uint4 codes =
+                            *reinterpret_cast<const uint4 *>(src + row * 128 + ((c ^ row % 8) << 4));
+                        const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+                        const uint32_t scale = *reinterpret_cast<const uint16_t *>(at) * 0x10001u;
+                        uint32_t v[16];
+                        if constexpr (E2M1) {
+                            const uint32_t factor = large ? kTwo126 : scale;
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const uint32_t c[4] = {codes[j].x, codes[j].y, codes[j].z, codes[j].w};
+                            for (int b = 0; b < 4; ++b)
+                                unpack_e2m1(w[b], factor, *reinterpret_cast<uint32_t(*)[4]>(v + 4 * b));
+                            if (large) {
+#pragma unroll
+                                for (int h = 0; h < 16; ++h)
+                                    v[h] = bf16x2_mul(v[h], scale);
+                            }
+                            tmem_store(a, v);
+                        } else {
+                            const uint32_t zero = *reinterpret_cast<const uint16_t *>(at + kZeroOff - kScaleOff) * 0x10001u;
+                            // the first part with a scale two steps short: it stays short of the
+                            // product, and the second part has its sign (so that an infinite
+                            // activation meets no 0 that the product is not)
+                            const uint32_t less = (scale & 0x7FFFu) > 1 ? 0x00020002u : 0u;
+                            const uint32_t minus = (scale - less) ^ 0x80008000u;
+                            uint32_t lo[16];
 #pragma unroll
                             for (int b = 0; b < 4; ++b) {
                                 uint32_t t[4];
-                                unpack_e2m1(c[b], large ? kTwo126 : scale[j], t);
+                                unpack_int(w[b], zero, t);
 #pragma unroll
-                                for (int h = 0; h < 4; ++h)
-                                    w[16 * j + 4 * b + h] = large ? bf16x2_mul(t[h], scale[j]) : t[h];
+                                for (int h = 0; h < 4; ++h) {
+                                    const uint32_t n = bf16x2_mul(t[h], minus);
+                                    lo[4 * b + h] = bf16x2_fma(t[h], scale, n);
+                                    v[4 * b + h] = n ^ 0x80008000u;
+                                }
                             }
+                            tmem_store(a, v);
+                            tmem_store(a + kACols / 2, lo);
                         }
-                        tmem_store(a, w);
-                    } else {
-                        uint32_t hi[16], lo[16];
-                        const uint32_t c[4] = {codes[0].x, codes[0].y, codes[0].z, codes[0].w};
-                        // the first part with a scale two steps short: it stays short of the
-                        // product, and the second part has its sign (so that an infinite
-                        // activation meets no 0 that the product is not)
-                        const uint32_t less = (scale[0] & 0x7FFFu) > 1 ? 0x00020002u : 0u;
-                        const uint32_t minus = (scale[0] - less) ^ 0x80008000u;
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            uint32_t t[4];
-                            unpack_int(c[b], zero[0], t);
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                const uint32_t n = bf16x2_mul(t[h], minus);
-                                lo[4 * b + h] = bf16x2_fma(t[h], scale[0], n);
-                                hi[4 * b + h] = n ^ 0x80008000u;
-                            }
-                        }
-                        tmem_store(a, hi);
-                        tmem_store(a + kACols / 2, lo);
                     }
                     tmem_store_wait();
                     tc_fence_before();
@@ -465,14 +516,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                         if (i == kBatches - 1)
                             mbar_arrive(&sh.empty[stage]);
                     }
+                    advance(buf, buf_phase, kBuffers);
                 }
                 if (!ok)
                     break;
-                advance();
+                advance(stage, phase, kStages);
             }
             if (ok)
                 ok = __all_sync(0xffffffffu,
-                                mbar_wait(&sh.sums_full, segments & 1, kTimeoutNs, abort_flag));
+                                wait_long(&sh.sums_full, segments & 1, kTimeoutNs, abort_flag));
             ++segments;
             // (all of the unpacking warps leave together: they meet at barriers below)
             if (!ok && lane == 0)
@@ -482,25 +534,38 @@ __global__ void __launch_bounds__(kThreads, 2)
                 break;
             }
             tc_fence_after();
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(my_lanes + 32 * half, r);
-            tmem_ld_wait();
-            tmem_regs_ready(r);
+            const bool whole = seg.s0 == 0 && seg.s1 == walk.steps;
+            const int rows = seg.m1 - seg.m0, slot = seg.s0 == 0 ? 1 : 0;
+#pragma unroll 1
+            for (int c = 0; c < rows; c += 8) {
+                float v[8];
+                tmem_load(my_lanes + c, v);
+                if (whole) {
+                    store_sums(p, sh, seg, v, row, c);
+                } else {
+                    float4 *to = sums_of(p, blockIdx.x * 2 + slot) + c / 4 * kPartRows + row;
+                    __stcg(to, make_float4(v[0], v[1], v[2], v[3]));
+                    __stcg(to + kPartRows, make_float4(v[4], v[5], v[6], v[7]));
+                }
+            }
+            if (!whole && utid == 0)
+                sh.run.cut[slot] = seg;
             tc_fence_before();
-            float v[kSums];
-#pragma unroll
-            for (int c = 0; c < kSums; ++c)
-                v[c] = __uint_as_float(r[c]);
-            if (seg.s0 == 0 && seg.s1 == walk.steps)
-                store_sums(p, sh, seg, v, row, half);
-            else
-                leave_sums<kSums / 4, 32 * kUnpackers>(
-                    p, sh.run, seg, *reinterpret_cast<float(*)[kSums / 4][4]>(v), used(seg), utid);
         }
-        join_cut_tiles<kSums / 4, 32 * kUnpackers>(
-            p, sh.run, utid, ok, used, [&](const Segment &s, const float(&v)[kSums / 4][4]) {
-                store_sums(p, sh, s, *reinterpret_cast<const float(*)[kSums]>(v), row, half);
-            });
+        join_cut_tiles<32 * kUnpackers>(p, sh.run, utid, ok, [&](const Segment &s, int from, int to) {
+            const int rows = s.m1 - s.m0;
+#pragma unroll 1
+            for (int c = 0; c < rows; c += 8) {
+                float v[8] = {};
+                for (int b = from; b <= to; ++b) {
+                    const float4 *theirs = sums_of(p, b * 2 + (b == from ? 1 : 0)) + c / 4 * kPartRows + row;
+                    const float4 x = __ldcg(theirs), y = __ldcg(theirs + kPartRows);
+                    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+                    v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+                }
+                store_sums(p, sh, s, v, row, c);
+            }
+        });
     }
     tc_fence_before();
     __syncthreads();

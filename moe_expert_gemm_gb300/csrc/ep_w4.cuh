@@ -292,32 +292,12 @@ __device__ __forceinline__ void store_tile(const W4Params &p, const Segment &s,
         }
 }
 
-// A cut tile: leaves a thread's sums, the first `used` of its NT fours, in the block's slot
-// for the tile its run begins inside (0) or ends inside (1).
-template <int NT, int THREADS>
-__device__ __forceinline__ void leave_sums(const W4Params &p, RunInfo &sh, const Segment &s,
-                                           const float (&acc)[NT][4], int used, int tid)
-{
-    const int slot = s.s0 == 0 ? 1 : 0;
-    float4 *mine = reinterpret_cast<float4 *>(p.workspace + kMaxBlocks * 16) +
-                   (blockIdx.x * 2 + slot) * static_cast<int64_t>(THREADS * NT);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-        if (nt < used)
-            __stcg(mine + nt * THREADS + tid,
-                   make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]));
-    if (tid == 0)
-        sh.cut[slot] = s;
-}
-
-// The block's cut tiles, after all else: of a tile's blocks the last one to come here adds
-// the sums of all of them, in block order. The THREADS threads that hold sums meet at named
-// barrier 1 (which orders the block's sums before the release of one thread). A warp that
-// gave up (`ok` false) takes all with it. used(segment): as given to leave_sums;
-// store(segment, sums): what is done with a whole tile's.
-template <int NT, int THREADS, typename Used, typename Store>
-__device__ __forceinline__ void join_cut_tiles(const W4Params &p, RunInfo &sh, int tid, bool ok,
-                                               Used used, Store store)
+// The block's cut tiles, after all else: of a tile's blocks the last one to come here calls
+// add(segment, c0, c1), which is to add what blocks c0 .. c1 left and to store it. The THREADS
+// threads that left sums meet at named barrier 1 (which orders the block's sums before the
+// release of one thread). A warp that gave up (`ok` false) takes all with it.
+template <int THREADS, typename Add>
+__device__ __forceinline__ void join_cut_tiles(const W4Params &p, RunInfo &sh, int tid, bool ok, Add add)
 {
     if (sh.runs.piece > 1)
         return;  // runs of whole tiles
@@ -337,28 +317,11 @@ __device__ __forceinline__ void join_cut_tiles(const W4Params &p, RunInfo &sh, i
         sh.last[slot] = last;
     }
     named_bar_sync(1, THREADS);
-    for (int slot = 0; slot < 2; ++slot) {
-        if (!sh.last[slot])
-            continue;
-        const Segment s = sh.cut[slot];
-        const int fours = used(s);
-        const int c0 = sh.runs.owner(s.first), c1 = sh.runs.owner(s.first + p.steps - 1);
-        float acc[NT][4] = {};
-        for (int c = c0; c <= c1; ++c) {
-            const float4 *theirs = reinterpret_cast<const float4 *>(p.workspace + kMaxBlocks * 16) +
-                                   (c * 2 + (c == c0 ? 1 : 0)) * static_cast<int64_t>(THREADS * NT);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                if (nt < fours) {
-                    const float4 v = __ldcg(theirs + nt * THREADS + tid);
-                    acc[nt][0] += v.x;
-                    acc[nt][1] += v.y;
-                    acc[nt][2] += v.z;
-                    acc[nt][3] += v.w;
-                }
+    for (int slot = 0; slot < 2; ++slot)
+        if (sh.last[slot]) {
+            const Segment s = sh.cut[slot];
+            add(s, sh.runs.owner(s.first), sh.runs.owner(s.first + p.steps - 1));
         }
-        store(s, acc);
-    }
 }
 
 }  // namespace w4

@@ -98,13 +98,19 @@ struct Scales {
     {
         alignas(16) uint32_t out[GS / 2];
         if constexpr (E2M1) {
+            // 2^(e - 1), the factor of a code as unpack_e2m1 forms it, or apart from the
+            // codes 2^(e - 127) (bf16: the exponent bits; 2^-127 is subnormal)
+            if (!apart) {  // two at a time: e + 126 has eight bits
 #pragma unroll
-            for (int i = 0; i < GS; ++i) {
-                const uint32_t e = scale.w[i / 4] >> (8 * (i % 4)) & 255;
-                // 2^(e - 1), the factor of a code as unpack_e2m1 forms it, or apart from
-                // the codes 2^(e - 127) (bf16: the exponent bits; 2^-127 is subnormal)
-                const uint32_t h = !apart ? (e + 126) << 7 : e == 255 ? 0x7FC0u : e == 0 ? 0x0040u : e << 7;
-                out[i / 2] = i % 2 ? out[i / 2] | h << 16 : h;
+                for (int i = 0; i < GS / 2; ++i)
+                    out[i] = (__byte_perm(scale.w[i / 2], 0, i % 2 ? 0x4342 : 0x4140) + 0x007E007Eu) << 7;
+            } else {
+#pragma unroll
+                for (int i = 0; i < GS; ++i) {
+                    const uint32_t e = scale.w[i / 4] >> (8 * (i % 4)) & 255;
+                    const uint32_t h = e == 255 ? 0x7FC0u : e == 0 ? 0x0040u : e << 7;
+                    out[i / 2] = i % 2 ? out[i / 2] | h << 16 : h;
+                }
             }
             copy_words<GS / 2>(to_scale, out);
         } else {
