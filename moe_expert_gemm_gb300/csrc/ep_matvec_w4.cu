@@ -435,14 +435,24 @@ static cudaError_t launch_nt(const CUtensorMap &tw, const W4Params &p, int num_s
 
 cudaError_t launch_matvec_w4(const CUtensorMap &tw, const W4Params &p, int num_sms, cudaStream_t s)
 {
-    // rows a pass serves: what an expert is expected to get, at most what it can get
+    // Rows a pass serves, by the rows that an expert is expected to get (some get more and
+    // take another pass). Measured with 32 experts of 7168 x 2048, us a call, e2m1 / int:
+    //   rows  4:   8 a pass  74 /  57, 16 a pass  80 /  70
+    //   rows  6:   8 a pass  83 /  65, 16 a pass  84 /  72
+    //   rows  8:   8 a pass 107 /  81, 16 a pass  86 /  74
+    //   rows 12:  16 a pass 103 /  89, 64 a pass 102 / 144
+    //   rows 16:  16 a pass 129 / 111, 64 a pass 103 / 144
+    //   rows 24:  16 a pass 178 / 152, 64 a pass 107 / 148
+    //   rows 64:  16 a pass 387 / 329, 64 a pass 167 / 230
+    // (64 a pass is the form of ep_matvec_w4_wide.cu, which takes integer weights as two
+    // numbers each.) A batch that fits one pass of the smaller form whole stays there.
     const int64_t tokens = static_cast<int64_t>(p.T) * p.n_ranks;
     int64_t rows = (tokens * p.top_k + static_cast<int64_t>(p.n_ranks) * p.El - 1) /
                    (static_cast<int64_t>(p.n_ranks) * p.El);
     rows = rows < p.max_rows ? rows : p.max_rows;
-    if (rows > 16)
+    if (p.max_rows > 16 && rows > (p.format == EP_W4_E2M1 ? 12 : 23))
         return launch_matvec_w4_wide(tw, p, num_sms, s);
-    if (rows > 8)
+    if (p.max_rows > 8 && rows > 6)
         return p.scale_vec ? launch_nt<2, true>(tw, p, num_sms, s) : launch_nt<2, false>(tw, p, num_sms, s);
     return p.scale_vec ? launch_nt<1, true>(tw, p, num_sms, s) : launch_nt<1, false>(tw, p, num_sms, s);
 }

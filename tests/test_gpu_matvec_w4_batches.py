@@ -20,7 +20,7 @@ def batch(c, rows):
 
 
 @pytest.mark.parametrize("fmt,group", FORMATS)
-@pytest.mark.parametrize("rows", [9, 17])
+@pytest.mark.parametrize("rows", [9, 17, 24])
 @pytest.mark.parametrize("N,K,counts", [
     (130, 384, [20, 33]), (126, 1408, [0, 9, 0, 47]), (514, 2048, [31, 1, 16, 17, 32]),
     (1000, 640, [17, 33, 0, 70]),
@@ -32,7 +32,7 @@ def test_w4_batches(N, K, counts, rows, fmt, group):
         c.check(batch(c, rows).run())
 
 
-@pytest.mark.parametrize("announced", [9, 17])
+@pytest.mark.parametrize("announced", [9, 17, 24])
 @pytest.mark.parametrize("rows", [1, 8, 9, 16, 17, 24, 31, 32, 33, 64, 65, 129])
 def test_w4_batch_row_counts(rows, announced):
     for fmt, group in (("int4z", 64), ("e2m1", 32)):
@@ -42,7 +42,7 @@ def test_w4_batch_row_counts(rows, announced):
         c.check(batch(c, announced).run())
 
 
-@pytest.mark.parametrize("announced", [1, 9, 17])
+@pytest.mark.parametrize("announced", [1, 9, 17, 24])
 def test_w4_many_steps_for_every_block(announced):
     """Rings that turn many times, tiles cut between blocks and whole ones, repeated."""
     counts = [40, 3, 0, 28, 17, 32, 5, 9]
@@ -57,7 +57,7 @@ def test_w4_many_steps_for_every_block(announced):
             np.testing.assert_array_equal(first, c.bits)
 
 
-@pytest.mark.parametrize("announced", [9, 17])
+@pytest.mark.parametrize("announced", [9, 17, 24])
 def test_w4_batches_keep_infinities_in_their_rows(announced):
     x = activations(40, 512, 4)
     x[3, 100], x[33, 511], x[8, 0] = np.inf, np.nan, -np.inf
@@ -71,7 +71,7 @@ def test_w4_batches_keep_infinities_in_their_rows(announced):
         assert (np.abs(out - y)[clean] <= 2.0 ** -7.9 * np.abs(y[clean]) + size[clean]).all()
 
 
-@pytest.mark.parametrize("announced", [9, 17])
+@pytest.mark.parametrize("announced", [9, 17, 24])
 def test_w4_batches_skip_bad_gather_indices(announced):
     T, K, N = 20, 320, 72
     c = batch(Call(activations(T, K, 8), [T], weights(1, N, K, "int4z", 32, 9), "int4z", 32),
