@@ -578,7 +578,8 @@ int ep_combine_backward(const ep_config *cfg, const ep_combine_backward_args *ar
  *                   EP_W4_E2M1: codes are e2m1 numbers (0, .5, 1, 1.5, 2, 3, 4, 6 and
  *                               their negatives from code 8 on); w_scales
  *                               [E_l][N][K/32] bytes, scale = 2^(byte - 127) (255: NaN);
- *                               group_size 32, w_zeros NULL
+ *                               group_size 32, w_zeros NULL. A weight of 2^128 or more
+ *                               may count as infinite
  *   expert_offsets  [E_l+1] the plan (ep_plan)
  *   max_rows        rows allocated for A (or gather_idx) and C
  *   local_activation  EP_ACT_NONE: C = bf16(y). EP_ACT_SWIGLU: W holds the N/2 gate rows,
@@ -591,9 +592,12 @@ int ep_combine_backward(const ep_config *cfg, const ep_combine_backward_args *ar
  *                   for the next. Calls that may run at the same time need one each.
  *   status          EP_STATUS_BOUNDS for a gather index outside the token tables (that
  *                   row of C is not written) or expert offsets that do not rise from
- *                   >= 0 to <= max_rows (nothing is written); EP_STATUS_TIMEOUT if a bounded wait inside the kernel ran out
+ *                   >= 0 to <= max_rows (nothing is written); EP_STATUS_TIMEOUT if a
+ *                   bounded wait inside the kernel ran out
  * Sums over k are taken in a fixed order: a call's result depends on its inputs alone
  * (and on the GPU's number of SMs), not on timing.
+ * How the sums over k are cut goes by the rows that cfg lets an expert expect
+ * (n_ranks * num_tokens * top_k over all experts) and by max_rows; any counts are served.
  */
 #define EP_W4_INT 0
 #define EP_W4_E2M1 1

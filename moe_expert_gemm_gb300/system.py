@@ -12,13 +12,16 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (EP_ACT_SWIGLU, EP_BF16, EP_FP8_1D2D, ep_combine_args, ep_combine_reduce, ep_config,
-               ep_dispatch_args, ep_dispatch_gather, ep_plan, ep_plan_out, ep_plan_sizes,
-               ep_scatter_args, ep_scatter_send, ep_send_args, ep_swiglu, ep_swiglu_args,
-               grouped_gemm_combine_send, ptr)
+from . import (EP_ACT_NONE, EP_ACT_SWIGLU, EP_BF16, EP_FP8_1D2D, EP_LOGITS_BF16, EP_LOGITS_F32,
+               EP_SCORE_SOFTMAX, ep_combine_args, ep_combine_backward, ep_combine_backward_args,
+               ep_combine_reduce, ep_config, ep_dispatch_args, ep_dispatch_gather, ep_matvec_w4,
+               ep_matvec_w4_sizes, ep_plan, ep_plan_out, ep_plan_sizes, ep_route, ep_route_args,
+               ep_route_backward, ep_route_backward_args, ep_scatter_args, ep_scatter_send,
+               ep_send_args, ep_swiglu, ep_swiglu_args, ep_w4_args, grouped_gemm_combine_send, ptr)
+from .w4 import W4Weights
 
 SENTINEL_BYTE = 0xFF  # received bf16 0xFFFF is a NaN: an unwritten slot cannot pass
-STATUS_PLAN, STATUS_SEND, STATUS_COMBINE = 0, 1, 2
+STATUS_PLAN, STATUS_SEND, STATUS_COMBINE, STATUS_ROUTE, STATUS_W4 = 0, 1, 2, 3, 4
 
 
 class EpSystem:
@@ -50,6 +53,8 @@ class EpSystem:
         self.ops: list[dict | None] = [None] * R
         self.gates: list[torch.Tensor | None] = [None] * R
         self.out: list[torch.Tensor | None] = [None] * R
+        self.routes: list[dict | None] = [None] * R
+        self.layer_w4: list[dict | None] = [None] * R
 
     # ------------------------------------------------------------- set-up
     def cfg(self, rank: int) -> ep_config:
@@ -249,6 +254,98 @@ class EpSystem:
         mark(2)
         self.send(rank, epoch, stream, p3_control=p3_control, overlap=overlap)
         mark(3)
+
+    # ------------------------------------------------- routing and its gradient
+    def route(self, rank: int, logits: torch.Tensor, score: int = EP_SCORE_SOFTMAX, bias=None,
+              n_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
+              renormalize: bool = True, scale: float = 1.0, stream=None):
+        """The rank's routing and gates on the device, from its router's logits [T][E]
+        (fp32 or bf16, rows any stride apart): in place of ``set_routing`` and ``set_gates``.
+        Every rank's routing stands before any rank's ``plan``."""
+        E = self.R * self.El
+        assert tuple(logits.shape) == (self.T, E) and logits.stride(1) == 1
+        if self.topk is None:
+            self.topk = torch.zeros((self.R, self.T, self.k), dtype=torch.int32,
+                                    device=self.device)
+        if self.gates[rank] is None:
+            self.gates[rank] = torch.zeros((self.T, self.k), device=self.device)
+        if self.out[rank] is None:
+            self.out[rank] = torch.zeros((self.T, self.N), dtype=torch.bfloat16,
+                                         device=self.device)
+        a = ep_route_args(logits=ptr(logits), logits_stride=logits.stride(0),
+                          logits_dtype=self._logits_dtype(logits), score=score, bias=ptr(bias),
+                          n_groups=n_groups, topk_groups=topk_groups, group_top=group_top,
+                          renormalize=int(renormalize), scale=scale,
+                          topk_ids=ptr(self.topk[rank]), gates=ptr(self.gates[rank]))
+        ep_route(self.cfg(rank), a, stream)
+        self.routes[rank] = dict(logits=logits, score=score, renormalize=int(renormalize),
+                                 scale=scale)
+
+    @staticmethod
+    def _logits_dtype(logits: torch.Tensor) -> int:
+        return {torch.float32: EP_LOGITS_F32, torch.bfloat16: EP_LOGITS_BF16}[logits.dtype]
+
+    def combine_backward(self, rank: int, dout: torch.Tensor, dgates=None, drows=None,
+                         stream=None):
+        """Gradients of ``combine``'s sum, of the gates ([T][k] fp32) and of the rows
+        ([T][k][N] bf16), each into a tensor that is given."""
+        a = ep_combine_backward_args(recv_buf=ptr(self.recv[rank]), gates=ptr(self.gates[rank]),
+                                     dout=ptr(dout), dgates=ptr(dgates), drows=ptr(drows))
+        ep_combine_backward(self.cfg(rank), a, stream)
+
+    def route_backward(self, rank: int, dgates: torch.Tensor, dlogits: torch.Tensor, stream=None):
+        """Gradient of the logits of ``route``'s last call, which must still stand, from the
+        gates'; into ``dlogits`` (their type and shape, rows any stride apart)."""
+        r = self.routes[rank]
+        a = ep_route_backward_args(logits=ptr(r["logits"]), logits_stride=r["logits"].stride(0),
+                                   logits_dtype=self._logits_dtype(r["logits"]),
+                                   score=r["score"], renormalize=r["renormalize"],
+                                   scale=r["scale"], topk_ids=ptr(self.topk[rank]),
+                                   dgates=ptr(dgates), dlogits=ptr(dlogits),
+                                   dlogits_stride=dlogits.stride(0),
+                                   status=self.status.data_ptr() + 4 * STATUS_ROUTE)
+        ep_route_backward(self.cfg(rank), a, stream)
+
+    # --------------------------------------------- a layer of few tokens, 4 bits
+    def set_layer_w4(self, rank: int, X: torch.Tensor, W1: W4Weights, W2: W4Weights):
+        """Operands of a MoE layer on 4-bit weights: the rank's tokens X
+        [max_tokens][H] bf16, its experts' up/gate weights W1 ([E_l][2I] rows of H, gate rows
+        first) and down-projection weights W2 ([E_l][H] rows of I), with H = N and I = K.
+        Allocates the layer's buffers and its two workspaces."""
+        assert self.dtype == "bf16" and tuple(X.shape) == (self.max_tokens, self.N)
+        dev, rows = self.device, max(ep_plan_sizes(self.cfg(rank)), 1)
+        self.layer_w4[rank] = dict(
+            X=X, W1=W1, W2=W2,
+            A=torch.zeros((rows, self.K), dtype=torch.bfloat16, device=dev),
+            C=torch.zeros((rows, self.N), dtype=torch.bfloat16, device=dev),
+            workspaces=[torch.zeros(ep_matvec_w4_sizes(c), dtype=torch.uint8, device=dev)
+                        for c in (self.cfg_up(rank), self.cfg(rank))])
+
+    def _w4_args(self, rank: int, w: W4Weights, C, workspace) -> ep_w4_args:
+        p = self.plans[rank]
+        return ep_w4_args(W=ptr(w.codes), w_scales=ptr(w.scales), w_zeros=ptr(w.zeros),
+                          w_format=w.w_format, group_size=w.group_size,
+                          expert_offsets=ptr(p["expert_offsets"]),
+                          max_rows=min(int(C.shape[0]), p["capacity"]), C=ptr(C),
+                          workspace=ptr(workspace), workspace_bytes=workspace.numel(),
+                          status=self.status.data_ptr() + 4 * STATUS_W4)
+
+    def layer_forward_w4(self, rank: int, epoch: int, stream=None):
+        """The layer's up/gate product with the activation in its epilogue (rows read where
+        the plan finds them, no dispatch), the down-projection, and the send of producer
+        ``rank`` (every ``layer_w4[r]["X"]`` must hold rank r's tokens)."""
+        L = self.layer_w4[rank]
+        up = self._w4_args(rank, L["W1"], L["A"], L["workspaces"][0])
+        for r in range(self.R):
+            up.x_ptrs[r] = ptr(self.layer_w4[r]["X"])
+        up.gather_idx = ptr(self.plans[rank]["gather_idx"])
+        up.local_activation = EP_ACT_SWIGLU
+        ep_matvec_w4(self.cfg_up(rank), up, stream)
+        down = self._w4_args(rank, L["W2"], L["C"], L["workspaces"][1])
+        down.A = ptr(L["A"])
+        down.local_activation = EP_ACT_NONE
+        ep_matvec_w4(self.cfg(rank), down, stream)
+        ep_scatter_send(self.cfg(rank), self.scatter_args(rank, epoch, L["C"]), stream)
 
     def send_traced(self, rank: int, epoch: int, records: int = 64, stream=None):
         """One send with per-tile timestamps; returns the decoded trace."""

@@ -1,4 +1,4 @@
-"""The 4-bit products with batch sizes that make a pass over the weights serve 16 and 32
+"""The 4-bit products with batch sizes that make a pass over the weights serve 16 and 64
 rows (the choice goes by the configuration's tokens), against the same 64-bit reference
 and bounds as the single-token form; ranges of rows below, at and past a pass."""
 
