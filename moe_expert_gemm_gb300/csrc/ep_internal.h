@@ -190,7 +190,9 @@ struct W4Params {
     int n_ranks, El, top_k, T, K, N;
     int format, group, swiglu;
     int steps;      // of 256 k
-    int scale_vec;  // a step's scales (and zero points) of a row are one aligned piece
+    int scale_vec;  // a step's scales (and zero points) of a row are one aligned piece; else
+                    // they are loaded one by one (11 tokens, 32 experts of 4096 x 2048, integer
+                    // codes in groups of 32: 32 us a call with pieces, 53 one by one)
     int64_t max_rows;
     const uint8_t *A;
     const uint8_t *x[EP_MAX_RANKS];

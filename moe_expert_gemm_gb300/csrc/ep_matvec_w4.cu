@@ -21,6 +21,10 @@
 //    of stages; three warps stage activations and scales; eight consumer warps own 16
 //    weight rows each, 8 of the tile's first half and 8 of its second: with SwiGLU the gate
 //    and the up row of the same output meet in one thread.
+//  * Measured: one token, 8 experts of 4096 x 7168 (integer codes, SwiGLU), 32 us a call for
+//    121 MB of codes and scales, 3.8 TB/s; 8 of 4096 x 1536 (e2m1) 11.9 us, of which the
+//    host's call is 6.5. Eight consumer warps take 290 instructions each a step of 16 KB:
+//    with consumers that only wait the first takes 26 us.
 #include <type_traits>
 
 #include "ep_w4.cuh"

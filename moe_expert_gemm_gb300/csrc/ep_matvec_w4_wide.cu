@@ -23,6 +23,9 @@
 //    have a ring each, so that nobody waits for more than what it reads.
 //  * What bounds it is the issue of instructions, 17 for a word of eight codes before all
 //    else; hence straight code for the staging warps, which have a row's piece in ten.
+//  * Measured: 128 tokens, 8 of 32 experts, 7168 x 2048 in e2m1: 110 us a call for 267 MB,
+//    2.4 TB/s, 270 TFLOP/s, the schedulers and the integer pipe 57 % busy; 92 us with codes
+//    that are not unpacked. The warp-wide matrix instructions took 167 us.
 #include "ep_w4.cuh"
 #include "ep_w4_scales.cuh"
 
@@ -76,7 +79,8 @@ __device__ __forceinline__ float4 *sums_of(const W4Params &p, int slot)
 }
 
 // mbar_wait for the many warps of this kernel: a waiting one is suspended for up to 10 us at
-// a time, as the polls of 28 warps an SM would take the unpacking ones' issue slots.
+// a time, as the polls of 20 warps an SM would take the unpacking ones' issue slots (128
+// tokens as above: 110 us, with waits that poll at the hardware's own intervals 118).
 __device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, uint64_t timeout_ns,
                                           volatile int *abort)
 {

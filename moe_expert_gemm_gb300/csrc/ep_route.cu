@@ -21,6 +21,14 @@
 //    cannot decide (groups closer than its error, NaN, too few unmasked experts, more than
 //    32 candidates) the token is done over by route_token.
 //  * route_token_kernel: everything else, by scanning shared memory.
+// The gradient likewise: a warp to a token with its values in registers up to 256 experts,
+// past that in shared memory.
+// Measured, us for 65536 tokens: 8 or 16 experts, bf16, 7 a thread to a token (the host's
+// time of a call), 21 a warp to a token; 32 / 256 experts 24 / 30 a warp to a token, 46 / 74
+// by scanning; 256 experts in 8 groups by sigmoid and bias 46 and 155 (67 MB of logits take
+// 10: 660 instructions a token bound it, of them a quarter the groups' two best, a third
+// the candidates' exact values and order). Gradient, softmax of 64 / 256 experts: 13 / 25 in
+// registers (256: 80 % of the copy rate), 29 / 46 in shared memory.
 #include <cuda_bf16.h>
 
 #include <cfloat>

@@ -31,9 +31,12 @@ struct Segment {
 
 // How the steps are cut into the blocks' runs. A tile's steps are kept together as long
 // as that costs less than the joining of cut tiles, which takes about as long as
-// kJoinSteps steps (1-token down projection of 8 experts, 4096 x 1536 each: 256 whole
-// tiles on 256 blocks).
-constexpr int kJoinSteps = 3;
+// kJoinSteps steps. Measured, whole tiles against cut ones (steps of the longest run):
+//   one token, 8 experts of 4096 x 1536:      11.9 us (6)  against 14.5 (5.1)
+//   11 tokens, 32 experts of 4096 x 2048:     29.9 us (32) against 32.3 (27)
+//   one token, 8 experts of 4096 x 7168:      31.7 us (56) against 32.8 (47)
+//   5 tokens, one matrix of 4096 x 14336:     60.8 us (56) against 17.3 (5.9)
+constexpr int kJoinSteps = 9;
 
 struct Runs {
     int per, rest;  // pieces of every run; the first `rest` runs have one more
