@@ -388,16 +388,27 @@ __global__ void __launch_bounds__(kThreads, 2)
     join_cut_tiles<32 * kConsumers>(p, sh.run, ctid, ok, [&](const Segment &s, int from, int to) {
         const int nts = (s.m1 - s.m0 + 7) / 8;
         float acc[NT][4] = {};
-        for (int b = from; b <= to; ++b) {
-            const float4 *theirs = sums + (b * 2 + (b == from ? 1 : 0)) * kSlot + ctid;
+        // (four blocks' sums under way at once: a tile of a long K has ten and more)
+        constexpr int kAhead = 4;
+        for (int b0 = from; b0 <= to; b0 += kAhead) {
+            float4 v[kAhead][NT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                if (nt < nts) {
-                    const float4 v = __ldcg(theirs + nt * 32 * kConsumers);
-                    acc[nt][0] += v.x;
-                    acc[nt][1] += v.y;
-                    acc[nt][2] += v.z;
-                    acc[nt][3] += v.w;
+            for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int b = b0 + i;
+                    v[i][nt] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (b <= to && nt < nts)
+                        v[i][nt] = __ldcg(sums + (b * 2 + (b == from ? 1 : 0)) * kSlot + ctid + nt * 32 * kConsumers);
+                }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    acc[nt][0] += v[i][nt].x;
+                    acc[nt][1] += v[i][nt].y;
+                    acc[nt][2] += v[i][nt].z;
+                    acc[nt][3] += v[i][nt].w;
                 }
         }
         store_tile<NT>(p, s, acc, row, q, sh.run.skips);

@@ -561,11 +561,24 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll 1
             for (int c = 0; c < rows; c += 8) {
                 float v[8] = {};
-                for (int b = from; b <= to; ++b) {
-                    const float4 *theirs = sums_of(p, b * 2 + (b == from ? 1 : 0)) + c / 4 * kPartRows + row;
-                    const float4 x = __ldcg(theirs), y = __ldcg(theirs + kPartRows);
-                    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-                    v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+                constexpr int kAhead = 4;  // blocks' sums under way at once
+                for (int b0 = from; b0 <= to; b0 += kAhead) {
+                    float4 x[kAhead], y[kAhead];
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) {
+                        const int b = b0 + i;
+                        x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (b <= to) {
+                            const float4 *theirs =
+                                sums_of(p, b * 2 + (b == from ? 1 : 0)) + c / 4 * kPartRows + row;
+                            x[i] = __ldcg(theirs), y[i] = __ldcg(theirs + kPartRows);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) {
+                        v[0] += x[i].x, v[1] += x[i].y, v[2] += x[i].z, v[3] += x[i].w;
+                        v[4] += y[i].x, v[5] += y[i].y, v[6] += y[i].z, v[7] += y[i].w;
+                    }
                 }
                 store_sums(p, sh, s, v, row, c);
             }
