@@ -191,8 +191,8 @@ struct W4Params {
     int format, group, swiglu;
     int steps;      // of 256 k
     int scale_vec;  // a step's scales (and zero points) of a row are one aligned piece; else
-                    // they are loaded one by one (11 tokens, 32 experts of 4096 x 2048, integer
-                    // codes in groups of 32: 32 us a call with pieces, 53 one by one)
+                    // they are put together from words (8 tokens, 8 of 32 experts, 7168 x 2048,
+                    // integer codes in groups of 32: 49 us a call; 7168 x 2016: 68)
     int64_t max_rows;
     const uint8_t *A;
     const uint8_t *x[EP_MAX_RANKS];

@@ -20,7 +20,8 @@ __device__ __forceinline__ void copy_words(void *dst, const void *src)
 }
 
 // GS bytes or halves from global memory as they lie there: one aligned load, or (VEC
-// false) one by one, the ones past `have` left out.
+// false) by words of which each holds at least one of the `have` that exist; what stands
+// past those is anything.
 template <int BYTES, bool VEC>
 struct Piece {
     static constexpr int kWords = (BYTES + 3) / 4;
@@ -38,15 +39,20 @@ struct Piece {
             w[0] = __ldg(reinterpret_cast<const uint32_t *>(from));
         else if constexpr (VEC)
             w[0] = __ldg(reinterpret_cast<const unsigned short *>(from));
-        else {
-            constexpr int kPer = 4 / sizeof(T);
+        else {  // the aligned words that hold some of it, shifted into place
+            const uint64_t at = reinterpret_cast<uint64_t>(from);
+            const uint32_t *word = reinterpret_cast<const uint32_t *>(at & ~3ull);
+            const int skip = static_cast<int>(at & 3), end = skip + static_cast<int>(sizeof(T)) * have;
+            uint32_t in[kWords + 1];
+#pragma unroll
+            for (int i = 0; i <= kWords; ++i) {
+                in[i] = 0;
+                if (4 * i < end && (i < kWords || skip > 0))
+                    in[i] = __ldg(word + i);
+            }
 #pragma unroll
             for (int i = 0; i < kWords; ++i)
-                w[i] = 0;
-#pragma unroll
-            for (int i = 0; i < BYTES / static_cast<int>(sizeof(T)); ++i)
-                if (i < have)
-                    w[i / kPer] |= static_cast<uint32_t>(__ldg(from + i)) << (8 * sizeof(T) * (i % kPer));
+                w[i] = __funnelshift_r(in[i], in[i + 1], 8 * skip);
         }
     }
 
@@ -71,6 +77,11 @@ struct Scales {
     {
         if constexpr (E2M1) {
             scale.load(static_cast<const uint8_t *>(p.scales) + at, have);
+            if (!VEC) {  // (none past the last group, as large() looks at all)
+#pragma unroll
+                for (int i = 0; i < scale.kWords; ++i)
+                    scale.w[i] &= have >= 4 * i + 4 ? ~0u : have <= 4 * i ? 0u : ~(~0u << 8 * (have - 4 * i));
+            }
         } else {
             scale.load(static_cast<const unsigned short *>(p.scales) + at, have);
             if (p.zeros)
