@@ -78,9 +78,8 @@ __device__ __forceinline__ float4 *sums_of(const W4Params &p, int slot)
            static_cast<int64_t>(slot) * (kRows / 4 * kPartRows);
 }
 
-// mbar_wait for the many warps of this kernel: a waiting one is suspended for up to 10 us at
-// a time, as the polls of 20 warps an SM would take the unpacking ones' issue slots (128
-// tokens as above: 110 us, with waits that poll at the hardware's own intervals 118).
+// mbar_wait with less code at each of the many waits of this kernel and a longer suspension
+// (128 tokens as above: 110 us, with mbar_wait 118).
 __device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, uint64_t timeout_ns,
                                           volatile int *abort)
 {
