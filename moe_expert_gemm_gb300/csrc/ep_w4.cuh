@@ -71,76 +71,76 @@ struct RunInfo {
 template <int CHUNK>
 __device__ __forceinline__ void plan_run(const W4Params &p, RunInfo &sh, int tiles, int lane)
 {
-            // units of every expert (chunks of its rows x column tiles), their sums, and from
-            // them where this block's run begins
-            constexpr int kSets = EP_MAX_LOCAL_EXPERTS / 32;
-            int lo[kSets], hi[kSets], upto[kSets];
-    #pragma unroll
-            for (int i = 0; i < kSets; ++i) {
-                const int e = 32 * i + lane;
-                lo[i] = e < p.El ? __ldg(p.expert_offsets + e) : 0;
-                hi[i] = e < p.El ? __ldg(p.expert_offsets + e + 1) : 0;
-            }
-            int units = 0;
-            bool bad = false;
-    #pragma unroll
-            for (int i = 0; i < kSets; ++i) {
-                upto[i] = 0;
-                if (32 * i >= p.El)
-                    break;
-                bad |= lo[i] < 0 || hi[i] < lo[i] || hi[i] > p.max_rows;
-                int sum = static_cast<int>((static_cast<unsigned>(hi[i] - lo[i]) + CHUNK - 1) / (CHUNK)) * tiles;
-    #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, sum, o);
-                    if (lane >= o)
-                        sum += v;
-                }
-                upto[i] = units + sum;
-                units = __shfl_sync(0xffffffffu, upto[i], 31);
-            }
-            bad = __any_sync(0xffffffffu, bad);
-            const int grid = static_cast<int>(gridDim.x), block = static_cast<int>(blockIdx.x);
-            const int total = units * p.steps;
-            const bool whole = (units + grid - 1) / grid * p.steps <= (total + grid - 1) / grid + kJoinSteps;
-            Runs runs;
-            runs.piece = whole ? p.steps : 1;
-            runs.per = (whole ? units : total) / grid;
-            runs.rest = (whole ? units : total) - runs.per * grid;
-            const int at = (block * runs.per + (block < runs.rest ? block : runs.rest)) * runs.piece;
-            const int todo = (runs.per + (block < runs.rest)) * runs.piece;
-            const int unit = at / p.steps;
-    #pragma unroll
-            for (int i = 0; i < kSets; ++i) {
-                if (32 * i >= p.El)
-                    break;
-                const int e = 32 * i + lane;
-                if (e < p.El) {
-                    sh.offsets[e] = lo[i];
-                    if (e == p.El - 1)
-                        sh.offsets[p.El] = hi[i];
-                }
-            }
-            if (lane == 0) {
-                sh.bad = bad;
-                sh.runs = runs;
-                if (bad && block == 0)
-                    atomicOr(p.status, EP_STATUS_BOUNDS);
-            }
-            // the expert whose units hold `unit`
-            int base = 0;
-    #pragma unroll
-            for (int i = 0; i < kSets; ++i) {
-                if (32 * i >= p.El)
-                    break;
-                const int up = __shfl_up_sync(0xffffffffu, upto[i], 1);
-                const int from = lane == 0 ? base : up;
-                if (from <= unit && unit < upto[i])
-                    sh.start = Start{32 * i + lane, unit - from, at - unit * p.steps, unit * p.steps, todo};
-                base = __shfl_sync(0xffffffffu, upto[i], 31);
-            }
-            if (lane == 0 && unit >= units)
-                sh.start.todo = 0;
+    // units of every expert (chunks of its rows x column tiles), their sums, and from
+    // them where this block's run begins
+    constexpr int kSets = EP_MAX_LOCAL_EXPERTS / 32;
+    int lo[kSets], hi[kSets], upto[kSets];
+#pragma unroll
+    for (int i = 0; i < kSets; ++i) {
+        const int e = 32 * i + lane;
+        lo[i] = e < p.El ? __ldg(p.expert_offsets + e) : 0;
+        hi[i] = e < p.El ? __ldg(p.expert_offsets + e + 1) : 0;
+    }
+    int units = 0;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kSets; ++i) {
+        upto[i] = 0;
+        if (32 * i >= p.El)
+            break;
+        bad |= lo[i] < 0 || hi[i] < lo[i] || hi[i] > p.max_rows;
+        int sum = static_cast<int>((static_cast<unsigned>(hi[i] - lo[i]) + CHUNK - 1) / CHUNK) * tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o)
+                sum += v;
+        }
+        upto[i] = units + sum;
+        units = __shfl_sync(0xffffffffu, upto[i], 31);
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    const int grid = static_cast<int>(gridDim.x), block = static_cast<int>(blockIdx.x);
+    const int total = units * p.steps;
+    const bool whole = (units + grid - 1) / grid * p.steps <= (total + grid - 1) / grid + kJoinSteps;
+    Runs runs;
+    runs.piece = whole ? p.steps : 1;
+    runs.per = (whole ? units : total) / grid;
+    runs.rest = (whole ? units : total) - runs.per * grid;
+    const int at = (block * runs.per + (block < runs.rest ? block : runs.rest)) * runs.piece;
+    const int todo = (runs.per + (block < runs.rest)) * runs.piece;
+    const int unit = at / p.steps;
+#pragma unroll
+    for (int i = 0; i < kSets; ++i) {
+        if (32 * i >= p.El)
+            break;
+        const int e = 32 * i + lane;
+        if (e < p.El) {
+            sh.offsets[e] = lo[i];
+            if (e == p.El - 1)
+                sh.offsets[p.El] = hi[i];
+        }
+    }
+    if (lane == 0) {
+        sh.bad = bad;
+        sh.runs = runs;
+        if (bad && block == 0)
+            atomicOr(p.status, EP_STATUS_BOUNDS);
+    }
+    // the expert whose units hold `unit`
+    int base = 0;
+#pragma unroll
+    for (int i = 0; i < kSets; ++i) {
+        if (32 * i >= p.El)
+            break;
+        const int up = __shfl_up_sync(0xffffffffu, upto[i], 1);
+        const int from = lane == 0 ? base : up;
+        if (from <= unit && unit < upto[i])
+            sh.start = Start{32 * i + lane, unit - from, at - unit * p.steps, unit * p.steps, todo};
+        base = __shfl_sync(0xffffffffu, upto[i], 31);
+    }
+    if (lane == 0 && unit >= units)
+        sh.start.todo = 0;
     if (lane == 0) {
         sh.skips = 0;
         sh.cut[0].e = sh.cut[1].e = -1;
