@@ -33,15 +33,17 @@ class W4Weights:
 
 def quantize_w4(w: torch.Tensor, w_format: int = EP_W4_INT, group_size: int = 32,
                 zeros: bool = True) -> W4Weights:
-    """The nearest codes for ``w`` [..., K]. EP_W4_INT: a group's scale is its range over 15
-    with a zero point each (``zeros``), or its largest magnitude over 7 around code 8;
-    EP_W4_E2M1: the smallest power of two at which no code saturates."""
+    """The nearest codes for ``w`` [..., K], whatever its strides; the results are contiguous.
+    EP_W4_INT: a group's scale is its range over 15 with a zero point each (``zeros``), or its
+    largest magnitude over 7 around code 8; EP_W4_E2M1: the smallest power of two at which no
+    code saturates."""
     K = w.shape[-1]
     if w_format not in (EP_W4_INT, EP_W4_E2M1):
         raise ValueError(f"w_format {w_format}")
     if group_size not in ((32,) if w_format == EP_W4_E2M1 else (32, 64, 128)) or K % group_size:
         raise ValueError(f"group_size {group_size} for K = {K}")
-    g = w.float().unflatten(-1, (K // group_size, group_size))
+    # (contiguous: elementwise results keep their input's strides, and the kernels go by address)
+    g = w.contiguous().float().unflatten(-1, (K // group_size, group_size))
     zero = None
     if w_format == EP_W4_E2M1:
         top = g.abs().amax(-1)
