@@ -24,6 +24,33 @@ SENTINEL_BYTE = 0xFF  # received bf16 0xFFFF is a NaN: an unwritten slot cannot 
 STATUS_PLAN, STATUS_SEND, STATUS_COMBINE, STATUS_ROUTE, STATUS_W4 = 0, 1, 2, 3, 4
 
 
+def _check_flat(name: str, t: torch.Tensor, count: int, dtype: torch.dtype, device: torch.device):
+    """The kernels go by address and size: a tensor of another type, size or device, or with
+    gaps or repeats in memory, would be read as something else or past its end."""
+    if t.dtype != dtype or t.numel() != count or not t.is_contiguous():
+        raise ValueError(f"{name}: {count} contiguous elements of {dtype} expected, got "
+                         f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()}")
+    if t.device.type != device.type or device.index not in (None, t.device.index):
+        raise ValueError(f"{name}: on {t.device}, expected on {device}")
+
+
+def _check_rows(name: str, t: torch.Tensor, rows: int, cols: int, dtypes, device: torch.device) -> int:
+    """Of a [rows][cols] tensor whose rows may lie any stride apart: that stride, as the calls
+    take it (0: back to back)."""
+    if tuple(t.shape) != (rows, cols) or t.dtype not in dtypes:
+        raise ValueError(f"{name}: [{rows}][{cols}] of {' or '.join(map(str, dtypes))} expected, "
+                         f"got {tuple(t.shape)} of {t.dtype}")
+    if t.device.type != device.type or device.index not in (None, t.device.index):
+        raise ValueError(f"{name}: on {t.device}, expected on {device}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row lie {t.stride(1)} apart")
+    if rows <= 1:
+        return 0  # (a single row's stride says nothing)
+    if t.stride(0) < cols:
+        raise ValueError(f"{name}: rows of {cols} elements lie {t.stride(0)} apart")
+    return t.stride(0)
+
+
 class EpSystem:
     def __init__(self, n_ranks: int, n_local_experts: int, top_k: int, tokens: int, K: int,
                  N: int, dtype: str = "bf16", device="cuda", max_tokens: int | None = None,
@@ -260,10 +287,12 @@ class EpSystem:
               n_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
               renormalize: bool = True, scale: float = 1.0, stream=None):
         """The rank's routing and gates on the device, from its router's logits [T][E]
-        (fp32 or bf16, rows any stride apart): in place of ``set_routing`` and ``set_gates``.
-        Every rank's routing stands before any rank's ``plan``."""
+        (fp32 or bf16, rows any stride of at least E apart) and an fp32 bias [E]: in place of
+        ``set_routing`` and ``set_gates``. Every rank's routing stands before any rank's ``plan``."""
         E = self.R * self.El
-        assert tuple(logits.shape) == (self.T, E) and logits.stride(1) == 1
+        stride = _check_rows("logits", logits, self.T, E, self._LOGITS, self.device)
+        if bias is not None:
+            _check_flat("bias", bias, E, torch.float32, self.device)
         if self.topk is None:
             self.topk = torch.zeros((self.R, self.T, self.k), dtype=torch.int32,
                                     device=self.device)
@@ -272,18 +301,16 @@ class EpSystem:
         if self.out[rank] is None:
             self.out[rank] = torch.zeros((self.T, self.N), dtype=torch.bfloat16,
                                          device=self.device)
-        a = ep_route_args(logits=ptr(logits), logits_stride=logits.stride(0),
-                          logits_dtype=self._logits_dtype(logits), score=score, bias=ptr(bias),
+        a = ep_route_args(logits=ptr(logits), logits_stride=stride,
+                          logits_dtype=self._LOGITS[logits.dtype], score=score, bias=ptr(bias),
                           n_groups=n_groups, topk_groups=topk_groups, group_top=group_top,
                           renormalize=int(renormalize), scale=scale,
                           topk_ids=ptr(self.topk[rank]), gates=ptr(self.gates[rank]))
         ep_route(self.cfg(rank), a, stream)
-        self.routes[rank] = dict(logits=logits, score=score, renormalize=int(renormalize),
-                                 scale=scale)
+        self.routes[rank] = dict(logits=logits, stride=stride, score=score,
+                                 renormalize=int(renormalize), scale=scale)
 
-    @staticmethod
-    def _logits_dtype(logits: torch.Tensor) -> int:
-        return {torch.float32: EP_LOGITS_F32, torch.bfloat16: EP_LOGITS_BF16}[logits.dtype]
+    _LOGITS = {torch.float32: EP_LOGITS_F32, torch.bfloat16: EP_LOGITS_BF16}
 
     def combine_backward(self, rank: int, dout: torch.Tensor, dgates=None, drows=None,
                          stream=None):
@@ -297,8 +324,8 @@ class EpSystem:
         """Gradient of the logits of ``route``'s last call, which must still stand, from the
         gates'; into ``dlogits`` (their type and shape, rows any stride apart)."""
         r = self.routes[rank]
-        a = ep_route_backward_args(logits=ptr(r["logits"]), logits_stride=r["logits"].stride(0),
-                                   logits_dtype=self._logits_dtype(r["logits"]),
+        a = ep_route_backward_args(logits=ptr(r["logits"]), logits_stride=r["stride"],
+                                   logits_dtype=self._LOGITS[r["logits"].dtype],
                                    score=r["score"], renormalize=r["renormalize"],
                                    scale=r["scale"], topk_ids=ptr(self.topk[rank]),
                                    dgates=ptr(dgates), dlogits=ptr(dlogits),
