@@ -314,22 +314,32 @@ class EpSystem:
 
     def combine_backward(self, rank: int, dout: torch.Tensor, dgates=None, drows=None,
                          stream=None):
-        """Gradients of ``combine``'s sum, of the gates ([T][k] fp32) and of the rows
-        ([T][k][N] bf16), each into a tensor that is given."""
+        """Gradients of ``combine``'s sum for its output's gradient ``dout`` [T][N] bf16, of the
+        gates ([T][k] fp32) and of the rows ([T][k][N] bf16, or the rank's receive buffer),
+        each into a tensor that is given. All of them contiguous."""
+        _check_flat("dout", dout, self.T * self.N, torch.bfloat16, self.device)
+        if dgates is not None:
+            _check_flat("dgates", dgates, self.T * self.k, torch.float32, self.device)
+        if drows is not None and drows is not self.recv[rank]:
+            _check_flat("drows", drows, self.T * self.k * self.N, torch.bfloat16, self.device)
         a = ep_combine_backward_args(recv_buf=ptr(self.recv[rank]), gates=ptr(self.gates[rank]),
                                      dout=ptr(dout), dgates=ptr(dgates), drows=ptr(drows))
         ep_combine_backward(self.cfg(rank), a, stream)
 
     def route_backward(self, rank: int, dgates: torch.Tensor, dlogits: torch.Tensor, stream=None):
         """Gradient of the logits of ``route``'s last call, which must still stand, from the
-        gates'; into ``dlogits`` (their type and shape, rows any stride apart)."""
+        gates' ([T][k] fp32, contiguous); into ``dlogits`` (their type and shape, rows any stride
+        of at least E apart)."""
         r = self.routes[rank]
+        _check_flat("dgates", dgates, self.T * self.k, torch.float32, self.device)
+        stride = _check_rows("dlogits", dlogits, self.T, self.R * self.El, (r["logits"].dtype,),
+                             self.device)
         a = ep_route_backward_args(logits=ptr(r["logits"]), logits_stride=r["stride"],
                                    logits_dtype=self._LOGITS[r["logits"].dtype],
                                    score=r["score"], renormalize=r["renormalize"],
                                    scale=r["scale"], topk_ids=ptr(self.topk[rank]),
                                    dgates=ptr(dgates), dlogits=ptr(dlogits),
-                                   dlogits_stride=dlogits.stride(0),
+                                   dlogits_stride=stride,
                                    status=self.status.data_ptr() + 4 * STATUS_ROUTE)
         ep_route_backward(self.cfg(rank), a, stream)
 

@@ -79,3 +79,81 @@ def test_route_of_one_token_needs_no_row_stride(calls, logits):
 def test_route_of_no_tokens(calls):
     make(0).route(0, torch.zeros(0, E))
     assert len(calls) == 1
+
+
+# ------------------------------------------------------------------ gradients
+
+
+def routed(tokens=T, dtype=torch.float32):
+    s = make(tokens)
+    for r in range(R):
+        s.route(r, torch.zeros(tokens, E, dtype=dtype))
+    return s
+
+
+BF16 = dict(dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("dout", dict(dout=torch.ones((), **BF16).expand(T, H))),  # the gradient of out.sum()
+    ("dout", dict(dout=torch.zeros(T, H))), ("dout", dict(dout=torch.zeros(T - 1, H, **BF16))),
+    ("dout", dict(dout=torch.zeros(H, T, **BF16).t())),
+    ("dout", dict(dout=torch.zeros(T, 2 * H, **BF16)[:, :H])),
+    ("dout", dict(dout=torch.zeros(T, H, device="meta", **BF16))),
+    ("dgates", dict(dgates=torch.zeros(T, K_TOP, **BF16))),
+    ("dgates", dict(dgates=torch.zeros(T, K_TOP - 1))),
+    ("dgates", dict(dgates=torch.zeros(K_TOP, T).t())),
+    ("drows", dict(drows=torch.zeros(T, K_TOP, H))),
+    ("drows", dict(drows=torch.zeros(T, H, **BF16))),
+    ("drows", dict(drows=torch.zeros(T, K_TOP, H + 8, **BF16)[..., :H])),
+])
+def test_combine_backward_refuses(calls, name, kw):
+    s = routed()
+    calls.clear()
+    args = dict(dout=torch.zeros(T, H, **BF16), dgates=torch.zeros(T, K_TOP))
+    args.update(kw)
+    with pytest.raises(ValueError, match=name):
+        s.combine_backward(0, **args)
+    assert not calls
+
+
+def test_combine_backward_takes_either_gradient_and_the_receive_buffer(calls):
+    s = routed()
+    calls.clear()
+    dout = torch.zeros(T, H, **BF16)
+    s.combine_backward(0, dout, dgates=torch.zeros(T, K_TOP))
+    s.combine_backward(0, dout, drows=torch.zeros(T, K_TOP, H, **BF16))
+    s.combine_backward(0, dout, drows=torch.zeros(T * K_TOP, H, **BF16))
+    s.combine_backward(1, dout, drows=s.recv[1])
+    assert [name for name, _ in calls] == ["ep_combine_backward"] * 4
+    assert calls[3][1].drows == s.recv[1].data_ptr()
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("dgates", dict(dgates=torch.zeros(T, K_TOP, **BF16))),
+    ("dgates", dict(dgates=torch.zeros(1, K_TOP).expand(T, K_TOP))),
+    ("dgates", dict(dgates=torch.zeros(T, K_TOP + 1))),
+    ("dlogits", dict(dlogits=torch.zeros(T, E, **BF16))),  # the logits are fp32
+    ("dlogits", dict(dlogits=torch.zeros(1, E).expand(T, E))),
+    ("dlogits", dict(dlogits=torch.zeros(E, T).t())),
+    ("dlogits", dict(dlogits=torch.zeros(T, E - 1))),
+    ("dlogits", dict(dlogits=torch.zeros(T, E, device="meta"))),
+])
+def test_route_backward_refuses(calls, name, kw):
+    s = routed()
+    calls.clear()
+    args = dict(dgates=torch.zeros(T, K_TOP), dlogits=torch.zeros(T, E))
+    args.update(kw)
+    with pytest.raises(ValueError, match=name):
+        s.route_backward(0, **args)
+    assert not calls
+
+
+def test_route_backward_takes_rows_any_stride_apart(calls):
+    s = routed(dtype=torch.bfloat16)
+    wide = torch.zeros(T, E + 2, **BF16)
+    s.route_backward(1, torch.zeros(T, K_TOP), wide[:, 1:E + 1])
+    assert calls[-1][1].dlogits == wide.data_ptr() + 2 and calls[-1][1].dlogits_stride == E + 2
+    one = routed(1)
+    one.route_backward(0, torch.zeros(1, K_TOP), torch.zeros(E, 1).t())
+    assert calls[-1][1].dlogits_stride == 0
