@@ -13,11 +13,12 @@ import numpy as np
 import torch
 
 from . import (EP_ACT_NONE, EP_ACT_SWIGLU, EP_BF16, EP_FP8_1D2D, EP_LOGITS_BF16, EP_LOGITS_F32,
-               EP_SCORE_SOFTMAX, ep_combine_args, ep_combine_backward, ep_combine_backward_args,
-               ep_combine_reduce, ep_config, ep_dispatch_args, ep_dispatch_gather, ep_matvec_w4,
-               ep_matvec_w4_sizes, ep_plan, ep_plan_out, ep_plan_sizes, ep_route, ep_route_args,
-               ep_route_backward, ep_route_backward_args, ep_scatter_args, ep_scatter_send,
-               ep_send_args, ep_swiglu, ep_swiglu_args, ep_w4_args, grouped_gemm_combine_send, ptr)
+               EP_SCORE_SOFTMAX, EP_W4_E2M1, EP_W4_INT, ep_combine_args, ep_combine_backward,
+               ep_combine_backward_args, ep_combine_reduce, ep_config, ep_dispatch_args,
+               ep_dispatch_gather, ep_matvec_w4, ep_matvec_w4_sizes, ep_plan, ep_plan_out,
+               ep_plan_sizes, ep_route, ep_route_args, ep_route_backward, ep_route_backward_args,
+               ep_scatter_args, ep_scatter_send, ep_send_args, ep_swiglu, ep_swiglu_args,
+               ep_w4_args, grouped_gemm_combine_send, ptr)
 from .w4 import W4Weights
 
 SENTINEL_BYTE = 0xFF  # received bf16 0xFFFF is a NaN: an unwritten slot cannot pass
@@ -347,9 +348,13 @@ class EpSystem:
     def set_layer_w4(self, rank: int, X: torch.Tensor, W1: W4Weights, W2: W4Weights):
         """Operands of a MoE layer on 4-bit weights: the rank's tokens X
         [max_tokens][H] bf16, its experts' up/gate weights W1 ([E_l][2I] rows of H, gate rows
-        first) and down-projection weights W2 ([E_l][H] rows of I), with H = N and I = K.
-        Allocates the layer's buffers and its two workspaces."""
+        first) and down-projection weights W2 ([E_l][H] rows of I), with H = N and I = K; all
+        contiguous. Allocates the layer's buffers and its two workspaces, on torch's current
+        stream."""
         assert self.dtype == "bf16" and tuple(X.shape) == (self.max_tokens, self.N)
+        _check_flat("X", X, self.max_tokens * self.N, torch.bfloat16, self.device)
+        self._check_w4("W1", W1, self.El * 2 * self.K, self.N)
+        self._check_w4("W2", W2, self.El * self.N, self.K)
         dev, rows = self.device, max(ep_plan_sizes(self.cfg(rank)), 1)
         self.layer_w4[rank] = dict(
             X=X, W1=W1, W2=W2,
@@ -357,6 +362,18 @@ class EpSystem:
             C=torch.zeros((rows, self.N), dtype=torch.bfloat16, device=dev),
             workspaces=[torch.zeros(ep_matvec_w4_sizes(c), dtype=torch.uint8, device=dev)
                         for c in (self.cfg_up(rank), self.cfg(rank))])
+
+    def _check_w4(self, name: str, w: W4Weights, rows: int, cols: int):
+        if w.group_size < 1 or cols % w.group_size:
+            raise ValueError(f"{name}: groups of {w.group_size} in rows of {cols}")
+        if w.w_format not in (EP_W4_INT, EP_W4_E2M1):
+            raise ValueError(f"{name}: w_format {w.w_format}")
+        groups = rows * (cols // w.group_size)
+        _check_flat(f"{name}.codes", w.codes, rows * cols // 2, torch.uint8, self.device)
+        _check_flat(f"{name}.scales", w.scales, groups,
+                    torch.uint8 if w.w_format == EP_W4_E2M1 else torch.bfloat16, self.device)
+        if w.zeros is not None:
+            _check_flat(f"{name}.zeros", w.zeros, groups, torch.uint8, self.device)
 
     def _w4_args(self, rank: int, w: W4Weights, C, workspace) -> ep_w4_args:
         p = self.plans[rank]

@@ -2,15 +2,23 @@
 address, so a tensor of another type, size or stride would be read past its end or as something
 else. No GPU: the library's calls are replaced by ones that keep their arguments."""
 
+import dataclasses
+
 import pytest
 import torch
 
 import moe_expert_gemm_gb300 as ep
 from moe_expert_gemm_gb300 import system
 from moe_expert_gemm_gb300.system import EpSystem
+from moe_expert_gemm_gb300.w4 import quantize_w4
 
 R, EL, K_TOP, T, INTER, H = 2, 3, 2, 5, 64, 128
 E = R * EL
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    ep.build()
 
 
 @pytest.fixture
@@ -157,3 +165,45 @@ def test_route_backward_takes_rows_any_stride_apart(calls):
     one = routed(1)
     one.route_backward(0, torch.zeros(1, K_TOP), torch.zeros(E, 1).t())
     assert calls[-1][1].dlogits_stride == 0
+
+
+# -------------------------------------------------------------- 4-bit weights
+
+
+def w4_layer(fmt=ep.EP_W4_INT, group=32, zeros=True):
+    gen = torch.Generator().manual_seed(0)
+    return (torch.zeros(T, H, **BF16),
+            quantize_w4(torch.randn(EL, 2 * INTER, H, generator=gen), fmt, group, zeros),
+            quantize_w4(torch.randn(EL, H, INTER, generator=gen), fmt, group, zeros))
+
+
+@pytest.mark.parametrize("fmt,group,zeros", [(ep.EP_W4_INT, 32, True), (ep.EP_W4_INT, 64, False),
+                                             (ep.EP_W4_E2M1, 32, False)])
+def test_layer_takes_quantized_weights(fmt, group, zeros):
+    make().set_layer_w4(0, *w4_layer(fmt, group, zeros))
+
+
+def test_layer_refuses_what_the_products_would_read_past():
+    X, W1, W2 = w4_layer()
+    change = dataclasses.replace
+    strided = torch.empty(EL, INTER // 2, H, dtype=torch.uint8).transpose(1, 2)
+    assert strided.shape == W2.codes.shape
+    for bad in [
+        (X.float(), W1, W2), (torch.zeros(T, 2 * H, **BF16)[:, :H], W1, W2),
+        (torch.zeros(1, H, **BF16).expand(T, H), W1, W2),
+        (X, W2, W1),                                             # the two exchanged
+        (X, change(W1, codes=W1.codes[:EL - 1]), W2),            # an expert short
+        (X, change(W1, scales=W1.scales[..., :1]), W2),
+        (X, change(W1, group_size=64), W2),                      # scales of groups of 32
+        (X, change(W1, scales=W1.scales.float()), W2),
+        (X, W1, change(W2, codes=strided)),
+        (X, W1, change(W2, zeros=W2.zeros[:, :1])),
+        (X, W1, change(W2, w_format=ep.EP_W4_E2M1)),             # bf16 scales
+        (X, W1, change(W2, w_format=2)), (X, W1, change(W2, group_size=48)),
+        (X, W1, change(W2, group_size=0)),
+        (X, W1, change(W2, codes=W2.codes.to("meta"))),
+    ]:
+        s = make()
+        with pytest.raises(ValueError):
+            s.set_layer_w4(0, *bad)
+        assert s.layer_w4[0] is None
