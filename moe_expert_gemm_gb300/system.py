@@ -9,6 +9,8 @@ over direct peer stores.
 
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -77,6 +79,7 @@ class EpSystem:
         self.block_counter = [torch.zeros(1, dtype=torch.int32, device=dev) for _ in range(R)]
         self.status = torch.zeros(8, dtype=torch.int32, device=dev)
         self.topk = None
+        self._route_ids = torch.zeros((R, tokens, top_k), dtype=torch.int32, device=dev)
         self.plans: list[dict | None] = [None] * R
         self.ops: list[dict | None] = [None] * R
         self.gates: list[torch.Tensor | None] = [None] * R
@@ -88,6 +91,18 @@ class EpSystem:
     def cfg(self, rank: int) -> ep_config:
         return ep_config(self.R, rank, self.El, self.k, self.T, self.max_tokens, self.K, self.N,
                          self.msg_bytes, self.dt_code, self.send_warps, self.signal_mode)
+
+    def _on(self, stream):
+        """What a call makes for itself is allocated and filled inside this context: on the
+        stream its kernel goes to, ahead of it. (On torch's current stream the fill could land
+        after the kernel, and the caller can order nothing inside one call.)"""
+        if self.device.type != "cuda":
+            return contextlib.nullcontext()
+        if stream is None or stream == 0:
+            stream = torch.cuda.default_stream(self.device)
+        elif isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, self.device)
+        return torch.cuda.stream(stream)
 
     def reset_buffers(self):
         for b in self.recv:
@@ -103,12 +118,13 @@ class EpSystem:
     def plan(self, rank: int, stream=None, max_rows: int | None = None) -> dict:
         cap = ep_plan_sizes(self.cfg(rank)) if max_rows is None else max_rows
         dev, El, R = self.device, self.El, self.R
-        p = dict(expert_offsets=torch.zeros(El + 1, dtype=torch.int32, device=dev),
-                 src_info=torch.zeros((max(cap, 1), 2), dtype=torch.int32, device=dev),
-                 seg_offsets=torch.zeros((El, R + 1), dtype=torch.int32, device=dev),
-                 send_counts=torch.zeros((El, R), dtype=torch.int32, device=dev),
-                 gather_idx=torch.zeros(max(cap, 1), dtype=torch.int32, device=dev),
-                 m_total=torch.zeros(1, dtype=torch.int32, device=dev), capacity=cap)
+        with self._on(stream):
+            p = dict(expert_offsets=torch.zeros(El + 1, dtype=torch.int32, device=dev),
+                     src_info=torch.zeros((max(cap, 1), 2), dtype=torch.int32, device=dev),
+                     seg_offsets=torch.zeros((El, R + 1), dtype=torch.int32, device=dev),
+                     send_counts=torch.zeros((El, R), dtype=torch.int32, device=dev),
+                     gather_idx=torch.zeros(max(cap, 1), dtype=torch.int32, device=dev),
+                     m_total=torch.zeros(1, dtype=torch.int32, device=dev), capacity=cap)
         out = ep_plan_out(ptr(p["expert_offsets"]), ptr(p["src_info"]), ptr(p["seg_offsets"]),
                           ptr(p["send_counts"]), ptr(p["gather_idx"]), ptr(p["m_total"]),
                           self.status.data_ptr() + 4 * STATUS_PLAN, cap)
@@ -295,13 +311,14 @@ class EpSystem:
         if bias is not None:
             _check_flat("bias", bias, E, torch.float32, self.device)
         if self.topk is None:
-            self.topk = torch.zeros((self.R, self.T, self.k), dtype=torch.int32,
-                                    device=self.device)
+            self.topk = self._route_ids  # of all ranks, whose calls may go to streams of their own
         if self.gates[rank] is None:
-            self.gates[rank] = torch.zeros((self.T, self.k), device=self.device)
+            with self._on(stream):
+                self.gates[rank] = torch.zeros((self.T, self.k), device=self.device)
         if self.out[rank] is None:
-            self.out[rank] = torch.zeros((self.T, self.N), dtype=torch.bfloat16,
-                                         device=self.device)
+            with self._on(stream):
+                self.out[rank] = torch.zeros((self.T, self.N), dtype=torch.bfloat16,
+                                             device=self.device)
         a = ep_route_args(logits=ptr(logits), logits_stride=stride,
                           logits_dtype=self._LOGITS[logits.dtype], score=score, bias=ptr(bias),
                           n_groups=n_groups, topk_groups=topk_groups, group_top=group_top,
@@ -405,7 +422,8 @@ class EpSystem:
         """One send with per-tile timestamps; returns the decoded trace."""
         n_sm = torch.cuda.get_device_properties(self.device).multi_processor_count
         stride = 2 + 4 * records
-        buf = torch.zeros(n_sm * stride, dtype=torch.int64, device=self.device)
+        with self._on(stream):
+            buf = torch.zeros(n_sm * stride, dtype=torch.int64, device=self.device)
         a = self.send_args(rank, epoch)
         a.trace = ptr(buf)
         a.trace_records = records
