@@ -73,8 +73,8 @@ template <bool DGATES, bool DROWS, int WPR>
 __global__ void __launch_bounds__(32 * kCombineBwdWarps)
     combine_backward_kernel(const CombineBackwardParams p)
 {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int pieces = p.N / 8;
     const int64_t rows = static_cast<int64_t>(p.T) * p.top_k;

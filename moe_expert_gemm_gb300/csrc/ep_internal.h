@@ -69,8 +69,10 @@ inline cudaError_t launch_send_kernel(Kern kern, int grid, int threads, int smem
 }
 
 // Launch of a kernel that begins with griddep_wait(): its blocks may take the place of the
-// previous kernel's as those leave, and wait there for that kernel's end and memory. The
-// stream's order is kept.
+// previous kernel's as those leave, and wait there for that kernel's end and memory. It lets its
+// own dependents start only after that wait, so that of the kernels before a dependent no more
+// than one is unfinished: a combine with EP_OVERLAP_INPUTS_READY, which does not wait, asks
+// its caller about the previous kernel alone.
 template <typename... Params, typename... Args>
 inline cudaError_t launch_behind(void (*kern)(Params...), unsigned grid, unsigned threads, size_t smem,
                                  cudaStream_t s, const Args &...args)

@@ -111,8 +111,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         sh.abort = 0;
     }
     const int tiles = (cols + tile_cols - 1) / tile_cols;
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     if (warp == 0)
         plan_run<8 * NT>(p, sh.run, tiles, lane);
     __syncthreads();

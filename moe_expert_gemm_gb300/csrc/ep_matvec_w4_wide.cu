@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         fence_mbar_init();
         sh.abort = 0;
     }
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     // (tensor memory only now: the previous kernel may still have wanted it)
     if (warp == 1) {
         tmem_alloc(&sh.tmem, kTmemCols);

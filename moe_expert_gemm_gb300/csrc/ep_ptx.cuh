@@ -486,7 +486,8 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar, uint16_t mask)
 
 // Programmatic dependent launch: this thread's part of the grid is done with the
 // work a dependent kernel may overlap; the dependent grid can start once every
-// thread block has signalled (or exited).
+// thread block has signalled (or exited). Never ahead of griddep_wait(): a dependent that does
+// not wait itself would start beside the kernel before this one.
 __device__ __forceinline__ void griddep_launch_dependents()
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -266,8 +266,8 @@ __device__ __noinline__ void route_token(const RouteParams &p, int64_t t, uint32
 template <typename T>
 __global__ void __launch_bounds__(kRouteThreads) route_token_kernel(const __grid_constant__ RouteParams p)
 {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     extern __shared__ uint32_t smem[];
     const int warp = threadIdx.x >> 5;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRouteThreads / 32) + warp;
@@ -351,8 +351,8 @@ enum Choice { kByLogit, kBySigmoid, kBySoftmax };
 template <typename T, int VPL, bool VEC, Choice BY>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __grid_constant__ RouteParams p)
 {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     constexpr int kMost = 16 / static_cast<int>(sizeof(T));
     constexpr int W = VEC ? (VPL < kMost ? VPL : kMost) : 1;
     constexpr int WB = VEC ? (VPL < 4 ? VPL : 4) : 1;  // of the bias
@@ -568,8 +568,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __gr
 template <typename T, int EP>
 __global__ void __launch_bounds__(128) route_thread_kernel(const __grid_constant__ RouteParams p)
 {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (t >= p.T)
         return;
@@ -659,8 +659,8 @@ template <typename T, int VPL, bool VEC>
 __global__ void __launch_bounds__(32 * kRouteWarps)
     route_backward_warp_kernel(const __grid_constant__ RouteBackwardParams p)
 {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     constexpr int kMost = 16 / static_cast<int>(sizeof(T));
     constexpr int W = VEC ? (VPL < kMost ? VPL : kMost) : 1;
     const int lane = threadIdx.x & 31;
@@ -748,8 +748,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 template <typename T>
 __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const __grid_constant__ RouteBackwardParams p)
 {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     extern __shared__ uint32_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = p.E, k = p.top_k;
