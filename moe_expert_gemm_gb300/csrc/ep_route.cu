@@ -333,10 +333,12 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float *out)
     }
 }
 
-// How far a choice value (or a sum of two) taken with the fast exponential and reciprocal
-// may lie from the fp32 formula's: e^-x is off by a few units in 2^-22 relative plus
-// |x| 2^-23, which the sigmoid's slope turns into less than 2^-21 absolute; a softmax
-// score is off by less; the addition of the bias rounds once on either side.
+// How far a choice value taken with the fast exponential and reciprocal may lie from the fp32
+// formula's: e^-x is off by a few units in 2^-22 relative plus |x| 2^-23, which the
+// sigmoid's slope turns into less than 2^-21 absolute; a softmax score is off by less; the
+// addition of the bias rounds once on either side, to within 2^-23 of the value, so that half
+// of the second term is left for a rounding of what is made of it. The largest (or second
+// largest) of some values is off by no more than a value of its size.
 __device__ __forceinline__ float choice_error(float v)
 {
     return 0x1p-20f + 0x1p-22f * fabsf(v);
@@ -465,8 +467,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __gr
             }
             keep = better < p.topk_groups;
         } else {
-            // the topk_groups-th largest worth and the one after it: too near each other
-            // (or equal), and the fp32 formula has to tell
+            // The groups with the topk_groups largest worths. The members of a sum are each off
+            // by their own size's error, which may be far above the sum's: where the least that a
+            // kept worth may be does not pass the most that another may be (or worths are
+            // equal), the fp32 formula has to tell.
             const uint32_t mine = choice_key(worth);
             uint32_t left = mine, last = 0;
             for (int g = 0; g < p.topk_groups; ++g) {
@@ -474,9 +478,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __gr
                 left = left == last ? 0 : left;
             }
             keep = mine >= last;
-            const float bar = key_value(last), after = key_value(__reduce_max_sync(kFull, left));
+            const bool any = a > -INFINITY;  // (else nothing of the group is left)
+            const float off = !any ? 0.f
+                              : choice_error(a) + 0x1p-23f * fabsf(worth) +
+                                    (p.two_of_group && b > -INFINITY ? choice_error(b) : 0.f);
+            const uint32_t least = __reduce_min_sync(kFull, keep ? choice_key(worth - off) : ~0u);
+            const uint32_t most_other = __reduce_max_sync(kFull, keep ? 0 : choice_key(worth + off));
             const unsigned kept = __ballot_sync(kFull, keep);
-            odd |= !(bar - after > 4.f * choice_error(bar)) ||
+            odd |= least <= most_other || least <= choice_key(-INFINITY) ||
                    __popc(kept) != p.topk_groups << p.lanes_log2;
         }
         if (!keep) {
