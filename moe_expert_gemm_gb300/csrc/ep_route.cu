@@ -114,6 +114,12 @@ __device__ __forceinline__ float sigmoid_f32(float x)
     return 1.f / (1.f + expf(-x));
 }
 
+// Whether a logit makes all of its token's gates NaN, whichever experts are chosen.
+__device__ __forceinline__ bool makes_nan(float x, bool sigmoid)
+{
+    return isnan(x) || (!sigmoid && x == INFINITY);
+}
+
 // Approximations (errors: choice_error). e^x by 2^(x log2 e).
 __device__ __forceinline__ float fast_exp(float x)
 {
@@ -162,7 +168,7 @@ __device__ __noinline__ void route_token(const RouteParams &p, int64_t t, uint32
     bool nan = false;
     for (int i = lane; i < E; i += 32) {
         const float x = Logit<T>::load(l + i);
-        nan |= isnan(x);
+        nan |= makes_nan(x, p.score == EP_SCORE_SIGMOID);
         if (x > Logit<T>::lowest)  // neither masked nor NaN
             top = fmaxf(top, x);
     }
@@ -600,7 +606,7 @@ __global__ void __launch_bounds__(128) route_thread_kernel(const __grid_constant
     float top = -INFINITY, total = 0.f;
 #pragma unroll
     for (int i = 0; i < EP; ++i) {
-        nan |= isnan(x[i]);
+        nan |= makes_nan(x[i], sigmoid);
         if (!(x[i] > Logit<T>::lowest))
             x[i] = -INFINITY;
         top = fmaxf(top, x[i]);
