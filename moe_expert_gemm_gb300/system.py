@@ -397,7 +397,7 @@ class EpSystem:
         return ep_w4_args(W=ptr(w.codes), w_scales=ptr(w.scales), w_zeros=ptr(w.zeros),
                           w_format=w.w_format, group_size=w.group_size,
                           expert_offsets=ptr(p["expert_offsets"]),
-                          max_rows=min(int(C.shape[0]), p["capacity"]), C=ptr(C),
+                          max_rows=min(int(C.shape[0]), int(p["gather_idx"].shape[0])), C=ptr(C),
                           workspace=ptr(workspace), workspace_bytes=workspace.numel(),
                           status=self.status.data_ptr() + 4 * STATUS_W4)
 
