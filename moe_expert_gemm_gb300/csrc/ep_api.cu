@@ -612,11 +612,11 @@ int ep_combine_backward(const ep_config *cfg, const ep_combine_backward_args *a,
     int rc = check_config(cfg);
     if (rc != EP_OK)
         return rc;
-    if (!a || (!a->dgates && !a->drows) || cfg->N % 8 != 0)
+    if (!a || cfg->N % 8 != 0)
         return EP_ERR_INVALID_ARG;
     if (cfg->num_tokens == 0)
         return EP_OK;
-    if (!a->dout || (a->dgates && !a->recv_buf) || (a->drows && !a->gates) ||
+    if ((!a->dgates && !a->drows) || !a->dout || (a->dgates && !a->recv_buf) || (a->drows && !a->gates) ||
         !aligned16(a->dout) || !aligned16(a->recv_buf) || !aligned16(a->drows) ||
         !aligned_to(a->gates, 4) || !aligned_to(a->dgates, 4))
         return EP_ERR_INVALID_ARG;

@@ -30,3 +30,17 @@ def test_no_tokens(fmt):
     assert (s.status_words() == 0).all(), s.status_words()
     for r in range(R):
         assert (s.counts[r][El * R:] == 3).all()
+
+
+def test_gradients_of_no_tokens():
+    R, El, k, H = 2, 3, 2, 128
+    s = EpSystem(R, El, k, 0, K=64, N=H, max_tokens=4)
+    empty = lambda *shape, dtype=torch.float32: torch.zeros(*shape, dtype=dtype, device="cuda")
+    for r in range(R):
+        s.route(r, empty(0, R * El))
+        s.combine_backward(r, empty(0, H, dtype=torch.bfloat16), dgates=empty(0, k))
+        s.combine_backward(r, empty(0, H, dtype=torch.bfloat16), drows=s.recv[r])
+        s.route_backward(r, empty(0, k), empty(0, R * El))
+    torch.cuda.synchronize()
+    assert (s.status_words() == 0).all()
+    assert all((b == 0xFF).all() for b in s.recv)
