@@ -477,7 +477,7 @@ int ep_combine_reduce(const ep_config *cfg, const ep_combine_args *args, ep_stre
  * chosen, lowest ids first, only where too few others are left (in the chosen groups);
  * its gate is 0. So every token gets top_k distinct valid ids, and one whose experts
  * are all masked gets zero gates. A NaN logit ranks as masked and makes the token's
- * gates NaN, as does +inf under the softmax.
+ * gates NaN, as does +inf under the softmax, whichever experts are chosen.
  * Limits (EP_ERR_UNSUPPORTED): top_k <= 32. EP_ERR_INVALID_ARG: n_groups does not
  * divide E, or topk_groups groups have fewer than top_k experts.
  */
@@ -574,7 +574,9 @@ int ep_combine_backward(const ep_config *cfg, const ep_combine_backward_args *ar
  *   w_format        EP_W4_INT:  W = (code - zero) * scale, codes 0..15;
  *                               w_scales [E_l][N][K/group_size] bf16, w_zeros the same
  *                               shape in bytes (0..15), or NULL: zero = 8 everywhere;
- *                               group_size 32, 64 or 128, dividing K
+ *                               group_size 32, 64 or 128, dividing K. Weights under scales
+ *                               below 2^-120 may be off by up to 2^-128 each where many
+ *                               rows are expected of an expert
  *                   EP_W4_E2M1: codes are e2m1 numbers (0, .5, 1, 1.5, 2, 3, 4, 6 and
  *                               their negatives from code 8 on); w_scales
  *                               [E_l][N][K/32] bytes, scale = 2^(byte - 127) (255: NaN);

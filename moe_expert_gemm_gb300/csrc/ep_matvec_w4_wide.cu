@@ -13,7 +13,8 @@
 //    power of two exactly (one of 2^128 or more counts as infinite). An integer code times
 //    its scale has up to 12 significant bits: it is split into two bf16 numbers, a product a
 //    little short of it and what that leaves (at most 8 bits: a fused multiply-add gives
-//    it exactly), and both are multiplied.
+//    it exactly, down to scales of 2^-120; below, bf16's own spacing cuts it), and both
+//    are multiplied.
 //  * k comes in the order in which a word's halves give it, (0,4) (1,5) (2,6) (3,7) of
 //    eight; the staging warps lay the activations out in that order too, in the 128-byte
 //    swizzle that the matrix engine reads.

@@ -19,7 +19,11 @@
 //    below, which leaves hardly more than k candidates. Those go to one lane each, get
 //    their exact fp32 value there, and are ranked by counting. Where the approximation
 //    cannot decide (groups closer than its error, NaN, too few unmasked experts, more than
-//    32 candidates) the token is done over by route_token.
+//    32 candidates) the token is done over by route_token. So is every token where fewer than
+//    top_k lanes hold experts of the kept groups: topk_groups * 32 / n_groups lanes, fewer
+//    if groups are small or their pieces leave lanes empty. 65536 tokens of 256 experts by
+//    sigmoid and bias, top 8, us: 8 groups keep 4 / 2 / 1: 45 / 59 / 187, 16 keep 3: 152,
+//    32 keep 4: 139 (252 experts in 9 groups, by the form below alone: 169).
 //  * route_token_kernel: everything else, by scanning shared memory.
 // The gradient likewise: a warp to a token with its values in registers up to 256 experts,
 // past that in shared memory.

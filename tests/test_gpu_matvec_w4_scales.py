@@ -129,3 +129,22 @@ def test_integer_scales_of_any_size_and_sign(announced, group):
         np.testing.assert_array_equal(np.isfinite(out[:, 6]), np.isfinite(y[:, 6]))
         ok = [n for n in range(N) if n not in (6, 7)]
         assert (np.abs(out - y)[:, ok] <= 2.0 ** -7.9 * np.abs(y[:, ok]) + size[:, ok] + 1e-37).all()
+
+
+@pytest.mark.parametrize("announced", FORM_ROWS)
+def test_integer_scales_next_to_the_smallest(announced):
+    """Scales around 2^-120 and subnormal ones. Split into two bf16 numbers, whose spacing there is
+    2^-133 (2^-127 after the factor of 64 that the codes leave out), a weight under a scale below
+    2^-120 may be off by half of that; with larger scales it is exact."""
+    rng = np.random.default_rng(1)
+    K, N = 256, 48
+    packed = rng.integers(0, 256, (1, N, K // 2), dtype=np.uint8)
+    bits = rng.integers(1, 0x0600, (1, N, K // 32)).astype(np.uint32)  # up to 2^-115
+    bits[0, ::2] = rng.integers(0x0380, 0x0600, (N // 2, K // 32))     # from 2^-120 on
+    scales = (bits << 16).view(np.float32)
+    x = activations(20, K, 5) * np.float32(2.0 ** 60)
+    c = batch(Call(x, [20], (packed, scales, None), "int4", 32), announced)
+    out = c.run()
+    y, size = c.want()
+    lost = np.abs(x.astype(np.float64)).sum(1)[:, None] * 2.0 ** -128 * (np.arange(N) % 2)
+    assert (np.abs(out - y) <= 2.0 ** -7.9 * np.abs(y) + size + 1.01 * lost).all()
