@@ -425,7 +425,8 @@ int ep_swiglu(const ep_config *cfg, const ep_swiglu_args *args, ep_stream_t stre
  *               overlaps the end of a send). EP_OVERLAP_INPUTS_READY: the same launch
  *               for a caller that guarantees the previous kernel writes none of the
  *               gates, the routing and `out` (e.g. it is this library's fused send):
- *               no wait, so the combine's reads start while that kernel finishes.
+ *               no wait, so the combine's reads start while that kernel finishes (the
+ *               combine does not end before it).
  * EP_SIGNAL_RANK_FLAG: each thread block acquires every source rank's flag once
  * (system scope) before reading the rows, as the fused consumer of
  * "ep_signal_completion" does. EP_SIGNAL_PER_EXPERT: before reducing a token, the

@@ -82,13 +82,24 @@ __device__ __forceinline__ bool acquire_source_flags(const CombineParams &p)
     return s_ok != 0;
 }
 
+// With EP_OVERLAP_INPUTS_READY nothing in the combine waits for the kernel before it, yet it
+// must not end before that one does: a kernel launched behind the combine waits for the
+// combine alone. The last block stays until then; the others make room as they finish.
+__device__ __forceinline__ void end_after_previous()
+{
+    if (blockIdx.x == gridDim.x - 1)
+        griddep_wait();
+}
+
 // top_k known at compile time: a warp takes U consecutive units and issues all U*K
 // loads before accumulating any of them.
 template <int K, int U>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineParams p)
 {
-    if (!acquire_source_flags(p))
+    if (!acquire_source_flags(p)) {
+        end_after_previous();
         return;
+    }
     if (p.overlap_previous == EP_OVERLAP_ANY)
         griddep_wait();  // gates (and out) may belong to the kernel before this one
     const int lane = threadIdx.x & 31;
@@ -128,6 +139,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
             store_out(p, tt[uu], vv[uu], acc);
         }
     }
+    end_after_previous();
 }
 
 // EP_SIGNAL_PER_EXPERT: wait for (acquire) the count word of global expert g in this
@@ -268,13 +280,16 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel_per_expert(con
         }
         u = stop;
     }
+    end_after_previous();
 }
 
 // any other top_k: one unit at a time, its rows streamed kLoads at a time
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel_any(const CombineParams p)
 {
-    if (!acquire_source_flags(p))
+    if (!acquire_source_flags(p)) {
+        end_after_previous();
         return;
+    }
     if (p.overlap_previous == EP_OVERLAP_ANY)
         griddep_wait();  // gates (and out) may belong to the kernel before this one
     const int lane = threadIdx.x & 31;
@@ -308,6 +323,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel_any(const Comb
         }
         store_out(p, t, v, acc);
     }
+    end_after_previous();
 }
 
 // Launch; with overlap_previous as a programmatic dependent of the previous kernel

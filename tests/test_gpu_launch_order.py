@@ -90,3 +90,36 @@ def test_gates_of_the_kernel_before_the_previous_one(between):
     assert (s.status_words() == 0).all()
     if "status" in keep:
         assert keep["status"].item() == 0
+
+
+@pytest.mark.parametrize("signal_mode", [0, 1])
+@pytest.mark.parametrize("top_k", [2, 3])
+def test_a_kernel_behind_the_combine_that_does_not_wait(top_k, signal_mode):
+    """A long kernel, a short combine of other buffers that does not wait for it, and a kernel that
+    reads what the long one writes: it has to come after both."""
+    gen = torch.Generator().manual_seed(4)
+    s = EpSystem(1, E, K_TOP, T, K=64, N=N)
+    logits = torch.randn(T, E, generator=gen).cuda()
+    dout = torch.randn(T, N, generator=gen).cuda().bfloat16()
+    drows = torch.zeros(T, K_TOP, N, dtype=torch.bfloat16, device="cuda")
+    small = EpSystem(1, 4, top_k, 3, K=64, N=64, signal_mode=signal_mode)
+    small.recv[0].view(torch.bfloat16).copy_(torch.randn(3 * top_k * 64, generator=gen))
+    small.counts[0].fill_(1 << 32 if signal_mode else 1)  # every signal of epoch 1 is there
+    small.set_routing(np.tile(np.arange(top_k), (1, 3, 1)))
+    small.set_gates(0, np.ones((3, top_k)))
+    for overlap in (ep.EP_OVERLAP_NONE, ep.EP_OVERLAP_INPUTS_READY, ep.EP_OVERLAP_ANY):
+        for _ in range(5):
+            s.route(0, logits, n_groups=8, topk_groups=1)
+            s.gates[0].fill_(float("nan"))
+            small.out[0].fill_(77.0)
+            drows.fill_(55.0)
+            torch.cuda.synchronize()
+            s.route(0, logits, n_groups=8, topk_groups=1)
+            small.combine(0, epoch=1, overlap=overlap)
+            s.combine_backward(0, dout, drows=drows)
+            torch.cuda.synchronize()
+            want = (s.gates[0][:, :, None] * dout[:, None, :].float()).to(torch.bfloat16)
+            assert torch.equal(drows, want), (drows != want).any(2).sum()
+            rows = small.recv[0].view(torch.bfloat16).view(3, top_k, 64).float().sum(1)
+            assert torch.allclose(small.out[0].float(), rows, rtol=2.0 ** -8, atol=1e-6)
+    assert (s.status_words() == 0).all() and (small.status_words() == 0).all()

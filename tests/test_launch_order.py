@@ -1,7 +1,9 @@
 """Kernels that are launched behind the one before them on the stream (programmatic dependent
 launch) let their own dependents start only once everything before them has completed, so that
 a dependent that does not wait, the combine whose inputs are ready, has no more than one
-unfinished kernel before it. Read off the sources, as no run can show the order reliably."""
+unfinished kernel before it. And no kernel ends before the one it was launched behind: what
+waits for the combine waits for what the combine did not wait for. Read off the sources, as no
+run can show the order reliably."""
 
 import os
 import re
@@ -43,3 +45,14 @@ def test_the_kernels_are_found():
                  "route_backward_kernel", "route_backward_warp_kernel", "combine_backward_kernel",
                  "matvec_w4_kernel", "matvec_w4_wide_kernel"):
         assert name in found, (name, found)
+
+
+def test_the_combine_ends_after_the_kernel_before_it():
+    """In each of its kernels, ahead of every way out."""
+    combines = list(kernels(os.path.join(CSRC, "ep_combine.cu")))
+    assert len(combines) == 3
+    for name, body in combines:
+        ends = [m.start() for m in re.finditer(r"\breturn;", body)] + [len(body)]
+        for end in ends:
+            before = body[:end].rstrip()
+            assert before.endswith("end_after_previous();"), (name, before[-80:])
