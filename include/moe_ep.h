@@ -22,7 +22,7 @@
  *    ORs an EP_STATUS_* bit into the caller's `status` word, skips the offending
  *    access and returns. Read the word after the stream has synchronised.
  *  - All device pointers must be 16-byte aligned (the router, its gradient, the
- *    combine's gradient and the 4-bit products ask less where they say so).
+ *    combine's gradient, the 4-bit products and what follows them ask less where they say so).
  *  - Logical ranks: on one GPU, the receive buffers of the other ranks are simply
  *    other device allocations; with peer access they may be peer memory.
  */
@@ -627,6 +627,187 @@ typedef struct {
 int ep_matvec_w4_sizes(const ep_config *cfg, int64_t *workspace_bytes);
 
 int ep_matvec_w4(const ep_config *cfg, const ep_w4_args *args, ep_stream_t stream);
+
+/* --------------------------------------------- norm in front of the layer */
+
+/*
+ * ep_add_rmsnorm -- what stands between the block before a layer and the layer: the
+ * residual's addition, the root-mean-square norm, and the layer's tokens in bf16 or as
+ * e4m3 rows with 1x128 scales (EP_FP8_1D2D's A and a_scales), of num_tokens rows. The
+ * pages start from a layer's tokens; these calls have no counterpart there.
+ *   h = x + residual,  r = 1 / sqrt(mean(h^2) + eps),  v = h * r * weight,
+ * in fp32, h not rounded in between.
+ * cfg gives num_tokens; its K, N, ranks and experts play no part.
+ *   x               [num_tokens][hidden] bf16
+ *   residual        the same shape in residual_dtype, or NULL: h = x
+ *   residual_dtype  EP_ROWS_BF16 or EP_ROWS_F32, of residual and sum
+ *   weight          [hidden] in weight_dtype
+ *   eps             >= 0. (Where it is 0, a row of zeros gives NaN, as the formula does.)
+ *   hidden          1 .. EP_MAX_NORM_HIDDEN (more: EP_ERR_UNSUPPORTED)
+ *   sum             h, rounded once, out; or NULL. May be x or residual, of the same type,
+ *                   address and stride
+ *   y               [num_tokens][hidden] bf16 out: v, rounded once; or NULL. May be x
+ *   q, q_scales     [num_tokens][hidden] e4m3 and [num_tokens][ceil(hidden/128)] fp32 out, or
+ *                   both NULL: of each 128 consecutive columns (the last group may be
+ *                   shorter) s = max(largest |v| / 448, 2^-126) and e4m3(v / s), to nearest
+ *                   even (v times the fp32 reciprocal of s). A group that holds NaN or an
+ *                   infinity is NaN as a whole, scale and codes.
+ *   *_stride        elements between rows (0: hidden). q and q_scales lie without gaps.
+ * One of sum, y and q is given. Pointers need no more than their type's alignment; rows of
+ * whole 16-byte pieces are faster. Where a row's values pass about 1e19 / sqrt(hidden) in size
+ * the fp32 sum of squares is infinite and the row's v zero.
+ */
+#define EP_ROWS_F32 0
+#define EP_ROWS_BF16 1
+#define EP_MAX_NORM_HIDDEN 16384
+
+typedef struct {
+    const void *x;
+    int64_t x_stride;
+    const void *residual;
+    int64_t residual_stride;
+    int32_t residual_dtype;
+    int32_t weight_dtype;
+    const void *weight;
+    float eps;
+    int32_t hidden;
+    void *sum;
+    int64_t sum_stride;
+    void *y;
+    int64_t y_stride;
+    void *q;
+    float *q_scales;
+} ep_add_rmsnorm_args;
+
+int ep_add_rmsnorm(const ep_config *cfg, const ep_add_rmsnorm_args *args, ep_stream_t stream);
+
+/*
+ * ep_add_rmsnorm_backward -- gradient of ep_add_rmsnorm's v (dy) and sum (dsum) with respect
+ * to h, which is that of x and of the residual alike, and to the weight:
+ *   g = dy * weight,  dh = r * (g - h * r^2 * mean(g * h)) + dsum,
+ *   dweight[c] = sum_t dy[t][c] * h[t][c] * r[t],
+ * in fp32, r formed anew from h.
+ *   h               [num_tokens][hidden] in h_dtype: ep_add_rmsnorm's sum (or x)
+ *   dy              [num_tokens][hidden] bf16
+ *   dsum            the same shape in h_dtype, or NULL: what comes along the residual
+ *   weight, weight_dtype, eps, hidden   as in ep_add_rmsnorm
+ *   dh              in h_dtype, out, or NULL. May be h or dsum (same address and stride)
+ *   dx              bf16, out, or NULL: the same gradient for an x beside an fp32 residual.
+ *                   May be dy
+ *   dweight         [hidden] fp32 out, or NULL. Summed in a fixed order (which goes by
+ *                   num_tokens and the GPU's number of SMs)
+ *   workspace       for dweight: ep_add_rmsnorm_backward_sizes bytes, 16-byte aligned, of any
+ *                   contents; calls that may run at the same time need one each
+ * One of dh, dx and dweight is given. num_tokens = 0 makes dweight zero.
+ */
+typedef struct {
+    const void *h;
+    int64_t h_stride;
+    int32_t h_dtype;
+    int32_t weight_dtype;
+    const void *dy;
+    int64_t dy_stride;
+    const void *dsum;
+    int64_t dsum_stride;
+    const void *weight;
+    float eps;
+    int32_t hidden;
+    void *dh;
+    int64_t dh_stride;
+    void *dx;
+    int64_t dx_stride;
+    float *dweight;
+    void *workspace;
+    int64_t workspace_bytes;
+} ep_add_rmsnorm_backward_args;
+
+/* Workspace bytes of ep_add_rmsnorm_backward calls for up to cfg's num_tokens. Host only. */
+int ep_add_rmsnorm_backward_sizes(const ep_config *cfg, int32_t hidden, int64_t *workspace_bytes);
+
+int ep_add_rmsnorm_backward(const ep_config *cfg, const ep_add_rmsnorm_backward_args *args,
+                            ep_stream_t stream);
+
+/* --------------------------------------------------- activation in 8 bits */
+
+/*
+ * ep_swiglu_e4m3 -- ep_swiglu for blockwise fp8 operands: v = SiLU(G[m][i]) * G[m][inter + i]
+ * in fp32 from the bf16 G, as e4m3 rows with the scales of each 128 columns, by the same rule
+ * as ep_add_rmsnorm's q and q_scales, for m below the plan's row count.
+ *   G               [max_rows][2*inter] bf16: the up/gate GEMM's rows, gate half first
+ *   q               [max_rows][inter] e4m3 out, 8-byte aligned: the down-projection's A
+ *   q_scales        [max_rows][ceil(inter/128)] fp32 out: its a_scales
+ *   expert_offsets  the plan of my_rank (row count at [E_l])
+ *   inter           a multiple of 8
+ * Rows at or past the row count are left as they were.
+ */
+typedef struct {
+    const void *G;
+    void *q;
+    float *q_scales;
+    const int32_t *expert_offsets;
+    int64_t max_rows;
+    int32_t inter;
+} ep_swiglu_e4m3_args;
+
+int ep_swiglu_e4m3(const ep_config *cfg, const ep_swiglu_e4m3_args *args, ep_stream_t stream);
+
+/* ------------------------------------------------- a layer of a few tokens */
+
+/*
+ * ep_layer_few -- a whole MoE layer for a few tokens (decode): rank my_rank's part of
+ *   out[t] = sum_j gates[t][j] * W2_e (SiLU(Wgate_e x_t) * (Wup_e x_t)),  e = topk_ids[t][j],
+ * over the slots whose expert lives on my_rank (expert id / n_local_experts == my_rank; the
+ * other ranks' slots add nothing: with one rank the layer, with several a term of its sum).
+ * No plan, dispatch, receive buffers or signals. K = the intermediate size I and N = the
+ * hidden size H, as for the down-projection; at most EP_MAX_FEW_TOKENS tokens and a top_k of
+ * at most 32 (else EP_ERR_UNSUPPORTED).
+ *   dtype EP_BF16        x, W1, W2 bf16; the activation is rounded to bf16 between the two
+ *                        products. K and N are multiples of 8.
+ *   dtype EP_FP8_1D2D    x, W1, W2 e4m3 with 1x128 and 128x128 fp32 scales; the activation goes
+ *                        to e4m3 with 1x128 scales by the rule of ep_swiglu_e4m3, from fp32.
+ *                        K and N are multiples of 128.
+ * (Other K and N: EP_ERR_UNSUPPORTED.) Sums are fp32 and out is rounded once.
+ *   x               [num_tokens][N], 16-byte aligned
+ *   x_scales        EP_FP8_1D2D only: [num_tokens][N/128] fp32
+ *   topk_ids        [num_tokens][top_k] global expert ids. One outside [0, n_ranks *
+ *                   n_local_experts) sets EP_STATUS_ROUTING and adds nothing; an expert that a
+ *                   token names twice counts with the sum of both gates
+ *   gates           [num_tokens][top_k] fp32
+ *   W1              [E_l][2K][N], gate rows first, 16-byte aligned
+ *   w1_scales       EP_FP8_1D2D only: [E_l][2K/128][N/128] fp32
+ *   W2              [E_l][N][K], 16-byte aligned
+ *   w2_scales       EP_FP8_1D2D only: [E_l][N/128][K/128] fp32
+ *   out             [num_tokens][N] bf16 out, every row (zeros where a token has no expert here)
+ *   workspace       device memory of ep_layer_few_sizes bytes, 16-byte aligned, zero before the
+ *                   first call that uses it; a call that ends without EP_STATUS_TIMEOUT leaves
+ *                   it ready for the next of the same configuration. Calls that may run at the
+ *                   same time need one each.
+ *   status          EP_STATUS_ROUTING as above; EP_STATUS_TIMEOUT if a bounded wait inside a
+ *                   kernel ran out
+ * The weights of an expert without tokens are not read. Sums are taken in a fixed order: a
+ * call's result depends on its inputs alone (and on the GPU's number of SMs), not on timing.
+ */
+#define EP_MAX_FEW_TOKENS 64
+
+typedef struct {
+    const void *x;
+    const float *x_scales;
+    const int32_t *topk_ids;
+    const float *gates;
+    const void *W1;
+    const float *w1_scales;
+    const void *W2;
+    const float *w2_scales;
+    void *out;
+    void *workspace;
+    int64_t workspace_bytes;
+    uint32_t *status;
+} ep_layer_few_args;
+
+/* Workspace bytes of ep_layer_few calls with this configuration. Host only. */
+int ep_layer_few_sizes(const ep_config *cfg, int64_t *workspace_bytes);
+
+int ep_layer_few(const ep_config *cfg, const ep_layer_few_args *args, ep_stream_t stream);
 
 /* ------------------------------------------------- peers in other processes */
 

@@ -44,6 +44,10 @@ EP_LOGITS_F32 = 0
 EP_LOGITS_BF16 = 1
 EP_W4_INT = 0
 EP_W4_E2M1 = 1
+EP_ROWS_F32 = 0
+EP_ROWS_BF16 = 1
+EP_MAX_NORM_HIDDEN = 16384
+EP_MAX_FEW_TOKENS = 64
 
 _c_i32, _c_i64, _c_u64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p
 
@@ -121,6 +125,32 @@ class ep_w4_args(ctypes.Structure):
                 ("workspace_bytes", _c_i64), ("status", _vp)]
 
 
+class ep_add_rmsnorm_args(ctypes.Structure):
+    _fields_ = [("x", _vp), ("x_stride", _c_i64), ("residual", _vp), ("residual_stride", _c_i64),
+                ("residual_dtype", _c_i32), ("weight_dtype", _c_i32), ("weight", _vp),
+                ("eps", ctypes.c_float), ("hidden", _c_i32), ("sum", _vp), ("sum_stride", _c_i64),
+                ("y", _vp), ("y_stride", _c_i64), ("q", _vp), ("q_scales", _vp)]
+
+
+class ep_add_rmsnorm_backward_args(ctypes.Structure):
+    _fields_ = [("h", _vp), ("h_stride", _c_i64), ("h_dtype", _c_i32), ("weight_dtype", _c_i32),
+                ("dy", _vp), ("dy_stride", _c_i64), ("dsum", _vp), ("dsum_stride", _c_i64),
+                ("weight", _vp), ("eps", ctypes.c_float), ("hidden", _c_i32), ("dh", _vp),
+                ("dh_stride", _c_i64), ("dx", _vp), ("dx_stride", _c_i64), ("dweight", _vp),
+                ("workspace", _vp), ("workspace_bytes", _c_i64)]
+
+
+class ep_swiglu_e4m3_args(ctypes.Structure):
+    _fields_ = [("G", _vp), ("q", _vp), ("q_scales", _vp), ("expert_offsets", _vp),
+                ("max_rows", _c_i64), ("inter", _c_i32)]
+
+
+class ep_layer_few_args(ctypes.Structure):
+    _fields_ = [("x", _vp), ("x_scales", _vp), ("topk_ids", _vp), ("gates", _vp), ("W1", _vp),
+                ("w1_scales", _vp), ("W2", _vp), ("w2_scales", _vp), ("out", _vp),
+                ("workspace", _vp), ("workspace_bytes", _c_i64), ("status", _vp)]
+
+
 EP_IPC_HANDLE_BYTES = 64
 
 
@@ -141,7 +171,8 @@ EXPORTS = ("ep_plan_sizes", "ep_plan", "grouped_gemm_combine_send", "ep_combine_
            "ep_strerror", "grouped_gemm_combine_send_noalloc", "ep_scatter_send",
            "ep_dispatch_gather", "ep_swiglu", "ep_ipc_export", "ep_ipc_import", "ep_ipc_close",
            "ep_route", "ep_route_backward", "ep_combine_backward", "ep_matvec_w4_sizes",
-           "ep_matvec_w4")
+           "ep_matvec_w4", "ep_add_rmsnorm", "ep_add_rmsnorm_backward_sizes",
+           "ep_add_rmsnorm_backward", "ep_swiglu_e4m3", "ep_layer_few_sizes", "ep_layer_few")
 
 
 def load(build_if_missing: bool = True):
@@ -171,14 +202,20 @@ def load(build_if_missing: bool = True):
     L.ep_ipc_close.argtypes = [ctypes.POINTER(ep_ipc_handle), _vp]
     for f, args in (("ep_route", ep_route_args), ("ep_route_backward", ep_route_backward_args),
                     ("ep_combine_backward", ep_combine_backward_args),
-                    ("ep_matvec_w4", ep_w4_args)):
+                    ("ep_matvec_w4", ep_w4_args), ("ep_add_rmsnorm", ep_add_rmsnorm_args),
+                    ("ep_add_rmsnorm_backward", ep_add_rmsnorm_backward_args),
+                    ("ep_swiglu_e4m3", ep_swiglu_e4m3_args), ("ep_layer_few", ep_layer_few_args)):
         getattr(L, f).argtypes = [ctypes.POINTER(ep_config), ctypes.POINTER(args), _vp]
-    L.ep_matvec_w4_sizes.argtypes = [ctypes.POINTER(ep_config), ctypes.POINTER(_c_i64)]
+    for f in ("ep_matvec_w4_sizes", "ep_layer_few_sizes"):
+        getattr(L, f).argtypes = [ctypes.POINTER(ep_config), ctypes.POINTER(_c_i64)]
+    L.ep_add_rmsnorm_backward_sizes.argtypes = [ctypes.POINTER(ep_config), _c_i32,
+                                                ctypes.POINTER(_c_i64)]
     for f in ("ep_plan_sizes", "ep_plan", "grouped_gemm_combine_send", "ep_combine_reduce",
               "grouped_gemm_combine_send_noalloc", "ep_scatter_send", "ep_dispatch_gather",
               "ep_swiglu", "ep_ipc_export", "ep_ipc_import", "ep_ipc_close",
               "ep_route", "ep_route_backward", "ep_combine_backward", "ep_matvec_w4_sizes",
-              "ep_matvec_w4"):
+              "ep_matvec_w4", "ep_add_rmsnorm", "ep_add_rmsnorm_backward_sizes",
+              "ep_add_rmsnorm_backward", "ep_swiglu_e4m3", "ep_layer_few_sizes", "ep_layer_few"):
         getattr(L, f).restype = ctypes.c_int
     L.ep_strerror.argtypes = [ctypes.c_int]
     L.ep_strerror.restype = ctypes.c_char_p
@@ -291,6 +328,45 @@ def ep_matvec_w4(cfg: ep_config, args: ep_w4_args, stream=None) -> int:
     """Expert products of a few rows on 4-bit weights with group scales."""
     return _check(load().ep_matvec_w4(ctypes.byref(cfg), ctypes.byref(args),
                                       stream_handle(stream)), "ep_matvec_w4")
+
+
+def ep_add_rmsnorm(cfg: ep_config, args: ep_add_rmsnorm_args, stream=None) -> int:
+    """The residual's addition and the norm in front of a layer, in bf16 or 8 bits with scales."""
+    return _check(load().ep_add_rmsnorm(ctypes.byref(cfg), ctypes.byref(args),
+                                        stream_handle(stream)), "ep_add_rmsnorm")
+
+
+def ep_add_rmsnorm_backward_sizes(cfg: ep_config, hidden: int) -> int:
+    """Workspace bytes of ep_add_rmsnorm_backward."""
+    out = _c_i64(0)
+    _check(load().ep_add_rmsnorm_backward_sizes(ctypes.byref(cfg), hidden, ctypes.byref(out)),
+           "ep_add_rmsnorm_backward_sizes")
+    return int(out.value)
+
+
+def ep_add_rmsnorm_backward(cfg: ep_config, args: ep_add_rmsnorm_backward_args, stream=None) -> int:
+    """Gradients of the norm: of its input (and the residual), of its weight."""
+    return _check(load().ep_add_rmsnorm_backward(ctypes.byref(cfg), ctypes.byref(args),
+                                                 stream_handle(stream)), "ep_add_rmsnorm_backward")
+
+
+def ep_swiglu_e4m3(cfg: ep_config, args: ep_swiglu_e4m3_args, stream=None) -> int:
+    """SiLU(gate) * up from the up/gate GEMM's rows, as e4m3 rows with 1x128 scales."""
+    return _check(load().ep_swiglu_e4m3(ctypes.byref(cfg), ctypes.byref(args),
+                                        stream_handle(stream)), "ep_swiglu_e4m3")
+
+
+def ep_layer_few_sizes(cfg: ep_config) -> int:
+    """Workspace bytes of ep_layer_few (zero the workspace before its first use)."""
+    out = _c_i64(0)
+    _check(load().ep_layer_few_sizes(ctypes.byref(cfg), ctypes.byref(out)), "ep_layer_few_sizes")
+    return int(out.value)
+
+
+def ep_layer_few(cfg: ep_config, args: ep_layer_few_args, stream=None) -> int:
+    """A whole MoE layer for a few tokens: the rank's experts' part of their outputs."""
+    return _check(load().ep_layer_few(ctypes.byref(cfg), ctypes.byref(args),
+                                      stream_handle(stream)), "ep_layer_few")
 
 
 def ep_ipc_export(dev_ptr) -> ep_ipc_handle:

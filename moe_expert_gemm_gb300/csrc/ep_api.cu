@@ -1,6 +1,7 @@
 // Host side of the C ABI: argument checks, TMA descriptors, launches.
 #include <cudaTypedefs.h>
 
+#include <cfloat>
 #include <climits>
 #include <cstring>
 #include <mutex>
@@ -139,6 +140,27 @@ bool valid_logits(int dtype, int score, int64_t stride, int E)
     return (dtype == EP_LOGITS_F32 || dtype == EP_LOGITS_BF16) &&
            (score == EP_SCORE_SOFTMAX || score == EP_SCORE_SIGMOID) &&
            (stride == 0 || (stride >= E && stride <= INT32_MAX));
+}
+
+int row_bytes(int dtype)
+{
+    return dtype == EP_ROWS_BF16 ? 2 : 4;
+}
+
+bool valid_row_type(int dtype)
+{
+    return dtype == EP_ROWS_F32 || dtype == EP_ROWS_BF16;
+}
+
+bool valid_norm(int hidden, float eps, int row_dtype, int weight_dtype)
+{
+    return hidden >= 1 && eps >= 0.f && eps <= FLT_MAX && valid_row_type(row_dtype) &&
+           valid_row_type(weight_dtype);
+}
+
+bool valid_stride(int64_t stride, int cols)
+{
+    return stride == 0 || (stride >= cols && stride <= INT32_MAX);
 }
 
 int cuda_status(cudaError_t e)
@@ -728,6 +750,228 @@ int ep_matvec_w4(const ep_config *cfg, const ep_w4_args *a, ep_stream_t stream)
         return EP_ERR_CUDA;
     return cuda_status(
         ep::launch_matvec_w4(tw, p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int ep_add_rmsnorm(const ep_config *cfg, const ep_add_rmsnorm_args *a, ep_stream_t stream)
+{
+    int rc = check_config(cfg);
+    if (rc != EP_OK)
+        return rc;
+    if (!a || !valid_norm(a->hidden, a->eps, a->residual_dtype, a->weight_dtype))
+        return EP_ERR_INVALID_ARG;
+    if (!valid_stride(a->x_stride, a->hidden) || !valid_stride(a->residual_stride, a->hidden) ||
+        !valid_stride(a->sum_stride, a->hidden) || !valid_stride(a->y_stride, a->hidden))
+        return EP_ERR_INVALID_ARG;
+    if (a->hidden > EP_MAX_NORM_HIDDEN)
+        return EP_ERR_UNSUPPORTED;  // a row stays in one block's registers
+    if (cfg->num_tokens == 0)
+        return EP_OK;
+    const int rb = row_bytes(a->residual_dtype);
+    if (!a->x || !a->weight || (!a->sum && !a->y && !a->q) || !a->q != !a->q_scales ||
+        !aligned_to(a->x, 2) || !aligned_to(a->residual, rb) || !aligned_to(a->sum, rb) ||
+        !aligned_to(a->weight, row_bytes(a->weight_dtype)) || !aligned_to(a->y, 2) ||
+        !aligned_to(a->q_scales, 4))
+        return EP_ERR_INVALID_ARG;
+    const int num_sms = sm_count();
+    if (num_sms <= 0)
+        return EP_ERR_CUDA;
+    ep::NormParams p;
+    p.T = cfg->num_tokens;
+    p.hidden = a->hidden;
+    p.eps = a->eps;
+    p.residual_bf16 = a->residual_dtype == EP_ROWS_BF16;
+    p.weight_bf16 = a->weight_dtype == EP_ROWS_BF16;
+    p.x = static_cast<const uint8_t *>(a->x);
+    p.residual = static_cast<const uint8_t *>(a->residual);
+    p.weight = static_cast<const uint8_t *>(a->weight);
+    p.sum = static_cast<uint8_t *>(a->sum);
+    p.y = static_cast<uint8_t *>(a->y);
+    p.q = static_cast<uint8_t *>(a->q);
+    p.q_scales = a->q_scales;
+    p.x_stride = a->x_stride ? a->x_stride : a->hidden;
+    p.residual_stride = a->residual_stride ? a->residual_stride : a->hidden;
+    p.sum_stride = a->sum_stride ? a->sum_stride : a->hidden;
+    p.y_stride = a->y_stride ? a->y_stride : a->hidden;
+    return cuda_status(ep::launch_norm(p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int ep_add_rmsnorm_backward_sizes(const ep_config *cfg, int32_t hidden, int64_t *workspace_bytes)
+{
+    int rc = check_config(cfg);
+    if (rc != EP_OK)
+        return rc;
+    if (!workspace_bytes || hidden < 1)
+        return EP_ERR_INVALID_ARG;
+    if (hidden > EP_MAX_NORM_HIDDEN)
+        return EP_ERR_UNSUPPORTED;
+    *workspace_bytes = ep::norm_backward_workspace_bytes(cfg->num_tokens, hidden);
+    return EP_OK;
+}
+
+int ep_add_rmsnorm_backward(const ep_config *cfg, const ep_add_rmsnorm_backward_args *a,
+                            ep_stream_t stream)
+{
+    int rc = check_config(cfg);
+    if (rc != EP_OK)
+        return rc;
+    if (!a || !valid_norm(a->hidden, a->eps, a->h_dtype, a->weight_dtype))
+        return EP_ERR_INVALID_ARG;
+    if (!valid_stride(a->h_stride, a->hidden) || !valid_stride(a->dy_stride, a->hidden) ||
+        !valid_stride(a->dsum_stride, a->hidden) || !valid_stride(a->dh_stride, a->hidden) ||
+        !valid_stride(a->dx_stride, a->hidden))
+        return EP_ERR_INVALID_ARG;
+    if (a->hidden > EP_MAX_NORM_HIDDEN)
+        return EP_ERR_UNSUPPORTED;
+    if ((!a->dh && !a->dx && !a->dweight) || !aligned_to(a->dweight, 4))
+        return EP_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (cfg->num_tokens == 0)
+        return a->dweight ? cuda_status(cudaMemsetAsync(a->dweight, 0, sizeof(float) * a->hidden, s))
+                          : EP_OK;
+    const int hb = row_bytes(a->h_dtype);
+    if (!a->h || !a->dy || !a->weight || !aligned_to(a->h, hb) || !aligned_to(a->dy, 2) ||
+        !aligned_to(a->dsum, hb) || !aligned_to(a->dh, hb) || !aligned_to(a->dx, 2) ||
+        !aligned_to(a->weight, row_bytes(a->weight_dtype)))
+        return EP_ERR_INVALID_ARG;
+    if (a->dweight &&
+        (!a->workspace || !aligned16(a->workspace) ||
+         a->workspace_bytes < ep::norm_backward_workspace_bytes(cfg->num_tokens, a->hidden)))
+        return EP_ERR_INVALID_ARG;
+    const int num_sms = sm_count();
+    if (num_sms <= 0)
+        return EP_ERR_CUDA;
+    ep::NormBackwardParams p;
+    p.T = cfg->num_tokens;
+    p.hidden = a->hidden;
+    p.eps = a->eps;
+    p.h_bf16 = a->h_dtype == EP_ROWS_BF16;
+    p.weight_bf16 = a->weight_dtype == EP_ROWS_BF16;
+    p.h = static_cast<const uint8_t *>(a->h);
+    p.dy = static_cast<const uint8_t *>(a->dy);
+    p.dsum = static_cast<const uint8_t *>(a->dsum);
+    p.weight = static_cast<const uint8_t *>(a->weight);
+    p.dh = static_cast<uint8_t *>(a->dh);
+    p.dx = static_cast<uint8_t *>(a->dx);
+    p.dweight = a->dweight;
+    p.parts = static_cast<float *>(a->workspace);
+    p.h_stride = a->h_stride ? a->h_stride : a->hidden;
+    p.dy_stride = a->dy_stride ? a->dy_stride : a->hidden;
+    p.dsum_stride = a->dsum_stride ? a->dsum_stride : a->hidden;
+    p.dh_stride = a->dh_stride ? a->dh_stride : a->hidden;
+    p.dx_stride = a->dx_stride ? a->dx_stride : a->hidden;
+    return cuda_status(ep::launch_norm_backward(p, num_sms, s));
+}
+
+int ep_swiglu_e4m3(const ep_config *cfg, const ep_swiglu_e4m3_args *a, ep_stream_t stream)
+{
+    int rc = check_config(cfg);
+    if (rc != EP_OK)
+        return rc;
+    if (!a || !a->G || !a->q || !a->q_scales || !a->expert_offsets)
+        return EP_ERR_INVALID_ARG;
+    if (a->inter < 8 || a->inter % 8 != 0 || !aligned16(a->G) || !aligned_to(a->q, 8) ||
+        !aligned_to(a->q_scales, 4) || !aligned_to(a->expert_offsets, 4) || a->max_rows < 1 ||
+        a->max_rows > INT32_MAX)
+        return EP_ERR_INVALID_ARG;
+    const int num_sms = sm_count();
+    if (num_sms <= 0)
+        return EP_ERR_CUDA;
+    ep::SwigluE4m3Params p;
+    p.El = cfg->n_local_experts;
+    p.inter = a->inter;
+    p.max_rows = a->max_rows;
+    p.G = static_cast<const uint8_t *>(a->G);
+    p.q = static_cast<uint8_t *>(a->q);
+    p.q_scales = a->q_scales;
+    p.expert_offsets = a->expert_offsets;
+    return cuda_status(ep::launch_swiglu_e4m3(p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// The limits and sizes of ep_layer_few; fills what cfg gives of p.
+int few_sizes(const ep_config *cfg, ep::FewParams *p)
+{
+    int rc = check_config(cfg);
+    if (rc != EP_OK)
+        return rc;
+    const bool fp8 = cfg->dtype == EP_FP8_1D2D;
+    const int step = fp8 ? 128 : 8;
+    if (cfg->num_tokens > EP_MAX_FEW_TOKENS || cfg->top_k > kMaxRouteTopK || cfg->K % step != 0 ||
+        cfg->N % step != 0)
+        return EP_ERR_UNSUPPORTED;
+    // rows of W1 and the kernels' steps are counted in 32 bits
+    const int64_t El = cfg->n_local_experts;
+    if (2ll * cfg->K >= INT32_MAX ||
+        El * ((cfg->K + 127ll) / 128) * ((cfg->N + 63ll) / 64) >= INT32_MAX ||
+        El * ((cfg->N + 127ll) / 128) * ((cfg->K + 63ll) / 64) >= INT32_MAX)
+        return EP_ERR_UNSUPPORTED;
+    std::memset(p, 0, sizeof *p);
+    p->El = cfg->n_local_experts;
+    p->n_ranks = cfg->n_ranks;
+    p->my_rank = cfg->my_rank;
+    p->top_k = cfg->top_k;
+    p->T = cfg->num_tokens;
+    p->H = cfg->N;
+    p->I = cfg->K;
+    p->fp8 = fp8;
+    return EP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ep_layer_few_sizes(const ep_config *cfg, int64_t *workspace_bytes)
+{
+    ep::FewParams p;
+    const int rc = few_sizes(cfg, &p);
+    if (rc != EP_OK)
+        return rc;
+    if (!workspace_bytes)
+        return EP_ERR_INVALID_ARG;
+    *workspace_bytes = ep::few_workspace_bytes(p);
+    return EP_OK;
+}
+
+int ep_layer_few(const ep_config *cfg, const ep_layer_few_args *a, ep_stream_t stream)
+{
+    ep::FewParams p;
+    const int rc = few_sizes(cfg, &p);
+    if (rc != EP_OK)
+        return rc;
+    if (!a)
+        return EP_ERR_INVALID_ARG;
+    if (p.T == 0)
+        return EP_OK;
+    if (!a->x || !a->topk_ids || !a->gates || !a->W1 || !a->W2 || !a->out || !a->workspace || !a->status)
+        return EP_ERR_INVALID_ARG;
+    if (!aligned16(a->x) || !aligned16(a->W1) || !aligned16(a->W2) || !aligned16(a->workspace) ||
+        !aligned_to(a->out, 2) || !aligned_to(a->topk_ids, 4) || !aligned_to(a->gates, 4) ||
+        !aligned_to(a->status, 4))
+        return EP_ERR_INVALID_ARG;
+    if (p.fp8 && (!a->x_scales || !a->w1_scales || !a->w2_scales || !aligned_to(a->x_scales, 4) ||
+                  !aligned_to(a->w1_scales, 4) || !aligned_to(a->w2_scales, 4)))
+        return EP_ERR_INVALID_ARG;
+    if (a->workspace_bytes < ep::few_workspace_bytes(p))
+        return EP_ERR_INVALID_ARG;
+    const int num_sms = sm_count();
+    if (num_sms <= 0)
+        return EP_ERR_CUDA;
+    p.x = static_cast<const uint8_t *>(a->x);
+    p.W1 = static_cast<const uint8_t *>(a->W1);
+    p.W2 = static_cast<const uint8_t *>(a->W2);
+    p.x_scales = a->x_scales;
+    p.w1_scales = a->w1_scales;
+    p.w2_scales = a->w2_scales;
+    p.topk_ids = a->topk_ids;
+    p.gates = a->gates;
+    p.out = static_cast<uint8_t *>(a->out);
+    p.workspace = static_cast<uint8_t *>(a->workspace);
+    p.status = a->status;
+    return cuda_status(ep::launch_layer_few(p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 const char *ep_strerror(int code)

@@ -208,6 +208,50 @@ struct W4Params {
     uint32_t *status;
 };
 
+// The norm in front of a layer and its gradient (ep_norm.cu). Strides in elements.
+struct NormParams {
+    int T, hidden;
+    float eps;
+    int residual_bf16, weight_bf16;
+    const uint8_t *x, *residual, *weight;
+    uint8_t *sum, *y, *q;
+    float *q_scales;
+    int64_t x_stride, residual_stride, sum_stride, y_stride;
+};
+
+struct NormBackwardParams {
+    int T, hidden;
+    float eps;
+    int h_bf16, weight_bf16;
+    const uint8_t *h, *dy, *dsum, *weight;
+    uint8_t *dh, *dx;
+    float *dweight, *parts;  // parts: [blocks][hidden]
+    int64_t h_stride, dy_stride, dsum_stride, dh_stride, dx_stride;
+};
+
+// The activation in 8 bits (ep_swiglu_e4m3.cu).
+struct SwigluE4m3Params {
+    int El, inter;
+    int64_t max_rows;
+    const uint8_t *G;
+    uint8_t *q;
+    float *q_scales;
+    const int32_t *expert_offsets;
+};
+
+// The layer of a few tokens (ep_layer_few.cu).
+struct FewParams {
+    int El, n_ranks, my_rank, top_k, T, H, I;
+    int fp8;
+    const uint8_t *x, *W1, *W2;
+    const float *x_scales, *w1_scales, *w2_scales;
+    const int32_t *topk_ids;
+    const float *gates;
+    uint8_t *out;
+    uint8_t *workspace;
+    uint32_t *status;
+};
+
 // A checked grouped_gemm_combine_send call, ready to launch: prepare_send runs every
 // host check (returning EP_ERR_* with nothing enqueued), encodes the tensor maps and
 // picks the kernel; launch_prepared_send enqueues it (EP_OK or EP_ERR_CUDA).
@@ -242,5 +286,12 @@ cudaError_t launch_matvec_w4(const CUtensorMap &tw, const W4Params &p, int num_s
                              cudaStream_t s);
 cudaError_t launch_matvec_w4_wide(const CUtensorMap &tw, const W4Params &p, int num_sms,
                                   cudaStream_t s);
+
+cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t s);
+int64_t norm_backward_workspace_bytes(int T, int hidden);
+cudaError_t launch_norm_backward(const NormBackwardParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_swiglu_e4m3(const SwigluE4m3Params &p, int num_sms, cudaStream_t s);
+int64_t few_workspace_bytes(const FewParams &p);
+cudaError_t launch_layer_few(const FewParams &p, int num_sms, cudaStream_t s);
 
 }  // namespace ep

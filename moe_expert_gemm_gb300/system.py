@@ -15,16 +15,20 @@ import numpy as np
 import torch
 
 from . import (EP_ACT_NONE, EP_ACT_SWIGLU, EP_BF16, EP_FP8_1D2D, EP_LOGITS_BF16, EP_LOGITS_F32,
-               EP_SCORE_SOFTMAX, EP_W4_E2M1, EP_W4_INT, ep_combine_args, ep_combine_backward,
+               EP_ROWS_BF16, EP_ROWS_F32, EP_SCORE_SOFTMAX, EP_W4_E2M1, EP_W4_INT, ep_add_rmsnorm,
+               ep_add_rmsnorm_args, ep_add_rmsnorm_backward, ep_add_rmsnorm_backward_args,
+               ep_add_rmsnorm_backward_sizes, ep_combine_args, ep_combine_backward,
                ep_combine_backward_args, ep_combine_reduce, ep_config, ep_dispatch_args,
-               ep_dispatch_gather, ep_matvec_w4, ep_matvec_w4_sizes, ep_plan, ep_plan_out,
-               ep_plan_sizes, ep_route, ep_route_args, ep_route_backward, ep_route_backward_args,
-               ep_scatter_args, ep_scatter_send, ep_send_args, ep_swiglu, ep_swiglu_args,
+               ep_dispatch_gather, ep_layer_few, ep_layer_few_args, ep_layer_few_sizes, ep_matvec_w4,
+               ep_matvec_w4_sizes, ep_plan, ep_plan_out, ep_plan_sizes, ep_route, ep_route_args,
+               ep_route_backward, ep_route_backward_args, ep_scatter_args, ep_scatter_send,
+               ep_send_args, ep_swiglu, ep_swiglu_args, ep_swiglu_e4m3, ep_swiglu_e4m3_args,
                ep_w4_args, grouped_gemm_combine_send, ptr)
 from .w4 import W4Weights
 
 SENTINEL_BYTE = 0xFF  # received bf16 0xFFFF is a NaN: an unwritten slot cannot pass
-STATUS_PLAN, STATUS_SEND, STATUS_COMBINE, STATUS_ROUTE, STATUS_W4 = 0, 1, 2, 3, 4
+STATUS_PLAN, STATUS_SEND, STATUS_COMBINE, STATUS_ROUTE, STATUS_W4, STATUS_FEW = 0, 1, 2, 3, 4, 5
+E4M3 = (torch.float8_e4m3fn, torch.uint8)  # codes, or their bytes
 
 
 def _check_flat(name: str, t: torch.Tensor, count: int, dtype: torch.dtype, device: torch.device):
@@ -86,6 +90,8 @@ class EpSystem:
         self.out: list[torch.Tensor | None] = [None] * R
         self.routes: list[dict | None] = [None] * R
         self.layer_w4: list[dict | None] = [None] * R
+        self.layer_fp8: list[dict | None] = [None] * R
+        self.layer_few_ops: list[dict | None] = [None] * R
 
     # ------------------------------------------------------------- set-up
     def cfg(self, rank: int) -> ep_config:
@@ -417,6 +423,174 @@ class EpSystem:
         down.local_activation = EP_ACT_NONE
         ep_matvec_w4(self.cfg(rank), down, stream)
         ep_scatter_send(self.cfg(rank), self.scatter_args(rank, epoch, L["C"]), stream)
+
+    # ------------------------------------------------ norm in front of the layer
+    _ROWS = {torch.float32: EP_ROWS_F32, torch.bfloat16: EP_ROWS_BF16}
+
+    def _check_weight(self, weight: torch.Tensor) -> int:
+        if weight.dtype not in self._ROWS:
+            raise ValueError(f"weight: of {weight.dtype}, expected {' or '.join(map(str, self._ROWS))}")
+        _check_flat("weight", weight, self.N, weight.dtype, self.device)
+        return self._ROWS[weight.dtype]
+
+    def add_rmsnorm(self, rank: int, x: torch.Tensor, weight: torch.Tensor, residual=None,
+                    eps: float = 1e-6, sum=None, y=None, q=None, q_scales=None, stream=None):
+        """The residual's addition and the norm of a rank's tokens x [T][N] bf16, into what is
+        given: ``sum`` (their sum, in the residual's type: fp32 or bf16; may be the residual), ``y``
+        (bf16; may be x), ``q`` and ``q_scales`` (e4m3 [T][N] and fp32 [T][ceil(N/128)], contiguous:
+        the blockwise fp8 products' operands). Rows of x, residual, sum and y may lie any stride
+        of at least N apart; weight [N] is fp32 or bf16."""
+        T, N = self.T, self.N
+        a = ep_add_rmsnorm_args(weight=ptr(weight), weight_dtype=self._check_weight(weight), eps=eps,
+                                hidden=N, x=ptr(x), residual=ptr(residual), sum=ptr(sum), y=ptr(y),
+                                q=ptr(q), q_scales=ptr(q_scales))
+        a.x_stride = _check_rows("x", x, T, N, (torch.bfloat16,), self.device)
+        stream_type = residual if residual is not None else sum
+        if stream_type is not None:
+            if stream_type.dtype not in self._ROWS:
+                raise ValueError(f"residual: of {stream_type.dtype}")
+            a.residual_dtype = self._ROWS[stream_type.dtype]
+        if residual is not None:
+            a.residual_stride = _check_rows("residual", residual, T, N, tuple(self._ROWS), self.device)
+        if sum is not None:
+            a.sum_stride = _check_rows("sum", sum, T, N, (stream_type.dtype,), self.device)
+        if y is not None:
+            a.y_stride = _check_rows("y", y, T, N, (torch.bfloat16,), self.device)
+        if q is not None:
+            self._check_e4m3("q", q, T, N)
+        if q_scales is not None:
+            _check_flat("q_scales", q_scales, T * ((N + 127) // 128), torch.float32, self.device)
+        ep_add_rmsnorm(self.cfg(rank), a, stream)
+
+    def _check_e4m3(self, name: str, t: torch.Tensor, rows: int, cols: int):
+        if t.dtype not in E4M3:
+            raise ValueError(f"{name}: of {t.dtype}, expected {' or '.join(map(str, E4M3))}")
+        _check_flat(name, t, rows * cols, t.dtype, self.device)
+
+    def add_rmsnorm_backward(self, rank: int, h: torch.Tensor, dy: torch.Tensor,
+                             weight: torch.Tensor, dsum=None, eps: float = 1e-6, dh=None, dx=None,
+                             dweight=None, stream=None):
+        """Gradients of ``add_rmsnorm`` at h (its ``sum``, or its x), for its y's gradient ``dy``
+        [T][N] bf16 and its sum's ``dsum`` (h's type), into what is given: ``dh`` (h's type; may be
+        h or dsum), ``dx`` (the same in bf16; may be dy), ``dweight`` [N] fp32."""
+        T, N = self.T, self.N
+        if h.dtype not in self._ROWS:
+            raise ValueError(f"h: of {h.dtype}, expected {' or '.join(map(str, self._ROWS))}")
+        a = ep_add_rmsnorm_backward_args(h=ptr(h), h_dtype=self._ROWS[h.dtype], dy=ptr(dy),
+                                         dsum=ptr(dsum), weight=ptr(weight),
+                                         weight_dtype=self._check_weight(weight), eps=eps, hidden=N,
+                                         dh=ptr(dh), dx=ptr(dx), dweight=ptr(dweight))
+        a.h_stride = _check_rows("h", h, T, N, (h.dtype,), self.device)
+        a.dy_stride = _check_rows("dy", dy, T, N, (torch.bfloat16,), self.device)
+        if dsum is not None:
+            a.dsum_stride = _check_rows("dsum", dsum, T, N, (h.dtype,), self.device)
+        if dh is not None:
+            a.dh_stride = _check_rows("dh", dh, T, N, (h.dtype,), self.device)
+        if dx is not None:
+            a.dx_stride = _check_rows("dx", dx, T, N, (torch.bfloat16,), self.device)
+        if dweight is not None:
+            _check_flat("dweight", dweight, N, torch.float32, self.device)
+            a.workspace_bytes = ep_add_rmsnorm_backward_sizes(self.cfg(rank), N)
+            with self._on(stream):  # (the call's own: freed to this stream's later calls)
+                workspace = torch.empty(max(a.workspace_bytes, 16), dtype=torch.uint8,
+                                        device=self.device)
+            a.workspace = ptr(workspace)
+        ep_add_rmsnorm_backward(self.cfg(rank), a, stream)
+
+    # --------------------------------------------------- a layer on fp8 operands
+    def _check_fp8_weights(self, name: str, w: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
+        self._check_e4m3(name, w, self.El * rows, cols)
+        _check_flat(f"{name} scales", scales, self.El * (rows // 128) * (cols // 128), torch.float32,
+                    self.device)
+
+    def set_layer_fp8(self, rank: int, q: torch.Tensor, q_scales: torch.Tensor, W1: torch.Tensor,
+                      w1_scales: torch.Tensor, W2: torch.Tensor, w2_scales: torch.Tensor):
+        """Operands of a whole MoE layer on blockwise fp8: the rank's tokens as e4m3 rows
+        [max_tokens][H] with scales [max_tokens][H/128] (``add_rmsnorm``'s q and q_scales), its
+        experts' weights W1 [E_l][2I][H] (gate rows first) and W2 [E_l][H][I] in e4m3 with scales
+        of 128x128 blocks; H = N and I = K, H a multiple of 512 (the dispatch moves the scales'
+        rows in pieces of 16 bytes), I of 128. Allocates the layer's buffers; after ``plan``."""
+        H, I = self.N, self.K
+        if self.dtype != "fp8_1d2d" or H % 512 or I % 128:
+            raise ValueError(f"an fp8 layer of dtype {self.dtype}, H = {H}, I = {I}")
+        self._check_e4m3("q", q, self.max_tokens, H)
+        _check_flat("q_scales", q_scales, self.max_tokens * (H // 128), torch.float32, self.device)
+        self._check_fp8_weights("W1", W1, w1_scales, 2 * I, H)
+        self._check_fp8_weights("W2", W2, w2_scales, H, I)
+        dev, rows = self.device, max(self.plans[rank]["capacity"], 1)
+        empty = lambda cols, dtype: torch.zeros((rows, cols), dtype=dtype, device=dev)
+        self.layer_fp8[rank] = dict(q=q, q_scales=q_scales, W1=W1, w1_scales=w1_scales,
+                                    A_in=empty(H, torch.uint8), in_scales=empty(H // 128, torch.float32),
+                                    G=empty(2 * I, torch.bfloat16))
+        self.ops[rank] = dict(A=empty(I, torch.uint8), a_scales=empty(I // 128, torch.float32),
+                              W=W2, w_scales=w2_scales)
+
+    def layer_forward_fp8(self, rank: int, epoch: int, stream=None):
+        """Dispatch of codes and scales, up/gate product, activation to e4m3, then the fused
+        down-projection + send of producer ``rank`` (every ``layer_fp8[r]`` must hold rank r's
+        tokens)."""
+        L, p, o = self.layer_fp8[rank], self.plans[rank], self.ops[rank]
+        for name, out, bytes_ in (("q", L["A_in"], self.N), ("q_scales", L["in_scales"], self.N // 32)):
+            d = ep_dispatch_args(gather_idx=ptr(p["gather_idx"]), expert_offsets=ptr(p["expert_offsets"]),
+                                 max_rows=int(L["A_in"].shape[0]), hidden=bytes_ // 2, A_in=ptr(out),
+                                 status=self.status.data_ptr() + 4 * STATUS_SEND)
+            for r in range(self.R):
+                d.x_ptrs[r] = ptr(self.layer_fp8[r][name])
+            ep_dispatch_gather(self.cfg(rank), d, stream)
+        up = self.send_args(rank, epoch, -1, L["G"])
+        up.A, up.a_scales, up.W, up.w_scales = (ptr(L[n]) for n in ("A_in", "in_scales", "W1", "w1_scales"))
+        cfg_up = self.cfg_up(rank)
+        cfg_up.dtype = EP_FP8_1D2D
+        grouped_gemm_combine_send(cfg_up, up, stream)
+        a = ep_swiglu_e4m3_args(ptr(L["G"]), ptr(o["A"]), ptr(o["a_scales"]), ptr(p["expert_offsets"]),
+                                int(L["G"].shape[0]), self.K)
+        ep_swiglu_e4m3(self.cfg(rank), a, stream)
+        self.send(rank, epoch, stream)
+
+    # ------------------------------------------------------ a layer of a few tokens
+    def set_layer_few(self, rank: int, W1: torch.Tensor, W2: torch.Tensor, w1_scales=None,
+                      w2_scales=None):
+        """A rank's experts for ``layer_few``: W1 [E_l][2I][H] (gate rows first) and W2 [E_l][H][I],
+        bf16, or in an fp8 system e4m3 with the fp32 scales of 128x128 blocks; all contiguous.
+        Allocates the rank's workspace, on torch's current stream."""
+        H, I = self.N, self.K
+        if self.dtype == "bf16":
+            _check_flat("W1", W1, self.El * 2 * I * H, torch.bfloat16, self.device)
+            _check_flat("W2", W2, self.El * H * I, torch.bfloat16, self.device)
+        else:
+            if w1_scales is None or w2_scales is None:
+                raise ValueError("fp8 weights come with their scales")
+            self._check_fp8_weights("W1", W1, w1_scales, 2 * I, H)
+            self._check_fp8_weights("W2", W2, w2_scales, H, I)
+        self.layer_few_ops[rank] = dict(
+            W1=W1, W2=W2, w1_scales=w1_scales, w2_scales=w2_scales,
+            workspace=torch.zeros(ep_layer_few_sizes(self.cfg(rank)), dtype=torch.uint8,
+                                  device=self.device))
+
+    def layer_few(self, rank: int, x: torch.Tensor, out: torch.Tensor, x_scales=None, source=None,
+                  stream=None):
+        """Rank ``rank``'s part of the layer's outputs, into ``out`` [T][N] bf16, for the tokens x
+        [T][N] of rank ``source`` (``rank`` itself if not given) with that rank's routing and gates
+        (``route``, or ``set_routing`` and ``set_gates``): bf16, or in an fp8 system e4m3 with scales
+        [T][N/128]. With one rank that is the layer; the ranks' parts add up to it. One call of a
+        rank at a time (they share its workspace)."""
+        L, T, N = self.layer_few_ops[rank], self.T, self.N
+        source = rank if source is None else source
+        if self.dtype == "bf16":
+            _check_flat("x", x, T * N, torch.bfloat16, self.device)
+        else:
+            self._check_e4m3("x", x, T, N)
+            if x_scales is None:
+                raise ValueError("fp8 tokens come with their scales")
+            _check_flat("x_scales", x_scales, T * (N // 128), torch.float32, self.device)
+        _check_flat("out", out, T * N, torch.bfloat16, self.device)
+        a = ep_layer_few_args(x=ptr(x), x_scales=ptr(x_scales), topk_ids=ptr(self.topk[source]),
+                              gates=ptr(self.gates[source]), W1=ptr(L["W1"]),
+                              w1_scales=ptr(L["w1_scales"]), W2=ptr(L["W2"]),
+                              w2_scales=ptr(L["w2_scales"]), out=ptr(out),
+                              workspace=ptr(L["workspace"]), workspace_bytes=L["workspace"].numel(),
+                              status=self.status.data_ptr() + 4 * STATUS_FEW)
+        ep_layer_few(self.cfg(rank), a, stream)
 
     def send_traced(self, rank: int, epoch: int, records: int = 64, stream=None):
         """One send with per-tile timestamps; returns the decoded trace."""
