@@ -69,6 +69,23 @@ bool encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint6
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same over [outer][rows][inner] without gaps, in boxes of one of `outer`.
+bool encode_3d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows,
+               uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows)
+{
+    EncodeTiledFn fn = tensor_map_encoder();
+    if (!fn)
+        return false;
+    cuuint64_t dims[3] = {inner, rows, outer};
+    cuuint64_t strides[2] = {row_bytes, row_bytes * rows};
+    cuuint32_t box[3] = {box_inner, box_rows, 1};
+    cuuint32_t elem_strides[3] = {1, 1, 1};
+    return fn(map, dt, 3, const_cast<void *>(base), dims, strides, box, elem_strides,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int check_config(const ep_config *c)
 {
     if (!c)
@@ -971,7 +988,19 @@ int ep_layer_few(const ep_config *cfg, const ep_layer_few_args *a, ep_stream_t s
     p.out = static_cast<uint8_t *>(a->out);
     p.workspace = static_cast<uint8_t *>(a->workspace);
     p.status = a->status;
-    return cuda_status(ep::launch_layer_few(p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
+    const CUtensorMapDataType dt =
+        p.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t elem = p.fp8 ? 1 : 2, H = p.H, I = p.I;
+    const uint32_t box_k = static_cast<uint32_t>(128 / elem);
+    ep::FewMaps maps;
+    if (!encode_3d(&maps.w1, dt, a->W1, H, 2 * I, p.El, H * elem, box_k, 128) ||
+        !encode_3d(&maps.w2, dt, a->W2, I, H, p.El, I * elem, box_k, 128) ||
+        !encode_2d(&maps.x, dt, a->x, H, p.T, H * elem, box_k, ep::few_columns(p.T)) ||
+        !encode_2d(&maps.h, dt, p.workspace + ep::few_workspace_rows(p.T), I,
+                   static_cast<uint64_t>(p.T) * p.top_k, I * elem, box_k, 16))
+        return EP_ERR_CUDA;
+    return cuda_status(
+        ep::launch_layer_few(maps, p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 const char *ep_strerror(int code)

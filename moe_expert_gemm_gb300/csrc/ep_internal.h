@@ -252,6 +252,14 @@ struct FewParams {
     uint32_t *status;
 };
 
+// Steps of 128 bytes along k: boxes of 128 weight rows (of one expert), of few_columns() tokens,
+// of 16 rows of the activation (which lies few_workspace_rows() bytes into the workspace).
+struct FewMaps {
+    CUtensorMap w1, x, w2, h;
+};
+int few_columns(int T);
+int64_t few_workspace_rows(int T);
+
 // A checked grouped_gemm_combine_send call, ready to launch: prepare_send runs every
 // host check (returning EP_ERR_* with nothing enqueued), encodes the tensor maps and
 // picks the kernel; launch_prepared_send enqueues it (EP_OK or EP_ERR_CUDA).
@@ -292,6 +300,6 @@ int64_t norm_backward_workspace_bytes(int T, int hidden);
 cudaError_t launch_norm_backward(const NormBackwardParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_swiglu_e4m3(const SwigluE4m3Params &p, int num_sms, cudaStream_t s);
 int64_t few_workspace_bytes(const FewParams &p);
-cudaError_t launch_layer_few(const FewParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_layer_few(const FewMaps &maps, const FewParams &p, int num_sms, cudaStream_t s);
 
 }  // namespace ep

@@ -1,6 +1,28 @@
-// A whole MoE layer for a few tokens: the up/gate products with the activation, then the down
-// products with the gates, a kernel each. Bound by the weights of the experts that have tokens.
-// This is the plain form: a warp takes one value of one token's activation, or of its output.
+// A whole MoE layer for a few tokens, in two kernels: the up/gate products with the activation,
+// and the down products with the gates.
+//
+//   h[row(t, e)] = SiLU(Wgate_e x_t) * (Wup_e x_t),   out[t] = sum_e g(t, e) W2_e h[row(t, e)]
+//
+// Every weight of an expert that has tokens is read once and meets at most 64 of them, so the
+// call is bound by the weights' bytes. They stream through shared memory (TMA, 128-byte swizzle)
+// into tcgen05.mma as its 128-row operand, straight from where they land; the tokens are the
+// product's columns, 16 at least: no instruction of any warp touches a weight.
+//
+//  * A step is 128 bytes of k by two tiles of 128 weight rows: up/gate, the gate rows of 128
+//    intermediate indices and their up rows, whose sums meet in the same lane of tensor memory;
+//    down, 256 rows of the output. The tokens' piece comes along, from the L2.
+//  * Work is a list of units of equal numbers of steps: up/gate, an expert's 128 indices; down,
+//    256 rows of the output with all experts one after the other, so that a token's sum over
+//    its experts never leaves the block. The list is cut into one run a block, of whole units or,
+//    where that balances better, anywhere (Runs); units that are cut are joined through the
+//    workspace by the last of their blocks, in block order.
+//  * Sums are taken out of tensor memory into registers (fp32), a thread to a weight row, with a
+//    factor: the gate at an expert's end (down), or, e4m3, the scales of each 128 k.
+//    Tensor memory holds two periods' sums, so that the products go on meanwhile.
+//  * The plan (who has which expert) is made by every block for itself from the ids, with a
+//    64-bit mask of tokens for each expert.
+//  * The second kernel starts while the first one's last blocks finish: a block makes its plan
+//    and fills its ring with weights before it waits for the activations.
 #include "ep_internal.h"
 #include "ep_ptx.cuh"
 #include "ep_rows.cuh"
@@ -9,130 +31,652 @@ namespace ep {
 
 namespace {
 
-constexpr int kFewThreads = 256;
+constexpr int kHalf = 128;                     // weight rows of one product
+constexpr int kWeightBytes = 2 * kHalf * 128;  // of a step
+constexpr int kMaxBlocks = 160;
+constexpr int kMaxRows = EP_MAX_FEW_TOKENS * 32;
+constexpr int kEpilogueWarps = 8;  // four for each half
+constexpr int kThreads = 32 * (4 + kEpilogueWarps);
+constexpr int kEpilogueThreads = 32 * kEpilogueWarps;
+constexpr int kPartBase = 4096;  // of the workspace; counters before it
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+static_assert(kMaxBlocks * 4 <= kPartBase, "counters");
 
-__device__ __forceinline__ float value(const uint8_t *base, int64_t i, bool fp8)
+// Steps that the joining of cut units is worth, and the fewest of a block.
+constexpr int kJoinSteps = 4, kMinSteps = 2;
+
+struct Segment {
+    int unit, s0, s1;  // steps [s0, s1) of the unit
+};
+
+// How the units' steps are cut into the blocks' runs.
+struct Runs {
+    int per, rest;  // pieces of every run; the first `rest` runs have one more
+    int piece;      // steps of a piece: 1, or a unit's
+
+    // The block whose run holds step i (of runs cut at any step).
+    __device__ int owner(int i) const
+    {
+        return i < rest * (per + 1) ? i / (per + 1) : rest + (i - rest * (per + 1)) / per;
+    }
+};
+
+template <int NT>
+constexpr int stages()
 {
-    if (fp8)
-        return __half2float(__nv_cvt_fp8_to_halfraw(base[i], __NV_E4M3));
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(base)[i]);
+    return NT == 16 ? 6 : 5;
 }
 
-__device__ __forceinline__ float warp_sum(float v)
+struct Shared {
+    uint64_t full[6], empty[6];
+    uint64_t sums_full[2], sums_empty[2];
+    uint64_t drained;
+    unsigned long long mask[EP_MAX_LOCAL_EXPERTS];  // tokens of each local expert
+    uint32_t tmem;
+    int abort;
+    int n_active, start, todo;  // active experts; the run
+    Runs runs;
+    Segment cut[2];  // the units the block's run begins and ends inside
+    int last[2];
+    uint16_t active[EP_MAX_LOCAL_EXPERTS];  // experts that have tokens, ascending
+    uint16_t place[EP_MAX_LOCAL_EXPERTS];   // of an expert among them
+    int16_t first[EP_MAX_LOCAL_EXPERTS];    // first row of the place's tokens
+    float gate[kMaxRows];                   // of each row (down)
+    float up[8][kHalf];                     // exchange of eight tokens' up sums
+    uint32_t size[8][4];                    // their largest magnitudes in 32 rows each
+};
+
+template <int NT>
+constexpr int smem_bytes()
 {
+    return 1024 + stages<NT>() * (kWeightBytes + NT * 128) + static_cast<int>(sizeof(Shared));
+}
+
+__device__ __forceinline__ void give_up(const FewParams &p, Shared &sh)
+{
+    atomicOr(p.status, EP_STATUS_TIMEOUT);
+    *reinterpret_cast<volatile int *>(&sh.abort) = 1;
+}
+
+// Which tokens each local expert has, the experts that have some, the first row of each, and
+// (down) every row's gate. All threads; ends with a barrier.
+template <bool DOWN>
+__device__ __forceinline__ void make_plan(const FewParams &p, Shared &sh)
+{
+    const int tid = threadIdx.x, slots = p.T * p.top_k, first = p.my_rank * p.El;
+    for (int e = tid; e < p.El; e += kThreads)
+        sh.mask[e] = 0;
+    __syncthreads();
+    bool bad = false;
+    for (int s = tid; s < slots; s += kThreads) {
+        const int id = __ldg(p.topk_ids + s), e = id - first;
+        bad |= id < 0 || id >= p.n_ranks * p.El;
+        if (id >= first && e < p.El)
+            atomicOr(&sh.mask[e], 1ull << (s / p.top_k));
+    }
+    if (!DOWN && bad && blockIdx.x == 0)
+        atomicOr(p.status, EP_STATUS_ROUTING);
+    __syncthreads();
+    if (tid < 32) {
+        int places = 0, rows = 0;
+        for (int e0 = 0; e0 < p.El; e0 += 32) {
+            const int e = e0 + tid, n = e < p.El ? __popcll(sh.mask[e]) : 0;
+            const uint32_t has = __ballot_sync(0xffffffffu, n > 0);
+            int upto = n;
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (tid >= o)
+                    upto += v;
+            }
+            if (n > 0) {
+                const int place = places + __popc(has & ((1u << tid) - 1));
+                sh.active[place] = static_cast<uint16_t>(e);
+                sh.place[e] = static_cast<uint16_t>(place);
+                sh.first[place] = static_cast<int16_t>(rows + upto - n);
+            }
+            places += __popc(has);
+            rows += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        if (tid == 0)
+            sh.n_active = places;
+    }
+    __syncthreads();
+    if (DOWN) {
+        for (int s = tid; s < slots; s += kThreads) {
+            const int t = s / p.top_k, j = s - t * p.top_k;
+            const int32_t *ids = p.topk_ids + t * p.top_k;
+            const int id = __ldg(ids + j), e = id - first;
+            if (id < first || e >= p.El)
+                continue;
+            // an expert named twice: the first slot has the sum of the gates
+            bool again = false;
+            for (int i = 0; i < j; ++i)
+                again |= __ldg(ids + i) == id;
+            if (again)
+                continue;
+            float g = __ldg(p.gates + s);
+            for (int i = j + 1; i < p.top_k; ++i)
+                if (__ldg(ids + i) == id)
+                    g += __ldg(p.gates + t * p.top_k + i);
+            sh.gate[sh.first[sh.place[e]] + __popcll(sh.mask[e] & ((1ull << t) - 1))] = g;
+        }
+    }
 }
 
-// The local expert of a slot; -1 if it lives elsewhere, -2 if nowhere.
-__device__ __forceinline__ int local_expert(const FewParams &p, int slot)
+// The segments of a block's run, one after the other.
+struct Walk {
+    int unit, s0, todo, steps;
+
+    __device__ Walk(const Shared &sh, int steps_)
+        : unit(steps_ ? sh.start / steps_ : 0), s0(steps_ ? sh.start - unit * steps_ : 0), todo(sh.todo), steps(steps_)
+    {
+    }
+
+    __device__ __forceinline__ bool next(Segment &s)
+    {
+        if (todo <= 0)
+            return false;
+        s.unit = unit++;
+        s.s0 = s0;
+        s.s1 = todo < steps - s0 ? s0 + todo : steps;
+        todo -= s.s1 - s.s0;
+        s0 = 0;
+        return true;
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void advance(int &i, T &phase, int n)
 {
-    const int id = __ldg(p.topk_ids + slot);
-    if (id < 0 || id >= p.n_ranks * p.El)
-        return -2;
-    return id / p.El == p.my_rank ? id % p.El : -1;
+    if (++i == n) {
+        i = 0;
+        phase ^= 1;
+    }
 }
 
 }  // namespace
 
-// a[slot][i] in fp32.
-__global__ void __launch_bounds__(kFewThreads) few_up_kernel(const FewParams p)
+int few_columns(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+
+int64_t few_workspace_rows(int T)
 {
-    griddep_wait();
-    griddep_launch_dependents();
-    float *a = reinterpret_cast<float *>(p.workspace);
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kFewThreads / 32);
-    const int64_t all = static_cast<int64_t>(p.T) * p.top_k * p.I;
-    for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kFewThreads / 32) + threadIdx.x / 32; w < all; w += warps) {
-        const int slot = static_cast<int>(w / p.I), i = static_cast<int>(w % p.I), t = slot / p.top_k;
-        const int e = local_expert(p, slot);
-        if (e < 0) {
-            if (e == -2 && i == 0 && lane == 0)
-                atomicOr(p.status, EP_STATUS_ROUTING);
-            continue;
-        }
-        const int64_t gate_row = static_cast<int64_t>(e) * 2 * p.I + i, up_row = gate_row + p.I;
-        float gate = 0.f, up = 0.f;
-        for (int k = lane; k < p.H; k += 32) {
-            const float x = value(p.x, static_cast<int64_t>(t) * p.H + k, p.fp8);
-            float wg = value(p.W1, gate_row * p.H + k, p.fp8), wu = value(p.W1, up_row * p.H + k, p.fp8);
-            if (p.fp8) {
-                const float s = p.x_scales[static_cast<int64_t>(t) * (p.H / 128) + k / 128];
-                wg *= s * p.w1_scales[gate_row / 128 * (p.H / 128) + k / 128];
-                wu *= s * p.w1_scales[up_row / 128 * (p.H / 128) + k / 128];
-            }
-            gate = fmaf(wg, x, gate);
-            up = fmaf(wu, x, up);
-        }
-        gate = warp_sum(gate);
-        up = warp_sum(up);
-        if (lane == 0)
-            a[w] = silu_f32(gate) * up;
-    }
+    return kPartBase + static_cast<int64_t>(kMaxBlocks) * 2 * few_columns(T) * 2 * kHalf * 4;
 }
 
-__global__ void __launch_bounds__(kFewThreads) few_down_kernel(const FewParams p)
+// In the workspace: counters, partial sums, the activation's rows, and (e4m3) their scales.
+static int64_t few_workspace_scales(const FewParams &p)
 {
-    griddep_wait();
-    griddep_launch_dependents();
-    const float *a = reinterpret_cast<const float *>(p.workspace);
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kFewThreads / 32);
-    const int64_t all = static_cast<int64_t>(p.T) * p.H;
-    for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kFewThreads / 32) + threadIdx.x / 32; w < all; w += warps) {
-        const int t = static_cast<int>(w / p.H), n = static_cast<int>(w % p.H);
-        float out = 0.f;
-        for (int j = 0; j < p.top_k; ++j) {
-            const int slot = t * p.top_k + j, e = local_expert(p, slot);
-            if (e < 0)
-                continue;
-            const int64_t row = static_cast<int64_t>(e) * p.H + n;
-            float y = 0.f;
-            for (int k0 = 0; k0 < p.I; k0 += 128) {
-                float v[4];
-                uint32_t bits = 0;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int k = k0 + 32 * u + lane;
-                    v[u] = k < p.I ? a[static_cast<int64_t>(slot) * p.I + k] : 0.f;
-                    bits = max(bits, rows::size_bits(v[u]));
-                }
-                const float s = rows::scale_of(__reduce_max_sync(0xffffffffu, bits));
-                float part = 0.f;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int k = k0 + 32 * u + lane;
-                    if (k >= p.I)
-                        continue;
-                    if (p.fp8) {
-                        const __nv_fp8_storage_t q = __nv_cvt_float_to_fp8(v[u] * (1.f / s), __NV_SATFINITE, __NV_E4M3);
-                        v[u] = __half2float(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3));
-                    } else {
-                        v[u] = __bfloat162float(__float2bfloat16_rn(v[u]));
-                    }
-                    part = fmaf(value(p.W2, row * p.I + k, p.fp8), v[u], part);
-                }
-                y = p.fp8 ? fmaf(s * p.w2_scales[row / 128 * (p.I / 128) + k0 / 128], part, y) : y + part;
-            }
-            out = fmaf(__ldg(p.gates + slot), warp_sum(y), out);
-        }
-        if (lane == 0)
-            reinterpret_cast<__nv_bfloat16 *>(p.out)[w] = __float2bfloat16_rn(out);
-    }
+    const int64_t rows = static_cast<int64_t>(p.T) * p.top_k;
+    return few_workspace_rows(p.T) + (rows * p.I * (p.fp8 ? 1 : 2) + 127) / 128 * 128;
 }
 
 int64_t few_workspace_bytes(const FewParams &p)
 {
-    return static_cast<int64_t>(p.T) * p.top_k * p.I * 4 + 16;
+    return few_workspace_scales(p) + (p.fp8 ? static_cast<int64_t>(p.T) * p.top_k * (p.I / 128) * 4 : 0);
 }
 
-cudaError_t launch_layer_few(const FewParams &p, int num_sms, cudaStream_t s)
+// NT: columns of a product at most, 16, 32 or 64.
+template <bool DOWN, bool FP8, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    few_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
+               const __grid_constant__ FewParams p, uint8_t *h_rows, float *h_scales)
 {
-    const cudaError_t e = launch_behind(few_up_kernel, 8 * num_sms, kFewThreads, 0, s, p);
-    return e != cudaSuccess ? e : launch_behind(few_down_kernel, 8 * num_sms, kFewThreads, 0, s, p);
+    constexpr int kStages = stages<NT>();
+    constexpr int kStage = kWeightBytes + NT * 128;
+    constexpr int kStepK = FP8 ? 128 : 64;
+    constexpr uint32_t kTmemCols = 4 * NT;  // two periods of two halves
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    Shared &sh = *reinterpret_cast<Shared *>(ring + kStages * kStage);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 64) {
+        tma_prefetch_map(&tw);
+        tma_prefetch_map(&tx);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.sums_full[i], 1);
+            mbar_init(&sh.sums_empty[i], kEpilogueWarps);
+        }
+        mbar_init(&sh.drained, 1);
+        fence_mbar_init();
+        sh.abort = 0;
+        sh.cut[0].unit = sh.cut[1].unit = -1;
+    }
+    if (!DOWN) {
+        griddep_wait();
+        griddep_launch_dependents();
+    }
+    // (the first kernel waited for all that came before it ahead of letting the second one start:
+    // ids, gates and weights are there; only what the first kernel writes is waited for below)
+    make_plan<DOWN>(p, sh);
+    const int tiles = DOWN ? (p.H + 2 * kHalf - 1) / (2 * kHalf) : (p.I + kHalf - 1) / kHalf;
+    const int expert_steps = ((DOWN ? p.I : p.H) + kStepK - 1) / kStepK;
+    const int units = DOWN ? tiles : tiles * sh.n_active;
+    const int steps = DOWN ? expert_steps * sh.n_active : expert_steps;
+    if (tid == 0) {
+        const int grid = static_cast<int>(gridDim.x), block = static_cast<int>(blockIdx.x);
+        const int total = units * steps;
+        int cut = (total + grid - 1) / grid;
+        cut = cut < kMinSteps ? kMinSteps : cut;
+        const bool whole = (units + grid - 1) / grid * steps <= cut + kJoinSteps;
+        const int blocks = whole || total / grid >= kMinSteps ? grid : (total + kMinSteps - 1) / kMinSteps;
+        Runs runs;
+        runs.piece = whole ? steps : 1;
+        runs.per = (whole ? units : total) / blocks;
+        runs.rest = (whole ? units : total) - runs.per * blocks;
+        sh.runs = runs;
+        sh.start = (block * runs.per + (block < runs.rest ? block : runs.rest)) * runs.piece;
+        sh.todo = block < blocks ? (runs.per + (block < runs.rest)) * runs.piece : 0;
+    }
+    if (warp == 1) {
+        tmem_alloc(&sh.tmem, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    volatile int *abort_flag = &sh.abort;
+    Walk walk(sh, steps);
+    Segment seg;
+    int stage = 0;
+    uint32_t phase = 0;
+
+    if (warp == 0) {
+        // ------------------------------------------- producer: weights and columns
+        if (lane == 0) {
+            // one step's place, coordinates and columns
+            struct At {
+                int unit, place, k;
+            };
+            auto start_of = [&](const Segment &s) {
+                return DOWN ? At{s.unit, s.s0 / expert_steps, s.s0 % expert_steps}
+                            : At{s.unit % tiles, s.unit / tiles, s.s0};
+            };
+            auto columns = [&](const At &at) {  // (in 16s)
+                return DOWN ? (__popcll(sh.mask[sh.active[at.place]]) + 15) / 16 : NT / 16;
+            };
+            auto load_weights = [&](const At &at, int i) {
+                const int e = sh.active[at.place], y0 = at.unit * (DOWN ? 2 * kHalf : kHalf);
+                uint8_t *dst = ring + i * kStage;
+                mbar_arrive_expect_tx(&sh.full[i], kWeightBytes + columns(at) * 2048);
+                tma_load_3d(dst, &tw, &sh.full[i], at.k * kStepK, y0, e);
+                tma_load_3d(dst + kHalf * 128, &tw, &sh.full[i], at.k * kStepK, y0 + (DOWN ? kHalf : p.I), e);
+            };
+            auto load_columns = [&](const At &at, int i) {
+                uint8_t *dst = ring + i * kStage + kWeightBytes;
+                if (DOWN) {
+                    const int n = columns(at), row = sh.first[at.place];
+                    for (int c = 0; c < n; ++c)
+                        tma_load_2d(dst + c * 2048, &tx, &sh.full[i], at.k * kStepK, row + 16 * c);
+                } else {
+                    tma_load_2d(dst, &tx, &sh.full[i], at.k * kStepK, 0);
+                }
+            };
+            int issued = 0;
+            bool ok = true;
+            if (DOWN) {
+                // a ring full of weights, then, once they are there, its columns
+                for (int pass = 0; pass < 2; ++pass) {
+                    Walk ahead = walk;
+                    int n = 0;
+                    if (pass == 1)
+                        griddep_wait();
+                    while (n < kStages && ahead.next(seg)) {
+                        At at = start_of(seg);
+                        for (int s = seg.s0; s < seg.s1 && n < kStages; ++s, ++n) {
+                            if (pass == 0)
+                                load_weights(at, n);
+                            else
+                                load_columns(at, n);
+                            if (++at.k == expert_steps)
+                                at.k = 0, ++at.place;
+                        }
+                    }
+                    issued = n;
+                }
+            }
+            int skip = issued;
+            while (ok && walk.next(seg)) {
+                At at = start_of(seg);
+                for (int s = seg.s0; s < seg.s1; ++s) {
+                    if (skip > 0) {
+                        --skip;
+                    } else {
+                        if (!mbar_wait(&sh.empty[stage], phase ^ 1, kTimeoutNs, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        load_weights(at, stage);
+                        load_columns(at, stage);
+                        ++issued;
+                    }
+                    advance(stage, phase, kStages);
+                    if (DOWN && ++at.k == expert_steps)
+                        at.k = 0, ++at.place;
+                    else if (!DOWN)
+                        ++at.k;
+                }
+            }
+            if (!ok) {
+                give_up(p, sh);
+                // the copies in flight land before the block's shared memory goes away
+                volatile int no_abort = 0;
+                for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+                    mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, 1000000, &no_abort);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- products
+        if (lane == 0) {
+            bool ok = true;
+            int buf = 0;
+            uint32_t buf_phase = 0;
+            while (ok && walk.next(seg)) {
+                int place = DOWN ? seg.s0 / expert_steps : 0, k = DOWN ? seg.s0 % expert_steps : seg.s0;
+                bool fresh = true;  // a period begins
+                uint32_t idesc = 0;
+                for (int s = seg.s0; s < seg.s1; ++s) {
+                    if (fresh) {
+                        const int n = DOWN ? __popcll(sh.mask[sh.active[place]]) : p.T;
+                        idesc = make_idesc(FP8 ? 0u : 1u, kHalf, (n + 15) / 16 * 16);
+                        ok = mbar_wait(&sh.sums_empty[buf], buf_phase ^ 1, kTimeoutNs, abort_flag);
+                    }
+                    ok = ok && mbar_wait(&sh.full[stage], phase, kTimeoutNs, abort_flag);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint32_t w = smem_u32(ring + stage * kStage), x = w + kWeightBytes;
+                    const uint32_t d = tmem + buf * 2 * NT;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint64_t a = desc_kmajor_sw128(w + half * kHalf * 128 + j * 32);
+                            const uint64_t b = desc_kmajor_sw128(x + j * 32);
+                            if (FP8)
+                                mma_f8(d + half * NT, a, b, idesc, !fresh || j > 0);
+                            else
+                                mma_f16(d + half * NT, a, b, idesc, !fresh || j > 0);
+                        }
+                    mma_commit(&sh.empty[stage]);
+                    advance(stage, phase, kStages);
+                    const bool expert_ends = ++k == expert_steps;
+                    fresh = FP8 || s + 1 == seg.s1 || (DOWN && expert_ends);
+                    if (fresh) {
+                        mma_commit(&sh.sums_full[buf]);
+                        advance(buf, buf_phase, 2);
+                    }
+                    if (expert_ends)
+                        k = 0, ++place;
+                }
+            }
+            if (!ok)
+                give_up(p, sh);
+            // every product issued has ended once this arrives
+            mma_commit(&sh.drained);
+            volatile int no_abort = 0;
+            mbar_wait(&sh.drained, 0, kTimeoutNs, &no_abort);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ sums, results
+        if (DOWN)
+            griddep_wait();
+        const int half = (warp - 4) / 4, quarter = warp & 3, row = 32 * quarter + lane;
+        const int etid = tid - 32 * 4;
+        const uint32_t my_sums = tmem + half * NT + (static_cast<uint32_t>(32 * quarter) << 16);
+        float *const parts = reinterpret_cast<float *>(p.workspace + kPartBase);
+        auto part_of = [&](int slot) { return parts + (static_cast<int64_t>(slot) * NT * 2 + half) * kHalf + row; };
+        const uint64_t all_tokens = p.T == 64 ? ~0ull : (1ull << p.T) - 1;
+        float acc[NT];
+
+        // A whole unit's sums in acc: the activation's rows, or the output's.
+        auto finish = [&](int unit) {
+            if constexpr (DOWN) {
+                const int n = unit * 2 * kHalf + half * kHalf + row;
+                if (n < p.H) {
+                    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + n;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        if (t < p.T)
+                            out[static_cast<int64_t>(t) * p.H] = __float2bfloat16_rn(acc[t]);
+                }
+            } else {
+                const int place = unit / tiles, i = (unit - place * tiles) * kHalf + row;
+                const uint64_t mask = sh.mask[sh.active[place]];
+                int64_t at = sh.first[place];  // the next token's row
+#pragma unroll
+                for (int t0 = 0; t0 < NT; t0 += 8) {
+                    const uint32_t here = static_cast<uint32_t>(mask >> t0) & 0xFF;
+                    if (!here)
+                        continue;
+                    if (half == 1) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            if (here >> c & 1)
+                                sh.up[c][row] = acc[t0 + c];
+                    }
+                    named_bar_sync(1, kEpilogueThreads);
+                    if (half == 0) {
+                        float v[8];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            if (!(here >> c & 1))
+                                continue;
+                            v[c] = silu_f32(acc[t0 + c]) * sh.up[c][row];
+                            if (FP8) {
+                                const uint32_t m = __reduce_max_sync(0xffffffffu, rows::size_bits(v[c]));
+                                if (lane == 0)
+                                    sh.size[c][quarter] = m;
+                            }
+                        }
+                        if (FP8)
+                            named_bar_sync(2, kHalf);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            if (!(here >> c & 1))
+                                continue;
+                            if (FP8) {
+                                const float s = rows::scale_of(max(max(sh.size[c][0], sh.size[c][1]),
+                                                                   max(sh.size[c][2], sh.size[c][3])));
+                                h_rows[at * p.I + i] = __nv_cvt_float_to_fp8(v[c] * (1.f / s), __NV_SATFINITE, __NV_E4M3);
+                                if (row == 0)
+                                    h_scales[at * (p.I / 128) + i / 128] = s;
+                            } else if (i < p.I) {
+                                reinterpret_cast<__nv_bfloat16 *>(h_rows)[at * p.I + i] = __float2bfloat16_rn(v[c]);
+                            }
+                            ++at;
+                        }
+                    } else {
+                        at += __popc(here);
+                    }
+                    named_bar_sync(1, kEpilogueThreads);
+                }
+            }
+        };
+        // The tokens whose sums a unit has.
+        auto tokens_of = [&](int unit) { return DOWN ? all_tokens : static_cast<uint64_t>(sh.mask[sh.active[unit / tiles]]); };
+
+        bool ok = true;
+        int buf = 0;
+        uint32_t buf_phase = 0;
+        while (walk.next(seg)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                acc[t] = 0.f;
+            int place = DOWN ? seg.s0 / expert_steps : seg.unit / tiles;
+            int k = DOWN ? seg.s0 % expert_steps : seg.s0;
+            const int tile = DOWN ? seg.unit : seg.unit % tiles;
+            for (int s = seg.s0; ok && s < seg.s1;) {
+                // one period: its steps, tokens and factors (of tokens `lane` and lane + 32)
+                const int e = sh.active[place];
+                const uint64_t mask = sh.mask[e];
+                int n = FP8 ? 1 : (DOWN ? expert_steps - k : seg.s1 - s);
+                n = n < seg.s1 - s ? n : seg.s1 - s;
+                float factor[NT > 32 ? 2 : 1];
+#pragma unroll
+                for (int i = 0; i < (NT > 32 ? 2 : 1); ++i) {
+                    const int t = 32 * i + lane;
+                    factor[i] = 1.f;
+                    if ((DOWN || FP8) && t < NT && (mask >> t & 1)) {
+                        const int r = sh.first[place] + __popcll(mask & ((1ull << t) - 1));
+                        if (FP8) {
+                            const int64_t groups = DOWN ? p.I / 128 : p.H / 128;
+                            const int n0 = DOWN ? tile * 2 * kHalf + half * kHalf : tile * kHalf + half * p.I;
+                            const int block = min(n0, (DOWN ? p.H : 2 * p.I) - 1) / 128;
+                            const int64_t blocks = DOWN ? p.H / 128 : p.I / 64;
+                            factor[i] = (DOWN ? h_scales[r * groups + k] : __ldg(p.x_scales + t * groups + k)) *
+                                        __ldg((DOWN ? p.w2_scales : p.w1_scales) + (e * blocks + block) * groups + k);
+                        }
+                        if (DOWN)
+                            factor[i] *= sh.gate[r];
+                    }
+                }
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(&sh.sums_full[buf], buf_phase, kTimeoutNs, abort_flag));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint32_t from = my_sums + buf * 2 * NT;
+                int col = 0;
+#pragma unroll
+                for (int t0 = 0; t0 < NT; t0 += 16) {
+                    const uint32_t here = static_cast<uint32_t>(mask >> t0) & 0xFFFF;
+                    if (!here)
+                        continue;
+                    uint32_t v[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        v[c] = 0;
+                        if (here >> c & 1)
+                            v[c] = tmem_ld_32x32b_x1(from + (DOWN ? col++ : t0 + c));
+                    }
+                    tmem_ld_wait();
+                    tmem_regs_ready(v);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        if (here >> c & 1) {
+                            const float f = __shfl_sync(0xffffffffu, factor[(t0 + c) / 32], (t0 + c) % 32);
+                            acc[t0 + c] = fmaf(f, __uint_as_float(v[c]), acc[t0 + c]);
+                        }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sh.sums_empty[buf]);
+                advance(buf, buf_phase, 2);
+                s += n;
+                if ((k += n) == expert_steps)
+                    k = 0, ++place;
+            }
+            // (all of these warps leave together: they meet at barriers below)
+            if (!ok && lane == 0)
+                give_up(p, sh);
+            if (!named_bar_and(1, kEpilogueThreads, ok)) {
+                ok = false;
+                break;
+            }
+            if (seg.s0 == 0 && seg.s1 == steps) {
+                finish(seg.unit);
+            } else {
+                const int slot = seg.s0 == 0 ? 1 : 0;
+                const uint64_t tokens = tokens_of(seg.unit);
+                float *to = part_of(blockIdx.x * 2 + slot);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (tokens >> t & 1)
+                        __stcg(to + t * 2 * kHalf, acc[t]);
+                if (etid == 0)
+                    sh.cut[slot] = seg;
+            }
+        }
+        // the block's cut units, after all else: the last of a unit's blocks to come here adds
+        // what they left, in block order
+        if (sh.runs.piece == 1 && named_bar_and(1, kEpilogueThreads, ok)) {
+            int *counters = reinterpret_cast<int *>(p.workspace);
+            if (etid == 0 || etid == 32) {
+                const int slot = etid / 32, unit = sh.cut[slot].unit;
+                int last = 0;
+                if (unit >= 0) {
+                    const int c0 = sh.runs.owner(unit * steps), c1 = sh.runs.owner(unit * steps + steps - 1);
+                    last = atom_add_acq_rel_gpu(counters + c0, 1) == c1 - c0;
+                    if (last)
+                        counters[c0] = 0;  // ready for the next call
+                }
+                sh.last[slot] = last;
+            }
+            named_bar_sync(1, kEpilogueThreads);
+            for (int slot = 0; slot < 2; ++slot) {
+                if (!sh.last[slot])
+                    continue;
+                const int unit = sh.cut[slot].unit;
+                const int c0 = sh.runs.owner(unit * steps), c1 = sh.runs.owner(unit * steps + steps - 1);
+                const uint64_t tokens = tokens_of(unit);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    acc[t] = 0.f;
+                for (int b = c0; b <= c1; ++b) {
+                    const float *theirs = part_of(b * 2 + (b == c0 ? 1 : 0));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        if (tokens >> t & 1)
+                            acc[t] += __ldcg(theirs + t * 2 * kHalf);
+                }
+                finish(unit);
+            }
+        }
+    } else if (DOWN && warp == 2) {
+        griddep_wait();
+        griddep_launch_dependents();
+        // no token has an expert here
+        if (sh.n_active == 0) {
+            const int64_t all = static_cast<int64_t>(p.T) * p.H;
+            for (int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane; i < all; i += static_cast<int64_t>(gridDim.x) * 32)
+                reinterpret_cast<__nv_bfloat16 *>(p.out)[i] = __float2bfloat16_rn(0.f);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        tmem_dealloc(tmem, kTmemCols);
+}
+
+template <bool FP8, int NT>
+static cudaError_t launch_form(const FewMaps &maps, const FewParams &p, int num_sms, cudaStream_t s)
+{
+    const auto up = few_kernel<false, FP8, NT>, down = few_kernel<true, FP8, NT>;
+    constexpr int smem = smem_bytes<NT>();
+    static_assert(smem <= 227 * 1024, "shared memory of a block");
+    cudaError_t e = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    const int grid = num_sms < kMaxBlocks ? num_sms : kMaxBlocks;
+    uint8_t *h_rows = p.workspace + few_workspace_rows(p.T);
+    float *h_scales = reinterpret_cast<float *>(p.workspace + few_workspace_scales(p));
+    e = launch_behind(up, grid, kThreads, smem, s, maps.w1, maps.x, p, h_rows, h_scales);
+    return e != cudaSuccess ? e
+                            : launch_behind(down, grid, kThreads, smem, s, maps.w2, maps.h, p, h_rows, h_scales);
+}
+
+cudaError_t launch_layer_few(const FewMaps &maps, const FewParams &p, int num_sms, cudaStream_t s)
+{
+    switch (few_columns(p.T)) {
+    case 16:
+        return p.fp8 ? launch_form<true, 16>(maps, p, num_sms, s) : launch_form<false, 16>(maps, p, num_sms, s);
+    case 32:
+        return p.fp8 ? launch_form<true, 32>(maps, p, num_sms, s) : launch_form<false, 32>(maps, p, num_sms, s);
+    default:
+        return p.fp8 ? launch_form<true, 64>(maps, p, num_sms, s) : launch_form<false, 64>(maps, p, num_sms, s);
+    }
 }
 
 }  // namespace ep
