@@ -8,21 +8,26 @@
 // into tcgen05.mma as its 128-row operand, straight from where they land; the tokens are the
 // product's columns, 16 at least: no instruction of any warp touches a weight.
 //
-//  * A step is 128 bytes of k by two tiles of 128 weight rows: up/gate, the gate rows of 128
-//    intermediate indices and their up rows, whose sums meet in the same lane of tensor memory;
-//    down, 256 rows of the output. The tokens' piece comes along, from the L2.
+//  * A step is two tiles of 128 weight rows by 128 bytes of k. Up/gate: the gate rows of 128
+//    intermediate indices and their up rows, whose sums meet in the same lane of tensor memory.
+//    Down: twice as much k of 128 rows of the output, so that few blocks share a row's sum. The
+//    tokens' pieces come along, from the L2.
 //  * Work is a list of units of equal numbers of steps: up/gate, an expert's 128 indices; down,
-//    256 rows of the output with all experts one after the other, so that a token's sum over
+//    128 rows of the output with all experts one after the other, so that a token's sum over
 //    its experts never leaves the block. The list is cut into one run a block, of whole units or,
 //    where that balances better, anywhere (Runs); units that are cut are joined through the
 //    workspace by the last of their blocks, in block order.
 //  * Sums are taken out of tensor memory into registers (fp32), a thread to a weight row, with a
 //    factor: the gate at an expert's end (down), or, e4m3, the scales of each 128 k.
-//    Tensor memory holds two periods' sums, so that the products go on meanwhile.
+//    Tensor memory holds two periods' sums, so that the products go on meanwhile. Two groups
+//    of four warps do that: one for the gate and one for the up rows, or (down) for half of
+//    the tokens each.
 //  * The plan (who has which expert) is made by every block for itself from the ids, with a
 //    64-bit mask of tokens for each expert.
 //  * The second kernel starts while the first one's last blocks finish: a block makes its plan
 //    and fills its ring with weights before it waits for the activations.
+#include <type_traits>
+
 #include "ep_internal.h"
 #include "ep_ptx.cuh"
 #include "ep_rows.cuh"
@@ -31,11 +36,11 @@ namespace ep {
 
 namespace {
 
-constexpr int kHalf = 128;                     // weight rows of one product
-constexpr int kWeightBytes = 2 * kHalf * 128;  // of a step
+constexpr int kTile = 128;                     // weight rows of one product
+constexpr int kWeightBytes = 2 * kTile * 128;  // of a step
 constexpr int kMaxBlocks = 160;
 constexpr int kMaxRows = EP_MAX_FEW_TOKENS * 32;
-constexpr int kEpilogueWarps = 8;  // four for each half
+constexpr int kEpilogueWarps = 8;  // two groups of four
 constexpr int kThreads = 32 * (4 + kEpilogueWarps);
 constexpr int kEpilogueThreads = 32 * kEpilogueWarps;
 constexpr int kPartBase = 4096;  // of the workspace; counters before it
@@ -61,12 +66,31 @@ struct Runs {
     }
 };
 
-template <int NT>
-constexpr int stages()
+template <bool DOWN, int NT>
+constexpr int stage_bytes()
 {
-    return NT == 16 ? 6 : 5;
+    return kWeightBytes + (DOWN ? 2 : 1) * NT * 128;
 }
 
+template <bool DOWN, int NT>
+constexpr int stages()
+{
+    return !DOWN && NT == 16 ? 6 : DOWN && NT == 64 ? 4 : 5;
+}
+
+// Exchange of eight tokens' up sums, and their largest magnitudes in 32 rows each.
+struct Exchange {
+    float up[8][kTile];
+    uint32_t size[8][4];
+};
+
+// Gates of each slot, of each row, and the slots' local experts (-1: not here).
+struct Gates {
+    float of_slot[kMaxRows], of_row[kMaxRows];
+    int16_t expert[kMaxRows];
+};
+
+template <bool DOWN>
 struct Shared {
     uint64_t full[6], empty[6];
     uint64_t sums_full[2], sums_empty[2];
@@ -81,18 +105,17 @@ struct Shared {
     uint16_t active[EP_MAX_LOCAL_EXPERTS];  // experts that have tokens, ascending
     uint16_t place[EP_MAX_LOCAL_EXPERTS];   // of an expert among them
     int16_t first[EP_MAX_LOCAL_EXPERTS];    // first row of the place's tokens
-    float gate[kMaxRows];                   // of each row (down)
-    float up[8][kHalf];                     // exchange of eight tokens' up sums
-    uint32_t size[8][4];                    // their largest magnitudes in 32 rows each
+    std::conditional_t<DOWN, Gates, Exchange> x;
 };
 
-template <int NT>
+template <bool DOWN, int NT>
 constexpr int smem_bytes()
 {
-    return 1024 + stages<NT>() * (kWeightBytes + NT * 128) + static_cast<int>(sizeof(Shared));
+    return 1024 + stages<DOWN, NT>() * stage_bytes<DOWN, NT>() + static_cast<int>(sizeof(Shared<DOWN>));
 }
 
-__device__ __forceinline__ void give_up(const FewParams &p, Shared &sh)
+template <typename S>
+__device__ __forceinline__ void give_up(const FewParams &p, S &sh)
 {
     atomicOr(p.status, EP_STATUS_TIMEOUT);
     *reinterpret_cast<volatile int *>(&sh.abort) = 1;
@@ -101,7 +124,7 @@ __device__ __forceinline__ void give_up(const FewParams &p, Shared &sh)
 // Which tokens each local expert has, the experts that have some, the first row of each, and
 // (down) every row's gate. All threads; ends with a barrier.
 template <bool DOWN>
-__device__ __forceinline__ void make_plan(const FewParams &p, Shared &sh)
+__device__ __forceinline__ void make_plan(const FewParams &p, Shared<DOWN> &sh)
 {
     const int tid = threadIdx.x, slots = p.T * p.top_k, first = p.my_rank * p.El;
     for (int e = tid; e < p.El; e += kThreads)
@@ -110,9 +133,14 @@ __device__ __forceinline__ void make_plan(const FewParams &p, Shared &sh)
     bool bad = false;
     for (int s = tid; s < slots; s += kThreads) {
         const int id = __ldg(p.topk_ids + s), e = id - first;
+        const bool here = id >= first && e < p.El;
         bad |= id < 0 || id >= p.n_ranks * p.El;
-        if (id >= first && e < p.El)
+        if (here)
             atomicOr(&sh.mask[e], 1ull << (s / p.top_k));
+        if constexpr (DOWN) {
+            sh.x.expert[s] = static_cast<int16_t>(here ? e : -1);
+            sh.x.of_slot[s] = __ldg(p.gates + s);
+        }
     }
     if (!DOWN && bad && blockIdx.x == 0)
         atomicOr(p.status, EP_STATUS_ROUTING);
@@ -142,24 +170,22 @@ __device__ __forceinline__ void make_plan(const FewParams &p, Shared &sh)
             sh.n_active = places;
     }
     __syncthreads();
-    if (DOWN) {
+    if constexpr (DOWN) {
         for (int s = tid; s < slots; s += kThreads) {
-            const int t = s / p.top_k, j = s - t * p.top_k;
-            const int32_t *ids = p.topk_ids + t * p.top_k;
-            const int id = __ldg(ids + j), e = id - first;
-            if (id < first || e >= p.El)
+            const int t = s / p.top_k, s0 = t * p.top_k, e = sh.x.expert[s];
+            if (e < 0)
                 continue;
             // an expert named twice: the first slot has the sum of the gates
             bool again = false;
-            for (int i = 0; i < j; ++i)
-                again |= __ldg(ids + i) == id;
+            for (int i = s0; i < s; ++i)
+                again |= sh.x.expert[i] == e;
             if (again)
                 continue;
-            float g = __ldg(p.gates + s);
-            for (int i = j + 1; i < p.top_k; ++i)
-                if (__ldg(ids + i) == id)
-                    g += __ldg(p.gates + t * p.top_k + i);
-            sh.gate[sh.first[sh.place[e]] + __popcll(sh.mask[e] & ((1ull << t) - 1))] = g;
+            float g = sh.x.of_slot[s];
+            for (int i = s + 1; i < s0 + p.top_k; ++i)
+                if (sh.x.expert[i] == e)
+                    g += sh.x.of_slot[i];
+            sh.x.of_row[sh.first[sh.place[e]] + __popcll(sh.mask[e] & ((1ull << t) - 1))] = g;
         }
     }
 }
@@ -168,7 +194,8 @@ __device__ __forceinline__ void make_plan(const FewParams &p, Shared &sh)
 struct Walk {
     int unit, s0, todo, steps;
 
-    __device__ Walk(const Shared &sh, int steps_)
+    template <typename S>
+    __device__ Walk(const S &sh, int steps_)
         : unit(steps_ ? sh.start / steps_ : 0), s0(steps_ ? sh.start - unit * steps_ : 0), todo(sh.todo), steps(steps_)
     {
     }
@@ -186,6 +213,14 @@ struct Walk {
     }
 };
 
+// Place of the n-th set bit.
+__device__ __forceinline__ int nth_bit(uint64_t bits, int n)
+{
+    const uint32_t lo = static_cast<uint32_t>(bits), hi = static_cast<uint32_t>(bits >> 32);
+    const int in_lo = __popc(lo);
+    return n < in_lo ? static_cast<int>(__fns(lo, 0, n + 1)) : 32 + static_cast<int>(__fns(hi, 0, n - in_lo + 1));
+}
+
 template <typename T>
 __device__ __forceinline__ void advance(int &i, T &phase, int n)
 {
@@ -201,7 +236,7 @@ int few_columns(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 
 int64_t few_workspace_rows(int T)
 {
-    return kPartBase + static_cast<int64_t>(kMaxBlocks) * 2 * few_columns(T) * 2 * kHalf * 4;
+    return kPartBase + static_cast<int64_t>(kMaxBlocks) * 2 * few_columns(T) * 2 * kTile * 4;
 }
 
 // In the workspace: counters, partial sums, the activation's rows, and (e4m3) their scales.
@@ -222,13 +257,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     few_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
                const __grid_constant__ FewParams p, uint8_t *h_rows, float *h_scales)
 {
-    constexpr int kStages = stages<NT>();
-    constexpr int kStage = kWeightBytes + NT * 128;
-    constexpr int kStepK = FP8 ? 128 : 64;
-    constexpr uint32_t kTmemCols = 4 * NT;  // two periods of two halves
+    constexpr int kStages = stages<DOWN, NT>();
+    constexpr int kStage = stage_bytes<DOWN, NT>();
+    constexpr int kBlockK = FP8 ? 128 : 64;            // k of 128 bytes
+    constexpr int kStepK = DOWN ? 2 * kBlockK : kBlockK;
+    constexpr int kUnitRows = kTile;                   // (of the gate, too, of the up matrix)
+    constexpr uint32_t kTmemCols = 4 * NT;  // two periods of two products' sums
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    Shared &sh = *reinterpret_cast<Shared *>(ring + kStages * kStage);
+    Shared<DOWN> &sh = *reinterpret_cast<Shared<DOWN> *>(ring + kStages * kStage);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 64) {
         tma_prefetch_map(&tw);
@@ -253,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (the first kernel waited for all that came before it ahead of letting the second one start:
     // ids, gates and weights are there; only what the first kernel writes is waited for below)
     make_plan<DOWN>(p, sh);
-    const int tiles = DOWN ? (p.H + 2 * kHalf - 1) / (2 * kHalf) : (p.I + kHalf - 1) / kHalf;
+    const int tiles = ((DOWN ? p.H : p.I) + kUnitRows - 1) / kUnitRows;
     const int expert_steps = ((DOWN ? p.I : p.H) + kStepK - 1) / kStepK;
     const int units = DOWN ? tiles : tiles * sh.n_active;
     const int steps = DOWN ? expert_steps * sh.n_active : expert_steps;
@@ -301,18 +338,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return DOWN ? (__popcll(sh.mask[sh.active[at.place]]) + 15) / 16 : NT / 16;
             };
             auto load_weights = [&](const At &at, int i) {
-                const int e = sh.active[at.place], y0 = at.unit * (DOWN ? 2 * kHalf : kHalf);
+                const int e = sh.active[at.place], y = at.unit * kUnitRows, x = at.k * kStepK;
                 uint8_t *dst = ring + i * kStage;
-                mbar_arrive_expect_tx(&sh.full[i], kWeightBytes + columns(at) * 2048);
-                tma_load_3d(dst, &tw, &sh.full[i], at.k * kStepK, y0, e);
-                tma_load_3d(dst + kHalf * 128, &tw, &sh.full[i], at.k * kStepK, y0 + (DOWN ? kHalf : p.I), e);
+                mbar_arrive_expect_tx(&sh.full[i], kWeightBytes + columns(at) * (DOWN ? 4096 : 2048));
+                tma_load_3d(dst, &tw, &sh.full[i], x, y, e);
+                tma_load_3d(dst + kTile * 128, &tw, &sh.full[i], DOWN ? x + kBlockK : x, DOWN ? y : y + p.I, e);
             };
             auto load_columns = [&](const At &at, int i) {
                 uint8_t *dst = ring + i * kStage + kWeightBytes;
                 if (DOWN) {
-                    const int n = columns(at), row = sh.first[at.place];
-                    for (int c = 0; c < n; ++c)
-                        tma_load_2d(dst + c * 2048, &tx, &sh.full[i], at.k * kStepK, row + 16 * c);
+                    const int n = columns(at), row = sh.first[at.place], x = at.k * kStepK;
+                    for (int c = 0; c < n; ++c) {
+                        tma_load_2d(dst + c * 2048, &tx, &sh.full[i], x, row + 16 * c);
+                        tma_load_2d(dst + NT * 128 + c * 2048, &tx, &sh.full[i], x + kBlockK, row + 16 * c);
+                    }
                 } else {
                     tma_load_2d(dst, &tx, &sh.full[i], at.k * kStepK, 0);
                 }
@@ -384,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int s = seg.s0; s < seg.s1; ++s) {
                     if (fresh) {
                         const int n = DOWN ? __popcll(sh.mask[sh.active[place]]) : p.T;
-                        idesc = make_idesc(FP8 ? 0u : 1u, kHalf, (n + 15) / 16 * 16);
+                        idesc = make_idesc(FP8 ? 0u : 1u, kTile, (n + 15) / 16 * 16);
                         ok = mbar_wait(&sh.sums_empty[buf], buf_phase ^ 1, kTimeoutNs, abort_flag);
                     }
                     ok = ok && mbar_wait(&sh.full[stage], phase, kTimeoutNs, abort_flag);
@@ -392,17 +431,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     tc_fence_after();
                     const uint32_t w = smem_u32(ring + stage * kStage), x = w + kWeightBytes;
+                    // the step's two tiles: other rows (up/gate) or k (down) of their own, or, bf16,
+                    // more of the same sum
                     const uint32_t d = tmem + buf * 2 * NT;
+                    constexpr bool one_sum = DOWN && !FP8;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const uint64_t a = desc_kmajor_sw128(w + half * kHalf * 128 + j * 32);
-                            const uint64_t b = desc_kmajor_sw128(x + j * 32);
+                        for (int j = 0; j < 4; ++j) {
+                            const uint64_t a = desc_kmajor_sw128(w + i * kTile * 128 + j * 32);
+                            const uint64_t b = desc_kmajor_sw128(x + (DOWN ? i * NT * 128 : 0) + j * 32);
+                            const uint32_t more = !fresh || j > 0 || (one_sum && i > 0);
                             if (FP8)
-                                mma_f8(d + half * NT, a, b, idesc, !fresh || j > 0);
+                                mma_f8(d + i * NT, a, b, idesc, more);
                             else
-                                mma_f16(d + half * NT, a, b, idesc, !fresh || j > 0);
+                                mma_f16(one_sum ? d : d + i * NT, a, b, idesc, more);
                         }
                     mma_commit(&sh.empty[stage]);
                     advance(stage, phase, kStages);
@@ -428,27 +471,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ sums, results
         if (DOWN)
             griddep_wait();
-        const int half = (warp - 4) / 4, quarter = warp & 3, row = 32 * quarter + lane;
+        const int group = (warp - 4) / 4, quarter = warp & 3, row = 32 * quarter + lane;
         const int etid = tid - 32 * 4;
-        const uint32_t my_sums = tmem + half * NT + (static_cast<uint32_t>(32 * quarter) << 16);
+        // this thread's row of `tokens` sums: of the gate or the up rows, or of half of the tokens
+        constexpr int kTokens = DOWN ? NT / 2 : NT;
+        const int base = DOWN ? group * kTokens : 0;
+        const uint32_t my_sums = tmem + (DOWN ? 0 : group * NT) + (static_cast<uint32_t>(32 * quarter) << 16);
         float *const parts = reinterpret_cast<float *>(p.workspace + kPartBase);
-        auto part_of = [&](int slot) { return parts + (static_cast<int64_t>(slot) * NT * 2 + half) * kHalf + row; };
-        const uint64_t all_tokens = p.T == 64 ? ~0ull : (1ull << p.T) - 1;
-        float acc[NT];
+        constexpr int kPartRows = DOWN ? kTile : 2 * kTile;  // of a part, by NT tokens
+        auto part_of = [&](int slot) {
+            return parts + (static_cast<int64_t>(slot) * NT + base) * kPartRows + (DOWN ? 0 : group * kTile) + row;
+        };
+        static_assert(kPartBase % 16 == 0, "sums are read in pieces of four");
+        // (bit t: token base + t)
+        auto mine = [&](uint64_t mask) {
+            return DOWN ? (mask >> base) & ((1ull << kTokens) - 1) : mask;
+        };
+        const uint64_t all_tokens = mine(p.T == 64 ? ~0ull : (1ull << p.T) - 1);
+        float acc[kTokens];
 
         // A whole unit's sums in acc: the activation's rows, or the output's.
         auto finish = [&](int unit) {
             if constexpr (DOWN) {
-                const int n = unit * 2 * kHalf + half * kHalf + row;
+                const int n = unit * kUnitRows + row;
                 if (n < p.H) {
-                    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + n;
+                    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + static_cast<int64_t>(base) * p.H + n;
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        if (t < p.T)
+                    for (int t = 0; t < kTokens; ++t)
+                        if (all_tokens >> t & 1)
                             out[static_cast<int64_t>(t) * p.H] = __float2bfloat16_rn(acc[t]);
                 }
             } else {
-                const int place = unit / tiles, i = (unit - place * tiles) * kHalf + row;
+                const int place = unit / tiles, i = (unit - place * tiles) * kUnitRows + row;
                 const uint64_t mask = sh.mask[sh.active[place]];
                 int64_t at = sh.first[place];  // the next token's row
 #pragma unroll
@@ -456,35 +510,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t here = static_cast<uint32_t>(mask >> t0) & 0xFF;
                     if (!here)
                         continue;
-                    if (half == 1) {
+                    if (group == 1) {
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
                             if (here >> c & 1)
-                                sh.up[c][row] = acc[t0 + c];
+                                sh.x.up[c][row] = acc[t0 + c];
                     }
                     named_bar_sync(1, kEpilogueThreads);
-                    if (half == 0) {
+                    if (group == 0) {
                         float v[8];
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
                             if (!(here >> c & 1))
                                 continue;
-                            v[c] = silu_f32(acc[t0 + c]) * sh.up[c][row];
+                            v[c] = silu_f32(acc[t0 + c]) * sh.x.up[c][row];
                             if (FP8) {
                                 const uint32_t m = __reduce_max_sync(0xffffffffu, rows::size_bits(v[c]));
                                 if (lane == 0)
-                                    sh.size[c][quarter] = m;
+                                    sh.x.size[c][quarter] = m;
                             }
                         }
                         if (FP8)
-                            named_bar_sync(2, kHalf);
+                            named_bar_sync(2, kTile);
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
                             if (!(here >> c & 1))
                                 continue;
                             if (FP8) {
-                                const float s = rows::scale_of(max(max(sh.size[c][0], sh.size[c][1]),
-                                                                   max(sh.size[c][2], sh.size[c][3])));
+                                const float s = rows::scale_of(max(max(sh.x.size[c][0], sh.x.size[c][1]),
+                                                                   max(sh.x.size[c][2], sh.x.size[c][3])));
                                 h_rows[at * p.I + i] = __nv_cvt_float_to_fp8(v[c] * (1.f / s), __NV_SATFINITE, __NV_E4M3);
                                 if (row == 0)
                                     h_scales[at * (p.I / 128) + i / 128] = s;
@@ -493,77 +547,118 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             ++at;
                         }
-                    } else {
-                        at += __popc(here);
                     }
                     named_bar_sync(1, kEpilogueThreads);
                 }
             }
         };
-        // The tokens whose sums a unit has.
-        auto tokens_of = [&](int unit) { return DOWN ? all_tokens : static_cast<uint64_t>(sh.mask[sh.active[unit / tiles]]); };
+
+        // The factors of a period's sums, of tokens base + lane (and + 32): e4m3, the tokens' and
+        // the weights' scales of one or (down) two blocks of k. Asked for a period ahead.
+        constexpr int kSets = kTokens > 32 ? 2 : 1, kBlocks = DOWN ? 2 : 1;
+        struct Scales {
+            float token[kSets][kBlocks], weight[kBlocks];
+        };
+        auto load_scales = [&](int place, int tile, int k) {
+            Scales sc = {};
+            if constexpr (FP8) {
+                const int e = sh.active[place];
+                const uint64_t mask = sh.mask[e];
+                const int groups = (DOWN ? p.I : p.H) / 128;
+                const float *w = (DOWN ? p.w2_scales + (static_cast<int64_t>(e) * (p.H / 128) + tile) * groups
+                                       : p.w1_scales + (static_cast<int64_t>(e) * (p.I / 64) + group * (p.I / 128) + tile) * groups);
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    const int kb = k * kBlocks + b;
+                    if (kb >= groups)
+                        break;  // (nothing is there: sums of 0)
+                    sc.weight[b] = __ldg(w + kb);
+#pragma unroll
+                    for (int i = 0; i < kSets; ++i) {
+                        const int t = base + 32 * i + lane;
+                        if (32 * i + lane < kTokens && (mask >> t & 1)) {
+                            const int r = DOWN ? sh.first[place] + __popcll(mask & ((1ull << t) - 1)) : t;
+                            sc.token[i][b] = (DOWN ? h_scales : p.x_scales)[static_cast<int64_t>(r) * groups + kb];
+                        }
+                    }
+                }
+            }
+            return sc;
+        };
 
         bool ok = true;
         int buf = 0;
         uint32_t buf_phase = 0;
         while (walk.next(seg)) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < kTokens; ++t)
                 acc[t] = 0.f;
             int place = DOWN ? seg.s0 / expert_steps : seg.unit / tiles;
             int k = DOWN ? seg.s0 % expert_steps : seg.s0;
             const int tile = DOWN ? seg.unit : seg.unit % tiles;
+            Scales sc = load_scales(place, tile, k);
             for (int s = seg.s0; ok && s < seg.s1;) {
-                // one period: its steps, tokens and factors (of tokens `lane` and lane + 32)
-                const int e = sh.active[place];
-                const uint64_t mask = sh.mask[e];
+                // one period: its steps, tokens and factors
+                const uint64_t mask = sh.mask[sh.active[place]], here = mine(mask);
                 int n = FP8 ? 1 : (DOWN ? expert_steps - k : seg.s1 - s);
                 n = n < seg.s1 - s ? n : seg.s1 - s;
-                float factor[NT > 32 ? 2 : 1];
+                int next_place = place, next_k = k + n;
+                if (next_k == expert_steps)
+                    next_k = 0, ++next_place;
+                float factor[kSets][kBlocks];
 #pragma unroll
-                for (int i = 0; i < (NT > 32 ? 2 : 1); ++i) {
-                    const int t = 32 * i + lane;
-                    factor[i] = 1.f;
-                    if ((DOWN || FP8) && t < NT && (mask >> t & 1)) {
-                        const int r = sh.first[place] + __popcll(mask & ((1ull << t) - 1));
-                        if (FP8) {
-                            const int64_t groups = DOWN ? p.I / 128 : p.H / 128;
-                            const int n0 = DOWN ? tile * 2 * kHalf + half * kHalf : tile * kHalf + half * p.I;
-                            const int block = min(n0, (DOWN ? p.H : 2 * p.I) - 1) / 128;
-                            const int64_t blocks = DOWN ? p.H / 128 : p.I / 64;
-                            factor[i] = (DOWN ? h_scales[r * groups + k] : __ldg(p.x_scales + t * groups + k)) *
-                                        __ldg((DOWN ? p.w2_scales : p.w1_scales) + (e * blocks + block) * groups + k);
-                        }
-                        if (DOWN)
-                            factor[i] *= sh.gate[r];
-                    }
+                for (int i = 0; i < kSets; ++i) {
+                    const int t = base + 32 * i + lane;
+                    float g = 1.f;
+                    if constexpr (DOWN)
+                        if (lane < kTokens && (mask >> t & 1))
+                            g = sh.x.of_row[sh.first[place] + __popcll(mask & ((1ull << t) - 1))];
+#pragma unroll
+                    for (int b = 0; b < kBlocks; ++b)
+                        factor[i][b] = !FP8 ? g : (!DOWN || b == 0 || k * 2 + 1 < p.I / 128) ? sc.token[i][b] * sc.weight[b] * g : 0.f;
                 }
+                if (s + n < seg.s1)
+                    sc = load_scales(next_place, tile, next_k);
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait(&sh.sums_full[buf], buf_phase, kTimeoutNs, abort_flag));
                 if (!ok)
                     break;
                 tc_fence_after();
-                const uint32_t from = my_sums + buf * 2 * NT;
-                int col = 0;
+                // columns: the tokens (up/gate), or the expert's tokens without gaps
+                uint32_t from = my_sums + buf * 2 * NT;
+                if (DOWN)
+                    from += __popcll(mask & ((1ull << base) - 1));
+                constexpr int kAtOnce = DOWN && FP8 ? 8 : kTokens < 16 ? kTokens : 16;
 #pragma unroll
-                for (int t0 = 0; t0 < NT; t0 += 16) {
-                    const uint32_t here = static_cast<uint32_t>(mask >> t0) & 0xFFFF;
-                    if (!here)
+                for (int t0 = 0; t0 < kTokens; t0 += kAtOnce) {
+                    const uint32_t now = static_cast<uint32_t>(here >> t0) & ((1u << kAtOnce) - 1);
+                    if (!now)
                         continue;
-                    uint32_t v[16];
+                    uint32_t v[kAtOnce * (DOWN && FP8 ? 2 : 1)];
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
+                    for (int c = 0; c < kAtOnce; ++c) {
                         v[c] = 0;
-                        if (here >> c & 1)
-                            v[c] = tmem_ld_32x32b_x1(from + (DOWN ? col++ : t0 + c));
+                        if (DOWN && FP8)
+                            v[kAtOnce + c] = 0;
+                        if (now >> c & 1) {
+                            v[c] = tmem_ld_32x32b_x1(DOWN ? from : from + t0 + c);
+                            if (DOWN && FP8)
+                                v[kAtOnce + c] = tmem_ld_32x32b_x1(from + NT);
+                            if (DOWN)
+                                ++from;
+                        }
                     }
                     tmem_ld_wait();
                     tmem_regs_ready(v);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        if (here >> c & 1) {
-                            const float f = __shfl_sync(0xffffffffu, factor[(t0 + c) / 32], (t0 + c) % 32);
+                    for (int c = 0; c < kAtOnce; ++c)
+                        if (now >> c & 1) {
+                            const float f = __shfl_sync(0xffffffffu, factor[(t0 + c) / 32][0], (t0 + c) % 32);
                             acc[t0 + c] = fmaf(f, __uint_as_float(v[c]), acc[t0 + c]);
+                            if (DOWN && FP8) {
+                                const float f1 = __shfl_sync(0xffffffffu, factor[(t0 + c) / 32][kBlocks - 1], (t0 + c) % 32);
+                                acc[t0 + c] = fmaf(f1, __uint_as_float(v[kAtOnce + c]), acc[t0 + c]);
+                            }
                         }
                 }
                 tc_fence_before();
@@ -572,8 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&sh.sums_empty[buf]);
                 advance(buf, buf_phase, 2);
                 s += n;
-                if ((k += n) == expert_steps)
-                    k = 0, ++place;
+                place = next_place, k = next_k;
             }
             // (all of these warps leave together: they meet at barriers below)
             if (!ok && lane == 0)
@@ -586,12 +680,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 finish(seg.unit);
             } else {
                 const int slot = seg.s0 == 0 ? 1 : 0;
-                const uint64_t tokens = tokens_of(seg.unit);
+                const uint64_t tokens = DOWN ? all_tokens : sh.mask[sh.active[seg.unit / tiles]];
                 float *to = part_of(blockIdx.x * 2 + slot);
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int t = 0; t < kTokens; ++t)
                     if (tokens >> t & 1)
-                        __stcg(to + t * 2 * kHalf, acc[t]);
+                        __stcg(to + t * kPartRows, acc[t]);
                 if (etid == 0)
                     sh.cut[slot] = seg;
             }
@@ -617,18 +711,81 @@ __global__ void __launch_bounds__(kThreads, 1)
                     continue;
                 const int unit = sh.cut[slot].unit;
                 const int c0 = sh.runs.owner(unit * steps), c1 = sh.runs.owner(unit * steps + steps - 1);
-                const uint64_t tokens = tokens_of(unit);
+                const int place = DOWN ? 0 : unit / tiles, i0 = (unit - place * tiles) * kUnitRows + 4 * lane;
+                const uint64_t tokens = DOWN ? (p.T == 64 ? ~0ull : (1ull << p.T) - 1) : sh.mask[sh.active[place]];
+                const int count = __popcll(tokens);
+                // A warp takes a token's 128 rows (gate and up, each), a lane four of them; kAtATime
+                // tokens' and kAhead blocks' sums are under way at once.
+                constexpr int kAtATime = NT / kEpilogueWarps < 4 ? NT / kEpilogueWarps : 4;
+                constexpr int kAhead = (DOWN ? 16 : 8) / kAtATime;
+                for (int j0 = warp - 4; j0 < count; j0 += kEpilogueWarps * kAtATime) {
+                    int token[kAtATime];
+                    float4 sum[kAtATime][DOWN ? 1 : 2];
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    acc[t] = 0.f;
-                for (int b = c0; b <= c1; ++b) {
-                    const float *theirs = part_of(b * 2 + (b == c0 ? 1 : 0));
+                    for (int a = 0; a < kAtATime; ++a) {
+                        const int j = j0 + a * kEpilogueWarps;
+                        token[a] = j < count ? nth_bit(tokens, j) : -1;
+                        for (int g = 0; g < (DOWN ? 1 : 2); ++g)
+                            sum[a][g] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                    for (int b0 = c0; b0 <= c1; b0 += kAhead) {
+                        float4 v[kAhead][kAtATime][DOWN ? 1 : 2];
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        if (tokens >> t & 1)
-                            acc[t] += __ldcg(theirs + t * 2 * kHalf);
+                        for (int h = 0; h < kAhead; ++h) {
+                            const int b = b0 + h, from = b * 2 + (b == c0 ? 1 : 0);
+#pragma unroll
+                            for (int a = 0; a < kAtATime; ++a)
+#pragma unroll
+                                for (int g = 0; g < (DOWN ? 1 : 2); ++g) {
+                                    v[h][a][g] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                    if (b <= c1 && token[a] >= 0)
+                                        v[h][a][g] = __ldcg(reinterpret_cast<const float4 *>(
+                                            parts + (static_cast<int64_t>(from) * NT + token[a]) * kPartRows + g * kTile + 4 * lane));
+                                }
+                        }
+#pragma unroll
+                        for (int h = 0; h < kAhead; ++h)
+#pragma unroll
+                            for (int a = 0; a < kAtATime; ++a)
+#pragma unroll
+                                for (int g = 0; g < (DOWN ? 1 : 2); ++g) {
+                                    sum[a][g].x += v[h][a][g].x, sum[a][g].y += v[h][a][g].y;
+                                    sum[a][g].z += v[h][a][g].z, sum[a][g].w += v[h][a][g].w;
+                                }
+                    }
+#pragma unroll
+                    for (int a = 0; a < kAtATime; ++a) {
+                        if (token[a] < 0)
+                            continue;
+                        const float4 g = sum[a][0];
+                        if constexpr (DOWN) {
+                            const float v[4] = {g.x, g.y, g.z, g.w};
+                            __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + static_cast<int64_t>(token[a]) * p.H + i0;
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                if (i0 + c < p.H)
+                                    out[c] = __float2bfloat16_rn(v[c]);
+                        } else {
+                            const float4 u = sum[a][1];
+                            const float v[4] = {silu_f32(g.x) * u.x, silu_f32(g.y) * u.y, silu_f32(g.z) * u.z, silu_f32(g.w) * u.w};
+                            const int64_t at = (sh.first[place] + j0 + a * kEpilogueWarps) * static_cast<int64_t>(p.I) + i0;
+                            if (FP8) {
+                                uint32_t m = 0;
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    m = max(m, rows::size_bits(v[c]));
+                                const float sc = rows::scale_of(__reduce_max_sync(0xffffffffu, m)), inv = 1.f / sc;
+                                *reinterpret_cast<uint32_t *>(h_rows + at) =
+                                    rows::e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+                                if (lane == 0)
+                                    h_scales[at / 128] = sc;
+                            } else if (i0 < p.I) {  // (a multiple of 8)
+                                *reinterpret_cast<uint2 *>(h_rows + at * 2) =
+                                    make_uint2(rows::pack(v[0], v[1]), rows::pack(v[2], v[3]));
+                            }
+                        }
+                    }
                 }
-                finish(unit);
             }
         }
     } else if (DOWN && warp == 2) {
@@ -652,19 +809,19 @@ template <bool FP8, int NT>
 static cudaError_t launch_form(const FewMaps &maps, const FewParams &p, int num_sms, cudaStream_t s)
 {
     const auto up = few_kernel<false, FP8, NT>, down = few_kernel<true, FP8, NT>;
-    constexpr int smem = smem_bytes<NT>();
-    static_assert(smem <= 227 * 1024, "shared memory of a block");
-    cudaError_t e = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    constexpr int up_smem = smem_bytes<false, NT>(), down_smem = smem_bytes<true, NT>();
+    static_assert(up_smem <= 227 * 1024 && down_smem <= 227 * 1024, "shared memory of a block");
+    cudaError_t e = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, up_smem);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, down_smem);
     if (e != cudaSuccess)
         return e;
     const int grid = num_sms < kMaxBlocks ? num_sms : kMaxBlocks;
     uint8_t *h_rows = p.workspace + few_workspace_rows(p.T);
     float *h_scales = reinterpret_cast<float *>(p.workspace + few_workspace_scales(p));
-    e = launch_behind(up, grid, kThreads, smem, s, maps.w1, maps.x, p, h_rows, h_scales);
+    e = launch_behind(up, grid, kThreads, up_smem, s, maps.w1, maps.x, p, h_rows, h_scales);
     return e != cudaSuccess ? e
-                            : launch_behind(down, grid, kThreads, smem, s, maps.w2, maps.h, p, h_rows, h_scales);
+                            : launch_behind(down, grid, kThreads, down_smem, s, maps.w2, maps.h, p, h_rows, h_scales);
 }
 
 cudaError_t launch_layer_few(const FewMaps &maps, const FewParams &p, int num_sms, cudaStream_t s)
