@@ -624,42 +624,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok)
                     break;
                 tc_fence_after();
-                // columns: the tokens (up/gate), or the expert's tokens without gaps
                 uint32_t from = my_sums + buf * 2 * NT;
-                if (DOWN)
+                if constexpr (DOWN) {
+                    // columns: the expert's tokens without gaps, each at one's own place in acc
                     from += __popcll(mask & ((1ull << base) - 1));
-                constexpr int kAtOnce = DOWN && FP8 ? 8 : kTokens < 16 ? kTokens : 16;
+                    constexpr int kAtOnce = FP8 || kTokens < 16 ? 8 : 16;
 #pragma unroll
-                for (int t0 = 0; t0 < kTokens; t0 += kAtOnce) {
-                    const uint32_t now = static_cast<uint32_t>(here >> t0) & ((1u << kAtOnce) - 1);
-                    if (!now)
-                        continue;
-                    uint32_t v[kAtOnce * (DOWN && FP8 ? 2 : 1)];
+                    for (int t0 = 0; t0 < kTokens; t0 += kAtOnce) {
+                        const uint32_t now = static_cast<uint32_t>(here >> t0) & ((1u << kAtOnce) - 1);
+                        if (!now)
+                            continue;
+                        uint32_t v[kAtOnce * kBlocks];
 #pragma unroll
-                    for (int c = 0; c < kAtOnce; ++c) {
-                        v[c] = 0;
-                        if (DOWN && FP8)
-                            v[kAtOnce + c] = 0;
-                        if (now >> c & 1) {
-                            v[c] = tmem_ld_32x32b_x1(DOWN ? from : from + t0 + c);
-                            if (DOWN && FP8)
-                                v[kAtOnce + c] = tmem_ld_32x32b_x1(from + NT);
-                            if (DOWN)
+                        for (int c = 0; c < kAtOnce; ++c) {
+                            v[c] = v[(kBlocks - 1) * kAtOnce + c] = 0;
+                            if (now >> c & 1) {
+                                v[c] = tmem_ld_32x32b_x1(from);
+                                if (FP8)
+                                    v[(kBlocks - 1) * kAtOnce + c] = tmem_ld_32x32b_x1(from + NT);
                                 ++from;
-                        }
-                    }
-                    tmem_ld_wait();
-                    tmem_regs_ready(v);
-#pragma unroll
-                    for (int c = 0; c < kAtOnce; ++c)
-                        if (now >> c & 1) {
-                            const float f = __shfl_sync(0xffffffffu, factor[(t0 + c) / 32][0], (t0 + c) % 32);
-                            acc[t0 + c] = fmaf(f, __uint_as_float(v[c]), acc[t0 + c]);
-                            if (DOWN && FP8) {
-                                const float f1 = __shfl_sync(0xffffffffu, factor[(t0 + c) / 32][kBlocks - 1], (t0 + c) % 32);
-                                acc[t0 + c] = fmaf(f1, __uint_as_float(v[kAtOnce + c]), acc[t0 + c]);
                             }
                         }
+                        tmem_ld_wait();
+                        tmem_regs_ready(v);
+#pragma unroll
+                        for (int c = 0; c < kAtOnce; ++c)
+                            if (now >> c & 1)
+#pragma unroll
+                                for (int b = 0; b < (FP8 ? 2 : 1); ++b) {
+                                    const float f = __shfl_sync(0xffffffffu, factor[0][b], t0 + c);
+                                    acc[t0 + c] = fmaf(f, __uint_as_float(v[b * kAtOnce + c]), acc[t0 + c]);
+                                }
+                    }
+                } else {
+                    // columns: the tokens (nobody uses the sums of those that are not the expert's)
+#pragma unroll
+                    for (int t0 = 0; t0 < kTokens; t0 += 16) {
+                        if (!(here >> t0 & 0xFFFF))
+                            continue;
+                        uint32_t v[16];
+                        tmem_ld_32x32b_x16(from + t0, v);
+                        tmem_ld_wait();
+                        tmem_regs_ready(v);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            if (FP8) {
+                                const float f = __shfl_sync(0xffffffffu, factor[t0 / 32][0], (t0 + c) % 32);
+                                acc[t0 + c] = fmaf(f, __uint_as_float(v[c]), acc[t0 + c]);
+                            } else {
+                                acc[t0 + c] = __uint_as_float(v[c]);
+                            }
+                        }
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
