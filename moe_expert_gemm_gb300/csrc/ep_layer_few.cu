@@ -95,7 +95,7 @@ struct Shared {
     uint64_t full[6], empty[6];
     uint64_t sums_full[2], sums_empty[2];
     uint64_t drained;
-    unsigned long long mask[EP_MAX_LOCAL_EXPERTS];  // tokens of each local expert
+    uint32_t mask[EP_MAX_LOCAL_EXPERTS][2];  // tokens of each local expert
     uint32_t tmem;
     int abort;
     int n_active, start, todo;  // active experts; the run
@@ -106,6 +106,8 @@ struct Shared {
     uint16_t place[EP_MAX_LOCAL_EXPERTS];   // of an expert among them
     int16_t first[EP_MAX_LOCAL_EXPERTS];    // first row of the place's tokens
     std::conditional_t<DOWN, Gates, Exchange> x;
+
+    __device__ uint64_t tokens(int e) const { return mask[e][0] | static_cast<uint64_t>(mask[e][1]) << 32; }
 };
 
 template <bool DOWN, int NT>
@@ -128,15 +130,16 @@ __device__ __forceinline__ void make_plan(const FewParams &p, Shared<DOWN> &sh)
 {
     const int tid = threadIdx.x, slots = p.T * p.top_k, first = p.my_rank * p.El;
     for (int e = tid; e < p.El; e += kThreads)
-        sh.mask[e] = 0;
+        sh.mask[e][0] = sh.mask[e][1] = 0;
     __syncthreads();
     bool bad = false;
     for (int s = tid; s < slots; s += kThreads) {
         const int id = __ldg(p.topk_ids + s), e = id - first;
         const bool here = id >= first && e < p.El;
         bad |= id < 0 || id >= p.n_ranks * p.El;
+        const int t = s / p.top_k;
         if (here)
-            atomicOr(&sh.mask[e], 1ull << (s / p.top_k));
+            atomicOr(&sh.mask[e][t / 32], 1u << t % 32);
         if constexpr (DOWN) {
             sh.x.expert[s] = static_cast<int16_t>(here ? e : -1);
             sh.x.of_slot[s] = __ldg(p.gates + s);
@@ -148,7 +151,7 @@ __device__ __forceinline__ void make_plan(const FewParams &p, Shared<DOWN> &sh)
     if (tid < 32) {
         int places = 0, rows = 0;
         for (int e0 = 0; e0 < p.El; e0 += 32) {
-            const int e = e0 + tid, n = e < p.El ? __popcll(sh.mask[e]) : 0;
+            const int e = e0 + tid, n = e < p.El ? __popcll(sh.tokens(e)) : 0;
             const uint32_t has = __ballot_sync(0xffffffffu, n > 0);
             int upto = n;
 #pragma unroll
@@ -185,7 +188,7 @@ __device__ __forceinline__ void make_plan(const FewParams &p, Shared<DOWN> &sh)
             for (int i = s + 1; i < s0 + p.top_k; ++i)
                 if (sh.x.expert[i] == e)
                     g += sh.x.of_slot[i];
-            sh.x.of_row[sh.first[sh.place[e]] + __popcll(sh.mask[e] & ((1ull << t) - 1))] = g;
+            sh.x.of_row[sh.first[sh.place[e]] + __popcll(sh.tokens(e) & ((1ull << t) - 1))] = g;
         }
     }
 }
@@ -212,14 +215,6 @@ struct Walk {
         return true;
     }
 };
-
-// Place of the n-th set bit.
-__device__ __forceinline__ int nth_bit(uint64_t bits, int n)
-{
-    const uint32_t lo = static_cast<uint32_t>(bits), hi = static_cast<uint32_t>(bits >> 32);
-    const int in_lo = __popc(lo);
-    return n < in_lo ? static_cast<int>(__fns(lo, 0, n + 1)) : 32 + static_cast<int>(__fns(hi, 0, n - in_lo + 1));
-}
 
 template <typename T>
 __device__ __forceinline__ void advance(int &i, T &phase, int n)
@@ -335,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             : At{s.unit % tiles, s.unit / tiles, s.s0};
             };
             auto columns = [&](const At &at) {  // (in 16s)
-                return DOWN ? (__popcll(sh.mask[sh.active[at.place]]) + 15) / 16 : NT / 16;
+                return DOWN ? (__popcll(sh.tokens(sh.active[at.place])) + 15) / 16 : NT / 16;
             };
             auto load_weights = [&](const At &at, int i) {
                 const int e = sh.active[at.place], y = at.unit * kUnitRows, x = at.k * kStepK;
@@ -422,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t idesc = 0;
                 for (int s = seg.s0; s < seg.s1; ++s) {
                     if (fresh) {
-                        const int n = DOWN ? __popcll(sh.mask[sh.active[place]]) : p.T;
+                        const int n = DOWN ? __popcll(sh.tokens(sh.active[place])) : p.T;
                         idesc = make_idesc(FP8 ? 0u : 1u, kTile, (n + 15) / 16 * 16);
                         ok = mbar_wait(&sh.sums_empty[buf], buf_phase ^ 1, kTimeoutNs, abort_flag);
                     }
@@ -503,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 const int place = unit / tiles, i = (unit - place * tiles) * kUnitRows + row;
-                const uint64_t mask = sh.mask[sh.active[place]];
+                const uint64_t mask = sh.tokens(sh.active[place]);
                 int64_t at = sh.first[place];  // the next token's row
 #pragma unroll
                 for (int t0 = 0; t0 < NT; t0 += 8) {
@@ -563,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Scales sc = {};
             if constexpr (FP8) {
                 const int e = sh.active[place];
-                const uint64_t mask = sh.mask[e];
+                const uint64_t mask = sh.tokens(e);
                 const int groups = (DOWN ? p.I : p.H) / 128;
                 const float *w = (DOWN ? p.w2_scales + (static_cast<int64_t>(e) * (p.H / 128) + tile) * groups
                                        : p.w1_scales + (static_cast<int64_t>(e) * (p.I / 64) + group * (p.I / 128) + tile) * groups);
@@ -599,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Scales sc = load_scales(place, tile, k);
             for (int s = seg.s0; ok && s < seg.s1;) {
                 // one period: its steps, tokens and factors
-                const uint64_t mask = sh.mask[sh.active[place]], here = mine(mask);
+                const uint64_t mask = sh.tokens(sh.active[place]), here = mine(mask);
                 int n = FP8 ? 1 : (DOWN ? expert_steps - k : seg.s1 - s);
                 n = n < seg.s1 - s ? n : seg.s1 - s;
                 int next_place = place, next_k = k + n;
@@ -696,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 finish(seg.unit);
             } else {
                 const int slot = seg.s0 == 0 ? 1 : 0;
-                const uint64_t tokens = DOWN ? all_tokens : sh.mask[sh.active[seg.unit / tiles]];
+                const uint64_t tokens = DOWN ? all_tokens : sh.tokens(sh.active[seg.unit / tiles]);
                 float *to = part_of(blockIdx.x * 2 + slot);
 #pragma unroll
                 for (int t = 0; t < kTokens; ++t)
@@ -728,19 +723,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int unit = sh.cut[slot].unit;
                 const int c0 = sh.runs.owner(unit * steps), c1 = sh.runs.owner(unit * steps + steps - 1);
                 const int place = DOWN ? 0 : unit / tiles, i0 = (unit - place * tiles) * kUnitRows + 4 * lane;
-                const uint64_t tokens = DOWN ? (p.T == 64 ? ~0ull : (1ull << p.T) - 1) : sh.mask[sh.active[place]];
+                const uint64_t tokens = DOWN ? (p.T == 64 ? ~0ull : (1ull << p.T) - 1) : sh.tokens(sh.active[place]);
                 const int count = __popcll(tokens);
                 // A warp takes a token's 128 rows (gate and up, each), a lane four of them; kAtATime
                 // tokens' and kAhead blocks' sums are under way at once.
                 constexpr int kAtATime = NT / kEpilogueWarps < 4 ? NT / kEpilogueWarps : 4;
                 constexpr int kAhead = (DOWN ? 16 : 8) / kAtATime;
+                uint64_t left = tokens;  // from this warp's next token on
+                auto skip = [&](int n) {
+                    for (int i = 0; i < n; ++i)
+                        left &= left - 1;
+                };
+                skip(warp - 4);
                 for (int j0 = warp - 4; j0 < count; j0 += kEpilogueWarps * kAtATime) {
                     int token[kAtATime];
                     float4 sum[kAtATime][DOWN ? 1 : 2];
 #pragma unroll
                     for (int a = 0; a < kAtATime; ++a) {
-                        const int j = j0 + a * kEpilogueWarps;
-                        token[a] = j < count ? nth_bit(tokens, j) : -1;
+                        token[a] = __ffsll(static_cast<long long>(left)) - 1;  // (-1: none)
+                        skip(kEpilogueWarps);
                         for (int g = 0; g < (DOWN ? 1 : 2); ++g)
                             sum[a][g] = make_float4(0.f, 0.f, 0.f, 0.f);
                     }
