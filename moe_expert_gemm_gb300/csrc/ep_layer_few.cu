@@ -47,8 +47,18 @@ constexpr int kPartBase = 4096;  // of the workspace; counters before it
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 static_assert(kMaxBlocks * 4 <= kPartBase, "counters");
 
-// Steps that the joining of cut units is worth, and the fewest of a block.
-constexpr int kJoinSteps = 4, kMinSteps = 2;
+// Steps that the joining of cut units is worth.
+constexpr int kJoinSteps = 4;
+
+// The fewest steps that a cut leaves a block: the last block of a unit adds a part for every
+// min_steps, each of which takes about as long as half a step does.
+__device__ __forceinline__ int min_steps(int steps)
+{
+    int s = 2;
+    while (s < 64 && 2 * s * s < steps)
+        ++s;
+    return s;
+}
 
 struct Segment {
     int unit, s0, s1;  // steps [s0, s1) of the unit
@@ -292,10 +302,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         const int grid = static_cast<int>(gridDim.x), block = static_cast<int>(blockIdx.x);
         const int total = units * steps;
+        const int least = min_steps(steps);
         int cut = (total + grid - 1) / grid;
-        cut = cut < kMinSteps ? kMinSteps : cut;
+        cut = cut < least ? least : cut;
         const bool whole = (units + grid - 1) / grid * steps <= cut + kJoinSteps;
-        const int blocks = whole || total / grid >= kMinSteps ? grid : (total + kMinSteps - 1) / kMinSteps;
+        const int blocks = whole || total / grid >= least ? grid : (total + least - 1) / least;
         Runs runs;
         runs.piece = whole ? steps : 1;
         runs.per = (whole ? units : total) / blocks;
@@ -332,12 +343,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto columns = [&](const At &at) {  // (in 16s)
                 return DOWN ? (__popcll(sh.tokens(sh.active[at.place])) + 15) / 16 : NT / 16;
             };
+            // (the L2 keeps tokens, activations and partial sums rather: 64 tokens, 8 of 16 experts
+            // of 4096 x 2048, 156 us a call, without 162)
+            const uint64_t once = policy_evict_first();
             auto load_weights = [&](const At &at, int i) {
                 const int e = sh.active[at.place], y = at.unit * kUnitRows, x = at.k * kStepK;
                 uint8_t *dst = ring + i * kStage;
                 mbar_arrive_expect_tx(&sh.full[i], kWeightBytes + columns(at) * (DOWN ? 4096 : 2048));
-                tma_load_3d(dst, &tw, &sh.full[i], x, y, e);
-                tma_load_3d(dst + kTile * 128, &tw, &sh.full[i], DOWN ? x + kBlockK : x, DOWN ? y : y + p.I, e);
+                tma_load_3d_once(dst, &tw, &sh.full[i], x, y, e, once);
+                tma_load_3d_once(dst + kTile * 128, &tw, &sh.full[i], DOWN ? x + kBlockK : x, DOWN ? y : y + p.I,
+                                 e, once);
             };
             auto load_columns = [&](const At &at, int i) {
                 uint8_t *dst = ring + i * kStage + kWeightBytes;
@@ -727,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int count = __popcll(tokens);
                 // A warp takes a token's 128 rows (gate and up, each), a lane four of them; kAtATime
                 // tokens' and kAhead blocks' sums are under way at once.
-                constexpr int kAtATime = NT / kEpilogueWarps < 4 ? NT / kEpilogueWarps : 4;
+                constexpr int kAtATime = DOWN || NT < 32 ? NT / kEpilogueWarps : 4;
                 constexpr int kAhead = (DOWN ? 16 : 8) / kAtATime;
                 uint64_t left = tokens;  // from this warp's next token on
                 auto skip = [&](int n) {

@@ -106,17 +106,6 @@ __device__ __forceinline__ void tma_load_2d_hint(void *smem_dst, const void *map
         : "memory");
 }
 
-// 3-D tiled load (the third dimension of the box is 1).
-__device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *map, uint64_t *bar, int32_t x,
-                                            int32_t y, int32_t z)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
-
 __device__ __forceinline__ uint64_t policy_evict_last()
 {
     uint64_t p;
@@ -129,6 +118,17 @@ __device__ __forceinline__ uint64_t policy_evict_first()
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
     return p;
+}
+
+// 3-D tiled load (the third dimension of the box is 1) of what is read once.
+__device__ __forceinline__ void tma_load_3d_once(void *smem_dst, const void *map, uint64_t *bar, int32_t x,
+                                                 int32_t y, int32_t z, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
+        : "memory");
 }
 
 // Untiled bulk copy from shared to global memory on the TMA engine (both addresses

@@ -90,6 +90,13 @@ __device__ __forceinline__ void store_piece(uint8_t *base, bool bf16, int c, int
     }
 }
 
+// SiLU(x) * u. The quotient by the fast division (error 2 units in the last place; 0 where e^-x
+// passes 2^126, where the true value is below 2^-119).
+__device__ __forceinline__ float silu_times(float x, float u)
+{
+    return __fdividef(x, 1.f + expf(-x)) * u;
+}
+
 // The bits of |v|: as integers they order finite values, infinities and NaN in that order.
 __device__ __forceinline__ uint32_t size_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 

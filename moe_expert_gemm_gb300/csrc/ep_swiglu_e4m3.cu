@@ -9,45 +9,62 @@ namespace ep {
 
 using namespace rows;
 
-constexpr int kSwigluE4m3Threads = 256;
+namespace {
 
-__global__ void __launch_bounds__(kSwigluE4m3Threads) swiglu_e4m3_kernel(const SwigluE4m3Params p)
+constexpr int kThreads = 256;
+constexpr int kRowsAhead = 4;  // of a thread, under way at once
+
+}  // namespace
+
+// A block takes tiles of kRowsAhead * (256 / width) rows, `width` threads (whole half warps) to a
+// row.
+__global__ void __launch_bounds__(kThreads) swiglu_e4m3_kernel(const SwigluE4m3Params p, int width)
 {
     griddep_wait();
     griddep_launch_dependents();
     int64_t m_total = __ldg(p.expert_offsets + p.El);
     m_total = m_total < 0 ? 0 : (m_total > p.max_rows ? p.max_rows : m_total);
     const int pieces = p.inter / kPiece, groups = (pieces + kGroupPieces - 1) / kGroupPieces;
-    // half warps count through all rows' groups
-    const int64_t all = m_total * groups;
-    const int lane = threadIdx.x % kGroupPieces;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (kSwigluE4m3Threads / kGroupPieces);
-    int64_t at = static_cast<int64_t>(blockIdx.x) * (kSwigluE4m3Threads / kGroupPieces) + threadIdx.x / kGroupPieces;
-    // (both halves of a warp stay for its shuffles)
-    for (; at - at % 2 < all; at += step) {
-        const int64_t m = at / groups;
-        const int c = (static_cast<int>(at - m * groups) * kGroupPieces + lane) * kPiece;
-        const bool there = at < all && c < p.inter;
-        float v[kPiece] = {};
-        if (there) {
-            float gate[kPiece], up[kPiece];
-            load_piece<true>(p.G + m * p.inter * 4, true, c, p.inter, gate);
-            load_piece<true>(p.G + (m * 2 + 1) * p.inter * 2, true, c, p.inter, up);
+    const int x = threadIdx.x % width, y = threadIdx.x / width, rows_at_once = kThreads / width;
+    const int rows = rows_at_once * kRowsAhead;
+    for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * rows; m0 < m_total; m0 += static_cast<int64_t>(gridDim.x) * rows) {
+        for (int c0 = 0; c0 < pieces; c0 += width) {
+            const int c = (c0 + x) * kPiece;
+            uint4 gate[kRowsAhead], up[kRowsAhead];
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j)
-                v[j] = silu_f32(gate[j]) * up[j];
+            for (int i = 0; i < kRowsAhead; ++i) {
+                const int64_t m = m0 + i * rows_at_once + y;
+                gate[i] = up[i] = make_uint4(0, 0, 0, 0);
+                if (m < m_total && c < p.inter) {
+                    const uint8_t *row = p.G + m * p.inter * 4 + c * 2;
+                    gate[i] = __ldcs(reinterpret_cast<const uint4 *>(row));
+                    up[i] = __ldcs(reinterpret_cast<const uint4 *>(row + p.inter * 2));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kRowsAhead; ++i) {
+                const int64_t m = m0 + i * rows_at_once + y;
+                float v[kPiece], u[kPiece];
+                unpack(gate[i], v);
+                unpack(up[i], u);
+#pragma unroll
+                for (int j = 0; j < kPiece; ++j)
+                    v[j] = silu_times(v[j], u[j]);
+                store_e4m3<true>(p.q + m * p.inter, p.q_scales + m * groups, m < m_total ? c : p.inter, p.inter, v);
+            }
         }
-        store_e4m3<true>(p.q + m * p.inter, p.q_scales + m * groups, there ? c : p.inter, p.inter, v);
     }
 }
 
 cudaError_t launch_swiglu_e4m3(const SwigluE4m3Params &p, int num_sms, cudaStream_t s)
 {
-    const int64_t groups = (p.inter + 127) / 128;
-    const int64_t blocks = (p.max_rows * groups * kGroupPieces + kSwigluE4m3Threads - 1) / kSwigluE4m3Threads;
-    const int64_t most = 8ll * num_sms;
-    return launch_behind(swiglu_e4m3_kernel, static_cast<unsigned>(blocks < most ? blocks : most),
-                         kSwigluE4m3Threads, 0, s, p);
+    int width = kGroupPieces;
+    while (width < kThreads && width * kPiece < p.inter)
+        width *= 2;
+    const int64_t rows = kThreads / width * kRowsAhead;
+    const int64_t blocks = (p.max_rows + rows - 1) / rows, most = 6ll * num_sms;
+    return launch_behind(swiglu_e4m3_kernel, static_cast<unsigned>(blocks < most ? blocks : most), kThreads, 0, s, p,
+                         width);
 }
 
 }  // namespace ep
