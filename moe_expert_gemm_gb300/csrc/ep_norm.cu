@@ -94,51 +94,82 @@ __device__ __forceinline__ void read_piece(const uint8_t *from, bool bf16, float
 }  // namespace
 
 // `bytes` of a row between global and shared memory, in units of `unit` bytes that both are
-// aligned to (a divisor of 16); what is left over in 2 or 1 byte each.
-template <typename U>
+// aligned to (a divisor of 16); what is left over byte by byte. ASYNC: to shared memory by
+// cp.async, which takes units of 4 and more.
+template <bool ASYNC, typename U>
 __device__ __forceinline__ void copy_units(uint8_t *to, const uint8_t *from, int bytes)
 {
-    for (int i = threadIdx.x; i < bytes / static_cast<int>(sizeof(U)); i += blockDim.x)
-        reinterpret_cast<U *>(to)[i] = reinterpret_cast<const U *>(from)[i];
+    constexpr int kUnit = sizeof(U);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < bytes / kUnit; i += blockDim.x) {
+        if constexpr (ASYNC && kUnit >= 4)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to) + i * kUnit),
+                         "l"(from + i * kUnit), "n"(kUnit)
+                         : "memory");
+        else
+            reinterpret_cast<U *>(to)[i] = reinterpret_cast<const U *>(from)[i];
+    }
 }
 
+template <bool ASYNC>
 __device__ __forceinline__ void copy_row(uint8_t *to, const uint8_t *from, int bytes, int unit)
 {
     switch (unit) {
     case 16:
-        copy_units<uint4>(to, from, bytes);
+        copy_units<ASYNC, uint4>(to, from, bytes);
         break;
     case 8:
-        copy_units<uint2>(to, from, bytes);
+        copy_units<ASYNC, uint2>(to, from, bytes);
         break;
     case 4:
-        copy_units<uint32_t>(to, from, bytes);
+        copy_units<ASYNC, uint32_t>(to, from, bytes);
         break;
     case 2:
-        copy_units<uint16_t>(to, from, bytes);
+        copy_units<ASYNC, uint16_t>(to, from, bytes);
         break;
     default:
-        copy_units<uint8_t>(to, from, bytes);
+        copy_units<ASYNC, uint8_t>(to, from, bytes);
     }
     for (int i = bytes / unit * unit + threadIdx.x; i < bytes; i += blockDim.x)
         to[i] = from[i];
 }
 
-// Rows of any alignment, by way of shared memory: x (then y), the residual (then sum), q, each
-// padded to whole pieces. A thread overwrites only the pieces that it alone has read.
-__global__ void __launch_bounds__(32 * kMaxWarps) norm_any_kernel(const NormParams p, const RowUnits units)
+// Rows of any alignment, by way of shared memory: x (then y) and the residual (then sum), each
+// padded to whole pieces, in two buffers that take turns where they fit; q. A thread overwrites
+// only the pieces that it alone has read.
+__global__ void __launch_bounds__(32 * kMaxWarps) norm_any_kernel(const NormParams p, const RowUnits units,
+                                                                 int buffers)
 {
     extern __shared__ __align__(16) uint8_t row[];
     __shared__ float2 part[2][kMaxWarps];
     int turn = 0;
     const int n = p.hidden, rb = p.residual_bf16 ? 2 : 4, padded = (n + kPiece - 1) / kPiece * kPiece;
-    uint8_t *const x = row, *const res = x + padded * 2, *const q = res + (p.residual || p.sum ? padded * rb : 0);
+    const int bytes = padded * (p.residual || p.sum ? 2 + rb : 2);
+    uint8_t *const q = row + buffers * bytes;
     griddep_wait();
     griddep_launch_dependents();
+    auto ask = [&](int64_t t, int buffer) {
+        if (t < p.T) {
+            uint8_t *const x = row + buffer * bytes;
+            copy_row<true>(x, p.x + t * p.x_stride * 2, n * 2, units.of[0]);
+            if (p.residual)
+                copy_row<true>(x + padded * 2, p.residual + t * p.residual_stride * rb, n * rb, units.of[1]);
+        }
+        copy_commit();
+    };
+    if (buffers > 1)
+        ask(blockIdx.x, 0);
+    int buffer = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        copy_row(x, p.x + t * p.x_stride * 2, n * 2, units.of[0]);
-        if (p.residual)
-            copy_row(res, p.residual + t * p.residual_stride * rb, n * rb, units.of[1]);
+        uint8_t *const x = row + buffer * bytes, *const res = x + padded * 2;
+        if (buffers > 1) {
+            ask(t + gridDim.x, buffer ^ 1);
+            copy_wait<1>();
+            buffer ^= 1;
+        } else {
+            ask(t, 0);
+            copy_wait<0>();
+        }
         __syncthreads();
         float h[kPieces][kPiece] = {};
         float squares = 0.f;
@@ -178,32 +209,51 @@ __global__ void __launch_bounds__(32 * kMaxWarps) norm_any_kernel(const NormPara
         }
         __syncthreads();
         if (p.sum)
-            copy_row(p.sum + t * p.sum_stride * rb, res, n * rb, units.of[2]);
+            copy_row<false>(p.sum + t * p.sum_stride * rb, res, n * rb, units.of[2]);
         if (p.y)
-            copy_row(p.y + t * p.y_stride * 2, x, n * 2, units.of[3]);
+            copy_row<false>(p.y + t * p.y_stride * 2, x, n * 2, units.of[3]);
         if (p.q)
-            copy_row(p.q + t * n, q, n, units.of[4]);
+            copy_row<false>(p.q + t * n, q, n, units.of[4]);
         __syncthreads();
     }
 }
 
 // The same for the gradient: h (then dh), dy (then dx), dsum.
 __global__ void __launch_bounds__(32 * kMaxWarps) norm_backward_any_kernel(const NormBackwardParams p,
-                                                                            const RowUnits units)
+                                                                            const RowUnits units, int buffers)
 {
     extern __shared__ __align__(16) uint8_t row[];
     __shared__ float2 part[2][kMaxWarps];
     int turn = 0;
     const int n = p.hidden, hb = p.h_bf16 ? 2 : 4, padded = (n + kPiece - 1) / kPiece * kPiece;
-    uint8_t *const h_row = row, *const dy_row = h_row + padded * hb, *const dsum_row = dy_row + padded * 2;
+    const int bytes = padded * (2 + hb * (p.dsum ? 2 : 1));
     griddep_wait();
     griddep_launch_dependents();
+    auto ask = [&](int64_t t, int buffer) {
+        if (t < p.T) {
+            uint8_t *const to = row + buffer * bytes;
+            copy_row<true>(to, p.h + t * p.h_stride * hb, n * hb, units.of[0]);
+            copy_row<true>(to + padded * hb, p.dy + t * p.dy_stride * 2, n * 2, units.of[1]);
+            if (p.dsum)
+                copy_row<true>(to + padded * (hb + 2), p.dsum + t * p.dsum_stride * hb, n * hb, units.of[2]);
+        }
+        copy_commit();
+    };
+    if (buffers > 1)
+        ask(blockIdx.x, 0);
+    int buffer = 0;
     float dw[kPieces][kPiece] = {};
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        copy_row(h_row, p.h + t * p.h_stride * hb, n * hb, units.of[0]);
-        copy_row(dy_row, p.dy + t * p.dy_stride * 2, n * 2, units.of[1]);
-        if (p.dsum)
-            copy_row(dsum_row, p.dsum + t * p.dsum_stride * hb, n * hb, units.of[2]);
+        uint8_t *const h_row = row + buffer * bytes, *const dy_row = h_row + padded * hb;
+        uint8_t *const dsum_row = dy_row + padded * 2;
+        if (buffers > 1) {
+            ask(t + gridDim.x, buffer ^ 1);
+            copy_wait<1>();
+            buffer ^= 1;
+        } else {
+            ask(t, 0);
+            copy_wait<0>();
+        }
         __syncthreads();
         float squares = 0.f, dot = 0.f;
 #pragma unroll
@@ -248,9 +298,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps) norm_backward_any_kernel(const
         }
         __syncthreads();
         if (p.dh)
-            copy_row(p.dh + t * p.dh_stride * hb, h_row, n * hb, units.of[3]);
+            copy_row<false>(p.dh + t * p.dh_stride * hb, h_row, n * hb, units.of[3]);
         if (p.dx)
-            copy_row(p.dx + t * p.dx_stride * 2, dy_row, n * 2, units.of[4]);
+            copy_row<false>(p.dx + t * p.dx_stride * 2, dy_row, n * 2, units.of[4]);
         __syncthreads();
     }
     if (p.dweight) {
@@ -530,11 +580,13 @@ cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t s)
     const Form f = form_for(p.hidden, 2 + (p.residual ? rb : 0));
     if (!vec || !f.stages) {
         const int most = 16 * num_sms;
-        const int smem = padded(p.hidden) * (2 + (p.residual || p.sum ? rb : 0) + (p.q ? 1 : 0));
+        const int row = padded(p.hidden) * (2 + (p.residual || p.sum ? rb : 0)), q = p.q ? padded(p.hidden) : 0;
+        const int buffers = 2 * row + q <= kSmemOfSm ? 2 : 1;
         const RowUnits units = {{unit_of(p.x, p.x_stride, 2), unit_of(p.residual, p.residual_stride, rb),
                                  unit_of(p.sum, p.sum_stride, rb), unit_of(p.y, p.y_stride, 2),
                                  unit_of(p.q, p.hidden, 1)}};
-        return launch_rows(norm_any_kernel, threads_for(p.hidden, kPieces), smem, p.T < most ? p.T : most, s, p, units);
+        return launch_rows(norm_any_kernel, threads_for(p.hidden, kPieces), buffers * row + q,
+                           p.T < most ? p.T : most, s, p, units, buffers);
     }
     const int most = f.per_sm * num_sms;
     const unsigned grid = p.T < most ? p.T : most;
@@ -566,8 +618,9 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, int num_sms, cudaS
         const RowUnits units = {{unit_of(p.h, p.h_stride, hb), unit_of(p.dy, p.dy_stride, 2),
                                  unit_of(p.dsum, p.dsum_stride, hb), unit_of(p.dh, p.dh_stride, hb),
                                  unit_of(p.dx, p.dx_stride, 2)}};
-        e = launch_rows(norm_backward_any_kernel, threads_for(p.hidden, kPieces),
-                        padded(p.hidden) * (2 + hb * (p.dsum ? 2 : 1)), grid, s, p, units);
+        const int row = padded(p.hidden) * (2 + hb * (p.dsum ? 2 : 1)), buffers = 2 * row <= kSmemOfSm ? 2 : 1;
+        e = launch_rows(norm_backward_any_kernel, threads_for(p.hidden, kPieces), buffers * row, grid, s, p, units,
+                        buffers);
     } else {
         auto go = [&](auto two, auto three, auto four) {
             return launch_rows(f.stages == 2 ? two : f.stages == 3 ? three : four, f.threads, f.smem, grid, s, p);
