@@ -88,11 +88,21 @@ constexpr int stages()
     return !DOWN && NT == 16 ? 6 : DOWN && NT == 64 ? 4 : 5;
 }
 
-// Exchange of eight tokens' up sums, and their largest magnitudes in 32 rows each.
+// Exchange of up to 16 tokens' sums: 128 gate rows, their 128 up rows.
+constexpr int kWindow = 16;
 struct Exchange {
-    float up[8][kTile];
-    uint32_t size[8][4];
+    alignas(16) float sums[kWindow][2 * kTile];  // (read in pieces of four)
 };
+
+// e4m3: the scales of some periods ahead, of the tokens (up/gate) or of the expert's rows (down),
+// and of the weights: gate and up rows, or two blocks of k.
+constexpr int kScaleStages = 8;
+template <int NT>
+struct Scales {
+    uint64_t full[kScaleStages], empty[kScaleStages];
+    float token[kScaleStages][2][NT], weight[kScaleStages][2];
+};
+struct Nothing {};
 
 // Gates of each slot, of each row, and the slots' local experts (-1: not here).
 struct Gates {
@@ -100,7 +110,7 @@ struct Gates {
     int16_t expert[kMaxRows];
 };
 
-template <bool DOWN>
+template <bool DOWN, bool FP8, int NT>
 struct Shared {
     uint64_t full[6], empty[6];
     uint64_t sums_full[2], sums_empty[2];
@@ -116,14 +126,15 @@ struct Shared {
     uint16_t place[EP_MAX_LOCAL_EXPERTS];   // of an expert among them
     int16_t first[EP_MAX_LOCAL_EXPERTS];    // first row of the place's tokens
     std::conditional_t<DOWN, Gates, Exchange> x;
+    std::conditional_t<FP8, Scales<NT>, Nothing> scales;
 
     __device__ uint64_t tokens(int e) const { return mask[e][0] | static_cast<uint64_t>(mask[e][1]) << 32; }
 };
 
-template <bool DOWN, int NT>
+template <bool DOWN, bool FP8, int NT>
 constexpr int smem_bytes()
 {
-    return 1024 + stages<DOWN, NT>() * stage_bytes<DOWN, NT>() + static_cast<int>(sizeof(Shared<DOWN>));
+    return 1024 + stages<DOWN, NT>() * stage_bytes<DOWN, NT>() + static_cast<int>(sizeof(Shared<DOWN, FP8, NT>));
 }
 
 template <typename S>
@@ -135,8 +146,8 @@ __device__ __forceinline__ void give_up(const FewParams &p, S &sh)
 
 // Which tokens each local expert has, the experts that have some, the first row of each, and
 // (down) every row's gate. All threads; ends with a barrier.
-template <bool DOWN>
-__device__ __forceinline__ void make_plan(const FewParams &p, Shared<DOWN> &sh)
+template <bool DOWN, typename S>
+__device__ __forceinline__ void make_plan(const FewParams &p, S &sh)
 {
     const int tid = threadIdx.x, slots = p.T * p.top_k, first = p.my_rank * p.El;
     for (int e = tid; e < p.El; e += kThreads)
@@ -226,6 +237,18 @@ struct Walk {
     }
 };
 
+// Four bytes to shared memory behind the thread's back, and its arrival at a barrier once all
+// that it has asked for is there.
+__device__ __forceinline__ void copy_word(float *to, const float *from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+
+__device__ __forceinline__ void copy_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ void advance(int &i, T &phase, int n)
 {
@@ -270,7 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kTmemCols = 4 * NT;  // two periods of two products' sums
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    Shared<DOWN> &sh = *reinterpret_cast<Shared<DOWN> *>(ring + kStages * kStage);
+    using Sh = Shared<DOWN, FP8, NT>;
+    Sh &sh = *reinterpret_cast<Sh *>(ring + kStages * kStage);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 64) {
         tma_prefetch_map(&tw);
@@ -284,6 +308,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.sums_empty[i], kEpilogueWarps);
         }
         mbar_init(&sh.drained, 1);
+        if constexpr (FP8)
+            for (int i = 0; i < kScaleStages; ++i) {
+                mbar_init(&sh.scales.full[i], 32);
+                mbar_init(&sh.scales.empty[i], kEpilogueWarps);
+            }
         fence_mbar_init();
         sh.abort = 0;
         sh.cut[0].unit = sh.cut[1].unit = -1;
@@ -500,6 +529,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t all_tokens = mine(p.T == 64 ? ~0ull : (1ull << p.T) - 1);
         float acc[kTokens];
 
+        // Up/gate: a warp's row of the activation, 4 of the unit's 128 indices a lane, from the sums.
+        auto store_activation = [&](int unit, int64_t r, const float4 &g, const float4 &u) {
+            const int i = unit % tiles * kUnitRows + 4 * lane;
+            const float v[4] = {rows::silu_times(g.x, u.x), rows::silu_times(g.y, u.y),
+                                rows::silu_times(g.z, u.z), rows::silu_times(g.w, u.w)};
+            if constexpr (FP8) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    m = max(m, rows::size_bits(v[c]));
+                const float scale = rows::scale_of(__reduce_max_sync(0xffffffffu, m)), inv = rows::inverse_of(scale);
+                *reinterpret_cast<uint32_t *>(h_rows + r * p.I + i) =
+                    rows::e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+                if (lane == 0)
+                    h_scales[r * (p.I / 128) + i / 128] = scale;
+            } else if (i < p.I) {  // (a multiple of 8)
+                *reinterpret_cast<uint2 *>(h_rows + (r * p.I + i) * 2) =
+                    make_uint2(rows::pack(v[0], v[1]), rows::pack(v[2], v[3]));
+            }
+        };
+
         // A whole unit's sums in acc: the activation's rows, or the output's.
         auto finish = [&](int unit) {
             if constexpr (DOWN) {
@@ -512,101 +562,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                             out[static_cast<int64_t>(t) * p.H] = __float2bfloat16_rn(acc[t]);
                 }
             } else {
-                const int place = unit / tiles, i = (unit - place * tiles) * kUnitRows + row;
+                const int place = unit / tiles;
                 const uint64_t mask = sh.tokens(sh.active[place]);
-                int64_t at = sh.first[place];  // the next token's row
+                int at = sh.first[place];  // the next token's row
 #pragma unroll
-                for (int t0 = 0; t0 < NT; t0 += 8) {
-                    const uint32_t here = static_cast<uint32_t>(mask >> t0) & 0xFF;
+                for (int t0 = 0; t0 < NT; t0 += kWindow) {
+                    const uint32_t here = static_cast<uint32_t>(mask >> t0) & 0xFFFF;
                     if (!here)
                         continue;
-                    if (group == 1) {
+                    int n = 0;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            if (here >> c & 1)
-                                sh.x.up[c][row] = acc[t0 + c];
-                    }
+                    for (int c = 0; c < kWindow; ++c)
+                        if (here >> c & 1)
+                            sh.x.sums[n++][group * kTile + row] = acc[t0 + c];
                     named_bar_sync(1, kEpilogueThreads);
-                    if (group == 0) {
-                        float v[8];
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            if (!(here >> c & 1))
-                                continue;
-                            v[c] = silu_f32(acc[t0 + c]) * sh.x.up[c][row];
-                            if (FP8) {
-                                const uint32_t m = __reduce_max_sync(0xffffffffu, rows::size_bits(v[c]));
-                                if (lane == 0)
-                                    sh.x.size[c][quarter] = m;
-                            }
-                        }
-                        if (FP8)
-                            named_bar_sync(2, kTile);
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            if (!(here >> c & 1))
-                                continue;
-                            if (FP8) {
-                                const float s = rows::scale_of(max(max(sh.x.size[c][0], sh.x.size[c][1]),
-                                                                   max(sh.x.size[c][2], sh.x.size[c][3])));
-                                h_rows[at * p.I + i] = __nv_cvt_float_to_fp8(v[c] * (1.f / s), __NV_SATFINITE, __NV_E4M3);
-                                if (row == 0)
-                                    h_scales[at * (p.I / 128) + i / 128] = s;
-                            } else if (i < p.I) {
-                                reinterpret_cast<__nv_bfloat16 *>(h_rows)[at * p.I + i] = __float2bfloat16_rn(v[c]);
-                            }
-                            ++at;
-                        }
+                    for (int j = warp - 4; j < n; j += kEpilogueWarps) {
+                        const float4 *sums = reinterpret_cast<const float4 *>(sh.x.sums[j]);
+                        store_activation(unit, at + j, sums[lane], sums[32 + lane]);
                     }
+                    at += n;
                     named_bar_sync(1, kEpilogueThreads);
                 }
             }
         };
 
-        // The factors of a period's sums, of tokens base + lane (and + 32): e4m3, the tokens' and
-        // the weights' scales of one or (down) two blocks of k. Asked for a period ahead.
+        // The factors of a period's sums are those of tokens base + lane (and + 32), of one or
+        // (down) two blocks of k.
         constexpr int kSets = kTokens > 32 ? 2 : 1, kBlocks = DOWN ? 2 : 1;
-        struct Scales {
-            float token[kSets][kBlocks], weight[kBlocks];
-        };
-        auto load_scales = [&](int place, int tile, int k) {
-            Scales sc = {};
-            if constexpr (FP8) {
-                const int e = sh.active[place];
-                const uint64_t mask = sh.tokens(e);
-                const int groups = (DOWN ? p.I : p.H) / 128;
-                const float *w = (DOWN ? p.w2_scales + (static_cast<int64_t>(e) * (p.H / 128) + tile) * groups
-                                       : p.w1_scales + (static_cast<int64_t>(e) * (p.I / 64) + group * (p.I / 128) + tile) * groups);
-#pragma unroll
-                for (int b = 0; b < kBlocks; ++b) {
-                    const int kb = k * kBlocks + b;
-                    if (kb >= groups)
-                        break;  // (nothing is there: sums of 0)
-                    sc.weight[b] = __ldg(w + kb);
-#pragma unroll
-                    for (int i = 0; i < kSets; ++i) {
-                        const int t = base + 32 * i + lane;
-                        if (32 * i + lane < kTokens && (mask >> t & 1)) {
-                            const int r = DOWN ? sh.first[place] + __popcll(mask & ((1ull << t) - 1)) : t;
-                            sc.token[i][b] = (DOWN ? h_scales : p.x_scales)[static_cast<int64_t>(r) * groups + kb];
-                        }
-                    }
-                }
-            }
-            return sc;
-        };
-
         bool ok = true;
         int buf = 0;
         uint32_t buf_phase = 0;
+        int sc = 0;
+        uint32_t sc_phase = 0;
         while (walk.next(seg)) {
 #pragma unroll
             for (int t = 0; t < kTokens; ++t)
                 acc[t] = 0.f;
             int place = DOWN ? seg.s0 / expert_steps : seg.unit / tiles;
             int k = DOWN ? seg.s0 % expert_steps : seg.s0;
-            const int tile = DOWN ? seg.unit : seg.unit % tiles;
-            Scales sc = load_scales(place, tile, k);
             for (int s = seg.s0; ok && s < seg.s1;) {
                 // one period: its steps, tokens and factors
                 const uint64_t mask = sh.tokens(sh.active[place]), here = mine(mask);
@@ -616,19 +609,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (next_k == expert_steps)
                     next_k = 0, ++next_place;
                 float factor[kSets][kBlocks];
+                if constexpr (FP8) {
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&sh.scales.full[sc], sc_phase, kTimeoutNs, abort_flag));
+                    if (!ok)
+                        break;
+                }
 #pragma unroll
                 for (int i = 0; i < kSets; ++i) {
                     const int t = base + 32 * i + lane;
+                    const bool there = 32 * i + lane < kTokens && (mask >> t & 1);
+                    const int r = __popcll(mask & ((1ull << t) - 1));  // among the expert's tokens
                     float g = 1.f;
                     if constexpr (DOWN)
-                        if (lane < kTokens && (mask >> t & 1))
-                            g = sh.x.of_row[sh.first[place] + __popcll(mask & ((1ull << t) - 1))];
+                        g = there ? sh.x.of_row[sh.first[place] + r] : 0.f;
 #pragma unroll
-                    for (int b = 0; b < kBlocks; ++b)
-                        factor[i][b] = !FP8 ? g : (!DOWN || b == 0 || k * 2 + 1 < p.I / 128) ? sc.token[i][b] * sc.weight[b] * g : 0.f;
+                    for (int b = 0; b < kBlocks; ++b) {
+                        factor[i][b] = g;
+                        if constexpr (FP8)
+                            // (a block past the end of k has no scales; its sums are 0)
+                            factor[i][b] = !there || (DOWN && 2 * k + b >= p.I / 128)
+                                               ? 0.f
+                                               : sh.scales.token[sc][b][DOWN ? r : t] *
+                                                     sh.scales.weight[sc][DOWN ? b : group] * g;
+                    }
                 }
-                if (s + n < seg.s1)
-                    sc = load_scales(next_place, tile, next_k);
+                if constexpr (FP8) {
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sh.scales.empty[sc]);
+                    advance(sc, sc_phase, kScaleStages);
+                }
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait(&sh.sums_full[buf], buf_phase, kTimeoutNs, abort_flag));
                 if (!ok)
@@ -742,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int count = __popcll(tokens);
                 // A warp takes a token's 128 rows (gate and up, each), a lane four of them; kAtATime
                 // tokens' and kAhead blocks' sums are under way at once.
-                constexpr int kAtATime = DOWN || NT < 32 ? NT / kEpilogueWarps : 4;
+                constexpr int kAtATime = NT == 16 ? 1 : DOWN ? NT / kEpilogueWarps : NT / 16;
                 constexpr int kAhead = (DOWN ? 16 : 8) / kAtATime;
                 uint64_t left = tokens;  // from this warp's next token on
                 auto skip = [&](int n) {
@@ -798,27 +809,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (i0 + c < p.H)
                                     out[c] = __float2bfloat16_rn(v[c]);
                         } else {
-                            const float4 u = sum[a][1];
-                            const float v[4] = {silu_f32(g.x) * u.x, silu_f32(g.y) * u.y, silu_f32(g.z) * u.z, silu_f32(g.w) * u.w};
-                            const int64_t at = (sh.first[place] + j0 + a * kEpilogueWarps) * static_cast<int64_t>(p.I) + i0;
-                            if (FP8) {
-                                uint32_t m = 0;
-#pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    m = max(m, rows::size_bits(v[c]));
-                                const float sc = rows::scale_of(__reduce_max_sync(0xffffffffu, m)), inv = 1.f / sc;
-                                *reinterpret_cast<uint32_t *>(h_rows + at) =
-                                    rows::e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-                                if (lane == 0)
-                                    h_scales[at / 128] = sc;
-                            } else if (i0 < p.I) {  // (a multiple of 8)
-                                *reinterpret_cast<uint2 *>(h_rows + at * 2) =
-                                    make_uint2(rows::pack(v[0], v[1]), rows::pack(v[2], v[3]));
-                            }
+                            store_activation(unit, sh.first[place] + j0 + a * kEpilogueWarps, g, sum[a][1]);
                         }
                     }
                 }
             }
+        }
+    } else if (FP8 && warp == 3) {
+        // ------------------------------------------------------------ scales, ahead
+        if constexpr (FP8) {
+            if (DOWN)
+                griddep_wait();
+            bool ok = true;
+            int sc = 0;
+            uint32_t sc_phase = 0;
+            const int groups = (DOWN ? p.I : p.H) / 128;
+            while (ok && walk.next(seg)) {
+                int place = DOWN ? seg.s0 / expert_steps : seg.unit / tiles;
+                int k = DOWN ? seg.s0 % expert_steps : seg.s0;
+                const int tile = DOWN ? seg.unit : seg.unit % tiles;
+                for (int s = seg.s0; s < seg.s1; ++s) {
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&sh.scales.empty[sc], sc_phase ^ 1, kTimeoutNs, abort_flag));
+                    if (!ok)
+                        break;
+                    const int64_t e = sh.active[place];
+                    if constexpr (DOWN) {
+                        const int n = __popcll(sh.tokens(sh.active[place])), first = sh.first[place];
+                        for (int b = 0; b < 2 && 2 * k + b < groups; ++b) {
+                            for (int i = lane; i < n; i += 32)
+                                copy_word(&sh.scales.token[sc][b][i], h_scales + static_cast<int64_t>(first + i) * groups + 2 * k + b);
+                            if (lane == 0)
+                                copy_word(&sh.scales.weight[sc][b], p.w2_scales + (e * (p.H / 128) + tile) * groups + 2 * k + b);
+                        }
+                    } else {
+                        for (int t = lane; t < p.T; t += 32)
+                            copy_word(&sh.scales.token[sc][0][t], p.x_scales + static_cast<int64_t>(t) * groups + k);
+                        if (lane < 2)
+                            copy_word(&sh.scales.weight[sc][lane], p.w1_scales + (e * (p.I / 64) + lane * (p.I / 128) + tile) * groups + k);
+                    }
+                    copy_arrive(&sh.scales.full[sc]);
+                    advance(sc, sc_phase, kScaleStages);
+                    if (++k == expert_steps)
+                        k = 0, ++place;
+                }
+            }
+            if (!ok && lane == 0)
+                give_up(p, sh);
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else if (DOWN && warp == 2) {
         griddep_wait();
@@ -841,7 +879,7 @@ template <bool FP8, int NT>
 static cudaError_t launch_form(const FewMaps &maps, const FewParams &p, int num_sms, cudaStream_t s)
 {
     const auto up = few_kernel<false, FP8, NT>, down = few_kernel<true, FP8, NT>;
-    constexpr int up_smem = smem_bytes<false, NT>(), down_smem = smem_bytes<true, NT>();
+    constexpr int up_smem = smem_bytes<false, FP8, NT>(), down_smem = smem_bytes<true, FP8, NT>();
     static_assert(up_smem <= 227 * 1024 && down_smem <= 227 * 1024, "shared memory of a block");
     cudaError_t e = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, up_smem);
     if (e == cudaSuccess)

@@ -109,13 +109,16 @@ __device__ __forceinline__ uint32_t size_bits(const float (&f)[kPiece])
     return m;
 }
 
-// Scale of a group whose largest magnitude has these bits: max(a / 448, 2^-126); NaN where the
-// group holds an infinity or NaN, so that the group is NaN as a whole.
+// Scale of a group whose largest magnitude has these bits: max(a / 448, 2^-126) to within two
+// half steps; NaN where the group holds an infinity or NaN, so that the group is NaN as a whole.
 __device__ __forceinline__ float scale_of(uint32_t bits)
 {
     return bits >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
-                               : fmaxf(__uint_as_float(bits) / 448.f, 1.17549435e-38f);
+                               : fmaxf(__uint_as_float(bits) * (1.f / 448.f), 1.17549435e-38f);
 }
+
+// Its reciprocal (2^-120 .. 2^126) to within two half steps.
+__device__ __forceinline__ float inverse_of(float scale) { return __fdividef(1.f, scale); }
 
 // e4m3 of v * inv, to nearest even. (v / scale passes 448 by fp32 roundings at most, which the
 // saturating conversion takes back; NaN gives NaN.)
@@ -149,7 +152,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t *q, float *scales, int c, int
     const float s = scale_of(half_warp_max(size_bits(f)));
     if (c >= n)
         return;
-    const uint2 codes = e4m3x8(f, 1.f / s);
+    const uint2 codes = e4m3x8(f, inverse_of(s));
     if (VEC) {
         *reinterpret_cast<uint2 *>(q + c) = codes;
     } else {
