@@ -4,11 +4,17 @@
 //   g = dy * weight,   dh = r * (g - h * r^2 * mean(g * h)) + dsum,   dweight = sum_t dy * h * r
 //
 // Both are bound by their rows' bytes. A row stays in one thread block from its load to its
-// stores: it is read once, and may be overwritten in place. Rows of whole 16-byte pieces are
-// copied to shared memory some rows ahead (cp.async), every thread the pieces that it will use
-// itself, so that nobody waits for anybody but in the row's sums; the weight stays in
-// registers. Rows of any other alignment go to shared memory and back in the widest pieces
-// that they allow, consecutive threads consecutive pieces.
+// stores: it is read once, and may be overwritten in place.
+//  * Rows come to shared memory a row or two ahead (cp.async). Rows of whole 16-byte pieces: every
+//    thread copies the pieces that it will use itself, so that nobody waits for anybody but in
+//    the row's sums, and stores them from its registers. Any other rows lie in shared memory as
+//    far from a 16-byte boundary as in memory, so that all but their ends still moves in
+//    aligned pieces, in and out; threads shift the words that they read.
+//  * Instructions come next to bytes here (the gradient's 43 a value took as long as its bytes):
+//    hence arithmetic on two values at a time, the weight in registers, and up to four pieces of
+//    eight values a thread, which share the row's sums and addresses.
+//  * dweight: a block adds its rows' terms in registers and leaves them in the workspace; a second
+//    kernel adds the blocks'.
 #include "ep_internal.h"
 #include "ep_ptx.cuh"
 #include "ep_rows.cuh"
@@ -19,17 +25,11 @@ using namespace rows;
 
 namespace {
 
-constexpr int kPieces = 2;      // of a thread, at most
-constexpr int kMaxWarps = 32;   // 2 pieces of 8 by 1024 threads: EP_MAX_NORM_HIDDEN values
-static_assert(kPieces * kPiece * 32 * kMaxWarps == EP_MAX_NORM_HIDDEN, "a row in a block");
+constexpr int kMaxThreads = 512;
+static_assert(4 * kPiece * kMaxThreads == EP_MAX_NORM_HIDDEN, "a row in a block");
 constexpr int kPartBlocks = 640;       // that leave partial sums of dweight, at most
 constexpr int kSmemOfSm = 216 * 1024;  // for rows under way
 constexpr int kMaxPerSm = 8;           // blocks
-
-// The widest pieces that the rows of a call's tensors allow.
-struct RowUnits {
-    int of[5];
-};
 
 // Sum over the block of two values, the same order for every thread. `part` is not used again
 // before another barrier of the block (two buffers that take turns).
@@ -44,13 +44,31 @@ __device__ __forceinline__ float2 block_sum(float a, float b, float2 *part)
     if (lane == 0)
         part[warp] = make_float2(a, b);
     __syncthreads();
-    float2 v = lane < warps ? part[lane] : make_float2(0.f, 0.f);
+    // (at most 16 warps: both halves of a warp do the same)
+    float2 v = lane % 16 < warps ? part[lane % 16] : make_float2(0.f, 0.f);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
+    for (int o = 8; o; o >>= 1) {
         v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
         v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
     }
     return v;
+}
+
+// The same of one value.
+__device__ __forceinline__ float block_sum(float a, float2 *part)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (lane == 0)
+        part[warp].x = a;
+    __syncthreads();
+    a = lane % 16 < warps ? part[lane % 16].x : 0.f;
+#pragma unroll
+    for (int o = 8; o; o >>= 1)
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
 }
 
 __device__ __forceinline__ void copy_async(uint32_t smem, const void *src)
@@ -66,7 +84,7 @@ __device__ __forceinline__ void copy_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A thread's pieces of one row of a tensor: 16 bytes of a piece lie blockDim.x apart.
+// A thread's piece of one row of a tensor: its 16-byte parts lie blockDim.x apart.
 __device__ __forceinline__ void copy_piece(uint8_t *to, const uint8_t *row, bool bf16, int c)
 {
     const uint32_t dst = smem_u32(to) + threadIdx.x * 16;
@@ -78,250 +96,217 @@ __device__ __forceinline__ void copy_piece(uint8_t *to, const uint8_t *row, bool
     }
 }
 
-__device__ __forceinline__ void read_piece(const uint8_t *from, bool bf16, float (&f)[kPiece])
+__device__ __forceinline__ Piece read_piece(const uint8_t *from, bool bf16)
 {
     const uint4 *p = reinterpret_cast<const uint4 *>(from) + threadIdx.x;
+    if (bf16)
+        return unpack(*p);
+    return piece_of(*reinterpret_cast<const float4 *>(p), *reinterpret_cast<const float4 *>(p + blockDim.x));
+}
+
+// How far a row begins behind a 16-byte boundary.
+__device__ __forceinline__ int skew_of(const void *row) { return static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15); }
+
+// `bytes` of a row to shared memory, to skew_of(from) behind a 16-byte boundary: asynchronously but
+// for the ends.
+__device__ __forceinline__ void copy_in(uint8_t *to, const uint8_t *from, int bytes)
+{
+    const int skew = skew_of(from), end = skew + bytes;
+    from -= skew;  // (whole 16 bytes from `first` to `last` lie inside the row)
+    const int first = skew ? 16 : 0, last = end & ~15;
+    for (int i = first + threadIdx.x * 16; i < last; i += blockDim.x * 16)
+        copy_async(smem_u32(to) + i, from + i);
+    const int head = min(first, end);
+    for (int i = skew + threadIdx.x; i < head; i += blockDim.x)
+        to[i] = from[i];
+    for (int i = max(last, head) + threadIdx.x; i < end; i += blockDim.x)
+        to[i] = from[i];
+}
+
+// The same back, from skew_of(to) behind a 16-byte boundary of shared memory.
+__device__ __forceinline__ void copy_out(uint8_t *to, const uint8_t *from, int bytes)
+{
+    const int skew = skew_of(to), end = skew + bytes;
+    to -= skew;
+    const int first = skew ? 16 : 0, last = end & ~15;
+    for (int i = first + threadIdx.x * 16; i < last; i += blockDim.x * 16)
+        *reinterpret_cast<uint4 *>(to + i) = *reinterpret_cast<const uint4 *>(from + i);
+    const int head = min(first, end);
+    for (int i = skew + threadIdx.x; i < head; i += blockDim.x)
+        to[i] = from[i];
+    for (int i = max(last, head) + threadIdx.x; i < end; i += blockDim.x)
+        to[i] = from[i];
+}
+
+// The N words that begin `skew` bytes behind a 16-byte boundary of shared memory (of which N + 4 are
+// there to be read).
+template <int N>
+__device__ __forceinline__ void read_skewed(const uint8_t *from, int skew, uint32_t (&out)[N])
+{
+    uint32_t w[N + 4];
+#pragma unroll
+    for (int i = 0; i < N + 4; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(from + i * 4);
+        w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
+    const int shift = (skew & 3) * 8;
+    auto take = [&](int first) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            out[i] = __funnelshift_r(w[first + i], first + i + 1 < N + 4 ? w[first + i + 1] : 0, shift);
+    };
+    switch (skew >> 2) {  // (the same for the whole block)
+    case 0:
+        take(0);
+        break;
+    case 1:
+        take(1);
+        break;
+    case 2:
+        take(2);
+        break;
+    default:
+        take(3);
+    }
+}
+
+// Values c .. c+7 of a row of n that copy_in brought, 0 past its end.
+__device__ __forceinline__ Piece read_any(const uint8_t *from, int skew, bool bf16, int c, int n)
+{
+    Piece p;
     if (bf16) {
-        unpack(*p, f);
+        uint32_t w[4];
+        read_skewed(from + c * 2, skew, w);
+        p = unpack(make_uint4(w[0], w[1], w[2], w[3]));
     } else {
-        const float4 a = *reinterpret_cast<const float4 *>(p);
-        const float4 b = *reinterpret_cast<const float4 *>(p + blockDim.x);
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-        f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+        uint32_t w[8];
+        read_skewed(from + c * 4, skew, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p.v[i] = two(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+    if (c + kPiece > n) {
+        float f[kPiece];
+        values_of(p, f);
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i)
+            f[i] = c + i < n ? f[i] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p.v[i] = two(f[2 * i], f[2 * i + 1]);
+    }
+    return p;
+}
+
+// And to where copy_out takes them from.
+__device__ __forceinline__ void write_any(uint8_t *to, int skew, bool bf16, int c, int n, const Piece &p)
+{
+    float f[kPiece];
+    values_of(p, f);
+    if (bf16) {
+        uint16_t *at = reinterpret_cast<uint16_t *>(to + skew) + c;
+        const uint4 v = pack(p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if (skew % 4 == 0 && c + kPiece <= n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                reinterpret_cast<uint32_t *>(at)[i] = w[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i)
+                if (c + i < n)
+                    at[i] = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
+        }
+    } else {
+        float *at = reinterpret_cast<float *>(to + skew) + c;
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i)
+            if (c + i < n)
+                at[i] = f[i];
+    }
+}
+
+__device__ __forceinline__ void write_any(uint8_t *to, int skew, int c, int n, uint2 codes)
+{
+    uint8_t *at = to + skew + c;
+    if (skew % 4 == 0 && c + kPiece <= n) {
+        reinterpret_cast<uint32_t *>(at)[0] = codes.x;
+        reinterpret_cast<uint32_t *>(at)[1] = codes.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i)
+            if (c + i < n)
+                at[i] = static_cast<uint8_t>((i < 4 ? codes.x : codes.y) >> (8 * (i & 3)));
+    }
+}
+
+// Bytes in shared memory of a row of n values: whole pieces, and 16 bytes for the skew.
+__host__ __device__ constexpr int room_of(int n, int value_bytes)
+{
+    return (n + kPiece - 1) / kPiece * kPiece * value_bytes / 16 * 16 + 32;
+}
+
+// This thread's pieces of the weight.
+template <int P>
+__device__ __forceinline__ void load_weight(const uint8_t *weight, bool bf16, int n, Piece (&w)[P])
+{
+    const bool aligned = reinterpret_cast<uintptr_t>(weight) % 16 == 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int c = (i * blockDim.x + threadIdx.x) * kPiece;
+        w[i] = zeros();
+        if (c >= n)
+            continue;
+        if (!aligned || c + kPiece > n)
+            w[i] = load_any(weight, bf16, c, n);
+        else if (bf16)
+            w[i] = unpack(*reinterpret_cast<const uint4 *>(weight + c * 2));
+        else
+            w[i] = piece_of(*reinterpret_cast<const float4 *>(weight + c * 4),
+                            *reinterpret_cast<const float4 *>(weight + c * 4 + 16));
+    }
+}
+
+__device__ __forceinline__ Piece scaled(const Piece &h, float r, const Piece &w)
+{
+    const Two rr = two(r, r);
+    Piece v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        v.v[j] = mul2(mul2(h.v[j], rr), w.v[j]);
+    return v;
+}
+
+// The gradient's terms of a piece: d += r (dy w - h back), dw += dy (h r).
+__device__ __forceinline__ void gradient(const Piece &h, const Piece &dy, const Piece &w, float r, float back, Piece &d,
+                                         Piece &dw)
+{
+    const Two rr = two(r, r), minus_back = two(-back, -back);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        d.v[j] = fma2(rr, fma2(h.v[j], minus_back, mul2(dy.v[j], w.v[j])), d.v[j]);
+        dw.v[j] = fma2(dy.v[j], mul2(h.v[j], rr), dw.v[j]);
+    }
+}
+
+// And those of its sums.
+__device__ __forceinline__ void gradient_sums(const Piece &h, const Piece &dy, const Piece &w, Two &squares, Two &dot)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        squares = fma2(h.v[j], h.v[j], squares);
+        dot = fma2(mul2(dy.v[j], w.v[j]), h.v[j], dot);
     }
 }
 
 }  // namespace
 
-// `bytes` of a row between global and shared memory, in units of `unit` bytes that both are
-// aligned to (a divisor of 16); what is left over byte by byte. ASYNC: to shared memory by
-// cp.async, which takes units of 4 and more.
-template <bool ASYNC, typename U>
-__device__ __forceinline__ void copy_units(uint8_t *to, const uint8_t *from, int bytes)
-{
-    constexpr int kUnit = sizeof(U);
-#pragma unroll 4
-    for (int i = threadIdx.x; i < bytes / kUnit; i += blockDim.x) {
-        if constexpr (ASYNC && kUnit >= 4)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to) + i * kUnit),
-                         "l"(from + i * kUnit), "n"(kUnit)
-                         : "memory");
-        else
-            reinterpret_cast<U *>(to)[i] = reinterpret_cast<const U *>(from)[i];
-    }
-}
-
-template <bool ASYNC>
-__device__ __forceinline__ void copy_row(uint8_t *to, const uint8_t *from, int bytes, int unit)
-{
-    switch (unit) {
-    case 16:
-        copy_units<ASYNC, uint4>(to, from, bytes);
-        break;
-    case 8:
-        copy_units<ASYNC, uint2>(to, from, bytes);
-        break;
-    case 4:
-        copy_units<ASYNC, uint32_t>(to, from, bytes);
-        break;
-    case 2:
-        copy_units<ASYNC, uint16_t>(to, from, bytes);
-        break;
-    default:
-        copy_units<ASYNC, uint8_t>(to, from, bytes);
-    }
-    for (int i = bytes / unit * unit + threadIdx.x; i < bytes; i += blockDim.x)
-        to[i] = from[i];
-}
-
-// Rows of any alignment, by way of shared memory: x (then y) and the residual (then sum), each
-// padded to whole pieces, in two buffers that take turns where they fit; q. A thread overwrites
-// only the pieces that it alone has read.
-__global__ void __launch_bounds__(32 * kMaxWarps) norm_any_kernel(const NormParams p, const RowUnits units,
-                                                                 int buffers)
-{
-    extern __shared__ __align__(16) uint8_t row[];
-    __shared__ float2 part[2][kMaxWarps];
-    int turn = 0;
-    const int n = p.hidden, rb = p.residual_bf16 ? 2 : 4, padded = (n + kPiece - 1) / kPiece * kPiece;
-    const int bytes = padded * (p.residual || p.sum ? 2 + rb : 2);
-    uint8_t *const q = row + buffers * bytes;
-    griddep_wait();
-    griddep_launch_dependents();
-    auto ask = [&](int64_t t, int buffer) {
-        if (t < p.T) {
-            uint8_t *const x = row + buffer * bytes;
-            copy_row<true>(x, p.x + t * p.x_stride * 2, n * 2, units.of[0]);
-            if (p.residual)
-                copy_row<true>(x + padded * 2, p.residual + t * p.residual_stride * rb, n * rb, units.of[1]);
-        }
-        copy_commit();
-    };
-    if (buffers > 1)
-        ask(blockIdx.x, 0);
-    int buffer = 0;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        uint8_t *const x = row + buffer * bytes, *const res = x + padded * 2;
-        if (buffers > 1) {
-            ask(t + gridDim.x, buffer ^ 1);
-            copy_wait<1>();
-            buffer ^= 1;
-        } else {
-            ask(t, 0);
-            copy_wait<0>();
-        }
-        __syncthreads();
-        float h[kPieces][kPiece] = {};
-        float squares = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
-            if (c < n) {
-                load_piece<true>(x, true, c, n, h[i]);
-                float r[kPiece] = {};
-                if (p.residual)
-                    load_piece<true>(res, p.residual_bf16, c, n, r);
-#pragma unroll
-                for (int j = 0; j < kPiece; ++j)
-                    h[i][j] = c + j < n ? h[i][j] + r[j] : 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j)
-                squares = fmaf(h[i][j], h[i][j], squares);
-        }
-        const float r = rsqrtf(block_sum(squares, 0.f, part[turn ^= 1]).x / n + p.eps);
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
-            float v[kPiece] = {};
-            if (c < n) {
-                if (p.sum)
-                    store_piece<true>(res, p.residual_bf16, c, n, h[i]);
-                load_piece<false>(p.weight, p.weight_bf16, c, n, v);
-#pragma unroll
-                for (int j = 0; j < kPiece; ++j)
-                    v[j] = h[i][j] * r * v[j];
-                if (p.y)
-                    store_piece<true>(x, true, c, n, v);
-            }
-            if (p.q)
-                store_e4m3<true>(q, p.q_scales + t * ((n + 127) / 128), c, n, v);
-        }
-        __syncthreads();
-        if (p.sum)
-            copy_row<false>(p.sum + t * p.sum_stride * rb, res, n * rb, units.of[2]);
-        if (p.y)
-            copy_row<false>(p.y + t * p.y_stride * 2, x, n * 2, units.of[3]);
-        if (p.q)
-            copy_row<false>(p.q + t * n, q, n, units.of[4]);
-        __syncthreads();
-    }
-}
-
-// The same for the gradient: h (then dh), dy (then dx), dsum.
-__global__ void __launch_bounds__(32 * kMaxWarps) norm_backward_any_kernel(const NormBackwardParams p,
-                                                                            const RowUnits units, int buffers)
-{
-    extern __shared__ __align__(16) uint8_t row[];
-    __shared__ float2 part[2][kMaxWarps];
-    int turn = 0;
-    const int n = p.hidden, hb = p.h_bf16 ? 2 : 4, padded = (n + kPiece - 1) / kPiece * kPiece;
-    const int bytes = padded * (2 + hb * (p.dsum ? 2 : 1));
-    griddep_wait();
-    griddep_launch_dependents();
-    auto ask = [&](int64_t t, int buffer) {
-        if (t < p.T) {
-            uint8_t *const to = row + buffer * bytes;
-            copy_row<true>(to, p.h + t * p.h_stride * hb, n * hb, units.of[0]);
-            copy_row<true>(to + padded * hb, p.dy + t * p.dy_stride * 2, n * 2, units.of[1]);
-            if (p.dsum)
-                copy_row<true>(to + padded * (hb + 2), p.dsum + t * p.dsum_stride * hb, n * hb, units.of[2]);
-        }
-        copy_commit();
-    };
-    if (buffers > 1)
-        ask(blockIdx.x, 0);
-    int buffer = 0;
-    float dw[kPieces][kPiece] = {};
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        uint8_t *const h_row = row + buffer * bytes, *const dy_row = h_row + padded * hb;
-        uint8_t *const dsum_row = dy_row + padded * 2;
-        if (buffers > 1) {
-            ask(t + gridDim.x, buffer ^ 1);
-            copy_wait<1>();
-            buffer ^= 1;
-        } else {
-            ask(t, 0);
-            copy_wait<0>();
-        }
-        __syncthreads();
-        float squares = 0.f, dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
-            if (c >= n)
-                break;
-            float h[kPiece], dy[kPiece], w[kPiece];
-            load_piece<true>(h_row, p.h_bf16, c, n, h);
-            load_piece<true>(dy_row, true, c, n, dy);
-            load_piece<false>(p.weight, p.weight_bf16, c, n, w);
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j)
-                if (c + j < n) {
-                    squares = fmaf(h[j], h[j], squares);
-                    dot = fmaf(dy[j] * w[j], h[j], dot);
-                }
-        }
-        const float2 sums = block_sum(squares, dot, part[turn ^= 1]);
-        const float r = rsqrtf(sums.x / n + p.eps), back = r * r * (sums.y / n);
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
-            if (c >= n)
-                break;
-            float h[kPiece], dy[kPiece], w[kPiece], d[kPiece] = {};
-            load_piece<true>(h_row, p.h_bf16, c, n, h);
-            load_piece<true>(dy_row, true, c, n, dy);
-            load_piece<false>(p.weight, p.weight_bf16, c, n, w);
-            if (p.dsum)
-                load_piece<true>(dsum_row, p.h_bf16, c, n, d);
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j) {
-                d[j] = fmaf(r, dy[j] * w[j] - h[j] * back, d[j]);
-                if (c + j < n)
-                    dw[i][j] = fmaf(dy[j], h[j] * r, dw[i][j]);
-            }
-            if (p.dh)
-                store_piece<true>(h_row, p.h_bf16, c, n, d);
-            if (p.dx)
-                store_piece<true>(dy_row, true, c, n, d);
-        }
-        __syncthreads();
-        if (p.dh)
-            copy_row<false>(p.dh + t * p.dh_stride * hb, h_row, n * hb, units.of[3]);
-        if (p.dx)
-            copy_row<false>(p.dx + t * p.dx_stride * 2, dy_row, n * 2, units.of[4]);
-        __syncthreads();
-    }
-    if (p.dweight) {
-        float *mine = p.parts + static_cast<int64_t>(blockIdx.x) * n;
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j) {
-                const int c = (i * blockDim.x + threadIdx.x) * kPiece + j;
-                if (c < n)
-                    mine[c] = dw[i][j];
-            }
-    }
-}
-
 // Rows of whole aligned pieces. P: pieces of a thread, S: rows under way.
 template <int P, int S>
-__global__ void __launch_bounds__(32 * kMaxWarps) norm_kernel(const NormParams p)
+__global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 1) norm_kernel(const NormParams p)
 {
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float2 part[2][kMaxWarps];
+    __shared__ float2 part[2][kMaxThreads / 32];
     const int n = p.hidden, rb = p.residual_bf16 ? 2 : 4;
     // of a thread's piece: x, then the residual
     const int x_bytes = blockDim.x * 16, piece_bytes = x_bytes * (p.residual ? 1 + rb / 2 : 1);
@@ -329,15 +314,16 @@ __global__ void __launch_bounds__(32 * kMaxWarps) norm_kernel(const NormParams p
     griddep_launch_dependents();
     auto ask = [&](int64_t t, int stage) {
         if (t < p.T) {
+            const uint8_t *const x = p.x + t * p.x_stride * 2, *const res = p.residual + t * p.residual_stride * rb;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const int c = (i * blockDim.x + threadIdx.x) * kPiece;
                 if (c >= n)
                     break;
                 uint8_t *to = ring + (stage * P + i) * piece_bytes;
-                copy_piece(to, p.x + t * p.x_stride * 2, true, c);
+                copy_piece(to, x, true, c);
                 if (p.residual)
-                    copy_piece(to + x_bytes, p.residual + t * p.residual_stride * rb, p.residual_bf16, c);
+                    copy_piece(to + x_bytes, res, p.residual_bf16, c);
             }
         }
         copy_commit();
@@ -345,60 +331,59 @@ __global__ void __launch_bounds__(32 * kMaxWarps) norm_kernel(const NormParams p
 #pragma unroll
     for (int i = 0; i < S - 1; ++i)
         ask(blockIdx.x + static_cast<int64_t>(i) * gridDim.x, i);
-    float w[P][kPiece] = {};
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * kPiece;
-        if (c < n)
-            load_piece<true>(p.weight, p.weight_bf16, c, n, w[i]);
-    }
+    Piece w[P];
+    load_weight(p.weight, p.weight_bf16, n, w);
     int stage = 0, turn = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         ask(t + static_cast<int64_t>(S - 1) * gridDim.x, stage == 0 ? S - 1 : stage - 1);
         copy_wait<S - 1>();
-        float h[P][kPiece] = {};
-        float squares = 0.f;
+        Piece h[P];
+        Two squares = 0;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * kPiece;
             const uint8_t *from = ring + (stage * P + i) * piece_bytes;
+            h[i] = zeros();
             if (c < n) {
-                read_piece(from, true, h[i]);
+                h[i] = read_piece(from, true);
                 if (p.residual) {
-                    float res[kPiece];
-                    read_piece(from + x_bytes, p.residual_bf16, res);
+                    const Piece res = read_piece(from + x_bytes, p.residual_bf16);
 #pragma unroll
-                    for (int j = 0; j < kPiece; ++j)
-                        h[i][j] += res[j];
+                    for (int j = 0; j < 4; ++j)
+                        h[i].v[j] = add2(h[i].v[j], res.v[j]);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j)
-                squares = fmaf(h[i][j], h[i][j], squares);
+            for (int j = 0; j < 4; ++j)
+                squares = fma2(h[i].v[j], h[i].v[j], squares);
         }
-        const float r = rsqrtf(block_sum(squares, 0.f, part[turn ^= 1]).x / n + p.eps);
+        const float r = rsqrtf(block_sum(sum_of(squares), part[turn ^= 1]) / n + p.eps);
+        uint8_t *const sum = p.sum + t * p.sum_stride * rb, *const y = p.y + t * p.y_stride * 2, *const q = p.q + t * n;
+        float *const scales = p.q_scales + t * ((n + 127) / 128);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * kPiece;
             if (c < n && p.sum)
-                store_piece<true>(p.sum + t * p.sum_stride * rb, p.residual_bf16, c, n, h[i]);
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j)
-                h[i][j] = h[i][j] * r * w[i][j];
+                store_piece(sum, p.residual_bf16, c, h[i]);
+            const Piece v = scaled(h[i], r, w[i]);
             if (c < n && p.y)
-                store_piece<true>(p.y + t * p.y_stride * 2, true, c, n, h[i]);
-            if (p.q)
-                store_e4m3<true>(p.q + t * n, p.q_scales + t * ((n + 127) / 128), c, n, h[i]);
+                store_piece(y, true, c, v);
+            if (p.q) {
+                const uint2 codes = quantise(v, scales, c, n);
+                if (c < n)
+                    *reinterpret_cast<uint2 *>(q + c) = codes;
+            }
         }
         stage = stage == S - 1 ? 0 : stage + 1;
     }
 }
 
 template <int P, int S>
-__global__ void __launch_bounds__(32 * kMaxWarps) norm_backward_kernel(const NormBackwardParams p)
+__global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 : P == 2 ? 3 : 1)
+    norm_backward_kernel(const NormBackwardParams p)
 {
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float2 part[2][kMaxWarps];
+    __shared__ float2 part[2][kMaxThreads / 32];
     const int n = p.hidden, hb = p.h_bf16 ? 2 : 4;
     // of a thread's piece: h, dy, then dsum
     const int dy_bytes = blockDim.x * 16, h_bytes = dy_bytes * (hb / 2);
@@ -407,16 +392,18 @@ __global__ void __launch_bounds__(32 * kMaxWarps) norm_backward_kernel(const Nor
     griddep_launch_dependents();
     auto ask = [&](int64_t t, int stage) {
         if (t < p.T) {
+            const uint8_t *const h = p.h + t * p.h_stride * hb, *const dy = p.dy + t * p.dy_stride * 2;
+            const uint8_t *const dsum = p.dsum + t * p.dsum_stride * hb;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const int c = (i * blockDim.x + threadIdx.x) * kPiece;
                 if (c >= n)
                     break;
                 uint8_t *to = ring + (stage * P + i) * piece_bytes;
-                copy_piece(to, p.h + t * p.h_stride * hb, p.h_bf16, c);
-                copy_piece(to + h_bytes, p.dy + t * p.dy_stride * 2, true, c);
+                copy_piece(to, h, p.h_bf16, c);
+                copy_piece(to + h_bytes, dy, true, c);
                 if (p.dsum)
-                    copy_piece(to + h_bytes + dy_bytes, p.dsum + t * p.dsum_stride * hb, p.h_bf16, c);
+                    copy_piece(to + h_bytes + dy_bytes, dsum, p.h_bf16, c);
             }
         }
         copy_commit();
@@ -424,55 +411,38 @@ __global__ void __launch_bounds__(32 * kMaxWarps) norm_backward_kernel(const Nor
 #pragma unroll
     for (int i = 0; i < S - 1; ++i)
         ask(blockIdx.x + static_cast<int64_t>(i) * gridDim.x, i);
-    float w[P][kPiece] = {}, dw[P][kPiece] = {};
+    Piece w[P], dw[P];
+    load_weight(p.weight, p.weight_bf16, n, w);
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * kPiece;
-        if (c < n)
-            load_piece<true>(p.weight, p.weight_bf16, c, n, w[i]);
-    }
+    for (int i = 0; i < P; ++i)
+        dw[i] = zeros();
     int stage = 0, turn = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         ask(t + static_cast<int64_t>(S - 1) * gridDim.x, stage == 0 ? S - 1 : stage - 1);
         copy_wait<S - 1>();
-        float squares = 0.f, dot = 0.f;
+        Two squares = 0, dot = 0;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * kPiece;
             const uint8_t *from = ring + (stage * P + i) * piece_bytes;
-            if (c >= n)
-                break;
-            float h[kPiece], dy[kPiece];
-            read_piece(from, p.h_bf16, h);
-            read_piece(from + h_bytes, true, dy);
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j) {
-                squares = fmaf(h[j], h[j], squares);
-                dot = fmaf(dy[j] * w[i][j], h[j], dot);
-            }
+            if (c < n)
+                gradient_sums(read_piece(from, p.h_bf16), read_piece(from + h_bytes, true), w[i], squares, dot);
         }
-        const float2 sums = block_sum(squares, dot, part[turn ^= 1]);
+        const float2 sums = block_sum(sum_of(squares), sum_of(dot), part[turn ^= 1]);
         const float r = rsqrtf(sums.x / n + p.eps), back = r * r * (sums.y / n);
+        uint8_t *const dh = p.dh + t * p.dh_stride * hb, *const dx = p.dx + t * p.dx_stride * 2;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * kPiece;
             const uint8_t *from = ring + (stage * P + i) * piece_bytes;
             if (c >= n)
                 break;
-            float h[kPiece], dy[kPiece], d[kPiece] = {};
-            read_piece(from, p.h_bf16, h);
-            read_piece(from + h_bytes, true, dy);
-            if (p.dsum)
-                read_piece(from + h_bytes + dy_bytes, p.h_bf16, d);
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j) {
-                d[j] = fmaf(r, dy[j] * w[i][j] - h[j] * back, d[j]);
-                dw[i][j] = fmaf(dy[j], h[j] * r, dw[i][j]);
-            }
+            Piece d = p.dsum ? read_piece(from + h_bytes + dy_bytes, p.h_bf16) : zeros();
+            gradient(read_piece(from, p.h_bf16), read_piece(from + h_bytes, true), w[i], r, back, d, dw[i]);
             if (p.dh)
-                store_piece<true>(p.dh + t * p.dh_stride * hb, p.h_bf16, c, n, d);
+                store_piece(dh, p.h_bf16, c, d);
             if (p.dx)
-                store_piece<true>(p.dx + t * p.dx_stride * 2, true, c, n, d);
+                store_piece(dx, true, c, d);
         }
         stage = stage == S - 1 ? 0 : stage + 1;
     }
@@ -482,7 +452,189 @@ __global__ void __launch_bounds__(32 * kMaxWarps) norm_backward_kernel(const Nor
         for (int i = 0; i < P; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * kPiece;
             if (c < n)
-                store_piece<true>(mine, false, c, n, dw[i]);
+                store_piece(mine, false, c, dw[i]);
+        }
+    }
+}
+
+// Rows of any alignment: x (then y) and the residual (then sum) in two buffers that take turns, where
+// they fit; q. (What is written has the skew of where it goes, so that it may overlap what other
+// threads read: between the two lies a barrier.)
+template <int P>
+__global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 1) norm_any_kernel(const NormParams p, int buffers)
+{
+    extern __shared__ __align__(16) uint8_t row[];
+    __shared__ float2 part[2][kMaxThreads / 32];
+    const int n = p.hidden, rb = p.residual_bf16 ? 2 : 4, x_room = room_of(n, 2);
+    const int room = x_room + (p.residual || p.sum ? room_of(n, rb) : 0);
+    uint8_t *const q_row = row + buffers * room;
+    griddep_wait();
+    griddep_launch_dependents();
+    auto ask = [&](int64_t t, int buffer) {
+        if (t < p.T) {
+            copy_in(row + buffer * room, p.x + t * p.x_stride * 2, n * 2);
+            if (p.residual)
+                copy_in(row + buffer * room + x_room, p.residual + t * p.residual_stride * rb, n * rb);
+        }
+        copy_commit();
+    };
+    if (buffers > 1)
+        ask(blockIdx.x, 0);
+    Piece w[P];
+    load_weight(p.weight, p.weight_bf16, n, w);
+    int buffer = 0, turn = 0;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        uint8_t *const x = row + buffer * room, *const res = x + x_room;
+        if (buffers > 1) {
+            ask(t + gridDim.x, buffer ^ 1);
+            copy_wait<1>();
+            buffer ^= 1;
+        } else {
+            ask(t, 0);
+            copy_wait<0>();
+        }
+        __syncthreads();
+        const int x_skew = skew_of(p.x + t * p.x_stride * 2);
+        const int res_skew = skew_of(p.residual + t * p.residual_stride * rb);
+        Piece h[P];
+        Two squares = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
+            h[i] = zeros();
+            if (c < n) {
+                h[i] = read_any(x, x_skew, true, c, n);
+                if (p.residual) {
+                    const Piece r = read_any(res, res_skew, p.residual_bf16, c, n);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        h[i].v[j] = add2(h[i].v[j], r.v[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                squares = fma2(h[i].v[j], h[i].v[j], squares);
+        }
+        const float r = rsqrtf(block_sum(sum_of(squares), part[turn ^= 1]) / n + p.eps);
+        uint8_t *const sum = p.sum + t * p.sum_stride * rb, *const y = p.y + t * p.y_stride * 2, *const q = p.q + t * n;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
+            if (c < n && p.sum)
+                write_any(res, skew_of(sum), p.residual_bf16, c, n, h[i]);
+            const Piece v = scaled(h[i], r, w[i]);
+            if (c < n && p.y)
+                write_any(x, skew_of(y), true, c, n, v);
+            if (p.q) {
+                const uint2 codes = quantise(v, p.q_scales + t * ((n + 127) / 128), c, n);
+                if (c < n)
+                    write_any(q_row, skew_of(q), c, n, codes);
+            }
+        }
+        __syncthreads();
+        if (p.sum)
+            copy_out(sum, res, n * rb);
+        if (p.y)
+            copy_out(y, x, n * 2);
+        if (p.q)
+            copy_out(q, q_row, n);
+        __syncthreads();
+    }
+}
+
+// The same for the gradient: h (then dh), dy (then dx), dsum.
+template <int P>
+__global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 : P == 2 ? 3 : 1)
+    norm_backward_any_kernel(const NormBackwardParams p, int buffers)
+{
+    extern __shared__ __align__(16) uint8_t row[];
+    __shared__ float2 part[2][kMaxThreads / 32];
+    const int n = p.hidden, hb = p.h_bf16 ? 2 : 4, h_room = room_of(n, hb), dy_room = room_of(n, 2);
+    const int room = dy_room + h_room * (p.dsum ? 2 : 1);
+    griddep_wait();
+    griddep_launch_dependents();
+    auto ask = [&](int64_t t, int buffer) {
+        if (t < p.T) {
+            uint8_t *const to = row + buffer * room;
+            copy_in(to, p.h + t * p.h_stride * hb, n * hb);
+            copy_in(to + h_room, p.dy + t * p.dy_stride * 2, n * 2);
+            if (p.dsum)
+                copy_in(to + h_room + dy_room, p.dsum + t * p.dsum_stride * hb, n * hb);
+        }
+        copy_commit();
+    };
+    if (buffers > 1)
+        ask(blockIdx.x, 0);
+    Piece w[P], dw[P];
+    load_weight(p.weight, p.weight_bf16, n, w);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        dw[i] = zeros();
+    int buffer = 0, turn = 0;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        uint8_t *const h_row = row + buffer * room, *const dy_row = h_row + h_room, *const dsum_row = dy_row + dy_room;
+        if (buffers > 1) {
+            ask(t + gridDim.x, buffer ^ 1);
+            copy_wait<1>();
+            buffer ^= 1;
+        } else {
+            ask(t, 0);
+            copy_wait<0>();
+        }
+        __syncthreads();
+        const int h_skew = skew_of(p.h + t * p.h_stride * hb), dy_skew = skew_of(p.dy + t * p.dy_stride * 2);
+        const int dsum_skew = skew_of(p.dsum + t * p.dsum_stride * hb);
+        Two squares = 0, dot = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
+            if (c < n)
+                gradient_sums(read_any(h_row, h_skew, p.h_bf16, c, n), read_any(dy_row, dy_skew, true, c, n), w[i],
+                              squares, dot);
+        }
+        const float2 sums = block_sum(sum_of(squares), sum_of(dot), part[turn ^= 1]);
+        const float r = rsqrtf(sums.x / n + p.eps), back = r * r * (sums.y / n);
+        uint8_t *const dh = p.dh + t * p.dh_stride * hb, *const dx = p.dx + t * p.dx_stride * 2;
+        Piece d[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
+            d[i] = zeros();
+            if (c >= n)
+                continue;
+            if (p.dsum)
+                d[i] = read_any(dsum_row, dsum_skew, p.h_bf16, c, n);
+            gradient(read_any(h_row, h_skew, p.h_bf16, c, n), read_any(dy_row, dy_skew, true, c, n), w[i], r, back,
+                     d[i], dw[i]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
+            if (c < n && p.dh)
+                write_any(h_row, skew_of(dh), p.h_bf16, c, n, d[i]);
+            if (c < n && p.dx)
+                write_any(dy_row, skew_of(dx), true, c, n, d[i]);
+        }
+        __syncthreads();
+        if (p.dh)
+            copy_out(dh, h_row, n * hb);
+        if (p.dx)
+            copy_out(dx, dy_row, n * 2);
+        __syncthreads();
+    }
+    if (p.dweight) {
+        float *mine = p.parts + static_cast<int64_t>(blockIdx.x) * n;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float f[kPiece];
+            values_of(dw[i], f);
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) {
+                const int c = (i * blockDim.x + threadIdx.x) * kPiece + j;
+                if (c < n)
+                    mine[c] = f[j];
+            }
         }
     }
 }
@@ -520,45 +672,32 @@ bool whole_pieces(const void *base, int64_t stride, int bytes)
     return !base || (reinterpret_cast<uintptr_t>(base) % 16 == 0 && stride * bytes % 16 == 0);
 }
 
-// The widest unit that all rows of a tensor start and go on in.
-int unit_of(const void *base, int64_t stride, int bytes)
-{
-    const uint64_t all = reinterpret_cast<uintptr_t>(base) | static_cast<uint64_t>(stride) * bytes | 16;
-    return static_cast<int>(all & (~all + 1));
-}
-
-int threads_for(int hidden, int pieces)
-{
-    const int per_thread = pieces * kPiece;
-    return ((hidden + per_thread - 1) / per_thread + 31) / 32 * 32;
-}
-
-// How a row of a launch is laid out: threads, pieces of each, rows under way (0: more than
-// shared memory holds) and blocks of an SM.
+// How a row of a launch is laid out: threads, pieces of each, rows under way and blocks of an SM.
 struct Form {
-    int threads, pieces, stages, per_sm, smem;
+    int threads, pieces, stages, per_sm;
 };
 
-Form form_for(int hidden, int value_bytes)
+// `two_upto`: the longest rows of two pieces a thread.
+Form form_for(int hidden, int value_bytes, int two_upto)
 {
     Form f;
-    f.pieces = hidden > kPiece * 512 ? 2 : 1;
-    f.threads = threads_for(hidden, f.pieces);
-    const int row = f.threads * f.pieces * kPiece * value_bytes;
-    f.per_sm = 1024 / f.threads < 1 ? 1 : 1024 / f.threads;
-    f.per_sm = f.per_sm > kMaxPerSm ? kMaxPerSm : f.per_sm;
+    f.pieces = hidden <= 1024 ? 1 : hidden <= two_upto ? 2 : 4;
+    const int per_thread = f.pieces * kPiece;
+    f.threads = ((hidden + per_thread - 1) / per_thread + 31) / 32 * 32;
+    const int row = f.threads * per_thread * value_bytes;
+    const int most = 1024 / f.threads;
+    f.per_sm = most < 1 ? 1 : most > kMaxPerSm ? kMaxPerSm : most;
     while (f.per_sm > 1 && 2 * row * f.per_sm > kSmemOfSm)
         --f.per_sm;
     f.stages = kSmemOfSm / (row * f.per_sm);
-    f.stages = f.stages > 4 ? 4 : f.stages < 2 ? 0 : f.stages;
-    f.smem = f.stages * row;
+    f.stages = f.stages > 3 ? 3 : f.stages;
     return f;
 }
 
 template <typename Kern, typename... Args>
 cudaError_t launch_rows(Kern kern, int threads, int smem, unsigned grid, cudaStream_t s, const Args &...args)
 {
-    if (smem > 48 * 1024) {
+    if (smem > 47 * 1024) {  // (48 KB with the kernel's own)
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess)
             return e;
@@ -566,35 +705,33 @@ cudaError_t launch_rows(Kern kern, int threads, int smem, unsigned grid, cudaStr
     return launch_behind(kern, grid, threads, smem, s, args...);
 }
 
-int padded(int hidden) { return (hidden + kPiece - 1) / kPiece * kPiece; }
-
 }  // namespace
 
 cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t s)
 {
     const int rb = p.residual_bf16 ? 2 : 4;
-    const bool vec = p.hidden % kPiece == 0 && whole_pieces(p.x, p.x_stride, 2) &&
-                     whole_pieces(p.residual, p.residual_stride, rb) && whole_pieces(p.sum, p.sum_stride, rb) &&
-                     whole_pieces(p.y, p.y_stride, 2) && whole_pieces(p.weight, 0, 4) &&
-                     reinterpret_cast<uintptr_t>(p.q) % 8 == 0;
-    const Form f = form_for(p.hidden, 2 + (p.residual ? rb : 0));
-    if (!vec || !f.stages) {
-        const int most = 16 * num_sms;
-        const int row = padded(p.hidden) * (2 + (p.residual || p.sum ? rb : 0)), q = p.q ? padded(p.hidden) : 0;
-        const int buffers = 2 * row + q <= kSmemOfSm ? 2 : 1;
-        const RowUnits units = {{unit_of(p.x, p.x_stride, 2), unit_of(p.residual, p.residual_stride, rb),
-                                 unit_of(p.sum, p.sum_stride, rb), unit_of(p.y, p.y_stride, 2),
-                                 unit_of(p.q, p.hidden, 1)}};
-        return launch_rows(norm_any_kernel, threads_for(p.hidden, kPieces), buffers * row + q,
-                           p.T < most ? p.T : most, s, p, units, buffers);
-    }
+    const bool whole = p.hidden % kPiece == 0 && whole_pieces(p.x, p.x_stride, 2) &&
+                       whole_pieces(p.residual, p.residual_stride, rb) && whole_pieces(p.sum, p.sum_stride, rb) &&
+                       whole_pieces(p.y, p.y_stride, 2) && reinterpret_cast<uintptr_t>(p.q) % 8 == 0;
+    const int bytes = 2 + (p.residual ? rb : 0);
+    const Form f = form_for(p.hidden, bytes, 8192);
     const int most = f.per_sm * num_sms;
     const unsigned grid = p.T < most ? p.T : most;
-    auto go = [&](auto two, auto three, auto four) {
-        return launch_rows(f.stages == 2 ? two : f.stages == 3 ? three : four, f.threads, f.smem, grid, s, p);
-    };
-    return f.pieces == 1 ? go(norm_kernel<1, 2>, norm_kernel<1, 3>, norm_kernel<1, 4>)
-                         : go(norm_kernel<2, 2>, norm_kernel<2, 3>, norm_kernel<2, 4>);
+    if (whole && f.stages >= 2) {
+        const int smem = f.stages * f.threads * f.pieces * kPiece * bytes;
+        auto go = [&](auto two, auto three) {
+            return launch_rows(f.stages == 2 ? two : three, f.threads, smem, grid, s, p);
+        };
+        return f.pieces == 1   ? go(norm_kernel<1, 2>, norm_kernel<1, 3>)
+               : f.pieces == 2 ? go(norm_kernel<2, 2>, norm_kernel<2, 3>)
+                               : go(norm_kernel<4, 2>, norm_kernel<4, 3>);
+    }
+    const int room = room_of(p.hidden, 2) + (p.residual || p.sum ? room_of(p.hidden, rb) : 0);
+    const int q_room = p.q ? room_of(p.hidden, 1) : 0, buffers = 2 * room + q_room <= kSmemOfSm ? 2 : 1;
+    return launch_rows(f.pieces == 1   ? norm_any_kernel<1>
+                       : f.pieces == 2 ? norm_any_kernel<2>
+                                       : norm_any_kernel<4>,
+                       f.threads, buffers * room + q_room, grid, s, p, buffers);
 }
 
 int64_t norm_backward_workspace_bytes(int T, int hidden)
@@ -605,28 +742,30 @@ int64_t norm_backward_workspace_bytes(int T, int hidden)
 cudaError_t launch_norm_backward(const NormBackwardParams &p, int num_sms, cudaStream_t s)
 {
     const int hb = p.h_bf16 ? 2 : 4;
-    const bool vec = p.hidden % kPiece == 0 && whole_pieces(p.h, p.h_stride, hb) &&
-                     whole_pieces(p.dy, p.dy_stride, 2) && whole_pieces(p.dsum, p.dsum_stride, hb) &&
-                     whole_pieces(p.dh, p.dh_stride, hb) && whole_pieces(p.dx, p.dx_stride, 2) &&
-                     whole_pieces(p.weight, 0, 4);
-    const Form f = form_for(p.hidden, 2 + hb * 2);  // (without dsum, too: the same order of dweight's sum)
+    const bool whole = p.hidden % kPiece == 0 && whole_pieces(p.h, p.h_stride, hb) &&
+                       whole_pieces(p.dy, p.dy_stride, 2) && whole_pieces(p.dsum, p.dsum_stride, hb) &&
+                       whole_pieces(p.dh, p.dh_stride, hb) && whole_pieces(p.dx, p.dx_stride, 2);
+    // (as with dsum, where there is none, too: the same order of dweight's sum)
+    const Form f = form_for(p.hidden, 2 + hb * 2, 4096);
     int most = f.per_sm * num_sms;
     most = most < kPartBlocks ? most : kPartBlocks;
     const unsigned grid = p.T < most ? p.T : most;
     cudaError_t e;
-    if (!vec || !f.stages) {
-        const RowUnits units = {{unit_of(p.h, p.h_stride, hb), unit_of(p.dy, p.dy_stride, 2),
-                                 unit_of(p.dsum, p.dsum_stride, hb), unit_of(p.dh, p.dh_stride, hb),
-                                 unit_of(p.dx, p.dx_stride, 2)}};
-        const int row = padded(p.hidden) * (2 + hb * (p.dsum ? 2 : 1)), buffers = 2 * row <= kSmemOfSm ? 2 : 1;
-        e = launch_rows(norm_backward_any_kernel, threads_for(p.hidden, kPieces), buffers * row, grid, s, p, units,
-                        buffers);
-    } else {
-        auto go = [&](auto two, auto three, auto four) {
-            return launch_rows(f.stages == 2 ? two : f.stages == 3 ? three : four, f.threads, f.smem, grid, s, p);
+    if (whole && f.stages >= 2) {
+        const int smem = f.stages * f.threads * f.pieces * kPiece * (2 + hb * (p.dsum ? 2 : 1));
+        auto go = [&](auto two, auto three) {
+            return launch_rows(f.stages == 2 ? two : three, f.threads, smem, grid, s, p);
         };
-        e = f.pieces == 1 ? go(norm_backward_kernel<1, 2>, norm_backward_kernel<1, 3>, norm_backward_kernel<1, 4>)
-                          : go(norm_backward_kernel<2, 2>, norm_backward_kernel<2, 3>, norm_backward_kernel<2, 4>);
+        e = f.pieces == 1   ? go(norm_backward_kernel<1, 2>, norm_backward_kernel<1, 3>)
+            : f.pieces == 2 ? go(norm_backward_kernel<2, 2>, norm_backward_kernel<2, 3>)
+                            : go(norm_backward_kernel<4, 2>, norm_backward_kernel<4, 3>);
+    } else {
+        const int room = room_of(p.hidden, 2) + room_of(p.hidden, hb) * (p.dsum ? 2 : 1);
+        const int buffers = 2 * room <= kSmemOfSm ? 2 : 1;
+        e = launch_rows(f.pieces == 1   ? norm_backward_any_kernel<1>
+                        : f.pieces == 2 ? norm_backward_any_kernel<2>
+                                        : norm_backward_any_kernel<4>,
+                        f.threads, buffers * room, grid, s, p, buffers);
     }
     if (e == cudaSuccess && p.dweight)
         e = launch_behind(norm_weight_kernel, (p.hidden + 31) / 32, 1024, 0, s, p, static_cast<int>(grid));

@@ -1,5 +1,5 @@
-// Rows in pieces of eight values: loads and stores in fp32 and bf16, and the quantisation of
-// 128 columns to e4m3 with one scale.
+// Rows in pieces of eight values: loads and stores in fp32 and bf16, arithmetic two values at a
+// time, and the quantisation of 128 columns to e4m3 with one scale.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -13,8 +13,68 @@ namespace rows {
 constexpr int kPiece = 8;         // values of a piece
 constexpr int kGroupPieces = 16;  // pieces of a scale's 128 columns: half a warp
 
-__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// Two fp32 values, as the packed instructions take them; each is rounded on its own.
+using Two = uint64_t;
+
+__device__ __forceinline__ Two two(float lo, float hi)
+{
+    Two t;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(t) : "f"(lo), "f"(hi));
+    return t;
+}
+
+__device__ __forceinline__ void split(Two t, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(t));
+}
+
+__device__ __forceinline__ float sum_of(Two t)
+{
+    float lo, hi;
+    split(t, lo, hi);
+    return lo + hi;
+}
+
+__device__ __forceinline__ Two add2(Two a, Two b)
+{
+    Two d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ Two mul2(Two a, Two b)
+{
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c)
+{
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// A piece's values.
+struct Piece {
+    Two v[4];
+};
+
+__device__ __forceinline__ Piece zeros()
+{
+    return Piece{{0, 0, 0, 0}};
+}
+
+__device__ __forceinline__ Two two_of(uint32_t bf16x2)
+{
+    return two(__uint_as_float(bf16x2 << 16), __uint_as_float(bf16x2 & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ Piece unpack(const uint4 &v)
+{
+    return Piece{{two_of(v.x), two_of(v.y), two_of(v.z), two_of(v.w)}};
+}
 
 __device__ __forceinline__ uint32_t pack(float lo, float hi)
 {
@@ -22,71 +82,54 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&b);
 }
 
-__device__ __forceinline__ void unpack(const uint4 &v, float (&f)[kPiece])
+__device__ __forceinline__ uint32_t pack(Two t)
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float lo, hi;
+    split(t, lo, hi);
+    return pack(lo, hi);
+}
+
+__device__ __forceinline__ uint4 pack(const Piece &p)
+{
+    return make_uint4(pack(p.v[0]), pack(p.v[1]), pack(p.v[2]), pack(p.v[3]));
+}
+
+__device__ __forceinline__ Piece piece_of(const float4 &a, const float4 &b)
+{
+    return Piece{{two(a.x, a.y), two(a.z, a.w), two(b.x, b.y), two(b.z, b.w)}};
+}
+
+__device__ __forceinline__ void values_of(const Piece &p, float (&f)[kPiece])
+{
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        f[2 * i] = lo_of(w[i]), f[2 * i + 1] = hi_of(w[i]);
+        split(p.v[i], f[2 * i], f[2 * i + 1]);
 }
 
-__device__ __forceinline__ uint4 pack(const float (&f)[kPiece])
+// Values c .. c+7 of a row of n at `base`, of any alignment (0 past the row's end).
+__device__ __forceinline__ Piece load_any(const uint8_t *base, bool bf16, int c, int n)
 {
-    return make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
-}
-
-// Values c .. c+7 of a row at `base` (of n values; 0 past its end). VEC: whole, aligned pieces.
-template <bool VEC>
-__device__ __forceinline__ void load_piece(const uint8_t *base, bool bf16, int c, int n, float (&f)[kPiece])
-{
-    if (bf16) {
-        const __nv_bfloat16 *r = reinterpret_cast<const __nv_bfloat16 *>(base) + c;
-        if (VEC) {
-            unpack(*reinterpret_cast<const uint4 *>(r), f);
-        } else {
+    float f[kPiece];
 #pragma unroll
-            for (int i = 0; i < kPiece; ++i)
-                f[i] = c + i < n ? __bfloat162float(r[i]) : 0.f;
-        }
-    } else {
-        const float *r = reinterpret_cast<const float *>(base) + c;
-        if (VEC) {
-            const float4 a = *reinterpret_cast<const float4 *>(r);
-            const float4 b = *reinterpret_cast<const float4 *>(r + 4);
-            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-            f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPiece; ++i)
-                f[i] = c + i < n ? r[i] : 0.f;
-        }
+    for (int i = 0; i < kPiece; ++i) {
+        f[i] = 0.f;
+        if (c + i < n)
+            f[i] = bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(base)[c + i])
+                        : reinterpret_cast<const float *>(base)[c + i];
     }
+    return Piece{{two(f[0], f[1]), two(f[2], f[3]), two(f[4], f[5]), two(f[6], f[7])}};
 }
 
-template <bool VEC>
-__device__ __forceinline__ void store_piece(uint8_t *base, bool bf16, int c, int n, const float (&f)[kPiece])
+// Whole, aligned pieces.
+__device__ __forceinline__ void store_piece(uint8_t *base, bool bf16, int c, const Piece &p)
 {
     if (bf16) {
-        __nv_bfloat16 *r = reinterpret_cast<__nv_bfloat16 *>(base) + c;
-        if (VEC) {
-            *reinterpret_cast<uint4 *>(r) = pack(f);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPiece; ++i)
-                if (c + i < n)
-                    r[i] = __float2bfloat16_rn(f[i]);
-        }
+        *reinterpret_cast<uint4 *>(base + c * 2) = pack(p);
     } else {
-        float *r = reinterpret_cast<float *>(base) + c;
-        if (VEC) {
-            *reinterpret_cast<float4 *>(r) = make_float4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<float4 *>(r + 4) = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPiece; ++i)
-                if (c + i < n)
-                    r[i] = f[i];
-        }
+        float f[kPiece];
+        values_of(p, f);
+        *reinterpret_cast<float4 *>(base + c * 4) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4 *>(base + c * 4 + 16) = make_float4(f[4], f[5], f[6], f[7]);
     }
 }
 
@@ -100,13 +143,22 @@ __device__ __forceinline__ float silu_times(float x, float u)
 // The bits of |v|: as integers they order finite values, infinities and NaN in that order.
 __device__ __forceinline__ uint32_t size_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-__device__ __forceinline__ uint32_t size_bits(const float (&f)[kPiece])
+// max(|a|, |b|, |c|), NaN if one of them is.
+__device__ __forceinline__ float max_size(float a, float b, float c)
 {
-    uint32_t m = 0;
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t size_bits(const Piece &p)
+{
+    float f[kPiece], m = 0.f;
+    values_of(p, f);
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i)
-        m = max(m, size_bits(f[i]));
-    return m;
+    for (int i = 0; i < kPiece; i += 2)
+        m = max_size(m, f[i], f[i + 1]);
+    return size_bits(m);
 }
 
 // Scale of a group whose largest magnitude has these bits: max(a / 448, 2^-126) to within two
@@ -129,10 +181,12 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
     return lo | hi << 16;
 }
 
-__device__ __forceinline__ uint2 e4m3x8(const float (&f)[kPiece], float inv)
+__device__ __forceinline__ uint2 e4m3x8(const Piece &p, float inv)
 {
-    return make_uint2(e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                      e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+    const Two i = two(inv, inv);
+    float f[kPiece];
+    values_of(Piece{{mul2(p.v[0], i), mul2(p.v[1], i), mul2(p.v[2], i), mul2(p.v[3], i)}}, f);
+    return make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
 }
 
 // Largest of the values of a half warp (all of its lanes take part).
@@ -144,25 +198,14 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t v)
     return v;
 }
 
-// Codes of piece c of a row's n columns, of a group that lies in this half warp (a piece past
-// the row's end counts as zeros), and by the group's first lane its scale.
-template <bool VEC>
-__device__ __forceinline__ void store_e4m3(uint8_t *q, float *scales, int c, int n, const float (&f)[kPiece])
+// Codes of piece c of a row's n columns, of a group that lies in this half warp (values past the
+// row's end are zeros), and by the group's first lane its scale.
+__device__ __forceinline__ uint2 quantise(const Piece &p, float *scales, int c, int n)
 {
-    const float s = scale_of(half_warp_max(size_bits(f)));
-    if (c >= n)
-        return;
-    const uint2 codes = e4m3x8(f, inverse_of(s));
-    if (VEC) {
-        *reinterpret_cast<uint2 *>(q + c) = codes;
-    } else {
-#pragma unroll
-        for (int i = 0; i < kPiece; ++i)
-            if (c + i < n)
-                q[c + i] = static_cast<uint8_t>((i < 4 ? codes.x : codes.y) >> (8 * (i & 3)));
-    }
-    if (c % (kPiece * kGroupPieces) == 0)
+    const float s = scale_of(half_warp_max(size_bits(p)));
+    if (c < n && c % (kPiece * kGroupPieces) == 0)
         scales[c / (kPiece * kGroupPieces)] = s;
+    return e4m3x8(p, inverse_of(s));
 }
 
 }  // namespace rows
