@@ -17,8 +17,8 @@
 //    its experts never leaves the block. The list is cut into one run a block, of whole units or,
 //    where that balances better, anywhere (Runs); units that are cut are joined through the
 //    workspace by the last of their blocks, in block order.
-//  * Sums are taken out of tensor memory into registers (fp32), a thread to a weight row, with a
-//    factor: the gate at an expert's end (down), or, e4m3, the scales of each 128 k.
+//  * Sums are taken out of tensor memory into registers (fp32), a thread to a weight row: e4m3, of
+//    each 128 k, with their scales; down, at an expert's end with the gates.
 //    Tensor memory holds two periods' sums, so that the products go on meanwhile. Two groups
 //    of four warps do that: one for the gate and one for the up rows, or (down) for half of
 //    the tokens each.
@@ -54,10 +54,8 @@ constexpr int kJoinSteps = 4;
 // min_steps, each of which takes about as long as half a step does.
 __device__ __forceinline__ int min_steps(int steps)
 {
-    int s = 2;
-    while (s < 64 && 2 * s * s < steps)
-        ++s;
-    return s;
+    const int s = static_cast<int>(ceilf(sqrtf(0.5f * steps)));
+    return s < 2 ? 2 : s > 64 ? 64 : s;
 }
 
 struct Segment {
@@ -145,17 +143,15 @@ __device__ __forceinline__ void give_up(const FewParams &p, S &sh)
 }
 
 // Which tokens each local expert has, the experts that have some, the first row of each, and
-// (down) every row's gate. All threads; ends with a barrier.
+// (down) every row's gate. All threads, the masks zero; the gates are there after another barrier.
+// (Past the first level of cache: the second kernel reads ids and gates before it waits.)
 template <bool DOWN, typename S>
 __device__ __forceinline__ void make_plan(const FewParams &p, S &sh)
 {
     const int tid = threadIdx.x, slots = p.T * p.top_k, first = p.my_rank * p.El;
-    for (int e = tid; e < p.El; e += kThreads)
-        sh.mask[e][0] = sh.mask[e][1] = 0;
-    __syncthreads();
     bool bad = false;
     for (int s = tid; s < slots; s += kThreads) {
-        const int id = __ldg(p.topk_ids + s), e = id - first;
+        const int id = __ldcg(p.topk_ids + s), e = id - first;
         const bool here = id >= first && e < p.El;
         bad |= id < 0 || id >= p.n_ranks * p.El;
         const int t = s / p.top_k;
@@ -163,7 +159,7 @@ __device__ __forceinline__ void make_plan(const FewParams &p, S &sh)
             atomicOr(&sh.mask[e][t / 32], 1u << t % 32);
         if constexpr (DOWN) {
             sh.x.expert[s] = static_cast<int16_t>(here ? e : -1);
-            sh.x.of_slot[s] = __ldg(p.gates + s);
+            sh.x.of_slot[s] = __ldcg(p.gates + s);
         }
     }
     if (!DOWN && bad && blockIdx.x == 0)
@@ -290,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kBlockK = FP8 ? 128 : 64;            // k of 128 bytes
     constexpr int kStepK = DOWN ? 2 * kBlockK : kBlockK;
     constexpr int kUnitRows = kTile;                   // (of the gate, too, of the up matrix)
-    constexpr uint32_t kTmemCols = 4 * NT;  // two periods of two products' sums
+    // two periods of two products' sums; e4m3, down: and NT columns of scratch
+    constexpr uint32_t kTmemCols = (DOWN && FP8 ? 8 : 4) * NT;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     using Sh = Shared<DOWN, FP8, NT>;
@@ -317,9 +314,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         sh.abort = 0;
         sh.cut[0].unit = sh.cut[1].unit = -1;
     }
+    for (int e = tid; e < p.El; e += kThreads)
+        sh.mask[e][0] = sh.mask[e][1] = 0;
+    __syncthreads();
     if (!DOWN) {
         griddep_wait();
         griddep_launch_dependents();
+    }
+    // (tensor memory only now: the previous kernel may still have wanted it. The second kernel's block
+    // finds its SM left by the first one's, which held as much shared memory)
+    if (warp == kThreads / 32 - 1) {
+        tmem_alloc(&sh.tmem, kTmemCols);
+        tmem_relinquish();
     }
     // (the first kernel waited for all that came before it ahead of letting the second one start:
     // ids, gates and weights are there; only what the first kernel writes is waited for below)
@@ -343,10 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         sh.runs = runs;
         sh.start = (block * runs.per + (block < runs.rest ? block : runs.rest)) * runs.piece;
         sh.todo = block < blocks ? (runs.per + (block < runs.rest)) * runs.piece : 0;
-    }
-    if (warp == 1) {
-        tmem_alloc(&sh.tmem, kTmemCols);
-        tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
@@ -586,9 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
 
-        // The factors of a period's sums are those of tokens base + lane (and + 32), of one or
-        // (down) two blocks of k.
-        constexpr int kSets = kTokens > 32 ? 2 : 1, kBlocks = DOWN ? 2 : 1;
+        // e4m3, down: the sums of the expert under way, its tokens without gaps.
+        float own[DOWN && FP8 ? kTokens : 1];
+        const uint32_t my_scratch = tmem + 4 * NT + group * kTokens + (static_cast<uint32_t>(32 * quarter) << 16);
         bool ok = true;
         int buf = 0;
         uint32_t buf_phase = 0;
@@ -598,6 +600,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int t = 0; t < kTokens; ++t)
                 acc[t] = 0.f;
+            if constexpr (DOWN && FP8)
+#pragma unroll
+                for (int t = 0; t < kTokens; ++t)
+                    own[t] = 0.f;
             int place = DOWN ? seg.s0 / expert_steps : seg.unit / tiles;
             int k = DOWN ? seg.s0 % expert_steps : seg.s0;
             for (int s = seg.s0; ok && s < seg.s1;) {
@@ -608,33 +614,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int next_place = place, next_k = k + n;
                 if (next_k == expert_steps)
                     next_k = 0, ++next_place;
-                float factor[kSets][kBlocks];
+                // lane i's factors: up/gate, of tokens i and i + 32; down, of the expert's i-th token of
+                // this half, two blocks of k
+                const int first = DOWN ? __popcll(mask & ((1ull << base) - 1)) : 0, count = __popcll(here);
+                float factor[2];
                 if constexpr (FP8) {
                     ok = __all_sync(0xffffffffu,
                                     mbar_wait(&sh.scales.full[sc], sc_phase, kTimeoutNs, abort_flag));
                     if (!ok)
                         break;
-                }
 #pragma unroll
-                for (int i = 0; i < kSets; ++i) {
-                    const int t = base + 32 * i + lane;
-                    const bool there = 32 * i + lane < kTokens && (mask >> t & 1);
-                    const int r = __popcll(mask & ((1ull << t) - 1));  // among the expert's tokens
-                    float g = 1.f;
-                    if constexpr (DOWN)
-                        g = there ? sh.x.of_row[sh.first[place] + r] : 0.f;
-#pragma unroll
-                    for (int b = 0; b < kBlocks; ++b) {
-                        factor[i][b] = g;
-                        if constexpr (FP8)
-                            // (a block past the end of k has no scales; its sums are 0)
-                            factor[i][b] = !there || (DOWN && 2 * k + b >= p.I / 128)
-                                               ? 0.f
-                                               : sh.scales.token[sc][b][DOWN ? r : t] *
-                                                     sh.scales.weight[sc][DOWN ? b : group] * g;
+                    for (int i = 0; i < 2; ++i) {
+                        // (a block past the end of k has no scales; its sums are 0)
+                        const bool there = DOWN ? lane < count && 2 * k + i < p.I / 128
+                                                : 32 * i + lane < NT && (mask >> (32 * i + lane) & 1);
+                        factor[i] = !there ? 0.f
+                                    : DOWN ? sh.scales.token[sc][i][first + lane] * sh.scales.weight[sc][i]
+                                           : sh.scales.token[sc][0][32 * i + lane] * sh.scales.weight[sc][group];
                     }
-                }
-                if constexpr (FP8) {
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&sh.scales.empty[sc]);
@@ -645,39 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok)
                     break;
                 tc_fence_after();
-                uint32_t from = my_sums + buf * 2 * NT;
-                if constexpr (DOWN) {
-                    // columns: the expert's tokens without gaps, each at one's own place in acc
-                    from += __popcll(mask & ((1ull << base) - 1));
-                    constexpr int kAtOnce = FP8 || kTokens < 16 ? 8 : 16;
-#pragma unroll
-                    for (int t0 = 0; t0 < kTokens; t0 += kAtOnce) {
-                        const uint32_t now = static_cast<uint32_t>(here >> t0) & ((1u << kAtOnce) - 1);
-                        if (!now)
-                            continue;
-                        uint32_t v[kAtOnce * kBlocks];
-#pragma unroll
-                        for (int c = 0; c < kAtOnce; ++c) {
-                            v[c] = v[(kBlocks - 1) * kAtOnce + c] = 0;
-                            if (now >> c & 1) {
-                                v[c] = tmem_ld_32x32b_x1(from);
-                                if (FP8)
-                                    v[(kBlocks - 1) * kAtOnce + c] = tmem_ld_32x32b_x1(from + NT);
-                                ++from;
-                            }
-                        }
-                        tmem_ld_wait();
-                        tmem_regs_ready(v);
-#pragma unroll
-                        for (int c = 0; c < kAtOnce; ++c)
-                            if (now >> c & 1)
-#pragma unroll
-                                for (int b = 0; b < (FP8 ? 2 : 1); ++b) {
-                                    const float f = __shfl_sync(0xffffffffu, factor[0][b], t0 + c);
-                                    acc[t0 + c] = fmaf(f, __uint_as_float(v[b * kAtOnce + c]), acc[t0 + c]);
-                                }
-                    }
-                } else {
+                const uint32_t from = my_sums + buf * 2 * NT + first;
+                if constexpr (!DOWN) {
                     // columns: the tokens (nobody uses the sums of those that are not the expert's)
 #pragma unroll
                     for (int t0 = 0; t0 < kTokens; t0 += 16) {
@@ -690,11 +656,78 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 16; ++c) {
                             if (FP8) {
-                                const float f = __shfl_sync(0xffffffffu, factor[t0 / 32][0], (t0 + c) % 32);
+                                const float f = __shfl_sync(0xffffffffu, factor[t0 / 32], (t0 + c) % 32);
                                 acc[t0 + c] = fmaf(f, __uint_as_float(v[c]), acc[t0 + c]);
                             } else {
                                 acc[t0 + c] = __uint_as_float(v[c]);
                             }
+                        }
+                    }
+                } else {
+                    // columns: the expert's tokens without gaps
+                    if constexpr (FP8) {
+#pragma unroll
+                        for (int c0 = 0; c0 < kTokens; c0 += 8) {
+                            if (c0 >= count)
+                                continue;
+                            uint32_t v[2][8];
+                            tmem_ld_32x32b_x8(from + c0, v[0]);
+                            tmem_ld_32x32b_x8(from + NT + c0, v[1]);
+                            tmem_ld_wait();
+                            tmem_regs_ready(v[0]);
+                            tmem_regs_ready(v[1]);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const float f = __shfl_sync(0xffffffffu, factor[i], c0 + c);
+                                    own[c0 + c] = fmaf(f, __uint_as_float(v[i][c]), own[c0 + c]);
+                                }
+                        }
+                    }
+                    if (next_k == 0 || s + n == seg.s1) {
+                        // the expert's sums, each to its token's place in acc, by way of tensor memory
+                        // (whose columns can be chosen at run time), with the gates
+                        uint32_t at = from;
+                        if constexpr (FP8) {
+                            at = my_scratch;
+#pragma unroll
+                            for (int c0 = 0; c0 < kTokens; c0 += 8) {
+                                uint32_t v[8];
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    v[c] = __float_as_uint(own[c0 + c]);
+                                    own[c0 + c] = 0.f;
+                                }
+                                if (c0 < count)
+                                    tmem_st_32x32b_x8(at + c0, v);
+                            }
+                            tmem_st_wait();
+                        }
+                        float gate = 0.f;
+                        if (lane < kTokens && (here >> lane & 1))
+                            gate = sh.x.of_row[sh.first[place] + first + __popcll(here & ((1ull << lane) - 1))];
+                        constexpr int kAtOnce = kTokens < 16 ? 8 : 16;
+#pragma unroll
+                        for (int t0 = 0; t0 < kTokens; t0 += kAtOnce) {
+                            const uint32_t now = static_cast<uint32_t>(here >> t0) & ((1u << kAtOnce) - 1);
+                            if (!now)
+                                continue;
+                            uint32_t v[kAtOnce];
+#pragma unroll
+                            for (int c = 0; c < kAtOnce; ++c) {
+                                v[c] = 0;
+                                if (now >> c & 1)
+                                    v[c] = tmem_ld_32x32b_x1(at++);
+                            }
+                            tmem_ld_wait();
+                            tmem_regs_ready(v);
+#pragma unroll
+                            for (int c = 0; c < kAtOnce; ++c)
+                                if (now >> c & 1) {
+                                    const float g = __shfl_sync(0xffffffffu, gate, t0 + c);
+                                    acc[t0 + c] = fmaf(g, __uint_as_float(v[c]), acc[t0 + c]);
+                                }
                         }
                     }
                 }
@@ -871,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1)
+    if (warp == kThreads / 32 - 1)
         tmem_dealloc(tmem, kTmemCols);
 }
 
