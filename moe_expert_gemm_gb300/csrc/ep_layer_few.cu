@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
         sh.abort = 0;
         sh.cut[0].unit = sh.cut[1].unit = -1;
+        sh.last[0] = sh.last[1] = 0;
     }
     for (int e = tid; e < p.El; e += kThreads)
         sh.mask[e][0] = sh.mask[e][1] = 0;
@@ -591,6 +592,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         // e4m3, down: the sums of the expert under way, its tokens without gaps.
         float own[DOWN && FP8 ? kTokens : 1];
         const uint32_t my_scratch = tmem + 4 * NT + group * kTokens + (static_cast<uint32_t>(32 * quarter) << 16);
+        // The block's sums of a cut unit are stored: counts it in. The part that a run begins with is
+        // counted long before the block before ends its own, the unit's first, which so is the
+        // one that joins: a block seldom has two units to join.
+        auto count_in = [&](int slot, bool ok) {
+            if (!named_bar_and(1, kEpilogueThreads, ok))
+                return false;
+            if (etid == 0) {
+                int *counters = reinterpret_cast<int *>(p.workspace);
+                const int unit = sh.cut[slot].unit;
+                const int c0 = sh.runs.owner(unit * steps), c1 = sh.runs.owner(unit * steps + steps - 1);
+                const int last = atom_add_acq_rel_gpu(counters + c0, 1) == c1 - c0;
+                if (last)
+                    counters[c0] = 0;  // ready for the next call
+                sh.last[slot] = last;
+            }
+            return true;
+        };
+
         bool ok = true;
         int buf = 0;
         uint32_t buf_phase = 0;
@@ -758,24 +777,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __stcg(to + t * kPartRows, acc[t]);
                 if (etid == 0)
                     sh.cut[slot] = seg;
+                ok = count_in(slot, ok);
+                if (!ok)
+                    break;
             }
         }
-        // the block's cut units, after all else: the last of a unit's blocks to come here adds
+        // the block's cut units, after all else: the last of a unit's blocks to count itself in adds
         // what they left, in block order
         if (sh.runs.piece == 1 && named_bar_and(1, kEpilogueThreads, ok)) {
-            int *counters = reinterpret_cast<int *>(p.workspace);
-            if (etid == 0 || etid == 32) {
-                const int slot = etid / 32, unit = sh.cut[slot].unit;
-                int last = 0;
-                if (unit >= 0) {
-                    const int c0 = sh.runs.owner(unit * steps), c1 = sh.runs.owner(unit * steps + steps - 1);
-                    last = atom_add_acq_rel_gpu(counters + c0, 1) == c1 - c0;
-                    if (last)
-                        counters[c0] = 0;  // ready for the next call
-                }
-                sh.last[slot] = last;
-            }
-            named_bar_sync(1, kEpilogueThreads);
             for (int slot = 0; slot < 2; ++slot) {
                 if (!sh.last[slot])
                     continue;
