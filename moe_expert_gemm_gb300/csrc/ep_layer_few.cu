@@ -47,14 +47,16 @@ constexpr int kPartBase = 4096;  // of the workspace; counters before it
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 static_assert(kMaxBlocks * 4 <= kPartBase, "counters");
 
-// Steps that the joining of cut units is worth.
+// How the list is cut. Steps that the joining of cut units is worth, and the fewest steps that a cut
+// leaves a block: the last block of a unit adds a part of its tokens' sums for each of them. The
+// times are flat around both: over 90 shapes of 1 to 64 tokens the geometric mean lies 0.8 % under
+// that of half of sqrt(steps) for any number of tokens, 0.6 % under that of a joining worth 3
+// steps, 0.4 % under that of 0.1 + tokens / 64 below the root (a single shape up to 20 % either way).
 constexpr int kJoinSteps = 4;
 
-// The fewest steps that a cut leaves a block: the last block of a unit adds a part for every
-// min_steps, each of which takes about as long as half a step does.
-__device__ __forceinline__ int min_steps(int steps)
+__device__ __forceinline__ int min_steps(int steps, int tokens)
 {
-    const int s = static_cast<int>(ceilf(sqrtf(0.5f * steps)));
+    const int s = static_cast<int>(ceilf(sqrtf((0.1f + tokens * 0.01f) * steps)));
     return s < 2 ? 2 : s > 64 ? 64 : s;
 }
 
@@ -116,7 +118,7 @@ struct Shared {
     uint32_t mask[EP_MAX_LOCAL_EXPERTS][2];  // tokens of each local expert
     uint32_t tmem;
     int abort;
-    int n_active, start, todo;  // active experts; the run
+    int n_active, rows, start, todo;  // active experts, their tokens; the run
     Runs runs;
     Segment cut[2];  // the units the block's run begins and ends inside
     int last[2];
@@ -186,8 +188,10 @@ __device__ __forceinline__ void make_plan(const FewParams &p, S &sh)
             places += __popc(has);
             rows += __shfl_sync(0xffffffffu, upto, 31);
         }
-        if (tid == 0)
+        if (tid == 0) {
             sh.n_active = places;
+            sh.rows = rows;
+        }
     }
     __syncthreads();
     if constexpr (DOWN) {
@@ -338,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         const int grid = static_cast<int>(gridDim.x), block = static_cast<int>(blockIdx.x);
         const int total = units * steps;
-        const int least = min_steps(steps);
+        const int least = min_steps(steps, DOWN ? p.T : sh.n_active ? sh.rows / sh.n_active : 0);
         int cut = (total + grid - 1) / grid;
         cut = cut < least ? least : cut;
         const bool whole = (units + grid - 1) / grid * steps <= cut + kJoinSteps;
