@@ -654,8 +654,9 @@ int ep_matvec_w4(const ep_config *cfg, const ep_w4_args *args, ep_stream_t strea
  *                   infinity is NaN as a whole, scale and codes.
  *   *_stride        elements between rows (0: hidden). q and q_scales lie without gaps.
  * One of sum, y and q is given. Pointers need no more than their type's alignment; rows of
- * whole 16-byte pieces are faster. Where a row's values pass about 1e19 / sqrt(hidden) in size
- * the fp32 sum of squares is infinite and the row's v zero.
+ * whole 16-byte pieces are faster. The sum of squares is fp32: where a row's values pass about
+ * 1e19 / sqrt(hidden) in size it is infinite and the row's v zero, values under 1e-23 add
+ * nothing to it.
  */
 #define EP_ROWS_F32 0
 #define EP_ROWS_BF16 1
@@ -780,8 +781,9 @@ int ep_swiglu_e4m3(const ep_config *cfg, const ep_swiglu_e4m3_args *args, ep_str
  *   out             [num_tokens][N] bf16 out, every row (zeros where a token has no expert here)
  *   workspace       device memory of ep_layer_few_sizes bytes, 16-byte aligned, zero before the
  *                   first call that uses it; a call that ends without EP_STATUS_TIMEOUT leaves
- *                   it ready for the next of the same configuration. Calls that may run at the
- *                   same time need one each.
+ *                   it ready for the next, of this configuration or of any other that it is
+ *                   large enough for (fewer tokens, say). Calls that may run at the same time
+ *                   need one each.
  *   status          EP_STATUS_ROUTING as above; EP_STATUS_TIMEOUT if a bounded wait inside a
  *                   kernel ran out
  * The weights of an expert without tokens are not read. Sums are taken in a fixed order: a

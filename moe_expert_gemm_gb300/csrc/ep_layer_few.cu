@@ -153,14 +153,14 @@ __device__ __forceinline__ void make_plan(const FewParams &p, S &sh)
     const int tid = threadIdx.x, slots = p.T * p.top_k, first = p.my_rank * p.El;
     bool bad = false;
     for (int s = tid; s < slots; s += kThreads) {
-        const int id = __ldcg(p.topk_ids + s), e = id - first;
-        const bool here = id >= first && e < p.El;
+        const int id = __ldcg(p.topk_ids + s), t = s / p.top_k;
+        const bool here = id >= first && id < first + p.El;
+        const int e = here ? id - first : -1;
         bad |= id < 0 || id >= p.n_ranks * p.El;
-        const int t = s / p.top_k;
         if (here)
             atomicOr(&sh.mask[e][t / 32], 1u << t % 32);
         if constexpr (DOWN) {
-            sh.x.expert[s] = static_cast<int16_t>(here ? e : -1);
+            sh.x.expert[s] = static_cast<int16_t>(e);
             sh.x.of_slot[s] = __ldcg(p.gates + s);
         }
     }

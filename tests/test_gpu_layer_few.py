@@ -84,10 +84,11 @@ SIZES = [
     (1, 8, 2, 128, 256), (1, 1, 1, 8, 8), (1, 4, 4, 64, 72), (2, 3, 2, 136, 264), (5, 12, 3, 248, 200),
     (7, 1, 1, 1000, 504), (16, 16, 4, 256, 128), (17, 5, 5, 512, 640), (33, 9, 2, 328, 96), (64, 6, 3, 384, 256),
     (64, 64, 8, 128, 128), (48, 256, 6, 64, 64), (3, 2, 1, 2056, 1000), (1, 4, 2, 1000, 4104), (64, 2, 2, 264, 1016),
+    (64, 256, 32, 64, 64), (63, 8, 8, 72, 136),
 ]
 SIZES_8 = [(1, 8, 2, 128, 256), (1, 1, 1, 128, 128), (5, 12, 3, 256, 384), (16, 16, 4, 384, 128),
            (17, 5, 5, 512, 640), (33, 9, 2, 128, 1152), (64, 6, 3, 384, 256), (64, 64, 8, 128, 128),
-           (2, 3, 2, 2176, 256), (1, 4, 2, 256, 4224), (64, 2, 2, 640, 896)]
+           (2, 3, 2, 2176, 256), (1, 4, 2, 256, 4224), (64, 2, 2, 640, 896), (64, 256, 32, 128, 128)]
 
 
 @pytest.mark.parametrize("T,E,k,H,I", SIZES)
@@ -239,3 +240,29 @@ def test_real_sizes(fp8):
     f = Few(T, E, k, H, I, fp8=fp8, seed=10)
     f.call()
     f.check()
+
+
+def test_one_workspace_for_many_configurations():
+    """Sized for the largest; what another configuration left in it does no harm."""
+    work, outs = None, []
+    for T, fp8 in [(64, False), (1, False), (20, True), (64, True), (33, False), (1, True), (5, False)]:
+        f = Few(T, 9, 3, 384, 640, fp8=fp8, seed=T)
+        if work is None:
+            work = torch.zeros(f.size + 64, dtype=torch.uint8, device="cuda")
+            work[f.size:] = 0x5A
+            largest = f.size
+        assert f.size <= largest
+        f.call(work=work)
+        f.check()
+        assert (work[largest:] == 0x5A).all()
+        work[4096:largest] = 0xFF  # NaN, in all but the counters
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_nothing_unwritten_is_used(fp8):
+    """Results are the same with NaN in the workspace's sums and rows."""
+    for T, E, k, H, I in [(11, 7, 2, 640, 384), (40, 3, 2, 128, 1152)]:
+        f = Few(T, E, k, H, I, fp8=fp8, seed=12)
+        f.work[4096:f.size] = 0xFF
+        f.call()
+        f.check()
