@@ -6,7 +6,7 @@
 // Both are bound by their rows' bytes. A row stays in one thread block from its load to its
 // stores: it is read once, and may be overwritten in place.
 //  * Rows come to shared memory a row or two ahead (cp.async). Rows of whole 16-byte pieces: every
-//    thread copies the pieces that it will use itself, so that nobody waits for anybody but in
+//    warp copies the pieces that it will use itself, so that nobody waits for anybody but in
 //    the row's sums, and stores them from its registers. Any other rows lie in shared memory as
 //    far from a 16-byte boundary as in memory, so that all but their ends still moves in
 //    aligned pieces, in and out; threads shift the words that they read.
@@ -15,6 +15,8 @@
 //    eight values a thread, which share the row's sums and addresses.
 //  * dweight: a block adds its rows' terms in registers and leaves them in the workspace; a second
 //    kernel adds the blocks'.
+#include <type_traits>
+
 #include "ep_internal.h"
 #include "ep_ptx.cuh"
 #include "ep_rows.cuh"
@@ -27,9 +29,11 @@ namespace {
 
 constexpr int kMaxThreads = 512;
 static_assert(4 * kPiece * kMaxThreads == EP_MAX_NORM_HIDDEN, "a row in a block");
-constexpr int kPartBlocks = 640;       // that leave partial sums of dweight, at most
 constexpr int kSmemOfSm = 216 * 1024;  // for rows under way
-constexpr int kMaxPerSm = 8;           // blocks
+constexpr int kMaxPerSm = 16;          // blocks
+
+// Blocks that leave partial sums of dweight, at most. (Short rows want many: 8192 x 1024, 22 us with 640.)
+__host__ __device__ constexpr int part_blocks(int hidden) { return hidden <= 1024 ? 1280 : 640; }
 
 // Sum over the block of two values, the same order for every thread. `part` is not used again
 // before another barrier of the block (two buffers that take turns).
@@ -84,24 +88,32 @@ __device__ __forceinline__ void copy_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A thread's piece of one row of a tensor: its 16-byte parts lie blockDim.x apart.
-__device__ __forceinline__ void copy_piece(uint8_t *to, const uint8_t *row, bool bf16, int c)
+// A warp's pieces c .. of one row of n values, one for each lane (c: this lane's). fp32 pieces are 32
+// bytes: there a lane copies 16 bytes of each half of the warp's 1024, so that every request is of
+// whole sectors.
+__device__ __forceinline__ void copy_piece(uint8_t *to, const uint8_t *row, bool bf16, int c, int n)
 {
-    const uint32_t dst = smem_u32(to) + threadIdx.x * 16;
     if (bf16) {
-        copy_async(dst, row + c * 2);
+        if (c < n)
+            copy_async(smem_u32(to) + threadIdx.x * 16, row + c * 2);
     } else {
-        copy_async(dst, row + c * 4);
-        copy_async(dst + blockDim.x * 16, row + c * 4 + 16);
+        const int lane = threadIdx.x & 31, first = c - lane * kPiece;  // of the warp
+        const uint32_t dst = smem_u32(to) + (threadIdx.x - lane) * 32 + lane * 16;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = first + i * 128 + lane * 4;
+            if (at < n)
+                copy_async(dst + i * 512, row + at * 4);
+        }
     }
 }
 
 __device__ __forceinline__ Piece read_piece(const uint8_t *from, bool bf16)
 {
-    const uint4 *p = reinterpret_cast<const uint4 *>(from) + threadIdx.x;
     if (bf16)
-        return unpack(*p);
-    return piece_of(*reinterpret_cast<const float4 *>(p), *reinterpret_cast<const float4 *>(p + blockDim.x));
+        return unpack(reinterpret_cast<const uint4 *>(from)[threadIdx.x]);
+    const float4 *p = reinterpret_cast<const float4 *>(from) + threadIdx.x * 2;
+    return piece_of(p[0], p[1]);
 }
 
 // How far a row begins behind a 16-byte boundary.
@@ -301,13 +313,15 @@ __device__ __forceinline__ void gradient_sums(const Piece &h, const Piece &dy, c
 
 }  // namespace
 
-// Rows of whole aligned pieces. P: pieces of a thread, S: rows under way.
-template <int P, int S>
+// Rows of whole aligned pieces. BF16: the residual stream's type; P: pieces of a thread, S: rows under
+// way.
+template <bool BF16, int P, int S>
 __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 1) norm_kernel(const NormParams p)
 {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 part[2][kMaxThreads / 32];
-    const int n = p.hidden, rb = p.residual_bf16 ? 2 : 4;
+    constexpr int rb = BF16 ? 2 : 4;
+    const int n = p.hidden;
     // of a thread's piece: x, then the residual
     const int x_bytes = blockDim.x * 16, piece_bytes = x_bytes * (p.residual ? 1 + rb / 2 : 1);
     griddep_wait();
@@ -318,12 +332,10 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const int c = (i * blockDim.x + threadIdx.x) * kPiece;
-                if (c >= n)
-                    break;
                 uint8_t *to = ring + (stage * P + i) * piece_bytes;
-                copy_piece(to, x, true, c);
+                copy_piece(to, x, true, c, n);
                 if (p.residual)
-                    copy_piece(to + x_bytes, res, p.residual_bf16, c);
+                    copy_piece(to + x_bytes, res, BF16, c, n);
             }
         }
         copy_commit();
@@ -335,8 +347,12 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
     load_weight(p.weight, p.weight_bf16, n, w);
     int stage = 0, turn = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        if (!BF16)
+            __syncwarp();  // (fp32 pieces are copied by the warp's other lanes)
         ask(t + static_cast<int64_t>(S - 1) * gridDim.x, stage == 0 ? S - 1 : stage - 1);
         copy_wait<S - 1>();
+        if (!BF16)
+            __syncwarp();
         Piece h[P];
         Two squares = 0;
 #pragma unroll
@@ -347,7 +363,7 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
             if (c < n) {
                 h[i] = read_piece(from, true);
                 if (p.residual) {
-                    const Piece res = read_piece(from + x_bytes, p.residual_bf16);
+                    const Piece res = read_piece(from + x_bytes, BF16);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         h[i].v[j] = add2(h[i].v[j], res.v[j]);
@@ -364,7 +380,7 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
         for (int i = 0; i < P; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * kPiece;
             if (c < n && p.sum)
-                store_piece(sum, p.residual_bf16, c, h[i]);
+                store_piece(sum, BF16, c, h[i]);
             const Piece v = scaled(h[i], r, w[i]);
             if (c < n && p.y)
                 store_piece(y, true, c, v);
@@ -378,13 +394,14 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
     }
 }
 
-template <int P, int S>
+template <bool BF16, int P, int S>
 __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 : P == 2 ? 3 : 1)
     norm_backward_kernel(const NormBackwardParams p)
 {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 part[2][kMaxThreads / 32];
-    const int n = p.hidden, hb = p.h_bf16 ? 2 : 4;
+    constexpr int hb = BF16 ? 2 : 4;
+    const int n = p.hidden;
     // of a thread's piece: h, dy, then dsum
     const int dy_bytes = blockDim.x * 16, h_bytes = dy_bytes * (hb / 2);
     const int piece_bytes = dy_bytes + h_bytes * (p.dsum ? 2 : 1);
@@ -397,13 +414,11 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const int c = (i * blockDim.x + threadIdx.x) * kPiece;
-                if (c >= n)
-                    break;
                 uint8_t *to = ring + (stage * P + i) * piece_bytes;
-                copy_piece(to, h, p.h_bf16, c);
-                copy_piece(to + h_bytes, dy, true, c);
+                copy_piece(to, h, BF16, c, n);
+                copy_piece(to + h_bytes, dy, true, c, n);
                 if (p.dsum)
-                    copy_piece(to + h_bytes + dy_bytes, dsum, p.h_bf16, c);
+                    copy_piece(to + h_bytes + dy_bytes, dsum, BF16, c, n);
             }
         }
         copy_commit();
@@ -418,15 +433,19 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
         dw[i] = zeros();
     int stage = 0, turn = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        if (!BF16)
+            __syncwarp();  // (fp32 pieces are copied by the warp's other lanes)
         ask(t + static_cast<int64_t>(S - 1) * gridDim.x, stage == 0 ? S - 1 : stage - 1);
         copy_wait<S - 1>();
+        if (!BF16)
+            __syncwarp();
         Two squares = 0, dot = 0;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * kPiece;
             const uint8_t *from = ring + (stage * P + i) * piece_bytes;
             if (c < n)
-                gradient_sums(read_piece(from, p.h_bf16), read_piece(from + h_bytes, true), w[i], squares, dot);
+                gradient_sums(read_piece(from, BF16), read_piece(from + h_bytes, true), w[i], squares, dot);
         }
         const float2 sums = block_sum(sum_of(squares), sum_of(dot), part[turn ^= 1]);
         const float r = rsqrtf(sums.x / n + p.eps), back = r * r * (sums.y / n);
@@ -437,10 +456,10 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
             const uint8_t *from = ring + (stage * P + i) * piece_bytes;
             if (c >= n)
                 break;
-            Piece d = p.dsum ? read_piece(from + h_bytes + dy_bytes, p.h_bf16) : zeros();
-            gradient(read_piece(from, p.h_bf16), read_piece(from + h_bytes, true), w[i], r, back, d, dw[i]);
+            Piece d = p.dsum ? read_piece(from + h_bytes + dy_bytes, BF16) : zeros();
+            gradient(read_piece(from, BF16), read_piece(from + h_bytes, true), w[i], r, back, d, dw[i]);
             if (p.dh)
-                store_piece(dh, p.h_bf16, c, d);
+                store_piece(dh, BF16, c, d);
             if (p.dx)
                 store_piece(dx, true, c, d);
         }
@@ -649,7 +668,7 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const NormBackwardPar
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
     float sum = 0.f;
     if (c < p.hidden) {
-#pragma unroll 4
+#pragma unroll 8
         for (int b = y; b < blocks; b += 32)
             sum += __ldcg(p.parts + static_cast<int64_t>(b) * p.hidden + c);
     }
@@ -678,14 +697,16 @@ struct Form {
 };
 
 // `two_upto`: the longest rows of two pieces a thread.
-Form form_for(int hidden, int value_bytes, int two_upto)
+// Blocks of an SM go by the registers that the kernels' launch bounds allow a thread, 64 or (`regs`
+// for two pieces, 128 for four) more: blocks past what is resident would begin when the others end.
+Form form_for(int hidden, int value_bytes, int two_upto, int regs)
 {
     Form f;
     f.pieces = hidden <= 1024 ? 1 : hidden <= two_upto ? 2 : 4;
     const int per_thread = f.pieces * kPiece;
     f.threads = ((hidden + per_thread - 1) / per_thread + 31) / 32 * 32;
     const int row = f.threads * per_thread * value_bytes;
-    const int most = 1024 / f.threads;
+    const int most = 65536 / (f.pieces == 1 ? 64 : f.pieces == 2 ? regs : 128) / f.threads;
     f.per_sm = most < 1 ? 1 : most > kMaxPerSm ? kMaxPerSm : most;
     while (f.per_sm > 1 && 2 * row * f.per_sm > kSmemOfSm)
         --f.per_sm;
@@ -714,17 +735,19 @@ cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t s)
                        whole_pieces(p.residual, p.residual_stride, rb) && whole_pieces(p.sum, p.sum_stride, rb) &&
                        whole_pieces(p.y, p.y_stride, 2) && reinterpret_cast<uintptr_t>(p.q) % 8 == 0;
     const int bytes = 2 + (p.residual ? rb : 0);
-    const Form f = form_for(p.hidden, bytes, 8192);
+    const Form f = form_for(p.hidden, bytes, 8192, 64);
     const int most = f.per_sm * num_sms;
     const unsigned grid = p.T < most ? p.T : most;
     if (whole && f.stages >= 2) {
         const int smem = f.stages * f.threads * f.pieces * kPiece * bytes;
-        auto go = [&](auto two, auto three) {
-            return launch_rows(f.stages == 2 ? two : three, f.threads, smem, grid, s, p);
+        auto go = [&](auto bf16) {
+            constexpr bool B = decltype(bf16)::value;
+            const auto kern = f.pieces == 1   ? (f.stages == 2 ? norm_kernel<B, 1, 2> : norm_kernel<B, 1, 3>)
+                              : f.pieces == 2 ? (f.stages == 2 ? norm_kernel<B, 2, 2> : norm_kernel<B, 2, 3>)
+                                              : (f.stages == 2 ? norm_kernel<B, 4, 2> : norm_kernel<B, 4, 3>);
+            return launch_rows(kern, f.threads, smem, grid, s, p);
         };
-        return f.pieces == 1   ? go(norm_kernel<1, 2>, norm_kernel<1, 3>)
-               : f.pieces == 2 ? go(norm_kernel<2, 2>, norm_kernel<2, 3>)
-                               : go(norm_kernel<4, 2>, norm_kernel<4, 3>);
+        return p.residual_bf16 ? go(std::true_type()) : go(std::false_type());
     }
     const int room = room_of(p.hidden, 2) + (p.residual || p.sum ? room_of(p.hidden, rb) : 0);
     const int q_room = p.q ? room_of(p.hidden, 1) : 0, buffers = 2 * room + q_room <= kSmemOfSm ? 2 : 1;
@@ -736,7 +759,7 @@ cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t s)
 
 int64_t norm_backward_workspace_bytes(int T, int hidden)
 {
-    return static_cast<int64_t>(T < kPartBlocks ? T : kPartBlocks) * hidden * 4;
+    return static_cast<int64_t>(T < part_blocks(hidden) ? T : part_blocks(hidden)) * hidden * 4;
 }
 
 cudaError_t launch_norm_backward(const NormBackwardParams &p, int num_sms, cudaStream_t s)
@@ -746,19 +769,22 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, int num_sms, cudaS
                        whole_pieces(p.dy, p.dy_stride, 2) && whole_pieces(p.dsum, p.dsum_stride, hb) &&
                        whole_pieces(p.dh, p.dh_stride, hb) && whole_pieces(p.dx, p.dx_stride, 2);
     // (as with dsum, where there is none, too: the same order of dweight's sum)
-    const Form f = form_for(p.hidden, 2 + hb * 2, 4096);
+    const Form f = form_for(p.hidden, 2 + hb * 2, 4096, 85);
     int most = f.per_sm * num_sms;
-    most = most < kPartBlocks ? most : kPartBlocks;
+    most = most < part_blocks(p.hidden) ? most : part_blocks(p.hidden);
     const unsigned grid = p.T < most ? p.T : most;
     cudaError_t e;
     if (whole && f.stages >= 2) {
         const int smem = f.stages * f.threads * f.pieces * kPiece * (2 + hb * (p.dsum ? 2 : 1));
-        auto go = [&](auto two, auto three) {
-            return launch_rows(f.stages == 2 ? two : three, f.threads, smem, grid, s, p);
+        auto go = [&](auto bf16) {
+            constexpr bool B = decltype(bf16)::value;
+            const auto kern =
+                f.pieces == 1   ? (f.stages == 2 ? norm_backward_kernel<B, 1, 2> : norm_backward_kernel<B, 1, 3>)
+                : f.pieces == 2 ? (f.stages == 2 ? norm_backward_kernel<B, 2, 2> : norm_backward_kernel<B, 2, 3>)
+                                : (f.stages == 2 ? norm_backward_kernel<B, 4, 2> : norm_backward_kernel<B, 4, 3>);
+            return launch_rows(kern, f.threads, smem, grid, s, p);
         };
-        e = f.pieces == 1   ? go(norm_backward_kernel<1, 2>, norm_backward_kernel<1, 3>)
-            : f.pieces == 2 ? go(norm_backward_kernel<2, 2>, norm_backward_kernel<2, 3>)
-                            : go(norm_backward_kernel<4, 2>, norm_backward_kernel<4, 3>);
+        e = p.h_bf16 ? go(std::true_type()) : go(std::false_type());
     } else {
         const int room = room_of(p.hidden, 2) + room_of(p.hidden, hb) * (p.dsum ? 2 : 1);
         const int buffers = 2 * room <= kSmemOfSm ? 2 : 1;

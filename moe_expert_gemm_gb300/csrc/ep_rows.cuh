@@ -120,7 +120,7 @@ __device__ __forceinline__ Piece load_any(const uint8_t *base, bool bf16, int c,
     return Piece{{two(f[0], f[1]), two(f[2], f[3]), two(f[4], f[5]), two(f[6], f[7])}};
 }
 
-// Whole, aligned pieces.
+// Whole pieces, 16-byte aligned, of global memory.
 __device__ __forceinline__ void store_piece(uint8_t *base, bool bf16, int c, const Piece &p)
 {
     if (bf16) {
@@ -128,8 +128,14 @@ __device__ __forceinline__ void store_piece(uint8_t *base, bool bf16, int c, con
     } else {
         float f[kPiece];
         values_of(p, f);
-        *reinterpret_cast<float4 *>(base + c * 4) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4 *>(base + c * 4 + 16) = make_float4(f[4], f[5], f[6], f[7]);
+        uint8_t *const to = base + c * 4;
+        if ((reinterpret_cast<uintptr_t>(base) & 31) == 0) {  // a whole sector at once
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(f[0]), "f"(f[1]),
+                         "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+        } else {
+            *reinterpret_cast<float4 *>(to) = make_float4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<float4 *>(to + 16) = make_float4(f[4], f[5], f[6], f[7]);
+        }
     }
 }
 
