@@ -695,7 +695,7 @@ int ep_add_rmsnorm(const ep_config *cfg, const ep_add_rmsnorm_args *args, ep_str
  *   dh              in h_dtype, out, or NULL. May be h or dsum (same address and stride)
  *   dx              bf16, out, or NULL: the same gradient for an x beside an fp32 residual.
  *                   May be dy
- *   dweight         [hidden] fp32 out, or NULL. Summed in a fixed order (which goes by
+ *   dweight         [hidden] fp32 out, or NULL. Summed in a fixed order (which goes by the types,
  *                   num_tokens and the GPU's number of SMs)
  *   workspace       for dweight: ep_add_rmsnorm_backward_sizes bytes, 16-byte aligned, of any
  *                   contents; calls that may run at the same time need one each

@@ -32,8 +32,9 @@ static_assert(4 * kPiece * kMaxThreads == EP_MAX_NORM_HIDDEN, "a row in a block"
 constexpr int kSmemOfSm = 216 * 1024;  // for rows under way
 constexpr int kMaxPerSm = 16;          // blocks
 
-// Blocks that leave partial sums of dweight, at most. (Short rows want many: 8192 x 1024, 22 us with 640.)
-__host__ __device__ constexpr int part_blocks(int hidden) { return hidden <= 1024 ? 1280 : 640; }
+// Blocks that leave partial sums of dweight, at most. (Short rows want many: 8192 x 256 12 us, with 640
+// 16.)
+__host__ __device__ constexpr int part_blocks(int hidden) { return hidden <= 2048 ? 1280 : 640; }
 
 // Sum over the block of two values, the same order for every thread. `part` is not used again
 // before another barrier of the block (two buffers that take turns).
@@ -699,7 +700,7 @@ struct Form {
 // `two_upto`: the longest rows of two pieces a thread.
 // Blocks of an SM go by the registers that the kernels' launch bounds allow a thread, 64 or (`regs`
 // for two pieces, 128 for four) more: blocks past what is resident would begin when the others end.
-Form form_for(int hidden, int value_bytes, int two_upto, int regs)
+Form form_for(int hidden, int value_bytes, int two_upto, int regs, int stages)
 {
     Form f;
     f.pieces = hidden <= 1024 ? 1 : hidden <= two_upto ? 2 : 4;
@@ -711,7 +712,7 @@ Form form_for(int hidden, int value_bytes, int two_upto, int regs)
     while (f.per_sm > 1 && 2 * row * f.per_sm > kSmemOfSm)
         --f.per_sm;
     f.stages = kSmemOfSm / (row * f.per_sm);
-    f.stages = f.stages > 3 ? 3 : f.stages;
+    f.stages = f.stages > stages ? stages : f.stages;
     return f;
 }
 
@@ -735,8 +736,14 @@ cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t s)
                        whole_pieces(p.residual, p.residual_stride, rb) && whole_pieces(p.sum, p.sum_stride, rb) &&
                        whole_pieces(p.y, p.y_stride, 2) && reinterpret_cast<uintptr_t>(p.q) % 8 == 0;
     const int bytes = 2 + (p.residual ? rb : 0);
-    const Form f = form_for(p.hidden, bytes, 8192, 64);
-    const int most = f.per_sm * num_sms;
+    const Form f = form_for(p.hidden, bytes, 8192, 64, 3);
+    // Of rows with a residual a block takes about 6 (fp32: 3), as the SMs' shares of the bandwidth are
+    // not equal and new blocks go to those that are ahead: 8192 x 7168 beside a bf16 residual 65 us in
+    // 4 waves of blocks (71.6 in one, 77 in 16), an fp32 one 96 in 8 (112 in one), 4096 wide 38.6 in
+    // 2 (41.9 in one). Without a residual one wave is best (7168 wide 38.4, two 40.2).
+    const int resident = f.per_sm * num_sms, rows = resident * (p.residual_bf16 ? 6 : 3);
+    const int waves = !p.residual || p.T < rows ? 1 : (p.T + rows / 2) / rows;
+    const int most = resident * waves;
     const unsigned grid = p.T < most ? p.T : most;
     if (whole && f.stages >= 2) {
         const int smem = f.stages * f.threads * f.pieces * kPiece * bytes;
@@ -769,7 +776,8 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, int num_sms, cudaS
                        whole_pieces(p.dy, p.dy_stride, 2) && whole_pieces(p.dsum, p.dsum_stride, hb) &&
                        whole_pieces(p.dh, p.dh_stride, hb) && whole_pieces(p.dx, p.dx_stride, 2);
     // (as with dsum, where there is none, too: the same order of dweight's sum)
-    const Form f = form_for(p.hidden, 2 + hb * 2, 4096, 85);
+    // Two rows under way: three took 8192 x 7168 in fp32 from 123 to 138 us, 8192 x 4096 in bf16 from 46 to 51.
+    const Form f = form_for(p.hidden, 2 + hb * 2, 4096, 85, 2);
     int most = f.per_sm * num_sms;
     most = most < part_blocks(p.hidden) ? most : part_blocks(p.hidden);
     const unsigned grid = p.T < most ? p.T : most;
@@ -778,10 +786,9 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, int num_sms, cudaS
         const int smem = f.stages * f.threads * f.pieces * kPiece * (2 + hb * (p.dsum ? 2 : 1));
         auto go = [&](auto bf16) {
             constexpr bool B = decltype(bf16)::value;
-            const auto kern =
-                f.pieces == 1   ? (f.stages == 2 ? norm_backward_kernel<B, 1, 2> : norm_backward_kernel<B, 1, 3>)
-                : f.pieces == 2 ? (f.stages == 2 ? norm_backward_kernel<B, 2, 2> : norm_backward_kernel<B, 2, 3>)
-                                : (f.stages == 2 ? norm_backward_kernel<B, 4, 2> : norm_backward_kernel<B, 4, 3>);
+            const auto kern = f.pieces == 1   ? norm_backward_kernel<B, 1, 2>
+                              : f.pieces == 2 ? norm_backward_kernel<B, 2, 2>
+                                              : norm_backward_kernel<B, 4, 2>;
             return launch_rows(kern, f.threads, smem, grid, s, p);
         };
         e = p.h_bf16 ? go(std::true_type()) : go(std::false_type());
