@@ -120,6 +120,18 @@ __device__ __forceinline__ Piece read_piece(const uint8_t *from, bool bf16)
 // How far a row begins behind a 16-byte boundary.
 __device__ __forceinline__ int skew_of(const void *row) { return static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15); }
 
+// The bytes of [skew, end) that whole 16-byte pieces leave out, at most 15 at either end: a thread of the
+// first warp each.
+__device__ __forceinline__ void copy_ends(uint8_t *to, const uint8_t *from, int skew, int end, int first, int last)
+{
+    if (threadIdx.x < 32) {
+        const int head = min(first, end), i = threadIdx.x % 16;
+        const int at = threadIdx.x < 16 ? skew + i : max(last, head) + i;
+        if (at < (threadIdx.x < 16 ? head : end))
+            to[at] = from[at];
+    }
+}
+
 // `bytes` of a row to shared memory, to skew_of(from) behind a 16-byte boundary: asynchronously but
 // for the ends.
 __device__ __forceinline__ void copy_in(uint8_t *to, const uint8_t *from, int bytes)
@@ -129,11 +141,7 @@ __device__ __forceinline__ void copy_in(uint8_t *to, const uint8_t *from, int by
     const int first = skew ? 16 : 0, last = end & ~15;
     for (int i = first + threadIdx.x * 16; i < last; i += blockDim.x * 16)
         copy_async(smem_u32(to) + i, from + i);
-    const int head = min(first, end);
-    for (int i = skew + threadIdx.x; i < head; i += blockDim.x)
-        to[i] = from[i];
-    for (int i = max(last, head) + threadIdx.x; i < end; i += blockDim.x)
-        to[i] = from[i];
+    copy_ends(to, from, skew, end, first, last);
 }
 
 // The same back, from skew_of(to) behind a 16-byte boundary of shared memory.
@@ -144,11 +152,7 @@ __device__ __forceinline__ void copy_out(uint8_t *to, const uint8_t *from, int b
     const int first = skew ? 16 : 0, last = end & ~15;
     for (int i = first + threadIdx.x * 16; i < last; i += blockDim.x * 16)
         *reinterpret_cast<uint4 *>(to + i) = *reinterpret_cast<const uint4 *>(from + i);
-    const int head = min(first, end);
-    for (int i = skew + threadIdx.x; i < head; i += blockDim.x)
-        to[i] = from[i];
-    for (int i = max(last, head) + threadIdx.x; i < end; i += blockDim.x)
-        to[i] = from[i];
+    copy_ends(to, from, skew, end, first, last);
 }
 
 // The N words that begin `skew` bytes behind a 16-byte boundary of shared memory (of which N + 4 are
