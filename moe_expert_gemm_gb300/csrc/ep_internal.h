@@ -69,7 +69,8 @@ inline cudaError_t launch_send_kernel(Kern kern, int grid, int threads, int smem
 }
 
 // Launch of a kernel that begins with griddep_wait(): its blocks may take the place of the
-// previous kernel's as those leave, and wait there for that kernel's end and memory. It lets its
+// previous kernel's as those leave, and wait there for that kernel's end and memory. (The second
+// kernel of the few-token layer reads before that wait what was there before the first began.) It lets its
 // own dependents start only after that wait, so that of the kernels before a dependent no more
 // than one is unfinished: a combine with EP_OVERLAP_INPUTS_READY, which does not wait, asks
 // its caller about the previous kernel alone.
