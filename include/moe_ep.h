@@ -646,7 +646,8 @@ int ep_matvec_w4(const ep_config *cfg, const ep_w4_args *args, ep_stream_t strea
  *   hidden          1 .. EP_MAX_NORM_HIDDEN (more: EP_ERR_UNSUPPORTED)
  *   sum             h, rounded once, out; or NULL. May be x or residual, of the same type,
  *                   address and stride
- *   y               [num_tokens][hidden] bf16 out: v, rounded once; or NULL. May be x
+ *   y               [num_tokens][hidden] bf16 out: v, rounded once; or NULL. May be x (same
+ *                   address and stride)
  *   q, q_scales     [num_tokens][hidden] e4m3 and [num_tokens][ceil(hidden/128)] fp32 out, or
  *                   both NULL: of each 128 consecutive columns (the last group may be
  *                   shorter) s = max(largest |v| / 448, 2^-126) and e4m3(v / s), to nearest
@@ -694,7 +695,7 @@ int ep_add_rmsnorm(const ep_config *cfg, const ep_add_rmsnorm_args *args, ep_str
  *   weight, weight_dtype, eps, hidden   as in ep_add_rmsnorm
  *   dh              in h_dtype, out, or NULL. May be h or dsum (same address and stride)
  *   dx              bf16, out, or NULL: the same gradient for an x beside an fp32 residual.
- *                   May be dy
+ *                   May be dy (same address and stride)
  *   dweight         [hidden] fp32 out, or NULL. Summed in a fixed order (which goes by the types,
  *                   num_tokens and the GPU's number of SMs)
  *   workspace       for dweight: ep_add_rmsnorm_backward_sizes bytes, 16-byte aligned, of any

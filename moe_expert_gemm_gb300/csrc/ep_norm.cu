@@ -484,12 +484,13 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
 // Rows of any alignment: x (then y) and the residual (then sum) in two buffers that take turns, where
 // they fit; q. (What is written has the skew of where it goes, so that it may overlap what other
 // threads read: between the two lies a barrier.)
-template <int P>
+template <bool BF16, int P>
 __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 1) norm_any_kernel(const NormParams p, int buffers)
 {
     extern __shared__ __align__(16) uint8_t row[];
     __shared__ float2 part[2][kMaxThreads / 32];
-    const int n = p.hidden, rb = p.residual_bf16 ? 2 : 4, x_room = room_of(n, 2);
+    constexpr int rb = BF16 ? 2 : 4;
+    const int n = p.hidden, x_room = room_of(n, 2);
     const int room = x_room + (p.residual || p.sum ? room_of(n, rb) : 0);
     uint8_t *const q_row = row + buffers * room;
     griddep_wait();
@@ -509,15 +510,12 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
     int buffer = 0, turn = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         uint8_t *const x = row + buffer * room, *const res = x + x_room;
-        if (buffers > 1) {
-            ask(t + gridDim.x, buffer ^ 1);
-            copy_wait<1>();
-            buffer ^= 1;
-        } else {
+        if (buffers == 1)
             ask(t, 0);
-            copy_wait<0>();
-        }
+        copy_wait<0>();
         __syncthreads();
+        if (buffers > 1)  // (where the row before this one has left by now)
+            ask(t + gridDim.x, buffer ^= 1);
         const int x_skew = skew_of(p.x + t * p.x_stride * 2);
         const int res_skew = skew_of(p.residual + t * p.residual_stride * rb);
         Piece h[P];
@@ -529,7 +527,7 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
             if (c < n) {
                 h[i] = read_any(x, x_skew, true, c, n);
                 if (p.residual) {
-                    const Piece r = read_any(res, res_skew, p.residual_bf16, c, n);
+                    const Piece r = read_any(res, res_skew, BF16, c, n);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         h[i].v[j] = add2(h[i].v[j], r.v[j]);
@@ -545,7 +543,7 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
         for (int i = 0; i < P; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * kPiece;
             if (c < n && p.sum)
-                write_any(res, skew_of(sum), p.residual_bf16, c, n, h[i]);
+                write_any(res, skew_of(sum), BF16, c, n, h[i]);
             const Piece v = scaled(h[i], r, w[i]);
             if (c < n && p.y)
                 write_any(x, skew_of(y), true, c, n, v);
@@ -562,18 +560,20 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
             copy_out(y, x, n * 2);
         if (p.q)
             copy_out(q, q_row, n);
-        __syncthreads();
+        if (buffers == 1)
+            __syncthreads();
     }
 }
 
 // The same for the gradient: h (then dh), dy (then dx), dsum.
-template <int P>
+template <bool BF16, int P>
 __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 : P == 2 ? 3 : 1)
     norm_backward_any_kernel(const NormBackwardParams p, int buffers)
 {
     extern __shared__ __align__(16) uint8_t row[];
     __shared__ float2 part[2][kMaxThreads / 32];
-    const int n = p.hidden, hb = p.h_bf16 ? 2 : 4, h_room = room_of(n, hb), dy_room = room_of(n, 2);
+    constexpr int hb = BF16 ? 2 : 4;
+    const int n = p.hidden, h_room = room_of(n, hb), dy_room = room_of(n, 2);
     const int room = dy_room + h_room * (p.dsum ? 2 : 1);
     griddep_wait();
     griddep_launch_dependents();
@@ -597,15 +597,12 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
     int buffer = 0, turn = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         uint8_t *const h_row = row + buffer * room, *const dy_row = h_row + h_room, *const dsum_row = dy_row + dy_room;
-        if (buffers > 1) {
-            ask(t + gridDim.x, buffer ^ 1);
-            copy_wait<1>();
-            buffer ^= 1;
-        } else {
+        if (buffers == 1)
             ask(t, 0);
-            copy_wait<0>();
-        }
+        copy_wait<0>();
         __syncthreads();
+        if (buffers > 1)  // (where the row before this one has left by now)
+            ask(t + gridDim.x, buffer ^= 1);
         const int h_skew = skew_of(p.h + t * p.h_stride * hb), dy_skew = skew_of(p.dy + t * p.dy_stride * 2);
         const int dsum_skew = skew_of(p.dsum + t * p.dsum_stride * hb);
         Two squares = 0, dot = 0;
@@ -613,7 +610,7 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
         for (int i = 0; i < P; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * kPiece;
             if (c < n)
-                gradient_sums(read_any(h_row, h_skew, p.h_bf16, c, n), read_any(dy_row, dy_skew, true, c, n), w[i],
+                gradient_sums(read_any(h_row, h_skew, BF16, c, n), read_any(dy_row, dy_skew, true, c, n), w[i],
                               squares, dot);
         }
         const float2 sums = block_sum(sum_of(squares), sum_of(dot), part[turn ^= 1]);
@@ -627,16 +624,18 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
             if (c >= n)
                 continue;
             if (p.dsum)
-                d[i] = read_any(dsum_row, dsum_skew, p.h_bf16, c, n);
-            gradient(read_any(h_row, h_skew, p.h_bf16, c, n), read_any(dy_row, dy_skew, true, c, n), w[i], r, back,
+                d[i] = read_any(dsum_row, dsum_skew, BF16, c, n);
+            gradient(read_any(h_row, h_skew, BF16, c, n), read_any(dy_row, dy_skew, true, c, n), w[i], r, back,
                      d[i], dw[i]);
         }
-        __syncthreads();
+        // what goes where it came from, byte by byte, overwrites nothing that another thread still reads
+        if ((p.dh && skew_of(dh) != h_skew) || (p.dx && skew_of(dx) != dy_skew))
+            __syncthreads();
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * kPiece;
             if (c < n && p.dh)
-                write_any(h_row, skew_of(dh), p.h_bf16, c, n, d[i]);
+                write_any(h_row, skew_of(dh), BF16, c, n, d[i]);
             if (c < n && p.dx)
                 write_any(dy_row, skew_of(dx), true, c, n, d[i]);
         }
@@ -645,7 +644,8 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
             copy_out(dh, h_row, n * hb);
         if (p.dx)
             copy_out(dx, dy_row, n * 2);
-        __syncthreads();
+        if (buffers == 1)
+            __syncthreads();
     }
     if (p.dweight) {
         float *mine = p.parts + static_cast<int64_t>(blockIdx.x) * n;
@@ -762,10 +762,14 @@ cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t s)
     }
     const int room = room_of(p.hidden, 2) + (p.residual || p.sum ? room_of(p.hidden, rb) : 0);
     const int q_room = p.q ? room_of(p.hidden, 1) : 0, buffers = 2 * room + q_room <= kSmemOfSm ? 2 : 1;
-    return launch_rows(f.pieces == 1   ? norm_any_kernel<1>
-                       : f.pieces == 2 ? norm_any_kernel<2>
-                                       : norm_any_kernel<4>,
-                       f.threads, buffers * room + q_room, grid, s, p, buffers);
+    auto go = [&](auto bf16) {
+        constexpr bool B = decltype(bf16)::value;
+        return launch_rows(f.pieces == 1   ? norm_any_kernel<B, 1>
+                           : f.pieces == 2 ? norm_any_kernel<B, 2>
+                                           : norm_any_kernel<B, 4>,
+                           f.threads, buffers * room + q_room, grid, s, p, buffers);
+    };
+    return p.residual_bf16 ? go(std::true_type()) : go(std::false_type());
 }
 
 int64_t norm_backward_workspace_bytes(int T, int hidden)
@@ -799,10 +803,14 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, int num_sms, cudaS
     } else {
         const int room = room_of(p.hidden, 2) + room_of(p.hidden, hb) * (p.dsum ? 2 : 1);
         const int buffers = 2 * room <= kSmemOfSm ? 2 : 1;
-        e = launch_rows(f.pieces == 1   ? norm_backward_any_kernel<1>
-                        : f.pieces == 2 ? norm_backward_any_kernel<2>
-                                        : norm_backward_any_kernel<4>,
-                        f.threads, buffers * room, grid, s, p, buffers);
+        auto go = [&](auto bf16) {
+            constexpr bool B = decltype(bf16)::value;
+            return launch_rows(f.pieces == 1   ? norm_backward_any_kernel<B, 1>
+                               : f.pieces == 2 ? norm_backward_any_kernel<B, 2>
+                                               : norm_backward_any_kernel<B, 4>,
+                               f.threads, buffers * room, grid, s, p, buffers);
+        };
+        e = p.h_bf16 ? go(std::true_type()) : go(std::false_type());
     }
     if (e == cudaSuccess && p.dweight)
         e = launch_behind(norm_weight_kernel, (p.hidden + 31) / 32, 1024, 0, s, p, static_cast<int>(grid));

@@ -106,6 +106,43 @@ def test_addresses_of_single_elements():
     ref.check_e4m3(q.view(torch.float8_e4m3fn), s, v, REL)
 
 
+@pytest.mark.parametrize("n,pad", [(1024, 0), (1111, 2), (203, 1), (4099, 5)])
+@pytest.mark.parametrize("h_type", [B, F])
+def test_gradient_addresses_of_single_elements(n, pad, h_type):
+    """The gradient's rows, each tensor's at another place behind a 16-byte boundary, with gaps of
+    another size each, and over an input."""
+    T = 13
+    gen = torch.Generator().manual_seed(n)
+
+    def rows(dtype, off, gap):
+        base = torch.randn(T * (n + gap) + 8, generator=gen).cuda().to(dtype)
+        return base[off:off + T * (n + gap)].view(T, n + gap)[:, :n], base
+
+    h, _ = rows(h_type, 1, pad)
+    dy, _ = rows(B, 3, pad + 1)
+    dsum, _ = rows(h_type, 2, 0)
+    dh, dh_base = rows(h_type, 3, 2 * pad)
+    dx, dx_base = rows(B, 7, pad)
+    w = rows(F, 1, 0)[0][0]
+    before = [b.clone() for b in (dh_base, dx_base)]
+    dw = torch.zeros(n, device="cuda")
+    back_call(h, dy, w, dsum, dh, dx, dw)
+    want, want_w, size, size_w = ref.norm_backward(h, dy, w, dsum, 1e-6)
+    off = 256 * F32 * size
+    assert ((dh.double() - want).abs() <= STEP[h_type] * (want.abs() + off) + off).all()
+    assert ((dx.double() - want).abs() <= BF16 * (want.abs() + off) + off).all()
+    assert ((dw.double() - want_w).abs() <= 128 * F32 * size_w).all()
+    for base, old, view, gap, at in ((dh_base, before[0], dh, 2 * pad, 3), (dx_base, before[1], dx, pad, 7)):
+        outside = torch.ones_like(base, dtype=torch.bool)
+        outside[at:at + T * (n + gap)].view(T, n + gap)[:, :n] = False
+        assert torch.equal(base[outside], old[outside])
+    over = dsum.clone() if dsum.is_contiguous() else dsum
+    moved = rows(h_type, 2, 0)[0]
+    moved.copy_(over)
+    back_call(h, dy, w, moved, moved)
+    assert torch.equal(moved, dh)
+
+
 def test_zeros_infinities_and_nan():
     n, T = 640, 6
     x = torch.randn(T, n, generator=torch.Generator().manual_seed(0)).cuda().to(B)
