@@ -919,7 +919,10 @@ int few_sizes(const ep_config *cfg, ep::FewParams *p)
     if (cfg->num_tokens > EP_MAX_FEW_TOKENS || cfg->top_k > kMaxRouteTopK || cfg->K % step != 0 ||
         cfg->N % step != 0)
         return EP_ERR_UNSUPPORTED;
-    // rows of W1 and the kernels' steps are counted in 32 bits
+    // an expert's matrices lie less than 2^40 bytes apart; rows of W1 and the kernels' steps are
+    // counted in 32 bits
+    if (cfg->K >= (1ll << 40) / (2 * (fp8 ? 1 : 2)) / cfg->N)
+        return EP_ERR_UNSUPPORTED;
     const int64_t El = cfg->n_local_experts;
     if (2ll * cfg->K >= INT32_MAX ||
         El * ((cfg->K + 127ll) / 128) * ((cfg->N + 63ll) / 64) >= INT32_MAX ||

@@ -134,7 +134,8 @@ def test_few_scales(name):
 @pytest.mark.parametrize("kw", [
     dict(num_tokens=65), dict(n_local_experts=64, top_k=33), dict(K=252), dict(N=132),
     dict(dtype=ep.EP_FP8_1D2D, K=320), dict(dtype=ep.EP_FP8_1D2D, N=192), dict(n_ranks=9),
-    dict(K=1 << 30), dict(n_local_experts=256, K=1 << 26, N=1 << 24),
+    dict(K=1 << 30), dict(n_local_experts=256, K=1 << 26, N=1 << 24), dict(K=1 << 19, N=1 << 19),
+    dict(dtype=ep.EP_FP8_1D2D, K=1 << 20, N=1 << 19),
 ])
 def test_few_limits(kw):
     n = ctypes.c_int64(0)
