@@ -750,7 +750,8 @@ cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t s)
     const int most = resident * waves;
     const unsigned grid = p.T < most ? p.T : most;
     if (whole && f.stages >= 2) {
-        const int smem = f.stages * f.threads * f.pieces * kPiece * bytes;
+        // (one row a block needs no second: no attribute to set, a tenth of a small call's host time)
+        const int smem = (p.T == static_cast<int>(grid) ? 1 : f.stages) * f.threads * f.pieces * kPiece * bytes;
         auto go = [&](auto bf16) {
             constexpr bool B = decltype(bf16)::value;
             const auto kern = f.pieces == 1   ? (f.stages == 2 ? norm_kernel<B, 1, 2> : norm_kernel<B, 1, 3>)
@@ -791,7 +792,8 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, int num_sms, cudaS
     const unsigned grid = p.T < most ? p.T : most;
     cudaError_t e;
     if (whole && f.stages >= 2) {
-        const int smem = f.stages * f.threads * f.pieces * kPiece * (2 + hb * (p.dsum ? 2 : 1));
+        const int smem = (p.T == static_cast<int>(grid) ? 1 : f.stages) * f.threads * f.pieces * kPiece *
+                         (2 + hb * (p.dsum ? 2 : 1));
         auto go = [&](auto bf16) {
             constexpr bool B = decltype(bf16)::value;
             const auto kern = f.pieces == 1   ? norm_backward_kernel<B, 1, 2>
