@@ -10,11 +10,15 @@
 //    the row's sums, and stores them from its registers. Any other rows lie in shared memory as
 //    far from a 16-byte boundary as in memory, so that all but their ends still moves in
 //    aligned pieces, in and out; threads shift the words that they read.
-//  * Instructions come next to bytes here (the gradient's 43 a value took as long as its bytes):
+//  * Instructions come next to bytes here (a gradient of 43 a value took as long as its bytes):
 //    hence arithmetic on two values at a time, the weight in registers, and up to four pieces of
 //    eight values a thread, which share the row's sums and addresses.
 //  * dweight: a block adds its rows' terms in registers and leaves them in the workspace; a second
 //    kernel adds the blocks'.
+//
+// Measured at 8192 x 7168 (GB300, of the copy bandwidth of 6.77 TB/s): beside a bf16 residual to e4m3
+// 64 us, 95 %; to bf16 73 us, 95 %; the gradient in bf16 with the residual's 74 us, 93 %, in fp32
+// 123 us, 99 %. 4096 x 3675, rows of other alignments: the gradient 58 us, 31 %.
 #include <type_traits>
 
 #include "ep_internal.h"
