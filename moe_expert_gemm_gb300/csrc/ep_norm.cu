@@ -124,39 +124,44 @@ __device__ __forceinline__ Piece read_piece(const uint8_t *from, bool bf16)
 // How far a row begins behind a 16-byte boundary.
 __device__ __forceinline__ int skew_of(const void *row) { return static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15); }
 
-// The bytes of [skew, end) that whole 16-byte pieces leave out, at most 15 at either end: a thread of the
-// first warp each.
-__device__ __forceinline__ void copy_ends(uint8_t *to, const uint8_t *from, int skew, int end, int first, int last)
+// Of `bytes` behind a skew, those that whole 16-byte pieces leave out are at most 15 at either end: a
+// thread of the first warp each. This thread's, or -1.
+__device__ __forceinline__ int end_of(int skew, int bytes)
 {
-    if (threadIdx.x < 32) {
-        const int head = min(first, end), i = threadIdx.x % 16;
-        const int at = threadIdx.x < 16 ? skew + i : max(last, head) + i;
-        if (at < (threadIdx.x < 16 ? head : end))
-            to[at] = from[at];
-    }
+    const int end = skew + bytes, head = min(skew ? 16 : 0, end), i = threadIdx.x % 16;
+    const int at = threadIdx.x < 16 ? skew + i : max(end & ~15, head) + i;
+    return threadIdx.x < 32 && at < (threadIdx.x < 16 ? head : end) ? at : -1;
 }
 
 // `bytes` of a row to shared memory, to skew_of(from) behind a 16-byte boundary: asynchronously but
-// for the ends.
-__device__ __forceinline__ void copy_in(uint8_t *to, const uint8_t *from, int bytes)
+// for the ends, of which this thread's byte is returned (put_end brings it to its place when the
+// copies have arrived, so that nobody waits for the one before the others).
+__device__ __forceinline__ uint8_t copy_in(uint8_t *to, const uint8_t *from, int bytes)
 {
-    const int skew = skew_of(from), end = skew + bytes;
-    from -= skew;  // (whole 16 bytes from `first` to `last` lie inside the row)
-    const int first = skew ? 16 : 0, last = end & ~15;
-    for (int i = first + threadIdx.x * 16; i < last; i += blockDim.x * 16)
+    const int skew = skew_of(from), at = end_of(skew, bytes);
+    from -= skew;  // (whole 16 bytes from the first to the last lie inside the row)
+    const int last = (skew + bytes) & ~15;
+    for (int i = (skew ? 16 : 0) + threadIdx.x * 16; i < last; i += blockDim.x * 16)
         copy_async(smem_u32(to) + i, from + i);
-    copy_ends(to, from, skew, end, first, last);
+    return at >= 0 ? from[at] : 0;
+}
+
+__device__ __forceinline__ void put_end(uint8_t *to, int skew, int bytes, uint8_t end)
+{
+    const int at = end_of(skew, bytes);
+    if (at >= 0)
+        to[at] = end;
 }
 
 // The same back, from skew_of(to) behind a 16-byte boundary of shared memory.
 __device__ __forceinline__ void copy_out(uint8_t *to, const uint8_t *from, int bytes)
 {
-    const int skew = skew_of(to), end = skew + bytes;
+    const int skew = skew_of(to), at = end_of(skew, bytes), last = (skew + bytes) & ~15;
     to -= skew;
-    const int first = skew ? 16 : 0, last = end & ~15;
-    for (int i = first + threadIdx.x * 16; i < last; i += blockDim.x * 16)
+    for (int i = (skew ? 16 : 0) + threadIdx.x * 16; i < last; i += blockDim.x * 16)
         *reinterpret_cast<uint4 *>(to + i) = *reinterpret_cast<const uint4 *>(from + i);
-    copy_ends(to, from, skew, end, first, last);
+    if (at >= 0)
+        to[at] = from[at];
 }
 
 // The N words that begin `skew` bytes behind a 16-byte boundary of shared memory (of which N + 4 are
@@ -499,11 +504,12 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
     uint8_t *const q_row = row + buffers * room;
     griddep_wait();
     griddep_launch_dependents();
+    uint8_t x_end = 0, res_end = 0;  // of the row asked for
     auto ask = [&](int64_t t, int buffer) {
         if (t < p.T) {
-            copy_in(row + buffer * room, p.x + t * p.x_stride * 2, n * 2);
+            x_end = copy_in(row + buffer * room, p.x + t * p.x_stride * 2, n * 2);
             if (p.residual)
-                copy_in(row + buffer * room + x_room, p.residual + t * p.residual_stride * rb, n * rb);
+                res_end = copy_in(row + buffer * room + x_room, p.residual + t * p.residual_stride * rb, n * rb);
         }
         copy_commit();
     };
@@ -514,14 +520,17 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
     int buffer = 0, turn = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         uint8_t *const x = row + buffer * room, *const res = x + x_room;
+        const int x_skew = skew_of(p.x + t * p.x_stride * 2);
+        const int res_skew = skew_of(p.residual + t * p.residual_stride * rb);
         if (buffers == 1)
             ask(t, 0);
         copy_wait<0>();
+        put_end(x, x_skew, n * 2, x_end);
+        if (p.residual)
+            put_end(res, res_skew, n * rb, res_end);
         __syncthreads();
         if (buffers > 1)  // (where the row before this one has left by now)
             ask(t + gridDim.x, buffer ^= 1);
-        const int x_skew = skew_of(p.x + t * p.x_stride * 2);
-        const int res_skew = skew_of(p.residual + t * p.residual_stride * rb);
         Piece h[P];
         Two squares = 0;
 #pragma unroll
@@ -581,13 +590,14 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
     const int room = dy_room + h_room * (p.dsum ? 2 : 1);
     griddep_wait();
     griddep_launch_dependents();
+    uint8_t h_end = 0, dy_end = 0, dsum_end = 0;  // of the row asked for
     auto ask = [&](int64_t t, int buffer) {
         if (t < p.T) {
             uint8_t *const to = row + buffer * room;
-            copy_in(to, p.h + t * p.h_stride * hb, n * hb);
-            copy_in(to + h_room, p.dy + t * p.dy_stride * 2, n * 2);
+            h_end = copy_in(to, p.h + t * p.h_stride * hb, n * hb);
+            dy_end = copy_in(to + h_room, p.dy + t * p.dy_stride * 2, n * 2);
             if (p.dsum)
-                copy_in(to + h_room + dy_room, p.dsum + t * p.dsum_stride * hb, n * hb);
+                dsum_end = copy_in(to + h_room + dy_room, p.dsum + t * p.dsum_stride * hb, n * hb);
         }
         copy_commit();
     };
@@ -601,14 +611,18 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
     int buffer = 0, turn = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         uint8_t *const h_row = row + buffer * room, *const dy_row = h_row + h_room, *const dsum_row = dy_row + dy_room;
+        const int h_skew = skew_of(p.h + t * p.h_stride * hb), dy_skew = skew_of(p.dy + t * p.dy_stride * 2);
+        const int dsum_skew = skew_of(p.dsum + t * p.dsum_stride * hb);
         if (buffers == 1)
             ask(t, 0);
         copy_wait<0>();
+        put_end(h_row, h_skew, n * hb, h_end);
+        put_end(dy_row, dy_skew, n * 2, dy_end);
+        if (p.dsum)
+            put_end(dsum_row, dsum_skew, n * hb, dsum_end);
         __syncthreads();
         if (buffers > 1)  // (where the row before this one has left by now)
             ask(t + gridDim.x, buffer ^= 1);
-        const int h_skew = skew_of(p.h + t * p.h_stride * hb), dy_skew = skew_of(p.dy + t * p.dy_stride * 2);
-        const int dsum_skew = skew_of(p.dsum + t * p.dsum_stride * hb);
         Two squares = 0, dot = 0;
 #pragma unroll
         for (int i = 0; i < P; ++i) {

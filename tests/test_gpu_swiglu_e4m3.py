@@ -78,3 +78,18 @@ def test_past_31_bits():
     call(G, q, s, rows)
     ref.check_e4m3(q[-2:], s[-2:], ref.swiglu(G[-2:]), REL)
     assert (s[:-2] == ref.TINY).all()
+
+
+# rows of several chunks of a block's threads, fewer and more of them than blocks; the last chunk's and
+# the last group's ends
+@pytest.mark.parametrize("rows,inter", [(5000, 1032), (70, 14344), (3001, 1352), (641, 4104), (20000, 136),
+                                        (9, 65544)])
+def test_rows_of_several_chunks(rows, inter):
+    gen = torch.Generator(device="cuda").manual_seed(rows + inter)
+    G = (2 * torch.randn(rows + 2, 2 * inter, generator=gen, device="cuda")).bfloat16()
+    q = torch.full((rows + 2, inter), 0x5A, dtype=torch.uint8, device="cuda")
+    s = torch.full((rows + 2, (inter + 127) // 128), 7.0, device="cuda")
+    call(G, q, s, rows)
+    torch.cuda.synchronize()
+    ref.check_e4m3(q[:rows].view(torch.float8_e4m3fn), s[:rows], ref.swiglu(G[:rows]), REL)
+    assert (q[rows:] == 0x5A).all() and (s[rows:] == 7).all()
