@@ -11,14 +11,14 @@
 //    far from a 16-byte boundary as in memory, so that all but their ends still moves in
 //    aligned pieces, in and out; threads shift the words that they read.
 //  * Instructions come next to bytes here (a gradient of 43 a value took as long as its bytes):
-//    hence arithmetic on two values at a time, the weight in registers, and up to four pieces of
-//    eight values a thread, which share the row's sums and addresses.
+//    hence arithmetic on two values at a time, the weight in registers, addresses that go on from
+//    row to row, and up to four pieces of eight values a thread, which share the row's sums.
 //  * dweight: a block adds its rows' terms in registers and leaves them in the workspace; a second
 //    kernel adds the blocks'.
 //
 // Measured at 8192 x 7168 (GB300, of the copy bandwidth of 6.77 TB/s): beside a bf16 residual to e4m3
 // 64 us, 95 %; to bf16 73 us, 95 %; the gradient in bf16 with the residual's 74 us, 93 %, in fp32
-// 123 us, 99 %. 4096 x 3675, rows of other alignments: the gradient 58 us, 31 %.
+// 123 us, 99 %. Rows of other alignments, 4096 x 3675: 34 us, 53 %, the gradient 49 us, 37 %.
 #include <type_traits>
 
 #include "ep_internal.h"
@@ -93,31 +93,39 @@ __device__ __forceinline__ void copy_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A warp's pieces c .. of one row of n values, one for each lane (c: this lane's). fp32 pieces are 32
-// bytes: there a lane copies 16 bytes of each half of the warp's 1024, so that every request is of
-// whole sectors.
-__device__ __forceinline__ void copy_piece(uint8_t *to, const uint8_t *row, bool bf16, int c, int n)
+// The column of this lane's piece i of P: a warp's pieces lie behind one another, 32 at a time.
+template <int P>
+__device__ __forceinline__ int column(int warp, int i)
 {
-    if (bf16) {
-        if (c < n)
-            copy_async(smem_u32(to) + threadIdx.x * 16, row + c * 2);
-    } else {
-        const int lane = threadIdx.x & 31, first = c - lane * kPiece;  // of the warp
-        const uint32_t dst = smem_u32(to) + (threadIdx.x - lane) * 32 + lane * 16;
+    return ((warp * P + i) * 32 + static_cast<int>(threadIdx.x & 31)) * kPiece;
+}
+
+// Bytes of 32 pieces.
+__host__ __device__ constexpr int warp_bytes(bool bf16) { return 32 * kPiece * (bf16 ? 2 : 4); }
+
+// A warp's part of a row of n values to shared memory, 16 bytes a lane at a time, so that every request is
+// of whole sectors.
+template <int P>
+__device__ __forceinline__ void copy_part(uint8_t *to, const uint8_t *row, bool bf16, int warp, int n)
+{
+    const int begin = warp * P * warp_bytes(bf16), left = n * (bf16 ? 2 : 4) - begin;
+    const uint32_t dst = smem_u32(to);
+    row += begin;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = first + i * 128 + lane * 4;
-            if (at < n)
-                copy_async(dst + i * 512, row + at * 4);
-        }
+    for (int i = 0; i < P * warp_bytes(bf16); i += 512) {
+        const int at = i + static_cast<int>(threadIdx.x & 31) * 16;
+        if (at < left)
+            copy_async(dst + at, row + at);
     }
 }
 
+// This lane's piece of 32 that are there.
 __device__ __forceinline__ Piece read_piece(const uint8_t *from, bool bf16)
 {
+    const int lane = threadIdx.x & 31;
     if (bf16)
-        return unpack(reinterpret_cast<const uint4 *>(from)[threadIdx.x]);
-    const float4 *p = reinterpret_cast<const float4 *>(from) + threadIdx.x * 2;
+        return unpack(reinterpret_cast<const uint4 *>(from)[lane]);
+    const float4 *p = reinterpret_cast<const float4 *>(from) + lane * 2;
     return piece_of(p[0], p[1]);
 }
 
@@ -274,12 +282,12 @@ __host__ __device__ constexpr int room_of(int n, int value_bytes)
 
 // This thread's pieces of the weight.
 template <int P>
-__device__ __forceinline__ void load_weight(const uint8_t *weight, bool bf16, int n, Piece (&w)[P])
+__device__ __forceinline__ void load_weight(const uint8_t *weight, bool bf16, int warp, int n, Piece (&w)[P])
 {
     const bool aligned = reinterpret_cast<uintptr_t>(weight) % 16 == 0;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * kPiece;
+        const int c = column<P>(warp, i);
         w[i] = zeros();
         if (c >= n)
             continue;
@@ -335,35 +343,41 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 part[2][kMaxThreads / 32];
     constexpr int rb = BF16 ? 2 : 4;
-    const int n = p.hidden;
-    // of a thread's piece: x, then the residual
-    const int x_bytes = blockDim.x * 16, piece_bytes = x_bytes * (p.residual ? 1 + rb / 2 : 1);
+    const int n = p.hidden, warps = blockDim.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // (for the compiler to see that its lanes agree)
+    // of a warp: x, then the residual
+    constexpr int x_bytes = P * warp_bytes(true);
+    const int bytes = x_bytes + (p.residual ? P * warp_bytes(BF16) : 0);
+    const float over_n = 1.f / n;
     griddep_wait();
     griddep_launch_dependents();
-    auto ask = [&](int64_t t, int stage) {
-        if (t < p.T) {
-            const uint8_t *const x = p.x + t * p.x_stride * 2, *const res = p.residual + t * p.residual_stride * rb;
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int c = (i * blockDim.x + threadIdx.x) * kPiece;
-                uint8_t *to = ring + (stage * P + i) * piece_bytes;
-                copy_piece(to, x, true, c, n);
-                if (p.residual)
-                    copy_piece(to + x_bytes, res, BF16, c, n);
-            }
+    // this block's rows and the way from one to the next
+    int64_t t = blockIdx.x;
+    const uint8_t *x = p.x + t * p.x_stride * 2, *res = p.residual + t * p.residual_stride * rb;
+    uint8_t *sum = p.sum + t * p.sum_stride * rb, *y = p.y + t * p.y_stride * 2, *q = p.q + t * n;
+    float *scales = p.q_scales + t * ((n + 127) / 128);
+    const int64_t blocks = gridDim.x, x_step = blocks * p.x_stride * 2, res_step = blocks * p.residual_stride * rb;
+    auto ask = [&](int ahead, int stage) {
+        if (t + ahead * blocks < p.T) {
+            const uint8_t *const from = x + ahead * x_step, *const res_from = res + ahead * res_step;
+            uint8_t *const to = ring + (stage * warps + warp) * bytes;
+            copy_part<P>(to, from, true, warp, n);
+            if (p.residual)
+                copy_part<P>(to + x_bytes, res_from, BF16, warp, n);
         }
         copy_commit();
     };
 #pragma unroll
     for (int i = 0; i < S - 1; ++i)
-        ask(blockIdx.x + static_cast<int64_t>(i) * gridDim.x, i);
+        ask(i, i);
     Piece w[P];
-    load_weight(p.weight, p.weight_bf16, n, w);
+    load_weight(p.weight, p.weight_bf16, warp, n, w);
     int stage = 0, turn = 0;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+    for (; t < p.T; t += blocks) {
+        uint8_t *const mine = ring + (stage * warps + warp) * bytes;
         if (!BF16)
-            __syncwarp();  // (fp32 pieces are copied by the warp's other lanes)
-        ask(t + static_cast<int64_t>(S - 1) * gridDim.x, stage == 0 ? S - 1 : stage - 1);
+            __syncwarp();  // (pieces are copied by the warp's other lanes)
+        ask(S - 1, stage == 0 ? S - 1 : stage - 1);
         copy_wait<S - 1>();
         if (!BF16)
             __syncwarp();
@@ -371,28 +385,22 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
         Two squares = 0;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
-            const uint8_t *from = ring + (stage * P + i) * piece_bytes;
-            h[i] = zeros();
-            if (c < n) {
-                h[i] = read_piece(from, true);
-                if (p.residual) {
-                    const Piece res = read_piece(from + x_bytes, BF16);
+            const int c = column<P>(warp, i);
+            h[i] = c < n ? read_piece(mine + i * warp_bytes(true), true) : zeros();
+            if (p.residual) {
+                const Piece r = c >= n ? zeros() : read_piece(mine + x_bytes + i * warp_bytes(BF16), BF16);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        h[i].v[j] = add2(h[i].v[j], res.v[j]);
-                }
+                for (int j = 0; j < 4; ++j)
+                    h[i].v[j] = add2(h[i].v[j], r.v[j]);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 squares = fma2(h[i].v[j], h[i].v[j], squares);
         }
-        const float r = rsqrtf(block_sum(sum_of(squares), part[turn ^= 1]) / n + p.eps);
-        uint8_t *const sum = p.sum + t * p.sum_stride * rb, *const y = p.y + t * p.y_stride * 2, *const q = p.q + t * n;
-        float *const scales = p.q_scales + t * ((n + 127) / 128);
+        const float r = rsqrtf(block_sum(sum_of(squares), part[turn ^= 1]) * over_n + p.eps);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
+            const int c = column<P>(warp, i);
             if (c < n && p.sum)
                 store_piece(sum, BF16, c, h[i]);
             const Piece v = scaled(h[i], r, w[i]);
@@ -405,6 +413,12 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
             }
         }
         stage = stage == S - 1 ? 0 : stage + 1;
+        x += x_step;
+        res += res_step;
+        sum += blocks * p.sum_stride * rb;
+        y += blocks * p.y_stride * 2;
+        q += blocks * n;
+        scales += blocks * ((n + 127) / 128);
     }
 }
 
@@ -415,78 +429,85 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 part[2][kMaxThreads / 32];
     constexpr int hb = BF16 ? 2 : 4;
-    const int n = p.hidden;
-    // of a thread's piece: h, dy, then dsum
-    const int dy_bytes = blockDim.x * 16, h_bytes = dy_bytes * (hb / 2);
-    const int piece_bytes = dy_bytes + h_bytes * (p.dsum ? 2 : 1);
+    const int n = p.hidden, warps = blockDim.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // (for the compiler to see that its lanes agree)
+    // of a warp: h, dy, then dsum
+    constexpr int h_bytes = P * warp_bytes(BF16), dy_bytes = P * warp_bytes(true);
+    const int bytes = dy_bytes + h_bytes * (p.dsum ? 2 : 1);
+    const float over_n = 1.f / n;
     griddep_wait();
     griddep_launch_dependents();
-    auto ask = [&](int64_t t, int stage) {
-        if (t < p.T) {
-            const uint8_t *const h = p.h + t * p.h_stride * hb, *const dy = p.dy + t * p.dy_stride * 2;
-            const uint8_t *const dsum = p.dsum + t * p.dsum_stride * hb;
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int c = (i * blockDim.x + threadIdx.x) * kPiece;
-                uint8_t *to = ring + (stage * P + i) * piece_bytes;
-                copy_piece(to, h, BF16, c, n);
-                copy_piece(to + h_bytes, dy, true, c, n);
-                if (p.dsum)
-                    copy_piece(to + h_bytes + dy_bytes, dsum, BF16, c, n);
-            }
+    int64_t t = blockIdx.x;
+    const uint8_t *h = p.h + t * p.h_stride * hb, *dy = p.dy + t * p.dy_stride * 2, *dsum = p.dsum + t * p.dsum_stride * hb;
+    uint8_t *dh = p.dh + t * p.dh_stride * hb, *dx = p.dx + t * p.dx_stride * 2;
+    const int64_t blocks = gridDim.x;
+    const int64_t h_step = blocks * p.h_stride * hb, dy_step = blocks * p.dy_stride * 2, dsum_step = blocks * p.dsum_stride * hb;
+    auto ask = [&](int ahead, int stage) {
+        if (t + ahead * blocks < p.T) {
+            const uint8_t *const h_from = h + ahead * h_step, *const dy_from = dy + ahead * dy_step;
+            const uint8_t *const dsum_from = dsum + ahead * dsum_step;
+            uint8_t *const to = ring + (stage * warps + warp) * bytes;
+            copy_part<P>(to, h_from, BF16, warp, n);
+            copy_part<P>(to + h_bytes, dy_from, true, warp, n);
+            if (p.dsum)
+                copy_part<P>(to + h_bytes + dy_bytes, dsum_from, BF16, warp, n);
         }
         copy_commit();
     };
 #pragma unroll
     for (int i = 0; i < S - 1; ++i)
-        ask(blockIdx.x + static_cast<int64_t>(i) * gridDim.x, i);
+        ask(i, i);
     Piece w[P], dw[P];
-    load_weight(p.weight, p.weight_bf16, n, w);
+    load_weight(p.weight, p.weight_bf16, warp, n, w);
 #pragma unroll
     for (int i = 0; i < P; ++i)
         dw[i] = zeros();
     int stage = 0, turn = 0;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+    for (; t < p.T; t += blocks) {
+        uint8_t *const mine = ring + (stage * warps + warp) * bytes;
         if (!BF16)
-            __syncwarp();  // (fp32 pieces are copied by the warp's other lanes)
-        ask(t + static_cast<int64_t>(S - 1) * gridDim.x, stage == 0 ? S - 1 : stage - 1);
+            __syncwarp();  // (pieces are copied by the warp's other lanes)
+        ask(S - 1, stage == 0 ? S - 1 : stage - 1);
         copy_wait<S - 1>();
         if (!BF16)
             __syncwarp();
         Two squares = 0, dot = 0;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
-            const uint8_t *from = ring + (stage * P + i) * piece_bytes;
+            const int c = column<P>(warp, i);
+            const uint8_t *const h_at = mine + i * warp_bytes(BF16), *const dy_at = mine + h_bytes + i * warp_bytes(true);
             if (c < n)
-                gradient_sums(read_piece(from, BF16), read_piece(from + h_bytes, true), w[i], squares, dot);
+                gradient_sums(read_piece(h_at, BF16), read_piece(dy_at, true), w[i], squares,
+                              dot);
         }
         const float2 sums = block_sum(sum_of(squares), sum_of(dot), part[turn ^= 1]);
-        const float r = rsqrtf(sums.x / n + p.eps), back = r * r * (sums.y / n);
-        uint8_t *const dh = p.dh + t * p.dh_stride * hb, *const dx = p.dx + t * p.dx_stride * 2;
+        const float r = rsqrtf(sums.x * over_n + p.eps), back = r * r * (sums.y * over_n);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
-            const uint8_t *from = ring + (stage * P + i) * piece_bytes;
+            const int c = column<P>(warp, i);
+            const uint8_t *const h_at = mine + i * warp_bytes(BF16), *const dy_at = mine + h_bytes + i * warp_bytes(true);
             if (c >= n)
                 break;
-            Piece d = p.dsum ? read_piece(from + h_bytes + dy_bytes, BF16) : zeros();
-            gradient(read_piece(from, BF16), read_piece(from + h_bytes, true), w[i], r, back, d, dw[i]);
+            Piece d = p.dsum ? read_piece(h_at + h_bytes + dy_bytes, BF16) : zeros();
+            gradient(read_piece(h_at, BF16), read_piece(dy_at, true), w[i], r, back, d, dw[i]);
             if (p.dh)
                 store_piece(dh, BF16, c, d);
             if (p.dx)
                 store_piece(dx, true, c, d);
         }
         stage = stage == S - 1 ? 0 : stage + 1;
+        h += h_step;
+        dy += dy_step;
+        dsum += dsum_step;
+        dh += blocks * p.dh_stride * hb;
+        dx += blocks * p.dx_stride * 2;
     }
     if (p.dweight) {
-        uint8_t *mine = reinterpret_cast<uint8_t *>(p.parts + static_cast<int64_t>(blockIdx.x) * n);
+        uint8_t *const to = reinterpret_cast<uint8_t *>(p.parts + static_cast<int64_t>(blockIdx.x) * n);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
-            if (c < n)
-                store_piece(mine, false, c, dw[i]);
-        }
+        for (int i = 0; i < P; ++i)
+            if (const int c = column<P>(warp, i); c < n)
+                store_piece(to, false, c, dw[i]);
     }
 }
 
@@ -499,6 +520,8 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
     extern __shared__ __align__(16) uint8_t row[];
     __shared__ float2 part[2][kMaxThreads / 32];
     constexpr int rb = BF16 ? 2 : 4;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const float over_n = 1.f / p.hidden;
     const int n = p.hidden, x_room = room_of(n, 2);
     const int room = x_room + (p.residual || p.sum ? room_of(n, rb) : 0);
     uint8_t *const q_row = row + buffers * room;
@@ -516,7 +539,7 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
     if (buffers > 1)
         ask(blockIdx.x, 0);
     Piece w[P];
-    load_weight(p.weight, p.weight_bf16, n, w);
+    load_weight(p.weight, p.weight_bf16, warp, n, w);
     int buffer = 0, turn = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         uint8_t *const x = row + buffer * room, *const res = x + x_room;
@@ -535,7 +558,7 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
         Two squares = 0;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
+            const int c = column<P>(warp, i);
             h[i] = zeros();
             if (c < n) {
                 h[i] = read_any(x, x_skew, true, c, n);
@@ -550,11 +573,11 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
             for (int j = 0; j < 4; ++j)
                 squares = fma2(h[i].v[j], h[i].v[j], squares);
         }
-        const float r = rsqrtf(block_sum(sum_of(squares), part[turn ^= 1]) / n + p.eps);
+        const float r = rsqrtf(block_sum(sum_of(squares), part[turn ^= 1]) * over_n + p.eps);
         uint8_t *const sum = p.sum + t * p.sum_stride * rb, *const y = p.y + t * p.y_stride * 2, *const q = p.q + t * n;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
+            const int c = column<P>(warp, i);
             if (c < n && p.sum)
                 write_any(res, skew_of(sum), BF16, c, n, h[i]);
             const Piece v = scaled(h[i], r, w[i]);
@@ -586,6 +609,8 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
     extern __shared__ __align__(16) uint8_t row[];
     __shared__ float2 part[2][kMaxThreads / 32];
     constexpr int hb = BF16 ? 2 : 4;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const float over_n = 1.f / p.hidden;
     const int n = p.hidden, h_room = room_of(n, hb), dy_room = room_of(n, 2);
     const int room = dy_room + h_room * (p.dsum ? 2 : 1);
     griddep_wait();
@@ -604,7 +629,7 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
     if (buffers > 1)
         ask(blockIdx.x, 0);
     Piece w[P], dw[P];
-    load_weight(p.weight, p.weight_bf16, n, w);
+    load_weight(p.weight, p.weight_bf16, warp, n, w);
 #pragma unroll
     for (int i = 0; i < P; ++i)
         dw[i] = zeros();
@@ -626,18 +651,18 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
         Two squares = 0, dot = 0;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
+            const int c = column<P>(warp, i);
             if (c < n)
                 gradient_sums(read_any(h_row, h_skew, BF16, c, n), read_any(dy_row, dy_skew, true, c, n), w[i],
                               squares, dot);
         }
         const float2 sums = block_sum(sum_of(squares), sum_of(dot), part[turn ^= 1]);
-        const float r = rsqrtf(sums.x / n + p.eps), back = r * r * (sums.y / n);
+        const float r = rsqrtf(sums.x * over_n + p.eps), back = r * r * (sums.y * over_n);
         uint8_t *const dh = p.dh + t * p.dh_stride * hb, *const dx = p.dx + t * p.dx_stride * 2;
         Piece d[P];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
+            const int c = column<P>(warp, i);
             d[i] = zeros();
             if (c >= n)
                 continue;
@@ -651,7 +676,7 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
             __syncthreads();
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * kPiece;
+            const int c = column<P>(warp, i);
             if (c < n && p.dh)
                 write_any(h_row, skew_of(dh), BF16, c, n, d[i]);
             if (c < n && p.dx)
@@ -673,7 +698,7 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
             values_of(dw[i], f);
 #pragma unroll
             for (int j = 0; j < kPiece; ++j) {
-                const int c = (i * blockDim.x + threadIdx.x) * kPiece + j;
+                const int c = column<P>(warp, i) + j;
                 if (c < n)
                     mine[c] = f[j];
             }
@@ -767,7 +792,7 @@ cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t s)
     const int waves = !p.residual || p.T < rows ? 1 : (p.T + rows / 2) / rows;
     const int most = resident * waves;
     const unsigned grid = p.T < most ? p.T : most;
-    if (whole && f.stages >= 2) {
+    if (whole) {
         // (one row a block needs no second: no attribute to set, a tenth of a small call's host time)
         const int smem = (p.T == static_cast<int>(grid) ? 1 : f.stages) * f.threads * f.pieces * kPiece * bytes;
         auto go = [&](auto bf16) {
@@ -809,13 +834,14 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, int num_sms, cudaS
     most = most < part_blocks(p.hidden) ? most : part_blocks(p.hidden);
     const unsigned grid = p.T < most ? p.T : most;
     cudaError_t e;
-    if (whole && f.stages >= 2) {
+    if (whole) {
         const int smem = (p.T == static_cast<int>(grid) ? 1 : f.stages) * f.threads * f.pieces * kPiece *
                          (2 + hb * (p.dsum ? 2 : 1));
         auto go = [&](auto bf16) {
             constexpr bool B = decltype(bf16)::value;
             const auto kern = f.pieces == 1   ? norm_backward_kernel<B, 1, 2>
                               : f.pieces == 2 ? norm_backward_kernel<B, 2, 2>
+                              : f.stages == 1 ? norm_backward_kernel<B, 4, 1>
                                               : norm_backward_kernel<B, 4, 2>;
             return launch_rows(kern, f.threads, smem, grid, s, p);
         };
