@@ -511,11 +511,11 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
     }
 }
 
-// Rows of any alignment: x (then y) and the residual (then sum) in two buffers that take turns, where
-// they fit; q. (What is written has the skew of where it goes, so that it may overlap what other
-// threads read: between the two lies a barrier.)
+// Rows of any alignment: x (then y) and the residual (then sum) in two buffers that take turns; q. (What
+// is written has the skew of where it goes, so that it may overlap what other threads read: between the
+// two lies a barrier.)
 template <bool BF16, int P>
-__global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 1) norm_any_kernel(const NormParams p, int buffers)
+__global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 1) norm_any_kernel(const NormParams p)
 {
     extern __shared__ __align__(16) uint8_t row[];
     __shared__ float2 part[2][kMaxThreads / 32];
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
     const float over_n = 1.f / p.hidden;
     const int n = p.hidden, x_room = room_of(n, 2);
     const int room = x_room + (p.residual || p.sum ? room_of(n, rb) : 0);
-    uint8_t *const q_row = row + buffers * room;
+    uint8_t *const q_row = row + 2 * room;
     griddep_wait();
     griddep_launch_dependents();
     uint8_t x_end = 0, res_end = 0;  // of the row asked for
@@ -536,8 +536,7 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
         }
         copy_commit();
     };
-    if (buffers > 1)
-        ask(blockIdx.x, 0);
+    ask(blockIdx.x, 0);
     Piece w[P];
     load_weight(p.weight, p.weight_bf16, warp, n, w);
     int buffer = 0, turn = 0;
@@ -545,15 +544,12 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
         uint8_t *const x = row + buffer * room, *const res = x + x_room;
         const int x_skew = skew_of(p.x + t * p.x_stride * 2);
         const int res_skew = skew_of(p.residual + t * p.residual_stride * rb);
-        if (buffers == 1)
-            ask(t, 0);
         copy_wait<0>();
         put_end(x, x_skew, n * 2, x_end);
         if (p.residual)
             put_end(res, res_skew, n * rb, res_end);
         __syncthreads();
-        if (buffers > 1)  // (where the row before this one has left by now)
-            ask(t + gridDim.x, buffer ^= 1);
+        ask(t + gridDim.x, buffer ^= 1);  // (where the row before this one has left by now)
         Piece h[P];
         Two squares = 0;
 #pragma unroll
@@ -596,12 +592,10 @@ __global__ void __launch_bounds__(P == 1 ? 128 : 512, P == 1 ? 8 : P == 2 ? 2 : 
             copy_out(y, x, n * 2);
         if (p.q)
             copy_out(q, q_row, n);
-        if (buffers == 1)
-            __syncthreads();
     }
 }
 
-// The same for the gradient: h (then dh), dy (then dx), dsum.
+// The same for the gradient: h (then dh), dy (then dx), dsum, in one buffer where two do not fit.
 template <bool BF16, int P>
 __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 : P == 2 ? 3 : 1)
     norm_backward_any_kernel(const NormBackwardParams p, int buffers)
@@ -797,21 +791,25 @@ cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t s)
         const int smem = (p.T == static_cast<int>(grid) ? 1 : f.stages) * f.threads * f.pieces * kPiece * bytes;
         auto go = [&](auto bf16) {
             constexpr bool B = decltype(bf16)::value;
-            const auto kern = f.pieces == 1   ? (f.stages == 2 ? norm_kernel<B, 1, 2> : norm_kernel<B, 1, 3>)
-                              : f.pieces == 2 ? (f.stages == 2 ? norm_kernel<B, 2, 2> : norm_kernel<B, 2, 3>)
-                                              : (f.stages == 2 ? norm_kernel<B, 4, 2> : norm_kernel<B, 4, 3>);
+            // (three rows fit but for the longest of either form beside an fp32 residual)
+            constexpr int two = B ? 3 : 2;
+            const auto kern = f.pieces == 1   ? norm_kernel<B, 1, 3>
+                              : f.pieces == 2 ? (f.stages == 2 ? norm_kernel<B, 2, two> : norm_kernel<B, 2, 3>)
+                                              : (f.stages == 2 ? norm_kernel<B, 4, two> : norm_kernel<B, 4, 3>);
             return launch_rows(kern, f.threads, smem, grid, s, p);
         };
         return p.residual_bf16 ? go(std::true_type()) : go(std::false_type());
     }
     const int room = room_of(p.hidden, 2) + (p.residual || p.sum ? room_of(p.hidden, rb) : 0);
-    const int q_room = p.q ? room_of(p.hidden, 1) : 0, buffers = 2 * room + q_room <= kSmemOfSm ? 2 : 1;
+    const int q_room = p.q ? room_of(p.hidden, 1) : 0;
+    static_assert(2 * (room_of(EP_MAX_NORM_HIDDEN, 2) + room_of(EP_MAX_NORM_HIDDEN, 4)) +
+                      room_of(EP_MAX_NORM_HIDDEN, 1) <= kSmemOfSm, "two rows and the codes");
     auto go = [&](auto bf16) {
         constexpr bool B = decltype(bf16)::value;
         return launch_rows(f.pieces == 1   ? norm_any_kernel<B, 1>
                            : f.pieces == 2 ? norm_any_kernel<B, 2>
                                            : norm_any_kernel<B, 4>,
-                           f.threads, buffers * room + q_room, grid, s, p, buffers);
+                           f.threads, 2 * room + q_room, grid, s, p);
     };
     return p.residual_bf16 ? go(std::true_type()) : go(std::false_type());
 }
@@ -839,9 +837,11 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, int num_sms, cudaS
                          (2 + hb * (p.dsum ? 2 : 1));
         auto go = [&](auto bf16) {
             constexpr bool B = decltype(bf16)::value;
+            // (two rows fit but for the longest in fp32)
+            constexpr int one = B ? 2 : 1;
             const auto kern = f.pieces == 1   ? norm_backward_kernel<B, 1, 2>
                               : f.pieces == 2 ? norm_backward_kernel<B, 2, 2>
-                              : f.stages == 1 ? norm_backward_kernel<B, 4, 1>
+                              : f.stages == 1 ? norm_backward_kernel<B, 4, one>
                                               : norm_backward_kernel<B, 4, 2>;
             return launch_rows(kern, f.threads, smem, grid, s, p);
         };

@@ -39,7 +39,8 @@ __device__ __forceinline__ Two silu2(Two x)
 }  // namespace
 
 // A block takes tiles of kRowsAhead * (256 / width) rows by the pieces of `width` threads (whole half
-// warps), which take turns through a row's chunks.
+// warps), which take turns through a row's chunks. ONE: there is one (65536 x 2048 107 us, in the other
+// form 108).
 template <bool ONE>
 __global__ void __launch_bounds__(kThreads) swiglu_e4m3_kernel(const SwigluE4m3Params p, int width)
 {
@@ -91,7 +92,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_e4m3_kernel(const SwigluE4m3P
 
 cudaError_t launch_swiglu_e4m3(const SwigluE4m3Params &p, int num_sms, cudaStream_t s)
 {
-    // Threads to a row: of 16, 32 .. 256 those of which a row leaves the fewest idle, the most of them.
+    // Threads to a row: of 16, 32 .. 256 those of which a row leaves the fewest idle, the most of them
+    // (30000 x 1032: 16 threads 29.6 us, 64 34.7, 256 42.9; 65536 x 2048: 256 threads 108, 16 111).
     const int pieces = p.inter / kPiece;
     int width = kGroupPieces, slots = INT_MAX;
     for (int w = kGroupPieces; w <= kThreads; w *= 2)
