@@ -739,7 +739,7 @@ int ep_add_rmsnorm_backward(const ep_config *cfg, const ep_add_rmsnorm_backward_
  *   q               [max_rows][inter] e4m3 out, 8-byte aligned: the down-projection's A
  *   q_scales        [max_rows][ceil(inter/128)] fp32 out: its a_scales
  *   expert_offsets  the plan of my_rank (row count at [E_l])
- *   inter           a multiple of 8
+ *   inter           a multiple of 8, at most 2^28 (else EP_ERR_UNSUPPORTED)
  * Rows at or past the row count are left as they were.
  */
 typedef struct {
@@ -768,7 +768,8 @@ int ep_swiglu_e4m3(const ep_config *cfg, const ep_swiglu_e4m3_args *args, ep_str
  *   dtype EP_FP8_1D2D    x, W1, W2 e4m3 with 1x128 and 128x128 fp32 scales; the activation goes
  *                        to e4m3 with 1x128 scales by the rule of ep_swiglu_e4m3, from fp32.
  *                        K and N are multiples of 128.
- * (Other K and N: EP_ERR_UNSUPPORTED.) Sums are fp32 and out is rounded once.
+ * (Other K and N, or experts whose W1 has 2^40 bytes: EP_ERR_UNSUPPORTED.) Sums are fp32 and out is
+ * rounded once.
  *   x               [num_tokens][N], 16-byte aligned
  *   x_scales        EP_FP8_1D2D only: [num_tokens][N/128] fp32
  *   topk_ids        [num_tokens][top_k] global expert ids. One outside [0, n_ranks *

@@ -890,6 +890,8 @@ int ep_swiglu_e4m3(const ep_config *cfg, const ep_swiglu_e4m3_args *a, ep_stream
         !aligned_to(a->q_scales, 4) || !aligned_to(a->expert_offsets, 4) || a->max_rows < 1 ||
         a->max_rows > INT32_MAX)
         return EP_ERR_INVALID_ARG;
+    if (a->inter > 1 << 28)  // (bytes of half a row are counted in 32 bits)
+        return EP_ERR_UNSUPPORTED;
     const int num_sms = sm_count();
     if (num_sms <= 0)
         return EP_ERR_CUDA;

@@ -107,6 +107,11 @@ def test_swiglu_refusals(kw):
     assert call("ep_swiglu_e4m3", cfg(), swiglu_args(**kw)) == BAD
 
 
+def test_swiglu_limit():
+    assert call("ep_swiglu_e4m3", cfg(), swiglu_args(inter=(1 << 28) + 8)) == UNSUP
+    assert call("ep_swiglu_e4m3", cfg(), swiglu_args(inter=1 << 30)) == UNSUP
+
+
 def few_args(**kw):
     base = dict(x=P, x_scales=P, topk_ids=P, gates=P, W1=P, w1_scales=P, W2=P, w2_scales=P, out=P,
                 workspace=P, workspace_bytes=1 << 40, status=P)
