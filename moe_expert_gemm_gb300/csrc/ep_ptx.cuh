@@ -76,6 +76,21 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
     }
 }
 
+// A ring's copies land before the block's shared memory goes away: waits, timeout_ns at most, for
+// the last copies into each of its N stages, of `issued` copies one stage after the other, by the barriers
+// that count their bytes. Always, not only where this thread gave up: nobody waits for the last copies
+// once one of those they are meant for has.
+template <int N>
+__device__ __forceinline__ void wait_for_copies(uint64_t *full, int issued, uint64_t timeout_ns)
+{
+    volatile int no_abort = 0;
+    const uint64_t t0 = globaltimer_ns();
+    for (int i = issued > N ? issued - N : 0; i < issued; ++i) {
+        const uint64_t spent = globaltimer_ns() - t0;
+        mbar_wait(&full[i % N], (i / N) & 1, spent < timeout_ns ? timeout_ns - spent : 0, &no_abort);
+    }
+}
+
 // ----------------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_prefetch_map(const void *map)
