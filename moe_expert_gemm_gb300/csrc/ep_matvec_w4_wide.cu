@@ -291,13 +291,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                     advance(stage, phase, kStages);
                 }
             }
-            if (!ok) {
+            if (!ok)
                 give_up(p, sh);
-                // the copies in flight land before the block's shared memory goes away
-                volatile int no_abort = 0;
-                for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-                    wait_long(&sh.full[i % kStages], (i / kStages) & 1, 1000000, &no_abort);
-            }
+            wait_for_copies<kStages>(sh.full, issued, kTimeoutNs);
         }
         __syncwarp();
     } else if (warp == 1) {

@@ -78,8 +78,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
 
 // A ring's copies land before the block's shared memory goes away: waits, timeout_ns at most, for
 // the last copies into each of its N stages, of `issued` copies one stage after the other, by the barriers
-// that count their bytes. Always, not only where this thread gave up: nobody waits for the last copies
-// once one of those they are meant for has.
+// that count their bytes (and other warps' arrivals, which may not come any more: then for as long as it
+// may). Always, not only where this thread gave up: nobody waits for the last copies once one of those
+// they are meant for has.
 template <int N>
 __device__ __forceinline__ void wait_for_copies(uint64_t *full, int issued, uint64_t timeout_ns)
 {

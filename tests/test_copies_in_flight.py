@@ -30,7 +30,8 @@ def statement(body, at):
 
 
 # (kernel, source)
-RINGS = [("few_kernel", "ep_layer_few.cu")]
+RINGS = [("few_kernel", "ep_layer_few.cu"), ("matvec_w4_kernel", "ep_matvec_w4.cu"),
+         ("matvec_w4_wide_kernel", "ep_matvec_w4_wide.cu")]
 
 
 @pytest.mark.parametrize("name,source", RINGS)
