@@ -459,6 +459,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ---------------------------------------------------------------- products
         if (lane == 0) {
+            // (the columns come after the first kernel: the waits' limits do not count its time)
+            if (DOWN)
+                griddep_wait();
             bool ok = true;
             int buf = 0;
             uint32_t buf_phase = 0;
