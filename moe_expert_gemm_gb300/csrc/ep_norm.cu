@@ -769,7 +769,8 @@ template <typename Kern, typename... Args>
 cudaError_t launch_rows(Kern kern, int threads, int smem, unsigned grid, cudaStream_t s, const Args &...args)
 {
     if (smem > 47 * 1024) {  // (48 KB with the kernel's own)
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        // (the attribute is the kernel's, not the call's: one value for all calls, as other threads set it, too)
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOfSm);
         if (e != cudaSuccess)
             return e;
     }
