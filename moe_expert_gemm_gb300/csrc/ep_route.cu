@@ -837,10 +837,13 @@ template <typename Kern, typename Params>
 static cudaError_t launch_rows(Kern kern, const Params &p, int warps, int64_t warp_bytes,
                                cudaStream_t s)
 {
+    // the most that any call takes (the token kernel's for every expert there may be)
+    constexpr int kMost = kRouteThreads / 32 * 4 * kTokenWords * EP_MAX_RANKS * EP_MAX_LOCAL_EXPERTS;
     const int smem = static_cast<int>(warps * warp_bytes);
     if (smem > 48 * 1024) {
+        // (the attribute is the kernel's, not the call's: one value for all calls, as other threads set it, too)
         const cudaError_t e =
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (e != cudaSuccess)
             return e;
     }
