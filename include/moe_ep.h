@@ -656,8 +656,9 @@ int ep_matvec_w4(const ep_config *cfg, const ep_w4_args *args, ep_stream_t strea
  *   *_stride        elements between rows (0: hidden). q and q_scales lie without gaps.
  * One of sum, y and q is given. Pointers need no more than their type's alignment; rows of
  * whole 16-byte pieces are faster. The sum of squares is fp32: where a row's values pass about
- * 1e19 / sqrt(hidden) in size it is infinite and the row's v zero, values under 1e-23 add
- * nothing to it.
+ * 1e19 / sqrt(hidden) in size it is infinite and the row's v zero; squares of values under
+ * 1e-19 lose bits, those of values under 1e-23 add nothing to it. (That matters where eps is as
+ * small.)
  */
 #define EP_ROWS_F32 0
 #define EP_ROWS_BF16 1

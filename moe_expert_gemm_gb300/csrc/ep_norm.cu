@@ -311,7 +311,8 @@ __device__ __forceinline__ Piece scaled(const Piece &h, float r, const Piece &w)
     return v;
 }
 
-// The gradient's terms of a piece: d += r (dy w - h back), dw += dy (h r).
+// The gradient's terms of a piece: d += r (dy w - h back), dw += dy (h r). (back is r (r mean(g h)), in this
+// order: r^2 alone leaves fp32 for rows of 2^-64 and less, r mean(g h) only where r g, the gradient, does.)
 __device__ __forceinline__ void gradient(const Piece &h, const Piece &dy, const Piece &w, float r, float back, Piece &d,
                                          Piece &dw)
 {
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
                               dot);
         }
         const float2 sums = block_sum(sum_of(squares), sum_of(dot), part[turn ^= 1]);
-        const float r = rsqrtf(sums.x * over_n + p.eps), back = r * r * (sums.y * over_n);
+        const float r = rsqrtf(sums.x * over_n + p.eps), back = r * (r * (sums.y * over_n));
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int c = column<P>(warp, i);
@@ -651,7 +652,7 @@ __global__ void __launch_bounds__(P == 1 ? 128 : P == 2 ? 256 : 512, P == 1 ? 8 
                               squares, dot);
         }
         const float2 sums = block_sum(sum_of(squares), sum_of(dot), part[turn ^= 1]);
-        const float r = rsqrtf(sums.x * over_n + p.eps), back = r * r * (sums.y * over_n);
+        const float r = rsqrtf(sums.x * over_n + p.eps), back = r * (r * (sums.y * over_n));
         uint8_t *const dh = p.dh + t * p.dh_stride * hb, *const dx = p.dx + t * p.dx_stride * 2;
         Piece d[P];
 #pragma unroll
