@@ -46,7 +46,9 @@ __global__ void __launch_bounds__(kThreads) swiglu_e4m3_kernel(const SwigluE4m3P
 {
     griddep_wait();
     griddep_launch_dependents();
-    int64_t m_total = __ldg(p.expert_offsets + p.El);
+    // (an ordinary load: the kernel before may write the offsets while this one is already there, and a load
+    // through the read-only path need not stay behind the wait)
+    int64_t m_total = p.expert_offsets[p.El];
     m_total = m_total < 0 ? 0 : (m_total > p.max_rows ? p.max_rows : m_total);
     const int pieces = p.inter / kPiece, groups = (pieces + kGroupPieces - 1) / kGroupPieces;
     const int x = threadIdx.x % width, y = threadIdx.x / width, rows_at_once = kThreads / width;
