@@ -741,7 +741,8 @@ int ep_add_rmsnorm_backward(const ep_config *cfg, const ep_add_rmsnorm_backward_
  *   q_scales        [max_rows][ceil(inter/128)] fp32 out: its a_scales
  *   expert_offsets  the plan of my_rank (row count at [E_l])
  *   inter           a multiple of 8, at most 2^28 (else EP_ERR_UNSUPPORTED)
- * Rows at or past the row count are left as they were.
+ * Rows at or past the row count are left as they were. SiLU is 0 where e^-gate leaves fp32, for
+ * gates of -89 and less (where it is under 2^-121 in size).
  */
 typedef struct {
     const void *G;

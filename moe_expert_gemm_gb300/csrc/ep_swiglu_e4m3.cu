@@ -19,21 +19,23 @@ constexpr int kRowsAhead = 4;  // of a thread, under way at once (65536 x 2048: 
 
 // x / (1 + e^-x) of two bf16 values. e^-x = 2^t * 2^d with t + d = -x log2 e: t is -x times
 // the first 16 bits of log2 e, exact as x has 8, and 2^d = 1 + d ln 2 to within (88 * 2^-17 ln 2)^2 / 2
-// = 1.1e-7. With the errors of ex2 (2^-22) and rcp (2^-23) and four roundings a value is off by at
-// most 12 half steps (quotients below 2^-126 become 0).
+// = 1.1e-7. With the errors of ex2 (2^-22) and rcp (2^-23) and three roundings a value is off by at
+// most 12 half steps. The quotient is of quarters: 1 + e^-x may pass 2^126, where rcp gives 0. (0 where
+// e^-x leaves fp32, for gates of -89 and less, where the value is under 2^-121.)
 __device__ __forceinline__ Two silu2(Two x)
 {
     constexpr float first = 1.44268798828125f, rest_ln2 = 4.8884952e-6f;
+    const Two quarter = two(0.25f, 0.25f);
     float t0, t1, e0, e1;
     split(mul2(x, two(-first, -first)), t0, t1);
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
-    const Two e = two(e0, e1);
+    const Two to_d = fma2(x, two(-0.25f * rest_ln2, -0.25f * rest_ln2), quarter);  // 2^d / 4
     float s0, s1;
-    split(add2(fma2(e, mul2(x, two(-rest_ln2, -rest_ln2)), e), two(1.f, 1.f)), s0, s1);
+    split(fma2(two(e0, e1), to_d, quarter), s0, s1);
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s0));
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s1));
-    return mul2(x, two(s0, s1));
+    return mul2(mul2(x, quarter), two(s0, s1));
 }
 
 }  // namespace
