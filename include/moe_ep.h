@@ -771,7 +771,8 @@ int ep_swiglu_e4m3(const ep_config *cfg, const ep_swiglu_e4m3_args *args, ep_str
  *                        to e4m3 with 1x128 scales by the rule of ep_swiglu_e4m3, from fp32.
  *                        K and N are multiples of 128.
  * (Other K and N, or experts whose W1 has 2^40 bytes: EP_ERR_UNSUPPORTED.) Sums are fp32 and out is
- * rounded once.
+ * rounded once. SiLU is 0 where e^-x leaves fp32, below -88.7 (where it is under 2^-121 in
+ * size).
  *   x               [num_tokens][N], 16-byte aligned
  *   x_scales        EP_FP8_1D2D only: [num_tokens][N/128] fp32
  *   topk_ids        [num_tokens][top_k] global expert ids. One outside [0, n_ranks *

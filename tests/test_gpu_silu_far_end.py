@@ -5,6 +5,8 @@ import pytest
 import torch
 
 import rows_reference as ref
+from rows_reference import BF16, E4M3, F32
+from test_gpu_layer_few import Few
 from test_gpu_swiglu_e4m3 import REL, call
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +63,36 @@ def test_products_near_the_largest():
     v[0, 517] = torch.inf  # (fp32: 2^128)
     ref.check_e4m3(q, s, v, REL)
     assert s.isnan().sum() == 1 and s[0, 4].isnan()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("gate", GATES)
+def test_layer_of_a_few_tokens(fp8, gate):
+    """One expert whose gates are all `gate` and whose second matrix is of 2^100."""
+    H = I = 128
+    f = Few(2, 1, 1, H, I, fp8=fp8)
+    f.gates.fill_(1)
+    for w in (f.x, f.W1):
+        w.copy_(torch.zeros(w.shape))
+    f.x[:, :2] = 1
+    f.W1[0, :I, 0] = -1 if fp8 else gate
+    up = 1 + torch.arange(I) % 8 / 8
+    f.W1[0, I:, 1] = up.to(f.W1.dtype).cuda()
+    w2 = 1 + torch.randint(0, 8, (H, I), generator=torch.Generator().manual_seed(0)) / 8
+    f.W2[0] = (w2 if fp8 else w2 * 2.0 ** 100).to(f.W2.dtype).cuda()
+    if fp8:
+        f.xs.fill_(1)
+        f.w1s.copy_(torch.tensor([-gate, 1.0]).view(1, 2, 1))
+        f.w2s.fill_(2.0 ** 100)
+    f.call()
+    torch.cuda.synchronize()
+    assert int(f.status) == 0
+    x = torch.tensor(gate, dtype=torch.float64)
+    a = (x * torch.sigmoid(x) * up.double())  # (the first product has one term a value: exact)
+    step = E4M3 * a.abs() + 2.0 ** -10 * ref.scales(a[None])[0] if fp8 else BF16 * a.abs()
+    want = 2.0 ** 100 * (w2.double() @ a)
+    off = 2.0 ** 100 * (w2.double() @ (step + (REL + (I + 8) * F32) * a.abs()))
+    got = f.out[0].double().cpu()
+    assert (got != 0).all()
+    assert ((got - want).abs() <= BF16 * (want.abs() + off) + off).all()
+    assert torch.equal(f.out[0], f.out[1])
