@@ -793,7 +793,7 @@ cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t s)
     // 4 waves of blocks (71.6 in one, 77 in 16), an fp32 one 96 in 8 (112 in one), 4096 wide 38.6 in
     // 2 (41.9 in one). Without a residual one wave is best (7168 wide 38.4, two 40.2).
     const int resident = f.per_sm * num_sms, rows = resident * (p.residual_bf16 ? 6 : 3);
-    const int waves = !p.residual || p.T < rows ? 1 : (p.T + rows / 2) / rows;
+    const int waves = !p.residual || p.T < rows ? 1 : static_cast<int>((int64_t{p.T} + rows / 2) / rows);
     const int most = resident * waves;
     const unsigned grid = p.T < most ? p.T : most;
     if (whole) {
