@@ -750,9 +750,9 @@ struct Form {
 // `two_upto`: the longest rows of two pieces a thread.
 // Blocks of an SM go by the registers that the kernels' launch bounds allow a thread, 64 or (`regs`
 // for two pieces, 128 for four) more: blocks past what is resident would begin when the others end.
-Form form_for(int hidden, int value_bytes, int two_upto, int regs, int stages)
+constexpr Form form_for(int hidden, int value_bytes, int two_upto, int regs, int stages)
 {
-    Form f;
+    Form f{};
     f.pieces = hidden <= 1024 ? 1 : hidden <= two_upto ? 2 : 4;
     const int per_thread = f.pieces * kPiece;
     f.threads = ((hidden + per_thread - 1) / per_thread + 31) / 32 * 32;
@@ -765,6 +765,32 @@ Form form_for(int hidden, int value_bytes, int two_upto, int regs, int stages)
     f.stages = f.stages > stages ? stages : f.stages;
     return f;
 }
+
+// The forms of both calls' whole rows, and the rows that their kernels keep under way: as many as fit, but
+// for the longest rows three (the gradient: two).
+constexpr Form norm_form(int hidden, int value_bytes) { return form_for(hidden, value_bytes, 8192, 64, 3); }
+constexpr int norm_stages(const Form &f, bool bf16) { return f.pieces == 1 || bf16 || f.stages > 2 ? 3 : 2; }
+
+// (the bytes as with dsum, where there is none, too: the same order of dweight's sum)
+// Two rows under way: three took 8192 x 7168 in fp32 from 123 to 138 us, 8192 x 4096 in bf16 from 46 to 51.
+constexpr Form backward_form(int hidden, int h_bytes) { return form_for(hidden, 2 + h_bytes * 2, 4096, 85, 2); }
+constexpr int backward_stages(const Form &f, bool bf16) { return f.pieces <= 2 || bf16 || f.stages > 1 ? 2 : 1; }
+
+// Every row that a kernel keeps under way has its place in shared memory.
+constexpr bool rows_fit()
+{
+    for (int hidden = kPiece; hidden <= EP_MAX_NORM_HIDDEN; hidden += kPiece)
+        for (int bytes = 2; bytes <= 4; bytes += 2) {  // of the residual stream's values
+            const Form alone = norm_form(hidden, 2), beside = norm_form(hidden, 2 + bytes);
+            const Form back = backward_form(hidden, bytes);
+            const bool bf16 = bytes == 2;
+            if (alone.stages < norm_stages(alone, bf16) || beside.stages < norm_stages(beside, bf16) ||
+                back.stages < backward_stages(back, bf16))
+                return false;
+        }
+    return true;
+}
+static_assert(rows_fit(), "the rows under way");
 
 template <typename Kern, typename... Args>
 cudaError_t launch_rows(Kern kern, int threads, int smem, unsigned grid, cudaStream_t s, const Args &...args)
@@ -787,7 +813,7 @@ cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t s)
                        whole_pieces(p.residual, p.residual_stride, rb) && whole_pieces(p.sum, p.sum_stride, rb) &&
                        whole_pieces(p.y, p.y_stride, 2) && reinterpret_cast<uintptr_t>(p.q) % 8 == 0;
     const int bytes = 2 + (p.residual ? rb : 0);
-    const Form f = form_for(p.hidden, bytes, 8192, 64, 3);
+    const Form f = norm_form(p.hidden, bytes);
     // Of rows with a residual a block takes about 6 (fp32: 3), as the SMs' shares of the bandwidth are
     // not equal and new blocks go to those that are ahead: 8192 x 7168 beside a bf16 residual 65 us in
     // 4 waves of blocks (71.6 in one, 77 in 16), an fp32 one 96 in 8 (112 in one), 4096 wide 38.6 in
@@ -798,14 +824,14 @@ cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t s)
     const unsigned grid = p.T < most ? p.T : most;
     if (whole) {
         // (one row a block needs no second: no attribute to set, a tenth of a small call's host time)
-        const int smem = (p.T == static_cast<int>(grid) ? 1 : f.stages) * f.threads * f.pieces * kPiece * bytes;
+        const int stages = norm_stages(f, p.residual_bf16);
+        const int smem = (p.T == static_cast<int>(grid) ? 1 : stages) * f.threads * f.pieces * kPiece * bytes;
         auto go = [&](auto bf16) {
             constexpr bool B = decltype(bf16)::value;
-            // (three rows fit but for the longest of either form beside an fp32 residual)
-            constexpr int two = B ? 3 : 2;
+            constexpr int two = B ? 3 : 2;  // (norm_stages)
             const auto kern = f.pieces == 1   ? norm_kernel<B, 1, 3>
-                              : f.pieces == 2 ? (f.stages == 2 ? norm_kernel<B, 2, two> : norm_kernel<B, 2, 3>)
-                                              : (f.stages == 2 ? norm_kernel<B, 4, two> : norm_kernel<B, 4, 3>);
+                              : f.pieces == 2 ? (stages == 2 ? norm_kernel<B, 2, two> : norm_kernel<B, 2, 3>)
+                                              : (stages == 2 ? norm_kernel<B, 4, two> : norm_kernel<B, 4, 3>);
             return launch_rows(kern, f.threads, smem, grid, s, p);
         };
         return p.residual_bf16 ? go(std::true_type()) : go(std::false_type());
@@ -835,24 +861,22 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, int num_sms, cudaS
     const bool whole = p.hidden % kPiece == 0 && whole_pieces(p.h, p.h_stride, hb) &&
                        whole_pieces(p.dy, p.dy_stride, 2) && whole_pieces(p.dsum, p.dsum_stride, hb) &&
                        whole_pieces(p.dh, p.dh_stride, hb) && whole_pieces(p.dx, p.dx_stride, 2);
-    // (as with dsum, where there is none, too: the same order of dweight's sum)
-    // Two rows under way: three took 8192 x 7168 in fp32 from 123 to 138 us, 8192 x 4096 in bf16 from 46 to 51.
-    const Form f = form_for(p.hidden, 2 + hb * 2, 4096, 85, 2);
+    const Form f = backward_form(p.hidden, hb);
     int most = f.per_sm * num_sms;
     if (p.dweight && most > part_blocks(p.hidden))  // (rows alone: 8192 x 512 12.1 us with this limit, 8.2 without)
         most = part_blocks(p.hidden);
     const unsigned grid = p.T < most ? p.T : most;
     cudaError_t e;
     if (whole) {
-        const int smem = (p.T == static_cast<int>(grid) ? 1 : f.stages) * f.threads * f.pieces * kPiece *
+        const int stages = backward_stages(f, p.h_bf16);
+        const int smem = (p.T == static_cast<int>(grid) ? 1 : stages) * f.threads * f.pieces * kPiece *
                          (2 + hb * (p.dsum ? 2 : 1));
         auto go = [&](auto bf16) {
             constexpr bool B = decltype(bf16)::value;
-            // (two rows fit but for the longest in fp32)
-            constexpr int one = B ? 2 : 1;
+            constexpr int one = B ? 2 : 1;  // (backward_stages)
             const auto kern = f.pieces == 1   ? norm_backward_kernel<B, 1, 2>
                               : f.pieces == 2 ? norm_backward_kernel<B, 2, 2>
-                              : f.stages == 1 ? norm_backward_kernel<B, 4, one>
+                              : stages == 1   ? norm_backward_kernel<B, 4, one>
                                               : norm_backward_kernel<B, 4, 2>;
             return launch_rows(kern, f.threads, smem, grid, s, p);
         };
