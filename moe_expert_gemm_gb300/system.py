@@ -509,7 +509,8 @@ class EpSystem:
         [max_tokens][H] with scales [max_tokens][H/128] (``add_rmsnorm``'s q and q_scales), its
         experts' weights W1 [E_l][2I][H] (gate rows first) and W2 [E_l][H][I] in e4m3 with scales
         of 128x128 blocks; H = N and I = K, H a multiple of 512 (the dispatch moves the scales'
-        rows in pieces of 16 bytes), I of 128. Allocates the layer's buffers; after ``plan``."""
+        rows in pieces of 16 bytes), I of 128. Allocates the layer's buffers, on torch's current
+        stream, but fills nothing; after ``plan``."""
         H, I = self.N, self.K
         if self.dtype != "fp8_1d2d" or H % 512 or I % 128:
             raise ValueError(f"an fp8 layer of dtype {self.dtype}, H = {H}, I = {I}")
@@ -518,7 +519,9 @@ class EpSystem:
         self._check_fp8_weights("W1", W1, w1_scales, 2 * I, H)
         self._check_fp8_weights("W2", W2, w2_scales, H, I)
         dev, rows = self.device, max(self.plans[rank]["capacity"], 1)
-        empty = lambda cols, dtype: torch.zeros((rows, cols), dtype=dtype, device=dev)
+        # (a fill could land on a call's rows where that goes to another stream; no row is read
+        # before it is written but by tiles that run past the last one, and those are not kept)
+        empty = lambda cols, dtype: torch.empty((rows, cols), dtype=dtype, device=dev)
         self.layer_fp8[rank] = dict(q=q, q_scales=q_scales, W1=W1, w1_scales=w1_scales,
                                     A_in=empty(H, torch.uint8), in_scales=empty(H // 128, torch.float32),
                                     G=empty(2 * I, torch.bfloat16))
