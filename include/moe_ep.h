@@ -790,7 +790,9 @@ int ep_swiglu_e4m3(const ep_config *cfg, const ep_swiglu_e4m3_args *args, ep_str
  *                   large enough for (fewer tokens, say). Calls that may run at the same time
  *                   need one each.
  *   status          EP_STATUS_ROUTING as above; EP_STATUS_TIMEOUT if a bounded wait inside a
- *                   kernel ran out
+ *                   kernel ran out: out is not to be used then, and the workspace is zeroed before
+ *                   its next call
+ *   timeout_ns      limit of each bounded wait (0: 2 s)
  * The weights of an expert without tokens are not read. Sums are taken in a fixed order: a
  * call's result depends on its inputs alone (and on the GPU's number of SMs), not on timing.
  */
@@ -809,6 +811,7 @@ typedef struct {
     void *workspace;
     int64_t workspace_bytes;
     uint32_t *status;
+    int64_t timeout_ns;
 } ep_layer_few_args;
 
 /* Workspace bytes of ep_layer_few calls with this configuration. Host only. */

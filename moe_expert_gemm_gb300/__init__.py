@@ -148,7 +148,8 @@ class ep_swiglu_e4m3_args(ctypes.Structure):
 class ep_layer_few_args(ctypes.Structure):
     _fields_ = [("x", _vp), ("x_scales", _vp), ("topk_ids", _vp), ("gates", _vp), ("W1", _vp),
                 ("w1_scales", _vp), ("W2", _vp), ("w2_scales", _vp), ("out", _vp),
-                ("workspace", _vp), ("workspace_bytes", _c_i64), ("status", _vp)]
+                ("workspace", _vp), ("workspace_bytes", _c_i64), ("status", _vp),
+                ("timeout_ns", _c_i64)]
 
 
 EP_IPC_HANDLE_BYTES = 64

@@ -993,6 +993,7 @@ int ep_layer_few(const ep_config *cfg, const ep_layer_few_args *a, ep_stream_t s
     p.out = static_cast<uint8_t *>(a->out);
     p.workspace = static_cast<uint8_t *>(a->workspace);
     p.status = a->status;
+    p.timeout_ns = a->timeout_ns > 0 ? static_cast<uint64_t>(a->timeout_ns) : kDefaultTimeoutNs;
     const CUtensorMapDataType dt =
         p.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const uint64_t elem = p.fp8 ? 1 : 2, H = p.H, I = p.I;

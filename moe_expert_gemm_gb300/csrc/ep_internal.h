@@ -251,6 +251,7 @@ struct FewParams {
     uint8_t *out;
     uint8_t *workspace;
     uint32_t *status;
+    uint64_t timeout_ns;
 };
 
 // Steps of 128 bytes along k: boxes of 128 weight rows (of one expert), of few_columns() tokens,

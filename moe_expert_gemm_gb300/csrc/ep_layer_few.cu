@@ -48,7 +48,7 @@ constexpr int kEpilogueWarps = 8;  // two groups of four
 constexpr int kThreads = 32 * (4 + kEpilogueWarps);
 constexpr int kEpilogueThreads = 32 * kEpilogueWarps;
 constexpr int kPartBase = 4096;  // of the workspace; counters before it
-constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr uint64_t kEndNs = 2000000000ull;  // for what is under way to end, whatever the call's limit
 static_assert(kMaxBlocks * 4 <= kPartBase, "counters");
 
 // How the list is cut. Steps that the joining of cut units is worth, and the fewest steps that a cut
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (skip > 0) {
                         --skip;
                     } else {
-                        if (!mbar_wait(&sh.empty[stage], phase ^ 1, kTimeoutNs, abort_flag)) {
+                        if (!mbar_wait(&sh.empty[stage], phase ^ 1, p.timeout_ns, abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok)
                 give_up(p, sh);
-            wait_for_copies<kStages>(sh.full, issued, kTimeoutNs);
+            wait_for_copies<kStages>(sh.full, issued, kEndNs);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -473,9 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (fresh) {
                         const int n = DOWN ? __popcll(sh.tokens(sh.active[place])) : p.T;
                         idesc = make_idesc(FP8 ? 0u : 1u, kTile, (n + 15) / 16 * 16);
-                        ok = mbar_wait(&sh.sums_empty[buf], buf_phase ^ 1, kTimeoutNs, abort_flag);
+                        ok = mbar_wait(&sh.sums_empty[buf], buf_phase ^ 1, p.timeout_ns, abort_flag);
                     }
-                    ok = ok && mbar_wait(&sh.full[stage], phase, kTimeoutNs, abort_flag);
+                    ok = ok && mbar_wait(&sh.full[stage], phase, p.timeout_ns, abort_flag);
                     if (!ok)
                         break;
                     tc_fence_after();
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // every product issued has ended once this arrives
             mma_commit(&sh.drained);
             volatile int no_abort = 0;
-            mbar_wait(&sh.drained, 0, kTimeoutNs, &no_abort);
+            mbar_wait(&sh.drained, 0, kEndNs, &no_abort);
         }
         __syncwarp();
     } else if (warp >= 4) {
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float factor[2];
                 if constexpr (FP8) {
                     ok = __all_sync(0xffffffffu,
-                                    mbar_wait(&sh.scales.full[sc], sc_phase, kTimeoutNs, abort_flag));
+                                    mbar_wait(&sh.scales.full[sc], sc_phase, p.timeout_ns, abort_flag));
                     if (!ok)
                         break;
 #pragma unroll
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     advance(sc, sc_phase, kScaleStages);
                 }
                 ok = __all_sync(0xffffffffu,
-                                mbar_wait(&sh.sums_full[buf], buf_phase, kTimeoutNs, abort_flag));
+                                mbar_wait(&sh.sums_full[buf], buf_phase, p.timeout_ns, abort_flag));
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -879,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int tile = DOWN ? seg.unit : seg.unit % tiles;
                 for (int s = seg.s0; s < seg.s1; ++s) {
                     ok = __all_sync(0xffffffffu,
-                                    mbar_wait(&sh.scales.empty[sc], sc_phase ^ 1, kTimeoutNs, abort_flag));
+                                    mbar_wait(&sh.scales.empty[sc], sc_phase ^ 1, p.timeout_ns, abort_flag));
                     if (!ok)
                         break;
                     const int64_t e = sh.active[place];

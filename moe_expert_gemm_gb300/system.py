@@ -576,7 +576,9 @@ class EpSystem:
         [T][N] of rank ``source`` (``rank`` itself if not given) with that rank's routing and gates
         (``route``, or ``set_routing`` and ``set_gates``): bf16, or in an fp8 system e4m3 with scales
         [T][N/128]. With one rank that is the layer; the ranks' parts add up to it. One call of a
-        rank at a time (they share its workspace)."""
+        rank at a time (they share its workspace). After a call that set
+        EP_STATUS_TIMEOUT (``timeout_ns`` of the system is the limit of its waits) ``reset_layer_few``
+        comes before the rank's next one."""
         L, T, N = self.layer_few_ops[rank], self.T, self.N
         source = rank if source is None else source
         if self.dtype == "bf16":
@@ -592,8 +594,14 @@ class EpSystem:
                               w1_scales=ptr(L["w1_scales"]), W2=ptr(L["W2"]),
                               w2_scales=ptr(L["w2_scales"]), out=ptr(out),
                               workspace=ptr(L["workspace"]), workspace_bytes=L["workspace"].numel(),
-                              status=self.status.data_ptr() + 4 * STATUS_FEW)
+                              status=self.status.data_ptr() + 4 * STATUS_FEW,
+                              timeout_ns=self.timeout_ns)
         ep_layer_few(self.cfg(rank), a, stream)
+
+    def reset_layer_few(self, rank: int, stream=None):
+        """The rank's workspace as ``set_layer_few`` leaves it, the same memory."""
+        with self._on(stream):
+            self.layer_few_ops[rank]["workspace"].zero_()
 
     def send_traced(self, rank: int, epoch: int, records: int = 64, stream=None):
         """One send with per-tile timestamps; returns the decoded trace."""
