@@ -784,19 +784,21 @@ int ep_swiglu_e4m3(const ep_config *cfg, const ep_swiglu_e4m3_args *args, ep_str
  *   W2              [E_l][N][K], 16-byte aligned
  *   w2_scales       EP_FP8_1D2D only: [E_l][N/128][K/128] fp32
  *   out             [num_tokens][N] bf16 out, every row (zeros where a token has no expert here)
- *   workspace       device memory of ep_layer_few_sizes bytes, 16-byte aligned, zero before the
- *                   first call that uses it; a call that ends without EP_STATUS_TIMEOUT leaves
- *                   it ready for the next, of this configuration or of any other that it is
- *                   large enough for (fewer tokens, say). Calls that may run at the same time
+ *   workspace       device memory of ep_layer_few_sizes bytes, 16-byte aligned, its first
+ *                   EP_FEW_COUNTER_BYTES zero before the first call that uses it (the rest of any
+ *                   contents); a call that ends without EP_STATUS_TIMEOUT leaves it ready for the
+ *                   next, of this configuration or of any other that it is large enough for (fewer
+ *                   tokens, say). Calls that may run at the same time
  *                   need one each.
  *   status          EP_STATUS_ROUTING as above; EP_STATUS_TIMEOUT if a bounded wait inside a
- *                   kernel ran out: out is not to be used then, and the workspace is zeroed before
- *                   its next call
+ *                   kernel ran out: out is not to be used then, and those bytes are zeroed before
+ *                   the workspace's next call
  *   timeout_ns      limit of each bounded wait (0: 2 s)
  * The weights of an expert without tokens are not read. Sums are taken in a fixed order: a
  * call's result depends on its inputs alone (and on the GPU's number of SMs), not on timing.
  */
 #define EP_MAX_FEW_TOKENS 64
+#define EP_FEW_COUNTER_BYTES 4096
 
 typedef struct {
     const void *x;

@@ -48,6 +48,7 @@ EP_ROWS_F32 = 0
 EP_ROWS_BF16 = 1
 EP_MAX_NORM_HIDDEN = 16384
 EP_MAX_FEW_TOKENS = 64
+EP_FEW_COUNTER_BYTES = 4096
 
 _c_i32, _c_i64, _c_u64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p
 
@@ -358,7 +359,7 @@ def ep_swiglu_e4m3(cfg: ep_config, args: ep_swiglu_e4m3_args, stream=None) -> in
 
 
 def ep_layer_few_sizes(cfg: ep_config) -> int:
-    """Workspace bytes of ep_layer_few (zero the workspace before its first use)."""
+    """Workspace bytes of ep_layer_few (zero the first EP_FEW_COUNTER_BYTES before its first use)."""
     out = _c_i64(0)
     _check(load().ep_layer_few_sizes(ctypes.byref(cfg), ctypes.byref(out)), "ep_layer_few_sizes")
     return int(out.value)

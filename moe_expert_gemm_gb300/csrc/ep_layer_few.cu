@@ -47,7 +47,7 @@ constexpr int kMaxRows = EP_MAX_FEW_TOKENS * 32;
 constexpr int kEpilogueWarps = 8;  // two groups of four
 constexpr int kThreads = 32 * (4 + kEpilogueWarps);
 constexpr int kEpilogueThreads = 32 * kEpilogueWarps;
-constexpr int kPartBase = 4096;  // of the workspace; counters before it
+constexpr int kPartBase = EP_FEW_COUNTER_BYTES;  // of the workspace; counters before it
 constexpr uint64_t kEndNs = 2000000000ull;  // for what is under way to end, whatever the call's limit
 static_assert(kMaxBlocks * 4 <= kPartBase, "counters");
 

@@ -14,8 +14,8 @@ import contextlib
 import numpy as np
 import torch
 
-from . import (EP_ACT_NONE, EP_ACT_SWIGLU, EP_BF16, EP_FP8_1D2D, EP_LOGITS_BF16, EP_LOGITS_F32,
-               EP_ROWS_BF16, EP_ROWS_F32, EP_SCORE_SOFTMAX, EP_W4_E2M1, EP_W4_INT, ep_add_rmsnorm,
+from . import (EP_ACT_NONE, EP_ACT_SWIGLU, EP_BF16, EP_FEW_COUNTER_BYTES, EP_FP8_1D2D, EP_LOGITS_BF16,
+               EP_LOGITS_F32, EP_ROWS_BF16, EP_ROWS_F32, EP_SCORE_SOFTMAX, EP_W4_E2M1, EP_W4_INT, ep_add_rmsnorm,
                ep_add_rmsnorm_args, ep_add_rmsnorm_backward, ep_add_rmsnorm_backward_args,
                ep_add_rmsnorm_backward_sizes, ep_combine_args, ep_combine_backward,
                ep_combine_backward_args, ep_combine_reduce, ep_config, ep_dispatch_args,
@@ -565,10 +565,10 @@ class EpSystem:
                 raise ValueError("fp8 weights come with their scales")
             self._check_fp8_weights("W1", W1, w1_scales, 2 * I, H)
             self._check_fp8_weights("W2", W2, w2_scales, H, I)
-        self.layer_few_ops[rank] = dict(
-            W1=W1, W2=W2, w1_scales=w1_scales, w2_scales=w2_scales,
-            workspace=torch.zeros(ep_layer_few_sizes(self.cfg(rank)), dtype=torch.uint8,
-                                  device=self.device))
+        workspace = torch.empty(ep_layer_few_sizes(self.cfg(rank)), dtype=torch.uint8, device=self.device)
+        workspace[:EP_FEW_COUNTER_BYTES].zero_()
+        self.layer_few_ops[rank] = dict(W1=W1, W2=W2, w1_scales=w1_scales, w2_scales=w2_scales,
+                                        workspace=workspace)
 
     def layer_few(self, rank: int, x: torch.Tensor, out: torch.Tensor, x_scales=None, source=None,
                   stream=None):
@@ -599,9 +599,9 @@ class EpSystem:
         ep_layer_few(self.cfg(rank), a, stream)
 
     def reset_layer_few(self, rank: int, stream=None):
-        """The rank's workspace as ``set_layer_few`` leaves it, the same memory."""
+        """The rank's workspace ready as ``set_layer_few`` leaves it, the same memory."""
         with self._on(stream):
-            self.layer_few_ops[rank]["workspace"].zero_()
+            self.layer_few_ops[rank]["workspace"][:EP_FEW_COUNTER_BYTES].zero_()
 
     def send_traced(self, rank: int, epoch: int, records: int = 64, stream=None):
         """One send with per-tile timestamps; returns the decoded trace."""
