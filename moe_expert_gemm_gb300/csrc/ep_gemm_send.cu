@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(224 + 32 * SEND, 1)
             volatile int no_abort = 0;
             for (int s = 0; s < STAGES; ++s)
                 if (used_mask & (1u << s))
-                    mbar_wait(&full[s], (last_parity >> s) & 1u, p.timeout_ns, &no_abort);
+                    mbar_wait(&full[s], (last_parity >> s) & 1u, kEndNs, &no_abort);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(224 + 32 * SEND, 1)
             // every MMA issued so far has finished once this commit lands
             mma_commit(mma_done);
             volatile int no_abort = 0;
-            mbar_wait(mma_done, 0, p.timeout_ns, &no_abort);
+            mbar_wait(mma_done, 0, kEndNs, &no_abort);
         }
         __syncwarp();
     } else if (warp < 6) {

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(352, 1)
             volatile int no_abort = 0;
             for (int s = 0; s < STAGES; ++s)
                 if (used_mask & (1u << s))
-                    fp8_wait(&full[s], (last_parity >> s) & 1u, p.timeout_ns, &no_abort);
+                    fp8_wait(&full[s], (last_parity >> s) & 1u, kEndNs, &no_abort);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(352, 1)
                 raise_abort(p.status, abort_flag);
             mma_commit(mma_done);
             volatile int no_abort = 0;
-            fp8_wait(mma_done, 0, p.timeout_ns, &no_abort);
+            fp8_wait(mma_done, 0, kEndNs, &no_abort);
         }
         __syncwarp();
     } else if (warp == 2) {

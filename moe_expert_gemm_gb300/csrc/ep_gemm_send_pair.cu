@@ -180,11 +180,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224 + 32 * SEND, 1)
                 raise_abort(p.status, abort_flag);
             volatile int no_abort = 0;
             if (leader) {
-                // the even CTA's full barriers count both CTAs' loads
-                for (int s = 0; s < STAGES; ++s)
+                // the even CTA's full barriers count both CTAs' loads (the odd one may not have
+                // issued its part of the last stages: kEndNs for all of them)
+                const uint64_t t0 = globaltimer_ns();
+                for (int s = 0; s < STAGES; ++s) {
+                    const uint64_t spent = globaltimer_ns() - t0;
                     if (used_mask & (1u << s))
-                        mbar_wait_cluster(&full[s], (last_parity >> s) & 1u, p.timeout_ns,
-                                          &no_abort);
+                        mbar_wait_cluster(&full[s], (last_parity >> s) & 1u,
+                                          spent < kEndNs ? kEndNs - spent : 0, &no_abort);
+                }
             } else if (!ok) {
                 // give loads already issued time to land before this CTA may exit
                 const uint64_t t0 = globaltimer_ns();
@@ -237,7 +241,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224 + 32 * SEND, 1)
                 raise_abort(p.status, abort_flag);
             mma_commit_pair(mma_done, 0x1);
             volatile int no_abort = 0;
-            mbar_wait_cluster(mma_done, 0, p.timeout_ns, &no_abort);
+            mbar_wait_cluster(mma_done, 0, kEndNs, &no_abort);
         }
         __syncwarp();
     } else if (warp < 6) {

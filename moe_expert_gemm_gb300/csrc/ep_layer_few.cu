@@ -48,7 +48,6 @@ constexpr int kEpilogueWarps = 8;  // two groups of four
 constexpr int kThreads = 32 * (4 + kEpilogueWarps);
 constexpr int kEpilogueThreads = 32 * kEpilogueWarps;
 constexpr int kPartBase = EP_FEW_COUNTER_BYTES;  // of the workspace; counters before it
-constexpr uint64_t kEndNs = 2000000000ull;  // for what is under way to end, whatever the call's limit
 static_assert(kMaxBlocks * 4 <= kPartBase, "counters");
 
 // How the list is cut. Steps that the joining of cut units is worth, and the fewest steps that a cut

@@ -76,6 +76,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
     }
 }
 
+// What a block that gives up has under way (copies, products) ends within this, whatever the call's own
+// limit: it takes some microseconds, and is waited for.
+constexpr uint64_t kEndNs = 2000000000ull;
+
 // A ring's copies land before the block's shared memory goes away: waits, timeout_ns at most, for
 // the last copies into each of its N stages, of `issued` copies one stage after the other, by the barriers
 // that count their bytes (and other warps' arrivals, which may not come any more: then for as long as it

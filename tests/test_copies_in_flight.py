@@ -46,3 +46,16 @@ def test_the_producer_waits_whether_or_not_it_gave_up(name, source):
     # on every way out
     issued = body[:calls[0]].rfind("int issued = 0;")
     assert issued > 0 and not re.search(r"\breturn;", body[issued:calls[0]])
+
+
+@pytest.mark.parametrize("name,source", [("few_kernel", "ep_layer_few.cu"), ("gemm_send_bf16_kernel", "ep_gemm_send.cu"),
+                                         ("gemm_send_fp8_kernel", "ep_gemm_send_fp8.cu"),
+                                         ("gemm_send_bf16_pair_kernel", "ep_gemm_send_pair.cu")])
+def test_a_calls_short_limit_does_not_cut_that_wait(name, source):
+    """The limit of a call's waits may be a nanosecond; what a block has under way ends all the same: waits that
+    nobody may abort have a limit of their own."""
+    body = dict(kernels(os.path.join(CSRC, source)))[name]
+    waits = re.findall(r"\w+_wait\w*\(([^;]*?)&no_abort\)", body) + re.findall(r"wait_for_copies<\w+>\(([^;]*?)\);", body)
+    assert len(waits) == 2, waits
+    for args in waits:
+        assert "kEndNs" in args and "p.timeout_ns" not in args, args
