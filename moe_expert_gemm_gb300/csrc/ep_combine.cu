@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
             const float *g = p.gates + tt[uu] * K;
 #pragma unroll
             for (int j = 0; j < K; ++j)
-                accumulate_row(acc, __ldg(g + j), r[uu][j]);
+                accumulate_row(acc, g[j], r[uu][j]);
             store_out(p, tt[uu], vv[uu], acc);
         }
     }
@@ -179,7 +179,7 @@ __device__ __forceinline__ bool token_arrived(const CombineParams &p, int64_t t,
     const int n_experts = p.n_ranks * p.El;
     bool ok = true;
     for (int j = lane; j < k; j += 32) {
-        const int g = __ldg(p.topk_ids + t * k + j);
+        const int g = p.topk_ids[t * k + j];
         if (g < 0 || g >= n_experts) {
             atomicOr(p.status, EP_STATUS_ROUTING);
             ok = false;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel_per_expert(con
                             acc[c] = 0.f;
 #pragma unroll
                         for (int jj = 0; jj < K; ++jj)
-                            accumulate_row(acc, __ldg(g + jj), r[uu][jj]);
+                            accumulate_row(acc, g[jj], r[uu][jj]);
                         store_out(p, t, vv[uu], acc);
                     }
                 } else {
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel_per_expert(con
 #pragma unroll
                         for (int jj = 0; jj < kLoads; ++jj)
                             if (j + jj < k)
-                                accumulate_row(acc, __ldg(g + j + jj), rr[jj]);
+                                accumulate_row(acc, g[j + jj], rr[jj]);
                     }
                     store_out(p, t, vv[0], acc);
                 }
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel_any(const Comb
 #pragma unroll
             for (int jj = 0; jj < kLoads; ++jj)
                 if (j + jj < k)
-                    accumulate_row(acc, __ldg(g + j + jj), r[jj]);
+                    accumulate_row(acc, g[j + jj], r[jj]);
         }
         store_out(p, t, v, acc);
     }

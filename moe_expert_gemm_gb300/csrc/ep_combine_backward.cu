@@ -37,7 +37,7 @@ __device__ __forceinline__ float row_pieces(const uint4 *dout, const uint4 *row,
         for (int u = 0; u < kUnroll; ++u) {
             const int v = v0 + u * step;
             if (v < pieces) {
-                d[u] = __ldg(dout + v);
+                d[u] = dout[v];
                 if (DGATES)
                     r[u] = __ldcs(row + v);
             }
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(32 * kCombineBwdWarps)
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * (kCombineBwdWarps / WPR) + (WPR == 1 ? warp : 0);
          row < rows; row += stride) {
         const int64_t t = row / p.top_k;
-        const float g = DROWS ? __ldg(p.gates + row) : 0.f;
+        const float g = DROWS ? p.gates[row] : 0.f;
         float sum = row_pieces<DGATES, DROWS>(
             reinterpret_cast<const uint4 *>(p.dout) + t * pieces,
             reinterpret_cast<const uint4 *>(p.recv_buf) + row * pieces,

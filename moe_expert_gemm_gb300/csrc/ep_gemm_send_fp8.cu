@@ -259,14 +259,14 @@ __global__ void __launch_bounds__(352, 1)
 #pragma unroll
             for (int j = 0; j < HC / 2; ++j)
                 acc[j] = 0ull;
-            float sa_next = __ldg(sa), sw_next = __ldg(sw);
+            float sa_next = *sa, sw_next = *sw;
             bool ok_t = push_ok;
             for (int kb = 0; kb < nkb && ok_t; ++kb, ++g) {
                 const float s = sa_next * sw_next;
                 const uint64_t s2 = pack_f32x2(__float_as_uint(s), __float_as_uint(s));
                 if (kb + 1 < nkb) {
-                    sa_next = __ldg(sa + kb + 1);
-                    sw_next = __ldg(sw + kb + 1);
+                    sa_next = sa[kb + 1];
+                    sw_next = sw[kb + 1];
                 }
                 const uint32_t pb = g % NBUF, pph = (g / NBUF) & 1u;
                 ok_t = fp8_wait(&pfull[pb], pph, p.timeout_ns, abort_flag);

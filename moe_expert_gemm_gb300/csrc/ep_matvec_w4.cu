@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                             __shfl_sync(0xffffffffu, mine, r0 + i));
                         v[i] = make_uint4(0, 0, 0, 0);
                         if (from && (VEC || k0 < p.K))
-                            v[i] = __ldg(from + k0 / 8);
+                            v[i] = from[k0 / 8];
                     }
                 };
                 load_rows(0);

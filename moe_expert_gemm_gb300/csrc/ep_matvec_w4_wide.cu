@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                     for (int i = i0; i < i0 + kLoads / 2; ++i)
                         if (from[i] && there)
-                            v[i] = __ldg(from[i] + at);
+                            v[i] = from[i][at];
                 };
                 load(0);
                 if (rows > kRows / 2)

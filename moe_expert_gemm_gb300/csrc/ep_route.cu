@@ -192,7 +192,7 @@ __device__ __noinline__ void route_token(const RouteParams &p, int64_t t, uint32
         const float x = Logit<T>::load(l + i);
         float v = x;
         if (p.bias)
-            v = (p.score == EP_SCORE_SIGMOID ? score[i] : score[i] / total) + __ldg(p.bias + i);
+            v = (p.score == EP_SCORE_SIGMOID ? score[i] : score[i] / total) + p.bias[i];
         key[i] = x > Logit<T>::lowest ? choice_key(v) : kKeyMasked;
     }
     __syncwarp();
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_warp_kernel(const __gr
         else if (BY == kBySoftmax || !p.renormalize)
             s = expf(cx - top) / total;
         if (BY != kByLogit)
-            cv = s + __ldg(p.bias + id);
+            cv = s + p.bias[id];
         order = static_cast<uint64_t>(choice_key(cv)) << 32 | ~static_cast<uint32_t>(id);
     }
     __syncwarp();
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(128) route_thread_kernel(const __grid_constant
     uint32_t key[EP];
 #pragma unroll
     for (int i = 0; i < EP; ++i) {
-        const float v = p.bias && i < E ? score(x[i]) + __ldg(p.bias + i) : x[i];
+        const float v = p.bias && i < E ? score(x[i]) + p.bias[i] : x[i];
         key[i] = i >= E ? kKeyOut : x[i] == -INFINITY ? kKeyMasked : choice_key(v);
     }
     float sx[EP], m = -INFINITY;  // logits of the chosen
@@ -702,8 +702,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
                 load_vec<W>(l + expert(i), y + i);
         }
     }
-    int id = lane < k ? __ldg(p.topk_ids + t * k + lane) : -1;
-    float dg = lane < k ? __ldg(p.dgates + t * k + lane) : 0.f;
+    int id = lane < k ? p.topk_ids[t * k + lane] : -1;
+    float dg = lane < k ? p.dgates[t * k + lane] : 0.f;
     if (lane < k && (id < 0 || id >= E)) {
         atomicOr(p.status, EP_STATUS_ROUTING);
         id = -1;
@@ -777,8 +777,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const __g
     if (t >= p.T)
         return;
     const T *l = static_cast<const T *>(p.logits) + t * p.stride;
-    int id = lane < k ? __ldg(p.topk_ids + t * k + lane) : -1;
-    float dg = lane < k ? __ldg(p.dgates + t * k + lane) : 0.f;
+    int id = lane < k ? p.topk_ids[t * k + lane] : -1;
+    float dg = lane < k ? p.dgates[t * k + lane] : 0.f;
     if (lane < k && (id < 0 || id >= E)) {
         atomicOr(p.status, EP_STATUS_ROUTING);
         id = -1;

@@ -64,7 +64,7 @@ __device__ __forceinline__ void store_counts(const SendParams &p, const SinkShar
     int c[EP_MAX_RANKS];
 #pragma unroll
     for (int dst = 0; dst < EP_MAX_RANKS; ++dst)
-        c[dst] = dst < R ? (cached ? sh->counts[e * R + dst] : __ldg(p.send_counts + e * R + dst))
+        c[dst] = dst < R ? (cached ? sh->counts[e * R + dst] : p.send_counts[e * R + dst])
                          : 0;
 #pragma unroll
     for (int dst = 0; dst < EP_MAX_RANKS; ++dst) {
@@ -87,7 +87,7 @@ __device__ __forceinline__ void store_tagged_counts(const SendParams &p, const S
 #pragma unroll
     for (int dst = 0; dst < EP_MAX_RANKS; ++dst) {
         if (dst < R) {
-            const int c = cached ? sh->counts[e * R + dst] : __ldg(p.send_counts + e * R + dst);
+            const int c = cached ? sh->counts[e * R + dst] : p.send_counts[e * R + dst];
             st_relaxed_sys_u64(sh->cnt[dst] + static_cast<int64_t>(e) * R + p.my_rank,
                                tag | static_cast<uint32_t>(c));
         }
@@ -170,8 +170,8 @@ __device__ __forceinline__ void sink_prologue(const SendParams &p, SinkShared *s
     const int n_cnt = p.sink_enabled && El * p.n_ranks <= kCountCache ? El * p.n_ranks : 0;
     const int n_all = n_cnt > El + 1 ? n_cnt : El + 1;
     for (int i = threadIdx.x; i < n_all; i += blockDim.x) {
-        const int eo = i <= El ? __ldg(p.expert_offsets + i) : 0;
-        const int cn = i < n_cnt ? __ldg(p.send_counts + i) : 0;
+        const int eo = i <= El ? p.expert_offsets[i] : 0;
+        const int cn = i < n_cnt ? p.send_counts[i] : 0;
         if (i <= El)
             sh->eoff[i] = eo;
         if (i < n_cnt)
@@ -238,9 +238,9 @@ __device__ __forceinline__ uint8_t *resolve_row(const SendParams &p, const SinkS
     const int *seg = p.seg_offsets + c.e * (R + 1);
     int dst = -1;
     for (int rk = 0; rk < R; ++rk)
-        if (m >= __ldg(seg + rk) && m < __ldg(seg + rk + 1))
+        if (m >= seg[rk] && m < seg[rk + 1])
             dst = rk;
-    const int2 si = __ldg(reinterpret_cast<const int2 *>(p.src_info) + m);
+    const int2 si = reinterpret_cast<const int2 *>(p.src_info)[m];
     if (dst < 0 || si.x < 0 || si.x >= p.max_tokens || si.y < 0 || si.y >= p.top_k) {
         atomicOr(p.status, EP_STATUS_BOUNDS);
         return nullptr;

@@ -78,8 +78,8 @@ __device__ __forceinline__ void plan_run(const W4Params &p, RunInfo &sh, int til
 #pragma unroll
     for (int i = 0; i < kSets; ++i) {
         const int e = 32 * i + lane;
-        lo[i] = e < p.El ? __ldg(p.expert_offsets + e) : 0;
-        hi[i] = e < p.El ? __ldg(p.expert_offsets + e + 1) : 0;
+        lo[i] = e < p.El ? p.expert_offsets[e] : 0;
+        hi[i] = e < p.El ? p.expert_offsets[e + 1] : 0;
     }
     int units = 0;
     bool bad = false;
@@ -202,7 +202,7 @@ __device__ __forceinline__ const uint8_t *row_of(const W4Params &p, int m)
     if (p.A)
         return p.A + static_cast<int64_t>(m) * p.K * 2;
     // (tokens * top_k of all ranks fit 31 bits)
-    const uint32_t gi = static_cast<uint32_t>(__ldg(p.gather_idx + m));
+    const uint32_t gi = static_cast<uint32_t>(p.gather_idx[m]);
     const uint32_t Tk = static_cast<uint32_t>(p.T) * p.top_k;
     if (gi >= Tk * p.n_ranks)
         return nullptr;

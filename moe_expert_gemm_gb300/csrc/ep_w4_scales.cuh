@@ -31,14 +31,14 @@ struct Piece {
     __device__ __forceinline__ void load(const T *from, int have)
     {
         if constexpr (VEC && BYTES == 16)
-            *this = from_uint4(__ldg(reinterpret_cast<const uint4 *>(from)));
+            *this = from_uint4(*reinterpret_cast<const uint4 *>(from));
         else if constexpr (VEC && BYTES == 8) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(from));
+            const uint2 v = *reinterpret_cast<const uint2 *>(from);
             w[0] = v.x, w[1] = v.y;
         } else if constexpr (VEC && BYTES == 4)
-            w[0] = __ldg(reinterpret_cast<const uint32_t *>(from));
+            w[0] = *reinterpret_cast<const uint32_t *>(from);
         else if constexpr (VEC)
-            w[0] = __ldg(reinterpret_cast<const unsigned short *>(from));
+            w[0] = *reinterpret_cast<const unsigned short *>(from);
         else {  // the aligned words that hold some of it, shifted into place
             const uint64_t at = reinterpret_cast<uint64_t>(from);
             const uint32_t *word = reinterpret_cast<const uint32_t *>(at & ~3ull);
@@ -48,7 +48,7 @@ struct Piece {
             for (int i = 0; i <= kWords; ++i) {
                 in[i] = 0;
                 if (4 * i < end && (i < kWords || skip > 0))
-                    in[i] = __ldg(word + i);
+                    in[i] = word[i];
             }
 #pragma unroll
             for (int i = 0; i < kWords; ++i)
