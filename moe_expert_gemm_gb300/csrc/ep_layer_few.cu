@@ -27,9 +27,10 @@
 //  * The second kernel starts while the first one's last blocks finish: a block makes its plan
 //    and fills its ring with weights before it waits for the activations.
 //
-// Measured (GB300, weights' bytes of the copy bandwidth of 6.77 TB/s): a token with 2 of 8 experts of
-// 4096 x 14336 113 us, 92 %; 16 tokens, 8 of 32 of 7168 x 2048 in e4m3 210 us, 98 %; 64 tokens, 8 of 16
-// of 4096 x 2048 142 us, 84 %; 5 tokens, 3 of 12 of 1496 x 1000 23 us, of which the bytes are 8.
+// Measured (GB300, several boxes; weights' bytes of the copy bandwidth of 6.77 TB/s): a token with 2 of 8
+// experts of 4096 x 14336 113 to 116 us, 90 to 92 %; 16 tokens, 8 of 32 of 7168 x 2048 in e4m3 210 to 222 us,
+// 93 to 98 %; 64 tokens, 8 of 16 of 4096 x 2048 142 to 145 us, 82 to 84 %; 5 tokens, 3 of 12 of 1496 x 1000
+// 23 to 25 us, of which the bytes are 8.
 #include <type_traits>
 
 #include "ep_internal.h"
@@ -51,10 +52,11 @@ constexpr int kPartBase = EP_FEW_COUNTER_BYTES;  // of the workspace; counters b
 static_assert(kMaxBlocks * 4 <= kPartBase, "counters");
 
 // How the list is cut. Steps that the joining of cut units is worth, and the fewest steps that a cut
-// leaves a block: the last block of a unit adds a part of its tokens' sums for each of them. The
-// times are flat around both: over 90 shapes of 1 to 64 tokens the geometric mean lies 0.8 % under
-// that of half of sqrt(steps) for any number of tokens, 0.6 % under that of a joining worth 3
-// steps, 0.4 % under that of 0.1 + tokens / 64 below the root (a single shape up to 20 % either way).
+// leaves a block: the last block of a unit adds a part of its tokens' sums for each of them. A
+// compromise, which the times do not single out: over 90 shapes of 1 to 64 tokens the geometric mean lies
+// 0.8 % under that of half of sqrt(steps) for any number of tokens, 0.6 % under that of a joining worth 3
+// steps, 0.4 % under that of 0.1 + tokens / 64 below the root, while a single shape moves by up to 20 %
+// either way, and shapes that neither touches by some per cent from run to run.
 constexpr int kJoinSteps = 4;
 
 __device__ __forceinline__ int min_steps(int steps, int tokens)

@@ -17,8 +17,8 @@
 //    kernel adds the blocks'.
 //
 // Measured at 8192 x 7168 (GB300, of the copy bandwidth of 6.77 TB/s): beside a bf16 residual to e4m3
-// 64 us, 95 %; to bf16 73 us, 95 %; the gradient in bf16 with the residual's 74 us, 93 %, in fp32
-// 123 us, 99 %. Rows of other alignments, 4096 x 3675: 34 us, 53 %, the gradient 49 us, 37 %.
+// 63 us, 97 %; to bf16 73 us, 95 %; the gradient in bf16 with the residual's 74 us, 93 %, in fp32
+// 122 us, 99 %. Rows of other alignments, 4096 x 3675: 32 us, 55 %, the gradient 48 us, 37 %.
 #include <type_traits>
 
 #include "ep_internal.h"
@@ -36,8 +36,8 @@ static_assert(4 * kPiece * kMaxThreads == EP_MAX_NORM_HIDDEN, "a row in a block"
 constexpr int kSmemOfSm = 216 * 1024;  // for rows under way
 constexpr int kMaxPerSm = 16;          // blocks
 
-// Blocks that leave partial sums of dweight, at most. (Short rows want many: 8192 x 256 9.3 us, with 640
-// 12.5.)
+// Blocks that leave partial sums of dweight, at most. (Short rows want many: 8192 x 256 8.8 us, with 640
+// 12.5; 8192 x 2048 26.9, with 640 29.6.)
 __host__ __device__ constexpr int part_blocks(int hidden) { return hidden <= 2048 ? 1280 : 640; }
 
 // Sum over the block of two values, the same order for every thread. `part` is not used again
@@ -894,8 +894,8 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, int num_sms, cudaS
         e = p.h_bf16 ? go(std::true_type()) : go(std::false_type());
     }
     if (e == cudaSuccess && p.dweight) {
-        // Many blocks, of short rows: more and narrower blocks here (8192 x 256 beside bf16 9.1 us, with 32
-        // columns 10.5; 8192 x 7168 77.8 us, with 32 columns 74.9).
+        // Many blocks, of short rows: more and narrower blocks here (8192 x 256 beside bf16 8.8 us, with 32
+        // columns 9.9, 8192 x 1024 16.4 and 18.3; 8192 x 7168 77.1 us, with 32 columns 74.3).
         const bool narrow = grid > 640;
         const int columns = narrow ? 8 : 32;
         e = launch_behind(narrow ? norm_weight_kernel<8> : norm_weight_kernel<32>, (p.hidden + columns - 1) / columns,
