@@ -27,7 +27,7 @@
 //  * The second kernel starts while the first one's last blocks finish: a block makes its plan
 //    and fills its ring with weights before it waits for the activations.
 //
-// Measured (GB300, several boxes; weights' bytes of the copy bandwidth of 6.77 TB/s): a token with 2 of 8
+// Measured (several GB300s; weights' bytes of the copy bandwidth of 6.77 TB/s): a token with 2 of 8
 // experts of 4096 x 14336 113 to 116 us, 90 to 92 %; 16 tokens, 8 of 32 of 7168 x 2048 in e4m3 210 to 222 us,
 // 93 to 98 %; 64 tokens, 8 of 16 of 4096 x 2048 142 to 145 us, 82 to 84 %; 5 tokens, 3 of 12 of 1496 x 1000
 // 23 to 25 us, of which the bytes are 8.

@@ -96,3 +96,16 @@ def test_layer_of_a_few_tokens(fp8, gate):
     assert (got != 0).all()
     assert ((got - want).abs() <= BF16 * (want.abs() + off) + off).all()
     assert torch.equal(f.out[0], f.out[1])
+
+
+@pytest.mark.parametrize("gate", [-89.0, -200.0, -2.0 ** 100])
+def test_layer_of_a_few_tokens_behind_the_end(gate):
+    f = Few(2, 1, 1, 128, 128)
+    f.gates.fill_(1)
+    f.x[:, 0] = 1
+    f.W1[0, :128] = 0
+    f.W1[0, :128, 0] = gate
+    f.W2.fill_(2.0 ** 100)
+    f.call()
+    torch.cuda.synchronize()
+    assert int(f.status) == 0 and (f.out == 0).all()
