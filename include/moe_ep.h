@@ -788,8 +788,7 @@ int ep_swiglu_e4m3(const ep_config *cfg, const ep_swiglu_e4m3_args *args, ep_str
  *                   EP_FEW_COUNTER_BYTES zero before the first call that uses it (the rest of any
  *                   contents); a call that ends without EP_STATUS_TIMEOUT leaves it ready for the
  *                   next, of this configuration or of any other that it is large enough for (fewer
- *                   tokens, say). Calls that may run at the same time
- *                   need one each.
+ *                   tokens, say). Calls that may run at the same time need one each.
  *   status          EP_STATUS_ROUTING as above; EP_STATUS_TIMEOUT if a bounded wait inside a
  *                   kernel ran out: out is not to be used then, and those bytes are zeroed before
  *                   the workspace's next call
